@@ -26,6 +26,7 @@
 #include <tuple>
 #include <vector>
 
+#include "attn.h"
 #include "lbgemm.h"
 #include "simt.h"
 #include "tc_params.h"
@@ -158,6 +159,7 @@ struct DeviceState {
   Scratch host_stage;   // device staging for lbgemm_run_host
   Scratch flush;        // buffer written between timed runs to evict L2
   Scratch quant;        // quantised activations of lbgemm_linear_quant
+  Scratch attn;         // partial results of the attention operators
   std::map<const void*, int> occupancy;
   // lbgemm_run_host's copy streams (host-to-device, device-to-host) and events
   cudaStream_t copy_in = nullptr, copy_out = nullptr;
@@ -2112,6 +2114,9 @@ lbgemm_status lbgemm_device_status(void* stream) {
   if (word != 0) {
     const int zero = 0;
     cudaMemcpy(d->status, &zero, sizeof zero, cudaMemcpyHostToDevice);
+    if (word == lbg::kStatusBadIndex)  // no time-out bit beside it
+      return fail(LBGEMM_ERR_INVALID_ARG,
+                  "a kernel met a position, slot, page or length out of range");
     return fail(LBGEMM_ERR_TIMEOUT, "a device-side wait ran out of time (status %d)", word);
   }
   return LBGEMM_OK;
@@ -2139,6 +2144,29 @@ lbgemm_status report_error(lbgemm_status st, const char* message) {
 }
 
 void ensure_defaults() { ensure_default_table(); }
+
+lbgemm_status report_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+
+lbgemm_status call_device(CallDevice* out) {
+  DeviceState* d = nullptr;
+  lbgemm_status st = device_state(&d);
+  if (st != LBGEMM_OK) return st;
+  out->sm_count = d->sm_count;
+  out->status = d->status;
+  out->state = d;
+  return LBGEMM_OK;
+}
+
+lbgemm_status attn_scratch_acquire(const CallDevice& dev, size_t bytes, cudaStream_t s,
+                                   void** ptr) {
+  return scratch_acquire(static_cast<DeviceState*>(dev.state)->attn, bytes, s, ptr);
+}
+
+lbgemm_status attn_scratch_release(const CallDevice& dev, cudaStream_t s, void* ptr) {
+  return scratch_release(static_cast<DeviceState*>(dev.state)->attn, s, ptr);
+}
+
+void count_launches(int n) { g_launches += n; }
 
 // Scratch bytes that lbgemm_run_ws(bits, M, N, K, A, B, C, variant, ...)
 // needs: the route the dispatch takes (variant < 0) or the tensor-core

@@ -1,0 +1,100 @@
+// attn.h -- parameters and launchers of the attention operators: per-head
+// norm with rotation (norm_rope.cu), the 4-bit paged cache (kv4_cache.cu) and
+// attention over it (kv4_attention.cu); their C ABI is in attn_api.cu.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "lbgemm.h"
+
+namespace lbg {
+
+// Device status word: a kernel met an index out of range (beside the time-out
+// bit of ptx.cuh).
+constexpr int kStatusBadIndex = 2;
+
+// ---- what api.cu keeps for every entry point ------------------------------------
+struct CallDevice {
+  int sm_count = 0;
+  int* status = nullptr;
+  void* state = nullptr;  // api.cu's record of the device
+};
+lbgemm_status report_error(lbgemm_status st, const char* message);
+lbgemm_status report_cuda_error(cudaError_t e, const char* what);
+lbgemm_status call_device(CallDevice* out);
+// The attention operators' scratch on this device; the caller holds one lock
+// from acquire to release.
+lbgemm_status attn_scratch_acquire(const CallDevice& dev, size_t bytes, cudaStream_t s, void** ptr);
+lbgemm_status attn_scratch_release(const CallDevice& dev, cudaStream_t s, void* ptr);
+void count_launches(int n);
+
+// ---- norm and rotation ------------------------------------------------------------
+// One side (queries or keys) of a call.  x, w: the forward input; in: what the
+// pass turns (x, or dy for the backward pass); out: y, or dx.
+struct NormRopeSide {
+  const void* x = nullptr;
+  const void* w = nullptr;
+  const void* in = nullptr;
+  void* out = nullptr;
+  float* dw = nullptr;
+  int64_t x_stride = 0, in_stride = 0, out_stride = 0;
+};
+struct NormRopeParams {
+  NormRopeSide side[2];  // queries, keys
+  int heads[2] = {0, 0};
+  int64_t tokens = 0;
+  int dim = 0, rot = 0, interleaved = 0;
+  float eps = 0.0f;
+  const float *cosines = nullptr, *sines = nullptr;
+  int64_t table_rows = 0;
+  const int64_t* positions = nullptr;
+  int* status = nullptr;
+};
+cudaError_t launch_norm_rope(int dtype, const NormRopeParams& p, int sm_count, cudaStream_t s);
+// partial: scratch of norm_rope_scratch() bytes (unused when no weight is given).
+size_t norm_rope_scratch(const NormRopeParams& p, int sm_count);
+cudaError_t launch_norm_rope_backward(int dtype, const NormRopeParams& p, int sm_count,
+                                      float* partial, int* launches, cudaStream_t s);
+
+// ---- the cache ----------------------------------------------------------------------
+struct Kv4Cache {
+  uint8_t* base = nullptr;
+  int64_t pages = 0, page_size = 0;
+  int heads = 0, dim = 0;
+};
+// Byte offsets inside a head's block of a page.
+__host__ __device__ inline int64_t kv4_block_bytes(int64_t dim, int64_t page_size) {
+  return page_size * (dim + 4);
+}
+
+struct Kv4CopyParams {  // write: K, V -> cache; read: cache -> K, V
+  Kv4Cache cache;
+  int64_t tokens = 0;
+  void *k = nullptr, *v = nullptr;
+  int64_t k_stride = 0, v_stride = 0;
+  const int64_t* slots = nullptr;
+  int* status = nullptr;
+};
+cudaError_t launch_kv4_write(int dtype, const Kv4CopyParams& p, int sm_count, cudaStream_t s);
+cudaError_t launch_kv4_read(int dtype, const Kv4CopyParams& p, int sm_count, cudaStream_t s);
+
+// ---- attention ------------------------------------------------------------------------
+struct Kv4AttnParams {
+  Kv4Cache cache;  // heads = heads_kv
+  int batch = 0, total_q = 0, max_q = 0, heads_q = 0, group = 0;
+  const void* q = nullptr;
+  int64_t q_stride = 0;
+  const int32_t *cu_q = nullptr, *page_table = nullptr, *kv_lens = nullptr;
+  int64_t table_width = 0;
+  int max_kv = 0, causal = 0, window = 0;
+  float scale = 0.0f;
+  void* o = nullptr;
+  float* lse = nullptr;
+  int* status = nullptr;
+};
+cudaError_t launch_kv4_attention(int dtype, const Kv4AttnParams& p, int sm_count, int* launches,
+                                 cudaStream_t s);
+
+}  // namespace lbg

@@ -1,0 +1,80 @@
+// attn_common.cuh -- element conversions shared by the attention operators.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace lbg {
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) {
+  return __bfloat162float(x);
+}
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half x) {
+  return __half2float(x);
+}
+template <>
+__device__ __forceinline__ float to_f32<float>(float x) {
+  return x;
+}
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) {
+  return __float2half_rn(x);
+}
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) {
+  return x;
+}
+
+// Eight consecutive elements at a 16-byte-aligned address (16-bit types) or
+// 32 bytes at one (fp32), as loaded: 16 or 32 bytes in registers.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) == 4 ? 2 : 1];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8_raw(const T* p) {
+  Raw8<T> r;
+  r.v[0] = reinterpret_cast<const uint4*>(p)[0];
+  if constexpr (sizeof(T) == 4) r.v[1] = reinterpret_cast<const uint4*>(p)[1];
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&f)[8]) {
+  const T* h = reinterpret_cast<const T*>(&r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = to_f32(h[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
+  unpack8(load8_raw(p), f);
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
+  Raw8<T> r;
+  T* h = reinterpret_cast<T*>(&r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = from_f32<T>(f[i]);
+  reinterpret_cast<uint4*>(p)[0] = r.v[0];
+  if constexpr (sizeof(T) == 4) reinterpret_cast<uint4*>(p)[1] = r.v[1];
+}
+
+// Value of the signed nibble in bits 0..3.
+__device__ __forceinline__ int nibble_value(uint32_t n) { return (int)((n & 15u) ^ 8u) - 8; }
+
+}  // namespace lbg

@@ -32,6 +32,10 @@ STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "ALIGNMENT", 3: "UNSUPPORTED", 4: 
                 5: "TIMEOUT", 6: "WORKSPACE"}
 
 
+# element types of the attention operators (lbgemm_dtype)
+BF16, F16, F32 = range(3)
+
+
 class LbgemmError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"lbgemm {STATUS_NAMES.get(status, status)}: {message}")
@@ -97,6 +101,21 @@ _SIGNATURES = {
                                      ctypes.POINTER(ctypes.c_int)]),
     "lbgemm_get_fused_stream_k": (_i32, []),
     "lbgemm_get_tail_split": (_i32, []),
+    "lbgemm_qk_norm_rope": (_i32, [_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                   _f32, _vp, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64,
+                                   _vp]),
+    "lbgemm_qk_norm_rope_backward": (_i32, [_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                                            _vp, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _i64,
+                                            _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp,
+                                            _vp]),
+    "lbgemm_kv4_page_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "lbgemm_kv4_write": (_i32, [_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
+                                _vp]),
+    "lbgemm_kv4_read": (_i32, [_i32, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64,
+                               _vp]),
+    "lbgemm_kv4_attention": (_i32, [_i32, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp,
+                                    _i64, _i64, _vp, _i64, _vp, _i64, _f32, _i32, _i64, _vp, _vp,
+                                    _vp]),
     "lbgemm_device_status": (_i32, [_vp]),
     "lbgemm_selftest_timeout": (_i32, [_vp]),
     "lbgemm_last_error": (ctypes.c_char_p, []),
@@ -445,6 +464,56 @@ def lbgemm_fused_schedule(M, N, K, tile_n, linear=False, sm_count=152):
 
 def lbgemm_get_tail_split() -> int:
     return load().lbgemm_get_tail_split()
+
+
+def lbgemm_qk_norm_rope(dtype, tokens, heads_q, heads_k, head_dim, Q, q_stride, K, k_stride, wq, wk,
+                        eps, cosines, sines, table_rows, positions, rot_dim, interleaved, Q_out,
+                        q_out_stride, K_out, k_out_stride, stream=None) -> None:
+    _check(load().lbgemm_qk_norm_rope(dtype, tokens, heads_q, heads_k, head_dim, _addr(Q), q_stride,
+                                      _addr(K), k_stride, _addr(wq), _addr(wk), eps,
+                                      _addr(cosines), _addr(sines), table_rows, _addr(positions),
+                                      rot_dim, int(bool(interleaved)), _addr(Q_out), q_out_stride,
+                                      _addr(K_out), k_out_stride, _stream(stream)))
+
+
+def lbgemm_qk_norm_rope_backward(dtype, tokens, heads_q, heads_k, head_dim, dQ_out, dq_out_stride,
+                                 dK_out, dk_out_stride, Q, q_stride, K, k_stride, wq, wk, eps,
+                                 cosines, sines, table_rows, positions, rot_dim, interleaved, dQ,
+                                 dq_stride, dK, dk_stride, dwq, dwk, stream=None) -> None:
+    _check(load().lbgemm_qk_norm_rope_backward(
+        dtype, tokens, heads_q, heads_k, head_dim, _addr(dQ_out), dq_out_stride, _addr(dK_out),
+        dk_out_stride, _addr(Q), q_stride, _addr(K), k_stride, _addr(wq), _addr(wk), eps,
+        _addr(cosines), _addr(sines), table_rows, _addr(positions), rot_dim,
+        int(bool(interleaved)), _addr(dQ), dq_stride, _addr(dK), dk_stride, _addr(dwq),
+        _addr(dwk), _stream(stream)))
+
+
+def lbgemm_kv4_page_bytes(heads, head_dim, page_size) -> int:
+    return load().lbgemm_kv4_page_bytes(heads, head_dim, page_size)
+
+
+def lbgemm_kv4_write(dtype, tokens, heads, head_dim, K, k_stride, V, v_stride, slots, cache, pages,
+                     page_size, stream=None) -> None:
+    _check(load().lbgemm_kv4_write(dtype, tokens, heads, head_dim, _addr(K), k_stride, _addr(V),
+                                   v_stride, _addr(slots), _addr(cache), pages, page_size,
+                                   _stream(stream)))
+
+
+def lbgemm_kv4_read(dtype, tokens, heads, head_dim, slots, cache, pages, page_size, K, k_stride, V,
+                    v_stride, stream=None) -> None:
+    _check(load().lbgemm_kv4_read(dtype, tokens, heads, head_dim, _addr(slots), _addr(cache), pages,
+                                  page_size, _addr(K), k_stride, _addr(V), v_stride,
+                                  _stream(stream)))
+
+
+def lbgemm_kv4_attention(dtype, batch, total_q, max_q, heads_q, heads_kv, head_dim, Q, q_stride,
+                         cu_q, cache, pages, page_size, page_table, table_width, kv_lens, max_kv,
+                         scale, causal, window, O, lse=None, stream=None) -> None:
+    _check(load().lbgemm_kv4_attention(dtype, batch, total_q, max_q, heads_q, heads_kv, head_dim,
+                                       _addr(Q), q_stride, _addr(cu_q), _addr(cache), pages,
+                                       page_size, _addr(page_table), table_width, _addr(kv_lens),
+                                       max_kv, scale, int(bool(causal)), window, _addr(O),
+                                       _addr(lse), _stream(stream)))
 
 
 def lbgemm_device_status(stream=None) -> None:

@@ -515,11 +515,134 @@ int lbgemm_get_fused_stream_k(void);
 lbgemm_status lbgemm_fused_schedule(int64_t M, int64_t N, int64_t K, int tile_n, int linear,
                                     int sm_count, int* splits, int* stream_pieces);
 
+/* ---- attention around a cache held in 4 bits ----------------------------------
+ * What an attention layer needs between two of the quantised linear layers
+ * above: RMS norm of each query and key head with the position rotation in
+ * the same pass (and its backward pass), a paged cache of keys and values in
+ * 4 bits, and attention of new tokens over that cache.
+ *
+ * Conventions of this group
+ *   - dtype: the element type of the 16- or 32-bit tensors of a call.
+ *   - A [tokens, heads, head_dim] tensor is given by its pointer and its token
+ *     stride in elements (so a slice of a joint projection needs no copy); a
+ *     token's heads are dense.  Pointers are 16-byte aligned and strides times
+ *     the element size multiples of 16 (LBGEMM_ERR_ALIGNMENT); tensors
+ *     documented without a stride are dense.
+ *   - Indexes in device memory (positions, slots, page numbers, lengths) are
+ *     checked by the kernels: one that is out of range touches no memory and
+ *     sets the device status word, and the next lbgemm_device_status() returns
+ *     LBGEMM_ERR_INVALID_ARG; the output of the tokens concerned is
+ *     unspecified.
+ *   - Norms, softmax statistics and sums are held in fp32; each result is
+ *     rounded to dtype once, to nearest even.  Results do not depend on the
+ *     order in which CTAs finish. */
+typedef enum { LBGEMM_BF16 = 0, LBGEMM_F16 = 1, LBGEMM_F32 = 2 } lbgemm_dtype;
+
+/* y = R(positions) . (x * rstd * w) for every head x of Q (heads_q per token)
+ * and K (heads_k), with rstd = 1 / sqrt(mean(x^2) + eps):
+ *   - wq, wk: [head_dim] of dtype; NULL leaves the norm of that tensor out
+ *     (rotation only).
+ *   - R turns the pairs of the first rot_dim channels: (a, b) -> (a cos - b
+ *     sin, a sin + b cos), pair j being channels (j, j + rot_dim / 2), or
+ *     (2j, 2j + 1) when `interleaved` is not 0; the other channels keep their
+ *     value.  cosines, sines: fp32 [table_rows, rot_dim / 2]; a token's row is
+ *     positions[token].  rot_dim = 0 (tables and positions then unused): norm
+ *     only.
+ * dtype: any.  head_dim: a multiple of 8 up to 512; rot_dim even, 0 ..
+ * head_dim; heads_q + heads_k >= 1 (either may be 0, its pointers unused).
+ * Q_out may be Q and K_out K with equal strides (in place); no other overlap. */
+lbgemm_status lbgemm_qk_norm_rope(int dtype, int64_t tokens, int64_t heads_q, int64_t heads_k,
+                                  int64_t head_dim, const void* Q, int64_t q_stride, const void* K,
+                                  int64_t k_stride, const void* wq, const void* wk, float eps,
+                                  const float* cosines, const float* sines, int64_t table_rows,
+                                  const int64_t* positions, int64_t rot_dim, int interleaved,
+                                  void* Q_out, int64_t q_out_stride, void* K_out,
+                                  int64_t k_out_stride, void* stream);
+
+/* Its backward pass: from the gradients of the outputs (dQ_out, dK_out) and
+ * the inputs of the forward call, with g = R(-position) . dy and xhat = x *
+ * rstd:
+ *   dx = rstd * (w g - xhat * mean(w g xhat)),   dw = sum over tokens and heads of g xhat
+ * (dx = g where the weight is NULL).  dQ, dK: dtype; dwq, dwk: fp32
+ * [head_dim], NULL exactly where the weight is NULL, written whole (zeros for
+ * no tokens).  The sums run in a fixed order: the same call gives the same
+ * bits.  dQ may be dQ_out and dK dK_out with equal strides.  Scratch for the
+ * weights' partial sums is taken as in lbgemm_run. */
+lbgemm_status lbgemm_qk_norm_rope_backward(
+    int dtype, int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t head_dim,
+    const void* dQ_out, int64_t dq_out_stride, const void* dK_out, int64_t dk_out_stride,
+    const void* Q, int64_t q_stride, const void* K, int64_t k_stride, const void* wq,
+    const void* wk, float eps, const float* cosines, const float* sines, int64_t table_rows,
+    const int64_t* positions, int64_t rot_dim, int interleaved, void* dQ, int64_t dq_stride,
+    void* dK, int64_t dk_stride, float* dwq, float* dwk, void* stream);
+
+/* The cache: `pages` pages of page_size tokens (a multiple of 16), for
+ * `heads` key-value heads of head_dim 64 or 128.  A vector (a token's key or
+ * value of one head) is stored as signed 4-bit codes, in the nibble format of
+ * bits 4 above, and one bf16 scale; it stands for code * scale.
+ * Layout: page p starts at p * lbgemm_kv4_page_bytes(); in it each head has a
+ * block of page_size * (head_dim + 4) bytes: key codes [page_size][head_dim /
+ * 2], value codes [page_size][head_dim / 2], key scales bf16 [page_size],
+ * value scales bf16 [page_size].  Slot s of a cache is token s % page_size of
+ * page s / page_size.  A page serves one sequence.  The buffer is the
+ * caller's; its contents need no initialisation.
+ * lbgemm_kv4_page_bytes: bytes of one page, 0 for sizes out of range. */
+size_t lbgemm_kv4_page_bytes(int64_t heads, int64_t head_dim, int64_t page_size);
+
+/* Quantises keys and values of `tokens` tokens into the slots given for them
+ * (int64 in device memory; a negative slot skips its token; slots of one call
+ * are distinct):
+ *   scale = bf16(max|x| * (1.0f / 7)), code = clamp(round_half_even(x / scale), -7, 7)
+ * with fp32 arithmetic and IEEE division, so codes are reproducible bit for
+ * bit.  All codes are 0 where the scale is 0 or not finite: a vector with an
+ * infinity or a NaN reads back as NaN in every channel.  dtype: any. */
+lbgemm_status lbgemm_kv4_write(int dtype, int64_t tokens, int64_t heads, int64_t head_dim,
+                               const void* K, int64_t k_stride, const void* V, int64_t v_stride,
+                               const int64_t* slots, void* cache, int64_t pages,
+                               int64_t page_size, void* stream);
+
+/* Reads the vectors of the given slots back: K[t], V[t] = code * scale in
+ * fp32, rounded to dtype; zeros for a negative slot.  dtype: any. */
+lbgemm_status lbgemm_kv4_read(int dtype, int64_t tokens, int64_t heads, int64_t head_dim,
+                              const int64_t* slots, const void* cache, int64_t pages,
+                              int64_t page_size, void* K, int64_t k_stride, void* V,
+                              int64_t v_stride, void* stream);
+
+/* Attention of new tokens over the cache, for `batch` sequences of ragged
+ * lengths:
+ *   o_i = sum_j softmax_j(scale * q_i . k_j) v_j,   lse_i = log sum_j exp(scale * q_i . k_j)
+ * over the cached tokens j that row i sees.  Sequence b has the query rows
+ * cu_q[b] .. cu_q[b+1]-1 of Q (cu_q: int32 [batch+1], ascending, cu_q[0] = 0,
+ * cu_q[batch] = total_q) and kv_lens[b] cached tokens (int32), the new
+ * tokens' own among them (write them first); cached token j is token j %
+ * page_size of page page_table[b * table_width + j / page_size] (int32;
+ * entries beyond the length are not read).  With n rows and length L, row i
+ * stands at position L - n + i.  causal != 0: it sees the tokens up to its
+ * position, and with window > 0 only the last `window` of them; causal = 0
+ * (window must be 0): all L.  A row that sees nothing (an empty cache, a
+ * negative position) gets o = 0 and lse = -inf; tokens it does not see have
+ * no effect on it, whatever their scales hold.
+ * max_q, max_kv: bounds that no sequence's rows and length exceed (they size
+ * the launch; table_width * page_size may be larger than max_kv).
+ * dtype: LBGEMM_BF16 or LBGEMM_F16.  heads_q: a multiple of heads_kv; query
+ * heads h * heads_q / heads_kv and the following share key-value head h.
+ * O: [total_q, heads_q, head_dim] of dtype; lse: fp32 [total_q, heads_q],
+ * natural logarithm, or NULL.  Scratch for partial results of a cut cache is
+ * taken as in lbgemm_run. */
+lbgemm_status lbgemm_kv4_attention(int dtype, int64_t batch, int64_t total_q, int64_t max_q,
+                                   int64_t heads_q, int64_t heads_kv, int64_t head_dim,
+                                   const void* Q, int64_t q_stride, const int32_t* cu_q,
+                                   const void* cache, int64_t pages, int64_t page_size,
+                                   const int32_t* page_table, int64_t table_width,
+                                   const int32_t* kv_lens, int64_t max_kv, float scale, int causal,
+                                   int64_t window, void* O, float* lse, void* stream);
+
 /* ---- status ------------------------------------------------------------------ */
 
 /* Synchronises `stream`, then returns LBGEMM_ERR_TIMEOUT if any kernel of this
- * library on the current device stopped on a wait limit since the last call
- * (and clears that record), else LBGEMM_OK. */
+ * library on the current device stopped on a wait limit since the last call,
+ * else LBGEMM_ERR_INVALID_ARG if one met an index out of range in device
+ * memory (and clears that record), else LBGEMM_OK. */
 lbgemm_status lbgemm_device_status(void* stream);
 
 /* Diagnostic of the failure path: launches a one-thread kernel that waits on
