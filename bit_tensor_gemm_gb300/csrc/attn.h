@@ -81,6 +81,29 @@ cudaError_t launch_kv4_write(int dtype, const Kv4CopyParams& p, int sm_count, cu
 cudaError_t launch_kv4_read(int dtype, const Kv4CopyParams& p, int sm_count, cudaStream_t s);
 
 // ---- attention ------------------------------------------------------------------------
+// Division of non-negative 32-bit numbers by a number known at launch, as a
+// multiplication: x / d = (x * mul) >> 32 >> shift, exact for x < 2^31.
+struct FastDiv {
+  uint32_t mul = 0, shift = 0, d = 1;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div) {
+    if (div == 1) return;  // (mul 0: the number itself)
+    while ((uint64_t(1) << shift) < div) ++shift;
+    shift -= 1;
+    mul = (uint32_t)(((uint64_t(1) << (32 + shift)) + div - 1) / div);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+    return mul ? __umulhi(x, mul) >> shift : x;
+  }
+#endif
+};
+
+// A call's work is cut into units of (sequence, key-value head, tile of query
+// rows, chunk of the tokens that the tile sees).  A row is a (token, head of
+// the group) pair, token-major.  A tile with one chunk writes its rows of O;
+// else every chunk writes its share (o normalised by its own sum, and the
+// log2 of that sum) and a second kernel joins the shares in chunk order.
 struct Kv4AttnParams {
   Kv4Cache cache;  // heads = heads_kv
   int batch = 0, total_q = 0, max_q = 0, heads_q = 0, group = 0;
@@ -93,8 +116,17 @@ struct Kv4AttnParams {
   void* o = nullptr;
   float* lse = nullptr;
   int* status = nullptr;
+  // the cut, and the shares' scratch
+  FastDiv by_group, by_page16;  // rows by group, groups of 16 tokens by pages
+  int tile_rows = 0, row_tiles = 0, chunk = 0, max_chunks = 1;
+  float* share_o = nullptr;     // [unit][row][dim]
+  float* share_lse = nullptr;   // [unit][row]
 };
-cudaError_t launch_kv4_attention(int dtype, const Kv4AttnParams& p, int sm_count, int* launches,
-                                 cudaStream_t s);
+// Fills in the cut for this device; the scratch that it needs (0: none).
+size_t kv4_attention_plan(Kv4AttnParams* p, int sm_count);
+cudaError_t launch_kv4_attention(int dtype, const Kv4AttnParams& p, int* launches, cudaStream_t s);
+
+// The kernel for few rows (kv4_rows.cu): tiles of 8 or 16 rows.
+cudaError_t launch_kv4_rows(int dtype, const Kv4AttnParams& p, cudaStream_t s);
 
 }  // namespace lbg

@@ -346,8 +346,25 @@ lbgemm_status lbgemm_kv4_attention(int dtype, int64_t batch, int64_t total_q, in
     p.lse = lse;
     p.status = dev.status;
     int launches = 0;
-    cudaError_t e = launch_kv4_attention(dtype, p, dev.sm_count, &launches, as_stream(stream));
-    if (e != cudaSuccess) return report_cuda_error(e, "attention launch");
+    cudaStream_t s = as_stream(stream);
+    cudaError_t e;
+    const size_t bytes = kv4_attention_plan(&p, dev.sm_count);
+    if (bytes == 0) {
+      e = launch_kv4_attention(dtype, p, &launches, s);
+      if (e != cudaSuccess) return report_cuda_error(e, "attention launch");
+    } else {
+      std::lock_guard<std::mutex> lock(g_attn_mu);
+      void* scratch = nullptr;
+      st = attn_scratch_acquire(dev, bytes, s, &scratch);
+      if (st != LBGEMM_OK) return st;
+      const int64_t units = (int64_t)p.batch * heads_kv * p.row_tiles * p.max_chunks;
+      p.share_o = static_cast<float*>(scratch);
+      p.share_lse = p.share_o + units * p.tile_rows * head_dim;
+      e = launch_kv4_attention(dtype, p, &launches, s);
+      st = attn_scratch_release(dev, s, scratch);
+      if (e != cudaSuccess) return report_cuda_error(e, "attention launch");
+      if (st != LBGEMM_OK) return st;
+    }
     count_launches(launches);
     return LBGEMM_OK;
   } catch (...) {
