@@ -99,11 +99,19 @@ struct FastDiv {
 #endif
 };
 
-// A call's work is cut into units of (sequence, key-value head, tile of query
-// rows, chunk of the tokens that the tile sees).  A row is a (token, head of
-// the group) pair, token-major.  A tile with one chunk writes its rows of O;
-// else every chunk writes its share (o normalised by its own sum, and the
-// log2 of that sum) and a second kernel joins the shares in chunk order.
+// A call's work is a row of steps: for each sequence, each tile of its query
+// rows and each key-value head, the steps of 128 tokens that the tile sees.
+// A row is a (token, head of the group) pair, token-major.  Every CTA takes an
+// equal run of steps.  A tile that lies within one run is written to O; of one
+// that is cut, every CTA writes its share (o normalised by its own sum, and
+// the log2 of that sum), and a second kernel joins the shares in CTA order.
+// A CTA has at most two shares: the rest of a tile begun before its run (0)
+// and the begin of one that goes on after it (1).
+// The record of a cut tile, written by the CTA that begins it; kept by tile
+// where the call has no more tiles than CTAs, else by CTA.
+struct Kv4Join {
+  int seq_tile, head, first_cta, last_cta;  // last_cta < 0: not cut
+};
 struct Kv4AttnParams {
   Kv4Cache cache;  // heads = heads_kv
   int batch = 0, total_q = 0, max_q = 0, heads_q = 0, group = 0;
@@ -118,15 +126,19 @@ struct Kv4AttnParams {
   int* status = nullptr;
   // the cut, and the shares' scratch
   FastDiv by_group, by_page16;  // rows by group, groups of 16 tokens by pages
-  int tile_rows = 0, row_tiles = 0, chunk = 0, max_chunks = 1;
-  float* share_o = nullptr;     // [unit][row][dim]
-  float* share_lse = nullptr;   // [unit][row]
+  int tile_rows = 0, row_tiles = 0, ctas = 0;
+  int joins = 0, by_tile = 0;   // records (0: no tile can be cut)
+  Kv4Join* join = nullptr;      // [joins]
+  float* share_o = nullptr;     // [cta][2][tile_rows][dim]
+  float* share_lse = nullptr;   // [cta][2][tile_rows]
 };
-// Fills in the cut for this device; the scratch that it needs (0: none).
+// Fills in the cut for this device; the scratch that it needs.
 size_t kv4_attention_plan(Kv4AttnParams* p, int sm_count);
+void kv4_attention_scratch(Kv4AttnParams* p, void* scratch);
 cudaError_t launch_kv4_attention(int dtype, const Kv4AttnParams& p, int* launches, cudaStream_t s);
 
 // The kernel for few rows (kv4_rows.cu): tiles of 8 or 16 rows.
+int kv4_rows_per_sm(int tile_rows);  // CTAs that an SM holds
 cudaError_t launch_kv4_rows(int dtype, const Kv4AttnParams& p, cudaStream_t s);
 
 }  // namespace lbg

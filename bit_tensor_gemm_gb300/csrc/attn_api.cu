@@ -357,9 +357,7 @@ lbgemm_status lbgemm_kv4_attention(int dtype, int64_t batch, int64_t total_q, in
       void* scratch = nullptr;
       st = attn_scratch_acquire(dev, bytes, s, &scratch);
       if (st != LBGEMM_OK) return st;
-      const int64_t units = (int64_t)p.batch * heads_kv * p.row_tiles * p.max_chunks;
-      p.share_o = static_cast<float*>(scratch);
-      p.share_lse = p.share_o + units * p.tile_rows * head_dim;
+      kv4_attention_scratch(&p, scratch);
       e = launch_kv4_attention(dtype, p, &launches, s);
       st = attn_scratch_release(dev, s, scratch);
       if (e != cudaSuccess) return report_cuda_error(e, "attention launch");

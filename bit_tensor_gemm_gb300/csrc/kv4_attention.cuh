@@ -8,45 +8,104 @@ namespace lbg {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+constexpr int kStepTokens = 128;
+
 // A tile of query rows of one sequence, and the tokens [first, last) that any
-// of its rows sees; `base` is `first` rounded down to a multiple of 32, where
-// its chunks start.
+// of its rows sees; `base` is `first` rounded down to a multiple of 128, where
+// its steps start.  A tile with rows has at least one step.
 struct RowTile {
-  int q0, n, len;        // the sequence's first query row, its queries, its tokens
+  int b, q0, n, len;     // the sequence, its first query row, its queries, its tokens
   int r0, rows;          // the tile's first row and its rows (0: nothing to do)
-  int first, last, base, chunks;
+  int first, last, base, steps;
 };
 
-__device__ __forceinline__ RowTile row_tile(const Kv4AttnParams& p, int b, int tile) {
+__device__ __forceinline__ RowTile row_tile(const Kv4AttnParams& p, int seq_tile) {
   RowTile t;
-  t.q0 = p.cu_q[b];
-  t.n = p.cu_q[b + 1] - t.q0;
-  t.len = p.kv_lens[b];
+  t.b = p.row_tiles == 1 ? seq_tile : seq_tile / p.row_tiles;
+  t.q0 = __ldg(p.cu_q + t.b);
+  t.n = __ldg(p.cu_q + t.b + 1) - t.q0;
+  t.len = __ldg(p.kv_lens + t.b);
   if (t.q0 < 0 || t.n < 0 || t.q0 > p.total_q - t.n || t.n > p.max_q || t.len < 0 ||
       t.len > p.max_kv) {
-    if (threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+    atomicOr(p.status, kStatusBadIndex);
     if (t.q0 < 0 || t.n < 0 || t.q0 > p.total_q - t.n || t.n > p.max_q) t.n = 0;
     t.len = min(max(t.len, 0), p.max_kv);
   }
-  t.r0 = tile * p.tile_rows;
-  t.rows = min(p.tile_rows, t.n * p.group - t.r0);
-  if (t.rows <= 0) {
-    t.rows = t.first = t.last = t.base = t.chunks = 0;
-    return t;
-  }
+  t.r0 = (seq_tile - t.b * p.row_tiles) * p.tile_rows;
+  t.rows = max(0, min(p.tile_rows, t.n * p.group - t.r0));
   t.first = 0;
   t.last = t.len;
   if (p.causal) {
     const int before = t.len - t.n;  // position of the first query
     const int i0 = (int)p.by_group((uint32_t)t.r0);
-    const int i1 = (int)p.by_group((uint32_t)(t.r0 + t.rows - 1));
+    const int i1 = (int)p.by_group((uint32_t)(t.r0 + max(t.rows, 1) - 1));
     t.last = min(t.len, before + i1 + 1);
     if (p.window) t.first = max(0, before + i0 - p.window + 1);
   }
   if (t.last <= t.first) t.first = t.last = 0;
-  t.base = t.first & ~31;
-  t.chunks = max(1, (t.last - t.base + p.chunk - 1) / p.chunk);
+  t.base = t.first & ~(kStepTokens - 1);
+  t.steps = t.rows == 0 ? 0 : max(1, (t.last - t.base + kStepTokens - 1) / kStepTokens);
   return t;
+}
+
+// This CTA's run of steps: it begins `off` steps into head `head` of sequence
+// tile `seq_tile`; `count` steps (0: none), the first of them being step `pos`
+// of the whole row, which is cut into runs of `per`.
+struct Run {
+  int seq_tile, head, off, count;
+  int64_t pos, per;
+};
+
+// Threads take equal segments of the sequence tiles, sum their steps, and the
+// one whose segment holds the run's begin looks it up.  THREADS: of the block.
+template <int THREADS>
+__device__ __forceinline__ Run find_run(const Kv4AttnParams& p, int min_steps) {
+  __shared__ int64_t warp_sum[THREADS / 32];
+  __shared__ Run run;
+  const int tiles = p.batch * p.row_tiles, seg = (tiles + THREADS - 1) / THREADS;
+  const int from = min(tiles, (int)threadIdx.x * seg), to = min(tiles, from + seg);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int64_t mine = 0;
+  for (int i = from; i < to; ++i) mine += row_tile(p, i).steps;
+  int64_t upto = mine;  // inclusive over the warp, then the block
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += v;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  int64_t total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  const int64_t heads = p.cache.heads;
+  total *= heads;
+  const int64_t per = max((int64_t)min_steps, (total + gridDim.x - 1) / (int64_t)gridDim.x);
+  const int64_t pos = per * blockIdx.x;
+  if (pos >= total) {
+    Run none = {0, 0, 0, 0, pos, per};
+    return none;
+  }
+  int64_t at = (before + upto - mine) * heads;  // steps before this thread's segment
+  if (pos >= at && pos < at + mine * heads) {
+    int i = from, n = 0;
+    for (; i < to; ++i) {
+      n = row_tile(p, i).steps;
+      if (pos < at + n * heads) break;
+      at += n * heads;
+    }
+    run.seq_tile = i;
+    run.head = (int)((pos - at) / n);
+    run.off = (int)(pos - at - (int64_t)run.head * n);
+    run.count = (int)min(per, total - pos);
+    run.pos = pos;
+    run.per = per;
+  }
+  __syncthreads();
+  return run;
 }
 
 // One past the last token that a row at query i of the sequence sees (may be
@@ -56,11 +115,6 @@ __device__ __forceinline__ int last_seen(const Kv4AttnParams& p, const RowTile& 
 }
 __device__ __forceinline__ int first_seen(const Kv4AttnParams& p, int last) {
   return p.window ? last - p.window : 0;
-}
-
-__device__ __forceinline__ int64_t unit_of(const Kv4AttnParams& p, int b, int head, int tile,
-                                           int chunk) {
-  return (((int64_t)b * p.cache.heads + head) * p.row_tiles + tile) * p.max_chunks + chunk;
 }
 
 // Offset into O (in rows of dim) of row r of a tile.

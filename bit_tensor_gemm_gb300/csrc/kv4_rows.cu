@@ -8,19 +8,26 @@
 // instructions per code low:
 //   - warp MMAs with the cached tokens (keys) or channels (values) as the 16
 //     rows and the query rows as the 8 columns, so 8 rows cost no padding;
-//   - a code becomes a float by one shift and one logical operation on two
-//     codes at once: n = code + 8 placed in the mantissa of 16.0 is 16 + n.
-//     For keys the constant 24 is taken out of the product by starting the
-//     accumulators at -24 sum(q); for values it is subtracted, since there the
-//     products add up over thousands of tokens and the constant would cost
-//     digits;
+//   - a code becomes an fp16 by one logical operation on two codes at once
+//     (and a shift for every second pair): n = code + 8 in the lowest bits of
+//     a half is the subnormal n 2^-24, in bits 4..7 it is 16 n 2^-24; MMAs take
+//     subnormals exactly.  Logic and shifts issue at half rate, and with 8
+//     floats a register built from exponents (three more of them per 8 codes)
+//     that pipe was the bound: 52 -> 33 us over 131072 tokens.
+//   - the constant 8 is taken out of the key product by starting the
+//     accumulators at -8 sum(q); for values it is subtracted in fp16 (exact),
+//     since there the products add up over thousands of tokens and the
+//     constant would cost digits;
+//   - queries enter as fp16 times a power of two of their row (exact for
+//     elements down to 2^-35 of the row's largest);
 //   - the order of channels in a product is free, so a lane's codes are used
 //     in the order in which they lie in memory;
 //   - the running maximum, and the largest weight seen, move only when a score
 //     or weight exceeds them 2^8 or 2^4 times, so almost no step rescales its
 //     accumulators.
-// Every warp streams its own tokens (32 a step) through its own ring of bulk
-// copies, with no barrier between warps until the end.
+// A CTA streams 128 tokens a step through a ring of bulk copies; each of its
+// four warps takes 32 of them, with a running maximum and sum of its own until
+// the end.  The warps issue the copies in turn.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -31,14 +38,17 @@
 namespace lbg {
 namespace {
 
-constexpr int kWarps = 4, kStages = 3, kStep = 32;
-constexpr float kLeastTop = 2.4074124e-35f;  // 2^-115: 2^11 over it is finite
+constexpr int kWarps = 4, kStages = 3, kTokens = 32, kStep = kStepTokens;
+constexpr int kMinSteps = 2;  // of a CTA's run
+static_assert(kWarps * kTokens == kStep, "a warp's share of a step");
+constexpr float kFar = 1.2676506e30f;       // 2^100
+constexpr float kLeastTop = 8.2718061e-25f;  // 2^-80
 
 template <int DIM>
 struct Ring {
   static constexpr int kCodes = kStep * DIM / 2;     // bytes of keys (or values) of a step
   static constexpr int kBytes = 2 * kCodes + 4 * kStep;
-  static constexpr int kTotal = kWarps * kStages * kBytes;
+  static constexpr int kTotal = kStages * kBytes;
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -49,40 +59,54 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes i and i + 4 of a word as two 16-bit floats 16 + (code + 8).  The
-// nibble goes to the top four bits of the mantissa of 16.0 (7 bits in bf16,
-// 10 in fp16), its sign bit flipped by the constant.
-template <bool BF16, int I>
-__device__ __forceinline__ uint32_t codes24(uint32_t w) {
-  constexpr int SHIFT = 4 * I - (BF16 ? 3 : 6);
-  constexpr uint32_t MASK = BF16 ? 0x00780078u : 0x03C003C0u;
-  constexpr uint32_t SET = BF16 ? 0x41C041C0u : 0x4E004E00u;
-  const uint32_t s = SHIFT >= 0 ? w >> (SHIFT >= 0 ? SHIFT : 0) : w << (SHIFT < 0 ? -SHIFT : 0);
-  return (s & MASK) ^ SET;
+// The same from other accumulators: d = c + a b.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], float c0, float c1, uint32_t a0,
+                                              uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %10, %11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
-// The same as the codes themselves, in fp16.
-template <int I>
-__device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
-  const uint32_t c = codes24<false, I>(w);
-  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&c), __half2half2(__half(24.0f)));
+
+// Codes 0 and 4 of a word (HIGH: 1 and 5) as two subnormal halves: (code + 8)
+// 2^-24, or 16 times that.  Codes 2, 6 and 3, 7 are those of the word >> 8.
+// One three-input operation, (w & mask) ^ eight: left to the compiler it became
+// two (45.1 -> XX us over 131072 tokens).
+template <bool HIGH>
+__device__ __forceinline__ uint32_t codes8(uint32_t w) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;"
+      : "=r"(d)
+      : "r"(w), "r"(HIGH ? 0x00F000F0u : 0x000F000Fu), "r"(HIGH ? 0x00800080u : 0x00080008u));
+  return d;
+}
+// The same without the 8: code 2^-24, or 16 times that (exact).
+template <bool HIGH>
+__device__ __forceinline__ uint32_t codes0(uint32_t w) {
+  const uint32_t c = codes8<HIGH>(w), eight = HIGH ? 0x00800080u : 0x00080008u;
+  const __half2 v =
+      __hsub2(*reinterpret_cast<const __half2*>(&c), *reinterpret_cast<const __half2*>(&eight));
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Four 8 x 8 matrices of halves, transposed: lane l gives the address of row
+// l % 8 of matrix l / 8 and gets rows 2 (l % 4) and + 1 of column l / 4 of each.
+__device__ __forceinline__ void load_transposed(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -99,442 +123,489 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 // Element order inside a warp (lane = 4 g + c):
 //   keys    MMA row g of a 16-token tile is token 2 g + e(g), row g + 8 the
 //           other token of that pair, e(g) = parity of the low two bits of g:
-//           so a lane's two tokens share one 32-bit word of scales, and reads
-//           of keys and values by the lanes of a phase fall on different
-//           banks (values: two lanes a bank, the least that 8-byte reads of
-//           64-byte rows allow).  A lane holds the channels c DIM/4 ... of its
-//           tokens; word w, code i and i + 4 make one register.
-//   values  lane (g, c) holds the channels g DIM/8 ... of the tokens of MMA
-//           rows 2c, 2c + 1, 2c + 8, 2c + 9; MMA tile i, row g is channel
-//           g DIM/8 + 2 i, row g + 8 the one after it.
+//           so a lane's two tokens share one 32-bit word of scales, and the
+//           key reads of a phase fall on different banks.  A lane holds the
+//           channels c DIM/4 ... of its tokens; of a word, codes i and i + 4
+//           make one register.
+//   values  transposing loads give a lane half word g of the 16-byte chunk q of
+//           the tokens of MMA rows 2c, 2c + 1 (then 2c + 8, 2c + 9) side by
+//           side: four codes each.  MMA tile 2 q + j, row g is channel 32 q +
+//           4 g + 2 j, row g + 8 the one after it.
 template <typename T, int DIM, int NT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     kv4_rows_kernel(const Kv4AttnParams p) {
-  constexpr bool BF16 = sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
   constexpr int KW = DIM / 32;   // 32-bit words of a key that a lane holds
-  constexpr int VW = DIM / 64;   // of a value
   constexpr int MT = DIM / 16;   // MMA tiles of channels
   constexpr int R = 8 * NT;
   using Rg = Ring<DIM>;
+  constexpr int ROW = DIM + 4;  // floats from a row to the next in the merge buffer
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
-  __shared__ float merge_m[kWarps][R], merge_l[kWarps][R];
+  __shared__ __align__(8) uint64_t bars[2][kStages];  // full, empty
+  __shared__ float merge_ref[kWarps][R], merge_l[kWarps][R];
   __shared__ int abort_flag;
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, c = lane % 4;
-  const int tile = (int)(blockIdx.x / (unsigned)p.max_chunks);
-  const int chunk = (int)(blockIdx.x - (unsigned)tile * p.max_chunks);
-  const int head = blockIdx.y, b = blockIdx.z;
-  const RowTile t = row_tile(p, b, tile);
-  if (chunk >= t.chunks) return;
-  const int begin = t.base + chunk * p.chunk;
-  const int end = min(t.last, begin + p.chunk);
-
-  const uint32_t bar0 = smem_addr(&bars[warp][0]);
-  const uint32_t ring = smem_addr(smem) + (uint32_t)(warp * kStages * Rg::kBytes);
+  const uint32_t full = smem_addr(&bars[0][0]), empty = smem_addr(&bars[1][0]);
+  if (threadIdx.x < kStages) {
+    mbar_init(full + 8 * threadIdx.x, 1);
+    mbar_init(empty + 8 * threadIdx.x, kWarps);
+  }
   if (threadIdx.x == 0) abort_flag = 0;
-  if (lane < kStages) mbar_init(bar0 + 8 * lane, 1);
   fence_barrier_init();
-  __syncthreads();
+  // the kernel that joins shares may be scheduled once every CTA has begun
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Run run = find_run<kWarps * 32>(p, kMinSteps);  // (with a barrier of the block)
+  if (p.joins > 0 && !p.by_tile && threadIdx.x == 0) p.join[blockIdx.x].last_cta = -1;
+  if (run.count == 0) return;
 
-  // ---- copies: this warp's step s covers the 32 tokens from
-  // begin + (s kWarps + warp) 32.  One copy per piece (keys, values, two
-  // arrays of scales) and run of tokens in one page: the whole step when
-  // pages are multiples of 32, else 16 tokens.
-  const int steps = max(0, (end - begin - warp * kStep + kWarps * kStep - 1) / (kWarps * kStep));
-  const int runs = p.cache.page_size % kStep ? 2 : 1, run_tokens = kStep / runs;
-  const int my_run = lane >> 2, piece = lane & 3;
-  const bool copies = lane < 4 * runs;
-  const int32_t* table = p.page_table + (int64_t)b * p.table_width;
-  const int page16 = (int)(p.cache.page_size / 16);
-  const uint32_t piece_bytes =
-      (uint32_t)(piece < 2 ? run_tokens * (DIM / 2) : run_tokens * 2);
-  const uint32_t piece_dst = (uint32_t)(piece < 2 ? piece * Rg::kCodes + my_run * run_tokens * (DIM / 2)
-                                                  : 2 * Rg::kCodes + (piece - 2) * 2 * kStep +
-                                                        my_run * run_tokens * 2);
-  const int64_t block_bytes = kv4_block_bytes(DIM, p.cache.page_size);
-  const int64_t piece_src = (int64_t)p.cache.page_size * (piece < 2 ? piece * (DIM / 2)
-                                                                    : DIM + (piece - 2) * 2);
-  auto step_token = [&](int s) { return begin + (s * kWarps + warp) * kStep; };
-  // page number of this lane's run in step s (-1: no copy)
-  auto page_of = [&](int s) -> int {
-    const int token = step_token(s) + my_run * run_tokens;
-    if (!copies || s >= steps || token >= end) return -1;
-    const int page = __ldg(table + p.by_page16((uint32_t)token / 16));
-    if (page >= 0 && page < p.cache.pages) return page;
-    atomicOr(p.status, kStatusBadIndex);
-    return -1;
+  // ---- copies.  Step s of the run: one copy per piece (keys, values, two
+  // arrays of scales: lane % 4) and stretch of tokens that certainly lie in one
+  // page (lane / 4).  Warp s % 4 issues step s + 2 when it begins step s, into
+  // the slot that step s - 1 leaves.
+  const uint32_t ring = smem_addr(smem);
+  const int page_size = (int)p.cache.page_size;
+  const int stretch =
+      page_size % 128 == 0 ? 128 : page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
+  const int piece = lane & 3, stretch_at = (lane >> 2) * stretch;  // its first token in a step
+  const uint32_t page16 = (uint32_t)page_size / 16;
+  const uint32_t row_bytes = piece < 2 ? DIM / 2 : 2;
+  const uint32_t piece_dst = ring +
+                             (piece < 2 ? piece * Rg::kCodes : 2 * Rg::kCodes + (piece - 2) * 2 * kStep) +
+                             stretch_at * row_bytes;
+  const int64_t block_bytes = kv4_block_bytes(DIM, page_size);
+  const uint8_t* piece_src =
+      p.cache.base + (int64_t)page_size * (piece < 2 ? piece * (DIM / 2) : DIM + (piece - 2) * 2);
+  // where the next step that this warp issues stands, and its lane's source
+  int is_tile = run.seq_tile, is_head = run.head, is_off = run.off, is_step = 0;
+  RowTile is = row_tile(p, is_tile);
+  const uint8_t* is_src = nullptr;
+  auto advance = [&](int by) {  // to a step `by` further on, and its page
+    is_step += by;
+    is_src = nullptr;
+    if (is_step >= run.count) return;
+    is_off += by;
+    while (is_off >= is.steps) {
+      is_off -= is.steps;
+      if (++is_head == p.cache.heads) {
+        is_head = 0;
+        do is = row_tile(p, ++is_tile);
+        while (is.steps == 0);  // (there is one with steps: the run goes on)
+      }
+    }
+    const int token = is.base + is_off * kStep + stretch_at;
+    if (stretch_at >= kStep || token >= is.last) return;
+    const uint32_t group = (uint32_t)token / 16, in_table = p.by_page16(group);
+    const int page = __ldg(p.page_table + (int64_t)is.b * p.table_width + in_table);
+    if ((uint32_t)page >= (uint32_t)p.cache.pages) {
+      atomicOr(p.status, kStatusBadIndex);
+      return;
+    }
+    is_src = piece_src + ((int64_t)page * p.cache.heads + is_head) * block_bytes +
+             (group - in_table * page16) * 16 * row_bytes;
   };
-  auto issue = [&](int s, int page) {
-    const uint32_t stage = (uint32_t)(s % kStages), bar = bar0 + 8 * stage;
-    uint32_t total = page >= 0 ? piece_bytes : 0;
-#pragma unroll
-    for (int off = 4; off >= 1; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    if (lane == 0) mbar_arrive_expect_tx(bar, total);
+  auto issue = [&]() {
+    const uint32_t slot = (uint32_t)(is_step % kStages), bar = full + 8 * slot;
+    const uint32_t lanes = __popc(__ballot_sync(0xffffffffu, is_src != nullptr));  // four a stretch
+    if (lane == 0) mbar_arrive_expect_tx(bar, lanes / 4 * stretch * (DIM + 4));
     __syncwarp();
-    if (page >= 0) {
-      const uint32_t group = (uint32_t)(step_token(s) + my_run * run_tokens) / 16;
-      const int inside = (int)(group - p.by_page16(group) * page16) * 16;
-      const uint8_t* src = p.cache.base + ((int64_t)page * p.cache.heads + head) * block_bytes +
-                           piece_src + inside * (piece < 2 ? DIM / 2 : 2);
-      bulk_load(ring + stage * Rg::kBytes + piece_dst, src, piece_bytes, bar);
-    }
+    if (is_src) bulk_load(piece_dst + slot * Rg::kBytes, is_src, stretch * row_bytes, bar);
   };
-  int next_page = page_of(0);
-#pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    const int page = next_page;
-    next_page = page_of(s + 1);
-    if (s < steps) issue(s, page);
+  advance(warp);
+  if (warp < kStages) {
+    if (is_step < run.count) issue();
+    // the first step that this warp issues in the loop
+    advance(warp == 0 ? kWarps + 2 : 2);
+  } else {
+    advance(2);
   }
 
-  // ---- queries: B fragments, column g of tile nt is row t.r0 + 8 nt + g
-  uint32_t q[NT][MT][2];
-  float bias[NT][2];   // -24 sum(q) of columns 2c, 2c + 1
-  int seen_to[NT][2];  // one past the last token that columns 2c, 2c + 1 see
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = 8 * nt + g;
-    uint32_t raw[DIM / 8];  // DIM / 4 elements: two a word
-#pragma unroll
-    for (int i = 0; i < DIM / 8; ++i) raw[i] = 0;
-    if (r < t.rows) {
-      const int row = t.r0 + r, i = (int)p.by_group((uint32_t)row);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const T*>(p.q) + (int64_t)(t.q0 + i) * p.q_stride +
-          (int64_t)(head * p.group + row - i * p.group) * DIM + c * (DIM / 4));
-#pragma unroll
-      for (int i4 = 0; i4 < DIM / 32; ++i4)
-        reinterpret_cast<uint4*>(raw)[i4] = __ldg(src + i4);
-    }
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < DIM / 8; ++i) {
-      const T* h = reinterpret_cast<const T*>(&raw[i]);
-      sum += to_f32(h[0]) + to_f32(h[1]);
-    }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) bias[nt][e] = -24.0f * __shfl_sync(0xffffffffu, sum, 4 * (2 * c + e));
-    // channels (d, d + 4) of a word of codes make a register
-#pragma unroll
-    for (int w = 0; w < KW; ++w)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        q[nt][2 * w + i / 2][i % 2] =
-            __byte_perm(raw[4 * w + i / 2], raw[4 * w + 2 + i / 2], i % 2 ? 0x7632 : 0x5410);
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      seen_to[nt][e] = last_seen(p, t, (int)p.by_group((uint32_t)(t.r0 + 8 * nt + 2 * c + e)));
-  }
-  // steps wholly inside [all_from, all_to) need no mask
-  const int i_last = (int)p.by_group((uint32_t)(t.r0 + t.rows - 1));
-  const int all_to = min(end, last_seen(p, t, (int)p.by_group((uint32_t)t.r0)));
-  const int all_from = p.window ? max(t.first, first_seen(p, last_seen(p, t, i_last))) : 0;
-
-  const float to_log2 = p.scale * kLog2e;
   const int eg = (g ^ (g >> 1)) & 1;        // e(g)
   const int tok_a = 2 * g + eg, tok_b = 2 * g + 1 - eg;
   const uint32_t sel_a = eg ? 0x3244u : 0x1044u, sel_b = eg ? 0x1044u : 0x3244u;
-  const int cp = c & 1;
-  // values: byte offsets of the tokens of rows 2c, 2c + 1, 2c + 8, 2c + 9
-  const uint32_t v_off[4] = {(uint32_t)(4 * c + cp) * (DIM / 2), (uint32_t)(4 * c + 3 - cp) * (DIM / 2),
-                             (uint32_t)(4 * c + 1 - cp) * (DIM / 2), (uint32_t)(4 * c + 2 + cp) * (DIM / 2)};
+  // values: this lane's row of the transposing loads
+  const int v_row = lane & 7, v_e = (v_row ^ (v_row >> 1)) & 1;
+  const uint32_t v_lane =
+      (uint32_t)((2 * v_row + (lane & 8 ? 1 - v_e : v_e)) * (DIM / 2) + (lane & 16)) +
+      (uint32_t)(Rg::kCodes + warp * kTokens * (DIM / 2));
 
-  // per column: the running maximum m (lagging by at most 2^8), the sum l of
-  // the weights 2^(t - m), and the unit of o: weights enter the value product
-  // in fp16 as (weight x value scale) 2^11 / wtop, where wtop has been the
-  // largest such weight of this column and is followed when one exceeds it
-  // 2^4 times: at most 2^15, and normal down to 2^-25 of the largest,
-  // whatever scores and scales look like
-  float o[MT][NT][4], m[NT][2], l[NT][2], wtop[NT][2];
+  bool dead = false;  // a wait ran out: no more waits and sums, but every barrier
+  int seq_tile = run.seq_tile, head = run.head, off = run.off, done = 0;
+  RowTile t = row_tile(p, seq_tile);
+  while (true) {
+    const int piece_steps = min(t.steps - off, run.count - done);
+    const int end = t.last;
+    // ---- queries: B fragments, column g of tile nt is row t.r0 + 8 nt + g
+    uint32_t q[NT][MT][2];
+    float bias[NT][2];   // -8 sum(q) of columns 2c, 2c + 1, in the accumulators' unit
+    int seen_to[NT][2];  // one past the last token that columns 2c, 2c + 1 see
+    // The tile's power of two: its largest element goes to 2^14 .. 2^15, so that
+    // in fp16 every element keeps its digits down to 2^-28 of that, and scores
+    // are off by at most 2^-39 of the tile's largest.
+    uint32_t raw[NT][DIM / 8];  // DIM / 4 elements of row 8 nt + g: two a word
+    float most = 0.0f;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      m[nt][e] = -3.0e38f;
-      l[nt][e] = 0.0f;
-      wtop[nt][e] = kLeastTop;
+      for (int i = 0; i < DIM / 8; ++i) raw[nt][i] = 0;
+      if (r < t.rows) {
+        const int row = t.r0 + r, i = (int)p.by_group((uint32_t)row);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const T*>(p.q) + (int64_t)(t.q0 + i) * p.q_stride +
+            (int64_t)(head * p.group + row - i * p.group) * DIM + c * (DIM / 4));
+#pragma unroll
+        for (int i4 = 0; i4 < DIM / 32; ++i4)
+          reinterpret_cast<uint4*>(raw[nt])[i4] = __ldg(src + i4);
+      }
+      const T* x = reinterpret_cast<const T*>(raw[nt]);
+#pragma unroll
+      for (int i = 0; i < DIM / 4; ++i) {
+        const float a = fabsf(to_f32(x[i]));
+        if (a < INFINITY) most = fmaxf(most, a);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int x = 16; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+    int k = 0;
+    if (most > 0.0f) k = min(max(14 - ((int)(__float_as_uint(most) >> 23) - 127), -103), 126);
+    const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+    // the accumulators' unit, 2^(24 - k), times scale log2(e)
+    const float factor = __uint_as_float((uint32_t)(127 + 24 - k) << 23) * (p.scale * kLog2e);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.0f;
-  }
-
-  bool ok = true;
-  for (int s = 0; s < steps; ++s) {
-    const uint32_t stage = (uint32_t)(s % kStages);
-    ok = ok && mbar_wait(bar0 + 8 * stage, (uint32_t)(s / kStages) & 1u, &abort_flag, p.status);
-    if (!ok) {  // a wait ran out: let the copies in flight land (again with a limit)
-      volatile int go_on = 0;
-      for (int k = 0; k < kStages && s + k < steps; ++k)
-        mbar_wait(bar0 + 8 * ((s + k) % kStages), (uint32_t)((s + k) / kStages) & 1u, &go_on,
-                  p.status, kWaitLimitNs / 8);
-      break;
+    for (int nt = 0; nt < NT; ++nt) {
+      const T* x = reinterpret_cast<const T*>(raw[nt]);
+      float sum = 0.0f;
+      // channels (d, d + 4) of a word of codes make a register; those of odd
+      // codes, whose halves are 16 times larger, are divided by 16
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = i % 2 ? up * 0.0625f : up;
+          const __half2 h = __floats2half2_rn(to_f32(x[8 * w + i]) * f, to_f32(x[8 * w + i + 4]) * f);
+          q[nt][2 * w + i / 2][i % 2] = *reinterpret_cast<const uint32_t*>(&h);
+          const float2 v = __half22float2(h);
+          sum += (v.x + v.y) * (i % 2 ? 16.0f : 1.0f);
+        }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        bias[nt][e] = __shfl_sync(0xffffffffu, sum, 4 * (2 * c + e)) * (-8.0f / 16777216.0f);
+        seen_to[nt][e] = last_seen(p, t, (int)p.by_group((uint32_t)(t.r0 + 8 * nt + 2 * c + e)));
+      }
     }
-    const uint8_t* buf = smem + (warp * kStages + stage) * Rg::kBytes;
-    const int token0 = step_token(s);
-    const bool masked = token0 < all_from || token0 + kStep > all_to;
+    // steps wholly inside [all_from, all_to) need no mask
+    const int i_last = (int)p.by_group((uint32_t)(t.r0 + t.rows - 1));
+    const int all_to = min(end, last_seen(p, t, (int)p.by_group((uint32_t)t.r0)));
+    const int all_from = p.window ? max(t.first, first_seen(p, last_seen(p, t, i_last))) : 0;
 
-    float sc[2][NT][4];  // scores of the step's two 16-token tiles, in log2 units
-    float vs[2][2];      // value scales of the lane's tokens
+    // Per column: the weights are 2^(t - ref), l their sum, and weight x value
+    // scale goes into the value product in fp16.  `ref` is such that the largest
+    // of those products so far was 2^10 .. 2^11 when it was set (and moves when
+    // one exceeds 2^15, or a weight 2^100): fp16 then holds them without loss
+    // down to 2^-24 of the largest, whatever scores and scales look like.
+    // m, wtop: the largest score, and the largest product relative to 2^m.
+    float o[MT][NT][4], ref[NT][2], l[NT][2], m[NT][2], wtop[NT][2];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const uint8_t* kp = buf + mt * 16 * (DIM / 2) + c * (DIM / 8);
-      uint32_t ka[KW], kb[KW];
-      if constexpr (KW == 4) {
-        *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(kp + tok_a * (DIM / 2));
-        *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(kp + tok_b * (DIM / 2));
-      } else {
-        *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(kp + tok_a * (DIM / 2));
-        *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(kp + tok_b * (DIM / 2));
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        ref[nt][e] = m[nt][e] = -3.0e38f;
+        l[nt][e] = wtop[nt][e] = 0.0f;
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        sc[mt][nt][0] = sc[mt][nt][2] = bias[nt][0];
-        sc[mt][nt][1] = sc[mt][nt][3] = bias[nt][1];
-      }
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        {
-          const uint32_t a0 = codes24<BF16, 0>(ka[w]), a1 = codes24<BF16, 0>(kb[w]);
-          const uint32_t a2 = codes24<BF16, 1>(ka[w]), a3 = codes24<BF16, 1>(kb[w]);
+        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+    }
+
+    for (int s = done; s < done + piece_steps; ++s) {
+      const uint32_t slot = (uint32_t)(s % kStages);
+      if (s + 2 == is_step && !dead) {
+        const int old = s - 1;  // the step whose slot this is
+        if (is_step < run.count) {
+          dead = !mbar_wait(empty + 8 * (old % kStages), (uint32_t)(old / kStages) & 1u, &abort_flag,
+                            p.status);
+          if (!dead) issue();
+        }
+        advance(kWarps);
+      }
+      if (!dead)
+        dead = !mbar_wait(full + 8 * slot, (uint32_t)(s / kStages) & 1u, &abort_flag, p.status);
+      const int token0 = t.base + (off + s - done) * kStep + warp * kTokens;
+      if (token0 < end && !dead) {
+        const uint8_t* buf = smem + slot * Rg::kBytes;
+        float acc[2][NT][4];     // q . (key codes) of the two 16-token tiles
+        float ks[2][2], vs[2][2];  // scales of the lane's tokens (keys': times factor)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint8_t* kp = buf + (warp * kTokens + mt * 16) * (DIM / 2) + c * (DIM / 8);
+          uint32_t ka[KW], kb[KW];
+          if constexpr (KW == 4) {
+            *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(kp + tok_a * (DIM / 2));
+            *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(kp + tok_b * (DIM / 2));
+          } else {
+            *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(kp + tok_a * (DIM / 2));
+            *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(kp + tok_b * (DIM / 2));
+          }
+#pragma unroll
+          for (int w = 0; w < KW; ++w)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // codes 0, 1 (with 4, 5), then 2, 3 (with 6, 7)
+              const uint32_t wa = i ? ka[w] >> 8 : ka[w], wb = i ? kb[w] >> 8 : kb[w];
+              const uint32_t a0 = codes8<false>(wa), a1 = codes8<false>(wb);
+              const uint32_t a2 = codes8<true>(wa), a3 = codes8<true>(wb);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (w == 0 && i == 0)
+                  mma16816_from(acc[mt][nt], bias[nt][0], bias[nt][1], a0, a1, a2, a3, q[nt][0][0],
+                                q[nt][0][1]);
+                else
+                  mma16816(acc[mt][nt], a0, a1, a2, a3, q[nt][2 * w + i][0], q[nt][2 * w + i][1]);
+              }
+            }
+          const uint8_t* scales = buf + 2 * Rg::kCodes + (warp * kTokens + mt * 16) * 2 + g * 4;
+          const uint32_t ks2 = *reinterpret_cast<const uint32_t*>(scales);
+          const uint32_t vs2 = *reinterpret_cast<const uint32_t*>(scales + 2 * kStep);
+          ks[mt][0] = __uint_as_float(__byte_perm(ks2, 0, sel_a)) * factor;
+          ks[mt][1] = __uint_as_float(__byte_perm(ks2, 0, sel_b)) * factor;
+          vs[mt][0] = __uint_as_float(__byte_perm(vs2, 0, sel_a));
+          vs[mt][1] = __uint_as_float(__byte_perm(vs2, 0, sel_b));
+        }
+        // scores that are masked, by bit (mt NT + nt) 4 + register
+        uint32_t hidden = 0;
+        if (token0 < all_from || token0 + kTokens > all_to) {
+#pragma unroll
+          for (int i = 0; i < 8 * NT; ++i) {
+            const int token = token0 + i / (4 * NT) * 16 + (i & 2 ? tok_b : tok_a);
+            const int to = seen_to[i / 4 % NT][i & 1];
+            if (token >= min(end, to) || token < max(t.first, first_seen(p, to))) hidden |= 1u << i;
+          }
+        }
+        // weights, and weights x value scales as B fragments of the value product
+        uint32_t pw[2][NT][2];
+        float part[NT][2];
+        __half2 most2 = __half2half2(__half(0.0f));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float sum[2];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              const float pa = ex2(fmaf(acc[mt][nt][e], ks[mt][0], -ref[nt][e]));
+              const float pb = ex2(fmaf(acc[mt][nt][2 + e], ks[mt][1], -ref[nt][e]));
+              sum[mt] = pa + pb;
+              w[mt][e] = pa * vs[mt][0];
+              w[mt][2 + e] = pb * vs[mt][1];
+            }
+            part[nt][e] = sum[0] + sum[1];
+          }
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const __half2 h = __floats2half2_rn(w[mt][2 * r], w[mt][2 * r + 1]);
+              most2 = __hmax2(most2, __habs2(h));
+              pw[mt][nt][r] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        // masked scores, or weights out of range: once more, with care
+        bool again = hidden != 0 || !__hble2(most2, __half2half2(__half(32768.0f)));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) again |= part[nt][0] > kFar || part[nt][1] > kFar;
+        if (__any_sync(0xffffffffu, again)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma16816<BF16>(sc[mt][nt], a0, a1, a2, a3, q[nt][2 * w][0], q[nt][2 * w][1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float t4[4], w4[4];  // scores; weights x value scales
+              float high = m[nt][e];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const bool hide = hidden >> ((i / 2 * NT + nt) * 4 + (i & 1) * 2 + e) & 1;
+                t4[i] = hide ? -INFINITY : acc[i / 2][nt][(i & 1) * 2 + e] * ks[i / 2][i & 1];
+                high = fmaxf(high, t4[i]);
+              }
+#pragma unroll
+              for (int x = 4; x <= 16; x <<= 1)
+                high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, x));
+              float top = wtop[nt][e] * ex2(m[nt][e] - high);
+              const float before = top;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                // what a row does not see has weight 0 whatever its scale
+                w4[i] = t4[i] == -INFINITY ? 0.0f : ex2(t4[i] - high) * vs[i / 2][i & 1];
+                top = fmaxf(top, fabsf(w4[i]));
+              }
+#pragma unroll
+              for (int x = 4; x <= 16; x <<= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              float next = ref[nt][e];
+              // (the eight lanes of a column agree on all of this)
+              if (high > m[nt][e] || top > before) {
+                // 2^(high - next) top = 2^10 .. 2^11, exactly so when top is a power of two
+                const float lead = fminf(fmaxf(top, kLeastTop), 1.0e30f);
+                next = high - (float)(10 - ((int)(__float_as_uint(lead) >> 23) - 127));
+              }
+              m[nt][e] = high;
+              wtop[nt][e] = top;
+              const float f = ex2(ref[nt][e] - next), up2 = ex2(high - next);
+              ref[nt][e] = next;
+              l[nt][e] *= f;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                o[i][nt][e] *= f;
+                o[i][nt][2 + e] *= f;
+              }
+              part[nt][e] = 0.0f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                part[nt][e] += ex2(t4[i] - next);
+                acc[i / 2][nt][(i & 1) * 2 + e] = w4[i] * up2;
+              }
+            }
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                pw[mt][nt][r] = pack_f16(acc[mt][nt][2 * r], acc[mt][nt][2 * r + 1]);
         }
-        {
-          const uint32_t a0 = codes24<BF16, 2>(ka[w]), a1 = codes24<BF16, 2>(kb[w]);
-          const uint32_t a2 = codes24<BF16, 3>(ka[w]), a3 = codes24<BF16, 3>(kb[w]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816<BF16>(sc[mt][nt], a0, a1, a2, a3, q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
-        }
-      }
-      const uint8_t* scales = buf + 2 * Rg::kCodes + mt * 32 + g * 4;
-      const uint32_t ks2 = *reinterpret_cast<const uint32_t*>(scales);
-      const uint32_t vs2 = *reinterpret_cast<const uint32_t*>(scales + 2 * kStep);
-      const float ks_a = __uint_as_float(__byte_perm(ks2, 0, sel_a)) * to_log2;
-      const float ks_b = __uint_as_float(__byte_perm(ks2, 0, sel_b)) * to_log2;
-      vs[mt][0] = __uint_as_float(__byte_perm(vs2, 0, sel_a));
-      vs[mt][1] = __uint_as_float(__byte_perm(vs2, 0, sel_b));
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        sc[mt][nt][0] *= ks_a;
-        sc[mt][nt][1] *= ks_a;
-        sc[mt][nt][2] *= ks_b;
-        sc[mt][nt][3] *= ks_b;
-      }
-    }
-    if (masked) {
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const int ta = token0 + mt * 16 + tok_a, tb = token0 + mt * 16 + tok_b;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int to = min(end, seen_to[nt][e]), from = max(t.first, first_seen(p, seen_to[nt][e]));
-            if (ta >= to || ta < from) sc[mt][nt][e] = -INFINITY;
-            if (tb >= to || tb < from) sc[mt][nt][2 + e] = -INFINITY;
-          }
-      }
-    }
-    // the running maximum, moved when it must (o keeps its digits: its unit moves)
-    bool move = false;
-    float high[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        high[nt][e] = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e]));
-        move |= high[nt][e] > m[nt][e] + 8.0f;
-      }
-    if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int off = 4; off <= 16; off <<= 1)
-            high[nt][e] = fmaxf(high[nt][e], __shfl_xor_sync(0xffffffffu, high[nt][e], off));
-          const float next = fmaxf(m[nt][e], high[nt][e]);
-          const float keep = ex2(m[nt][e] - next);
-          m[nt][e] = next;
-          l[nt][e] *= keep;
-          wtop[nt][e] *= keep;
-        }
-    }
-    // weights: sc becomes weight x value scale
-    move = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float most = 0.0f;
+          for (int e = 0; e < 2; ++e) l[nt][e] += part[nt][e];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const float pa = ex2(sc[mt][nt][e] - m[nt][e]), pb = ex2(sc[mt][nt][2 + e] - m[nt][e]);
-          l[nt][e] += pa + pb;
-          float wa = pa * vs[mt][0], wb = pb * vs[mt][1];
-          if (masked) {  // what a row does not see has weight 0 whatever its scale
-            if (sc[mt][nt][e] == -INFINITY) wa = 0.0f;
-            if (sc[mt][nt][2 + e] == -INFINITY) wb = 0.0f;
+          uint32_t b[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            b[nt][0] = transpose8x8(pw[mt][nt][0]);
+            b[nt][1] = transpose8x8(pw[mt][nt][1]);
           }
-          sc[mt][nt][e] = wa;
-          sc[mt][nt][2 + e] = wb;
-          most = fmaxf(most, fmaxf(fabsf(wa), fabsf(wb)));
+#pragma unroll
+          for (int u = 0; u < DIM / 64; ++u) {
+            uint32_t v[4];
+            load_transposed(v, ring + slot * Rg::kBytes + v_lane + mt * 16 * (DIM / 2) + u * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // MMA tile 4 u + i: codes 0, 1, then 2, 3 of a chunk
+              const uint32_t x = i & 1 ? v[i & 2] >> 8 : v[i & 2];
+              const uint32_t y = i & 1 ? v[(i & 2) + 1] >> 8 : v[(i & 2) + 1];
+              const uint32_t a0 = codes0<false>(x), a1 = codes0<true>(x);
+              const uint32_t a2 = codes0<false>(y), a3 = codes0<true>(y);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(o[4 * u + i][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+            }
+          }
         }
-        high[nt][e] = most;
-        move |= most > 16.0f * wtop[nt][e] || wtop[nt][e] < kLeastTop;
       }
-    if (__any_sync(0xffffffffu, move)) {
+      __syncwarp();  // every lane has read its part of the slot
+      if (lane == 0) mbar_arrive(empty + 8 * slot);
+    }
+
+    // ---- join the warps: o, l relative to the largest reference
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x <= 16; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
+        if (g == 0) {
+          merge_ref[warp][8 * nt + 2 * c + e] = ref[nt][e];
+          merge_l[warp][8 * nt + 2 * c + e] = l[nt][e];
+        }
+      }
+    // a buffer [row][MMA tile][g][2] that the warps add to in turn, rows 4 floats
+    // apart from a multiple of 32: the accesses of a phase fall on different banks
+    float* mo = reinterpret_cast<float*>(smem + Rg::kTotal);
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      __syncthreads();
+      if (w != warp) continue;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          const int r = 8 * nt + 2 * c + e;
+          float all = merge_ref[0][r];
 #pragma unroll
-          for (int off = 4; off <= 16; off <<= 1)
-            high[nt][e] = fmaxf(high[nt][e], __shfl_xor_sync(0xffffffffu, high[nt][e], off));
-          const float next = fminf(fmaxf(fmaxf(wtop[nt][e], high[nt][e]), kLeastTop), 3.0e38f);
-          const float f = wtop[nt][e] / next;
-          wtop[nt][e] = next;
+          for (int i = 1; i < kWarps; ++i) all = fmaxf(all, merge_ref[i][r]);
+          // the halves' unit: 2^-24, and 2^-20 for odd channels
+          const float f = ex2(ref[nt][e] - all) * 16777216.0f;
+          float2* dst = reinterpret_cast<float2*>(mo + r * ROW + 2 * g);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            o[i][nt][e] *= f;
-            o[i][nt][2 + e] *= f;
+            float2 v = make_float2(o[i][nt][e] * f, o[i][nt][2 + e] * (f * 0.0625f));
+            if (w > 0) {
+              v.x += dst[8 * i].x;
+              v.y += dst[8 * i].y;
+            }
+            dst[8 * i] = v;
           }
         }
     }
-    // their products with the values
-    float to_unit[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) to_unit[nt][e] = __fdividef(2048.0f, wtop[nt][e]);
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      uint32_t b0[NT], b1[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        b0[nt] = transpose8x8(pack_f16(sc[mt][nt][0] * to_unit[nt][0], sc[mt][nt][1] * to_unit[nt][1]));
-        b1[nt] = transpose8x8(pack_f16(sc[mt][nt][2] * to_unit[nt][0], sc[mt][nt][3] * to_unit[nt][1]));
-      }
-      const uint8_t* vp = buf + Rg::kCodes + mt * 16 * (DIM / 2) + g * (DIM / 16);
-      uint32_t v[4][VW];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (VW == 2)
-          *reinterpret_cast<uint2*>(v[k]) = *reinterpret_cast<const uint2*>(vp + v_off[k]);
-        else
-          v[k][0] = *reinterpret_cast<const uint32_t*>(vp + v_off[k]);
-      }
-#pragma unroll
-      for (int w = 0; w < VW; ++w)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          // the four codes of this half word, of two tokens side by side
-          const uint32_t x = __byte_perm(v[0][w], v[1][w], half ? 0x7632 : 0x5410);
-          const uint32_t y = __byte_perm(v[2][w], v[3][w], half ? 0x7632 : 0x5410);
-          const int i = w * 4 + half * 2;
-          {
-            const uint32_t a0 = codes_f16<0>(x), a1 = codes_f16<1>(x);
-            const uint32_t a2 = codes_f16<0>(y), a3 = codes_f16<1>(y);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[i][nt], a0, a1, a2, a3, b0[nt], b1[nt]);
-          }
-          {
-            const uint32_t a0 = codes_f16<2>(x), a1 = codes_f16<3>(x);
-            const uint32_t a2 = codes_f16<2>(y), a3 = codes_f16<3>(y);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816<false>(o[i + 1][nt], a0, a1, a2, a3, b0[nt], b1[nt]);
-          }
-        }
+    __syncthreads();
+    const bool whole = piece_steps == t.steps;
+    const int64_t share = ((int64_t)blockIdx.x * 2 + (off == 0)) * p.tile_rows;
+    if (p.joins > 0 && off == 0 && (!whole || p.by_tile) && threadIdx.x == 0) {
+      const int64_t last = (run.pos + done + t.steps - 1) / run.per;  // the CTA of its last step
+      p.join[p.by_tile ? seq_tile * p.cache.heads + head : (int)blockIdx.x] =
+          Kv4Join{seq_tile, head, (int)blockIdx.x, whole ? -1 : (int)last};
     }
-    __syncwarp();  // every lane has read the stage
-    const int page = next_page;
-    next_page = page_of(s + kStages + 1);
-    if (s + kStages < steps) issue(s + kStages, page);
+    // a thread takes 4 channels of a row: 32 q + 4 g8 and on, tiles 2 q and 2 q + 1
+    for (int i = threadIdx.x; i < R * (DIM / 4); i += kWarps * 32) {
+      const int r = i / (DIM / 4), d = i % (DIM / 4) * 4, chunk_q = d / 32, g8 = d / 4 % 8;
+      if (r >= t.rows) continue;
+      float all = merge_ref[0][r], sum = 0.0f;
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) all = fmaxf(all, merge_ref[w][r]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += merge_l[w][r] * ex2(merge_ref[w][r] - all);
+      const float* src = mo + r * ROW + 32 * chunk_q + 2 * g8;
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      const float2 y = *reinterpret_cast<const float2*>(src + 16);
+      const bool none = sum == 0.0f;
+      const float inv = none ? 0.0f : 1.0f / sum;
+      const float lse = none ? -INFINITY : all + log2f(sum);
+      if (whole) {
+        const int64_t at = out_row(p, t, head, t.r0 + r);
+        T h[4] = {from_f32<T>(x.x * inv), from_f32<T>(x.y * inv), from_f32<T>(y.x * inv),
+                  from_f32<T>(y.y * inv)};
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + at * DIM + d) =
+            *reinterpret_cast<const uint2*>(h);
+        if (p.lse && d == 0) p.lse[at] = lse * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(p.share_o + (share + r) * DIM + d) =
+            make_float4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
+        if (d == 0) p.share_lse[share + r] = lse;
+      }
+    }
+    done += piece_steps;
+    if (done == run.count) break;
+    __syncthreads();  // the merge buffers are free again
+    off = 0;
+    if (++head == p.cache.heads) {
+      head = 0;
+      do t = row_tile(p, ++seq_tile);
+      while (t.steps == 0);
+    }
   }
-
-  // ---- join the warps: o, l relative to the common maximum
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-      for (int off = 4; off <= 16; off <<= 1)
-        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
-      if (g == 0) {
-        merge_m[warp][8 * nt + 2 * c + e] = m[nt][e];
-        merge_l[warp][8 * nt + 2 * c + e] = l[nt][e];
-      }
-    }
-  __syncthreads();  // (also: every ring is drained or abandoned)
-  if (abort_flag) return;
-  float* mo = reinterpret_cast<float*>(smem);  // [warp][row][DIM]
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 8 * nt + 2 * c + e;
-      float all = merge_m[0][r];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) all = fmaxf(all, merge_m[w][r]);
-      const float f = ex2(m[nt][e] - all) * (wtop[nt][e] * (1.0f / 2048.0f));
-      float* dst = mo + (warp * R + r) * DIM + g * (DIM / 8);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        dst[2 * i] = o[i][nt][e] * f;
-        dst[2 * i + 1] = o[i][nt][2 + e] * f;
-      }
-    }
-  __syncthreads();
-  const bool whole = t.chunks == 1;
-  const int64_t unit_at = unit_of(p, b, head, tile, chunk);
-  for (int i = threadIdx.x; i < R * (DIM / 4); i += kWarps * 32) {
-    const int r = i / (DIM / 4), d = i % (DIM / 4) * 4;
-    if (r >= t.rows) continue;
-    float all = merge_m[0][r], sum = 0.0f;
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) all = fmaxf(all, merge_m[w][r]);
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      sum += merge_l[w][r] * ex2(merge_m[w][r] - all);
-      const float4 x = *reinterpret_cast<const float4*>(mo + (w * R + r) * DIM + d);
-      v.x += x.x;
-      v.y += x.y;
-      v.z += x.z;
-      v.w += x.w;
-    }
-    const bool none = sum == 0.0f;
-    const float inv = none ? 0.0f : 1.0f / sum;
-    v.x *= inv;
-    v.y *= inv;
-    v.z *= inv;
-    v.w *= inv;
-    const float lse = none ? -INFINITY : all + log2f(sum);
-    if (whole) {
-      const int64_t at = out_row(p, t, head, t.r0 + r);
-      T h[4] = {from_f32<T>(v.x), from_f32<T>(v.y), from_f32<T>(v.z), from_f32<T>(v.w)};
-      *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + at * DIM + d) =
-          *reinterpret_cast<const uint2*>(h);
-      if (p.lse && d == 0) p.lse[at] = lse * kLn2;
-    } else {
-      *reinterpret_cast<float4*>(p.share_o + (unit_at * p.tile_rows + r) * DIM + d) = v;
-      if (d == 0) p.share_lse[unit_at * p.tile_rows + r] = lse;
-    }
+  if (dead) {  // let the copies in flight land (again with a limit)
+    volatile int go_on = 0;
+    for (int k = max(0, run.count - kStages); k < run.count; ++k)
+      mbar_wait(full + 8 * (k % kStages), (uint32_t)(k / kStages) & 1u, &go_on, p.status,
+                kWaitLimitNs / 8);
   }
 }
 
 template <typename T, int DIM, int NT>
 cudaError_t launch_tile(const Kv4AttnParams& p, cudaStream_t s) {
-  const int merge = kWarps * 8 * NT * DIM * 4;
-  const int smem = Ring<DIM>::kTotal > merge ? Ring<DIM>::kTotal : merge;
+  const int smem = Ring<DIM>::kTotal + 8 * NT * (DIM + 4) * 4;
   auto kernel = kv4_rows_kernel<T, DIM, NT>;
   static std::atomic<uint64_t> set{0};  // devices on which the kernel has its shared memory
   int dev = 0;
@@ -545,9 +616,7 @@ cudaError_t launch_tile(const Kv4AttnParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     set |= uint64_t(1) << dev;
   }
-  const dim3 grid((unsigned)(p.max_chunks * p.row_tiles), (unsigned)p.cache.heads,
-                  (unsigned)p.batch);
-  kernel<<<grid, kWarps * 32, smem, s>>>(p);
+  kernel<<<p.ctas, kWarps * 32, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -559,6 +628,8 @@ cudaError_t launch_typed(const Kv4AttnParams& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+int kv4_rows_per_sm(int tile_rows) { return tile_rows == 8 ? 4 : 3; }
 
 cudaError_t launch_kv4_rows(int dtype, const Kv4AttnParams& p, cudaStream_t s) {
   return dtype == LBGEMM_BF16 ? launch_typed<__nv_bfloat16>(p, s) : launch_typed<__half>(p, s);
