@@ -141,4 +141,7 @@ cudaError_t launch_kv4_attention(int dtype, const Kv4AttnParams& p, int* launche
 int kv4_rows_per_sm(int tile_rows);  // CTAs that an SM holds
 cudaError_t launch_kv4_rows(int dtype, const Kv4AttnParams& p, cudaStream_t s);
 
+// The kernel for more (kv4_tiles.cu): tiles of 256 rows, one CTA an SM.
+cudaError_t launch_kv4_tiles(int dtype, const Kv4AttnParams& p, cudaStream_t s);
+
 }  // namespace lbg

@@ -17,6 +17,10 @@
 namespace lbg {
 namespace {
 
+// Rows of a tile (query tokens x heads of a group) up to which the kernel for
+// few rows runs.
+constexpr int64_t kFewRows = 16;
+
 // Joins the shares of a tile's row: with share c's o_c and lse_c (log2),
 //   o = sum_c 2^(lse_c - lse) o_c,  lse = log2 sum_c 2^lse_c.
 // A block per (record, row): teams of DIM / 4 threads take every TEAMS-th share
@@ -115,12 +119,13 @@ size_t kv4_attention_plan(Kv4AttnParams* p, int sm_count) {
   const int64_t rows = (int64_t)p->max_q * p->group;
   p->by_group = FastDiv((uint32_t)p->group);
   p->by_page16 = FastDiv((uint32_t)(p->cache.page_size / 16));
-  p->tile_rows = rows <= 8 ? 8 : 16;
+  p->tile_rows = rows <= 8 ? 8 : rows <= kFewRows ? 16 : 256;
   p->row_tiles = (int)((rows + p->tile_rows - 1) / p->tile_rows);
   // one wave of CTAs, or fewer where the longest lengths would not fill it
   const int64_t steps = (int64_t)p->batch * p->row_tiles * p->cache.heads *
                         (p->max_kv / kStepTokens + 2);
-  p->ctas = (int)std::min<int64_t>((int64_t)sm_count * kv4_rows_per_sm(p->tile_rows), steps);
+  const int per_sm = p->tile_rows == 256 ? 1 : kv4_rows_per_sm(p->tile_rows);
+  p->ctas = (int)std::min<int64_t>((int64_t)sm_count * per_sm, steps);
   // (tiles of one step each cannot be cut)
   const int64_t tiles = (int64_t)p->batch * p->row_tiles * p->cache.heads;
   p->by_tile = tiles <= p->ctas;
@@ -137,7 +142,7 @@ void kv4_attention_scratch(Kv4AttnParams* p, void* scratch) {
 }
 
 cudaError_t launch_kv4_attention(int dtype, const Kv4AttnParams& p, int* launches, cudaStream_t s) {
-  cudaError_t e = launch_kv4_rows(dtype, p, s);
+  cudaError_t e = p.tile_rows == 256 ? launch_kv4_tiles(dtype, p, s) : launch_kv4_rows(dtype, p, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (p.joins > 0) {

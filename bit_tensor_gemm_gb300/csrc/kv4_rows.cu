@@ -33,6 +33,7 @@
 #include <atomic>
 
 #include "kv4_attention.cuh"
+#include "kv4_codes.cuh"
 #include "ptx.cuh"
 
 namespace lbg {
@@ -41,9 +42,6 @@ namespace {
 constexpr int kWarps = 4, kStages = 3, kTokens = 32, kStep = kStepTokens;
 constexpr int kMinSteps = 2;  // of a CTA's run
 static_assert(kWarps * kTokens == kStep, "a warp's share of a step");
-constexpr float kFar = 1.2676506e30f;       // 2^100
-constexpr float kLeastTop = 8.2718061e-25f;  // 2^-80
-
 template <int DIM>
 struct Ring {
   static constexpr int kCodes = kStep * DIM / 2;     // bytes of keys (or values) of a step
@@ -79,27 +77,6 @@ __device__ __forceinline__ void mma16816_from(float (&d)[4], float c0, float c1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
-// Codes 0 and 4 of a word (HIGH: 1 and 5) as two subnormal halves: (code + 8)
-// 2^-24, or 16 times that.  Codes 2, 6 and 3, 7 are those of the word >> 8.
-// One three-input operation, (w & mask) ^ eight: left to the compiler it became
-// two (45.1 -> XX us over 131072 tokens).
-template <bool HIGH>
-__device__ __forceinline__ uint32_t codes8(uint32_t w) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0x6A;"
-      : "=r"(d)
-      : "r"(w), "r"(HIGH ? 0x00F000F0u : 0x000F000Fu), "r"(HIGH ? 0x00800080u : 0x00080008u));
-  return d;
-}
-// The same without the 8: code 2^-24, or 16 times that (exact).
-template <bool HIGH>
-__device__ __forceinline__ uint32_t codes0(uint32_t w) {
-  const uint32_t c = codes8<HIGH>(w), eight = HIGH ? 0x00800080u : 0x00080008u;
-  const __half2 v =
-      __hsub2(*reinterpret_cast<const __half2*>(&c), *reinterpret_cast<const __half2*>(&eight));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // Four 8 x 8 matrices of halves, transposed: lane l gives the address of row
 // l % 8 of matrix l / 8 and gets rows 2 (l % 4) and + 1 of column l / 4 of each.
 __device__ __forceinline__ void load_transposed(uint32_t (&r)[4], uint32_t addr) {
@@ -113,11 +90,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Element order inside a warp (lane = 4 g + c):
@@ -327,12 +299,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
         if (is_step < run.count) {
           dead = !mbar_wait(empty + 8 * (old % kStages), (uint32_t)(old / kStages) & 1u, &abort_flag,
                             p.status);
+          dead = __any_sync(0xffffffffu, dead);  // (the lanes go on together)
           if (!dead) issue();
         }
         advance(kWarps);
       }
       if (!dead)
         dead = !mbar_wait(full + 8 * slot, (uint32_t)(s / kStages) & 1u, &abort_flag, p.status);
+      dead = __any_sync(0xffffffffu, dead);
       const int token0 = t.base + (off + s - done) * kStep + warp * kTokens;
       if (token0 < end && !dead) {
         const uint8_t* buf = smem + slot * Rg::kBytes;
