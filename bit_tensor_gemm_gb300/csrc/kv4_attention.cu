@@ -19,32 +19,33 @@ namespace {
 
 // Rows of a tile (query tokens x heads of a group) up to which the kernel for
 // few rows runs.
-constexpr int64_t kFewRows = 16;
+constexpr int64_t kFewRows = 32;
 
 // Joins the shares of a tile's row: with share c's o_c and lse_c (log2),
 //   o = sum_c 2^(lse_c - lse) o_c,  lse = log2 sum_c 2^lse_c.
-// A block per (record, row): teams of DIM / 4 threads take every TEAMS-th share
-// and are added in order.
+// TEAMS teams of DIM / 4 threads a block.  PER_ROW teams take every PER_ROW-th
+// share of a row and are added in order: all of them where a tile has few rows
+// (it may have many shares), one for tiles of 256 (few shares).
 constexpr int kJoinThreads = 256;
 
-template <typename T, int DIM>
+template <typename T, int DIM, bool MANY_ROWS>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnParams p) {
-  constexpr int LANES = DIM / 4, TEAMS = kJoinThreads / LANES;
-  const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES, row = blockIdx.y;
+  constexpr int LANES = DIM / 4, TEAMS = kJoinThreads / LANES, PER_ROW = MANY_ROWS ? 1 : TEAMS;
+  const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
+  const int row = MANY_ROWS ? blockIdx.y * TEAMS + team : blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (by tile, one without rows has no record: the tile is looked at first)
-  if (p.by_tile && row >= row_tile(p, blockIdx.x / p.cache.heads).rows) return;
+  const int first_row = MANY_ROWS ? blockIdx.y * TEAMS : row;
+  if (p.by_tile && first_row >= row_tile(p, blockIdx.x / p.cache.heads).rows) return;
   const Kv4Join j = p.join[blockIdx.x];
   if (j.last_cta < 0) return;
   const RowTile t = row_tile(p, j.seq_tile);
-  if (row >= t.rows) return;
+  const bool live = row < t.rows;
   // share 0 of the tile is its first CTA's share 1, the others' share 0 follow
-  const int shares = j.last_cta - j.first_cta + 1;
+  const int shares = live ? j.last_cta - j.first_cta + 1 : 0;
   auto index = [&](int c) -> int64_t {
     return (int64_t)((j.first_cta + c) * 2 + (c == 0)) * p.tile_rows + row;
   };
-  __shared__ float4 sh[TEAMS][LANES];
-  __shared__ float sum_sh[TEAMS];
   // the largest lse, and whether one is a NaN
   float top = -INFINITY;
   int nan = 0;
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnPar
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float sum = 0.0f;
 #pragma unroll 4
-  for (int c = team; c < shares; c += TEAMS) {
+  for (int c = MANY_ROWS ? 0 : team; c < shares; c += PER_ROW) {
     const int64_t at = index(c);
     const float w = ex2(p.share_lse[at] - ref);
     const float4 v = reinterpret_cast<const float4*>(p.share_o + at * DIM)[lane];
@@ -73,19 +74,24 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnPar
     acc.z += w * v.z;
     acc.w += w * v.w;
   }
-  sh[team][lane] = acc;
-  if (lane == 0) sum_sh[team] = sum;
-  __syncthreads();
-  if (team != 0) return;
+  if constexpr (!MANY_ROWS) {
+    __shared__ float4 sh[TEAMS][LANES];
+    __shared__ float sum_sh[TEAMS];
+    sh[team][lane] = acc;
+    if (lane == 0) sum_sh[team] = sum;
+    __syncthreads();
+    if (team != 0) return;
 #pragma unroll
-  for (int g = 1; g < TEAMS; ++g) {
-    const float4 v = sh[g][lane];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
-    sum += sum_sh[g];
+    for (int g = 1; g < TEAMS; ++g) {
+      const float4 v = sh[g][lane];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+      sum += sum_sh[g];
+    }
   }
+  if (!live) return;
   const float inv = nan ? NAN : sum > 0.0f ? 1.0f / sum : 0.0f;
   const int64_t at = out_row(p, t, j.head, t.r0 + row);
   T h[4] = {from_f32<T>(acc.x * inv), from_f32<T>(acc.y * inv), from_f32<T>(acc.z * inv),
@@ -96,11 +102,13 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnPar
     p.lse[at] = nan ? NAN : sum > 0.0f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <typename T>
-cudaError_t launch_join(const Kv4AttnParams& p, cudaStream_t s) {
+template <typename T, int DIM>
+cudaError_t launch_join_dim(const Kv4AttnParams& p, cudaStream_t s) {
+  const bool many = p.tile_rows == 256;
+  const int rows = (int)std::min<int64_t>(p.tile_rows, (int64_t)p.max_q * p.group);
+  const int per_block = many ? kJoinThreads / (DIM / 4) : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.joins,
-                     (unsigned)std::min<int64_t>(p.tile_rows, (int64_t)p.max_q * p.group));
+  cfg.gridDim = dim3((unsigned)p.joins, (unsigned)((rows + per_block - 1) / per_block));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   // may be scheduled while the last shares are computed; it waits for them itself
@@ -109,8 +117,13 @@ cudaError_t launch_join(const Kv4AttnParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.cache.dim == 64 ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, 64>, p)
-                           : cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, 128>, p);
+  return many ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, DIM, true>, p)
+              : cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, DIM, false>, p);
+}
+
+template <typename T>
+cudaError_t launch_join(const Kv4AttnParams& p, cudaStream_t s) {
+  return p.cache.dim == 64 ? launch_join_dim<T, 64>(p, s) : launch_join_dim<T, 128>(p, s);
 }
 
 }  // namespace

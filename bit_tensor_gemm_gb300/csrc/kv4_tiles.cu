@@ -5,15 +5,19 @@
 // A CTA (one an SM) holds the queries of two 128-row tiles X = 0, 1 in shared
 // memory and walks over the cached tokens in steps of 128:
 //
-//   converters (4 warps)   codes of a step -> fp16 in shared memory, keys for
-//                          S = Q K^T and values for O += P V, each once for
-//                          both tiles; codes as subnormal halves code 2^-24
-//                          (every second one 16 times that), as in kv4_rows.cu
-//   one thread             the MMAs: O_X += P_X V of step j - 1, then S_X = Q_X
+//   converters (4 warps for keys, 3 for values)
+//                          codes of a step -> fp16 in shared memory, for S = Q
+//                          K^T and O += P V, each once for both tiles; codes as
+//                          subnormal halves code 2^-24 (every second one 16
+//                          times that), as in kv4_rows.cu
+//   one warp               the MMAs: O_X += P_X V of step j - 1, then S_X = Q_X
 //                          K^T of step j, for X = 0, then 1
-//   softmax (4 warps an X) a thread a row: weights 2^(t - ref) from S_X, times
-//                          the value scales as fp16 back to tensor memory, over
-//                          the S they came from
+//   softmax (4 warps an X) weights 2^(t - ref) from S_X, times the value scales
+//                          as fp16 back to tensor memory, over the S they came
+//                          from.  A thread takes four rows' pairs of columns
+//                          (the layout of a warp MMA's sums): with a thread a
+//                          row each scale was read once a row, and these reads
+//                          alone held shared memory for 2048 cycles a step
 //
 // While the tensor cores work for one tile, the other tile's softmax runs.
 // Bound: the MMAs, 4 x 128 x DIM flops per row and step; the converters' and
@@ -32,7 +36,11 @@
 namespace lbg {
 namespace {
 
-constexpr int kThreads = 512;  // warps 0..3, 4..7 softmax, 8..11 converters, 12 MMAs
+// Warps 0..3, 4..7 softmax, 8..11 keys, 12 MMAs, 13..15 values.  Launched with
+// 128 registers a thread (512 threads: all of the SM's); the softmax warps then
+// go up to 176 and the others down to 80: 176 + 176 + 80 + 80 = 4 x 128 in each
+// quarter of the register file.
+constexpr int kThreads = 512;
 constexpr int kStep = kStepTokens;
 constexpr int kMinSteps = 4;
 constexpr int kScaleSlots = 4;
@@ -44,10 +52,11 @@ struct Smem {
   static constexpr int kK = kQ + 2 * kTile;      // [2] keys
   static constexpr int kV = kK + 2 * kTile;      // [2] values
   static constexpr int kScales = kV + 2 * kTile; // [4][2][128] fp32: keys' x factor, values'
-  static constexpr int kBars = kScales + kScaleSlots * 2 * kStep * 4;
+  static constexpr int kTops = kScales + kScaleSlots * 2 * kStep * 4;  // [2][4][256] fp32
+  static constexpr int kBars = kTops + 2 * 4 * 256 * 4;
   static constexpr int kNumBars = 8 + kScaleSlots + 1 + 7;
   static constexpr int kMisc = kBars + 8 * kNumBars;
-  static constexpr int kBytes = kMisc + 64 + 1024;  // slack to align to 1024
+  static constexpr int kBytes = kMisc + 96 + 1024;  // slack to align to 1024
 };
 
 // Chunk j (16 bytes) of row r of a 128-byte-swizzled block of rows of 128 bytes.
@@ -65,9 +74,48 @@ __device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr, uint32_t blo
   return d;
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+// 16 TMEM lanes x 64 columns: register 4 b + i of lane (g, c) is column 8 b + 2 c +
+// i % 2 of TMEM lane g + 8 (i / 2).
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31},"
+      " [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x64(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
+      " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+// 16 TMEM lanes x 32 columns of pairs of halves: register 2 b + i of lane (g, c) is
+// column 4 b + c of TMEM lane g + 8 i.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0],"
       " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
@@ -96,6 +144,21 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
+
+// 16 bytes that this SM reads once: past the L1, which is small beside this much
+// shared memory.
+__device__ __forceinline__ uint4 load_once(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
 // Walks the steps of a run: which tile, head and step of the tile.
@@ -169,19 +232,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
   float* factor_slot = reinterpret_cast<float*>(smem + S::kMisc + 8);
   float* most_slots = reinterpret_cast<float*>(smem + S::kMisc + 16);  // [8]
   float* scales = reinterpret_cast<float*>(smem + S::kScales);
+  // the present tile, for the MMAs and converters: steps, and those each half sees
+  volatile int* piece = reinterpret_cast<volatile int*>(smem + S::kMisc + 48);  // count, from, to, from, to
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full(i), 128);
       mbar_init(k_empty(i), 1);
-      mbar_init(v_full(i), 128);
+      mbar_init(v_full(i), 96);
       mbar_init(v_empty(i), 1);
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), 128);
       mbar_init(o_full(i), 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(scale_full(i), 128);
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(scale_full(i), 128 + 96);
     mbar_init(q_full, 256);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -209,195 +274,207 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
     dead = __any_sync(0xffffffffu, dead);
   };
 
-  if (warp >= 12) {
-    // ---------------- the MMAs: one thread ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 12 && lane == 0 && run.count > 0) {
-      Cursor c;
-      c.start(p, run);
-      uint32_t step = 0, tile = 0;      // of the run: steps so far, tiles so far
-      uint32_t n_p[2] = {0, 0};         // weights of half X consumed so far
-      for (int done = 0; done < run.count; ++tile) {
-        const int count = min(c.t.steps - c.off, run.count - done);
-        int from[2], to[2];  // of each half, in steps of this piece
-        for (int x = 0; x < 2; ++x) {
-          const HalfTile h = half_tile(p, c.t, x);
-          from[x] = min(max(h.from - c.off, 0), count);
-          to[x] = min(max(h.to - c.off, from[x]), count);
-        }
-        wait(q_full, tile);
-        for (int j = 0; j <= count; ++j) {
-          const uint32_t sj = step + j, sv = step + j - 1;  // run steps of the keys, values
-          bool have_k = false, have_v = false;
-          for (int x = 0; x < 2; ++x) {
-            if (j > from[x] && j <= to[x]) {  // O_X += P_X V of step j - 1
-              if (!have_v) wait(v_full(sv & 1), sv >> 1);
-              have_v = true;
-              wait(p_full(x), n_p[x]++);
-              if (!dead) {
-                tc_fence_after();
-                const uint32_t vbase = sbase + S::kV + (sv & 1) * S::kTile;
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 12) {
+      // ---------------- the MMAs ----------------
+      // The whole warp walks, lane 0 issues: what it passes stays warp-uniform and
+      // the descriptors of a step are sums of few registers and constants.  (One
+      // thread that computed each descriptor took 2900 cycles to issue the eight
+      // MMAs of O += P V, against 512 to run them.)
+      if (run.count > 0) {
+        const uint64_t q_desc = smem_desc_sw128(sbase + S::kQ), k_desc = smem_desc_sw128(sbase + S::kK);
+        const uint64_t v_desc = smem_desc_rows_k(sbase + S::kV, kBlock);
+        uint32_t step = 0, tile = 0;     // of the run: steps so far, tiles so far
+        uint32_t n_p0 = 0, n_p1 = 0;     // weights of each half consumed so far
+        // O_X += P_X V of run step sv; S_X = Q_X K^T of run step sj
+        auto issue_o = [&](auto half, uint32_t sv, bool first, bool last, uint32_t& n_p) {
+          constexpr int X = decltype(half)::value;
+          warp_wait(p_full(X), n_p++);
+          if (dead) return;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t v = v_desc + (sv & 1) * (S::kTile >> 4);
 #pragma unroll
-                for (int k = 0; k < kStep / 16; ++k)
-                  mma_f16_ts(tmem + kColO + 128 * x, tmem + 128 * x + 8 * k,
-                             smem_desc_rows_k(vbase + 2048 * k, kBlock), kIdescO,
-                             j - 1 > from[x] || k > 0);
-                if (j == to[x]) mma_commit(o_full(x));
-              }
+            for (int k = 0; k < kStep / 16; ++k)
+              mma_f16_ts(tmem + kColO + 128 * X, tmem + 128 * X + 8 * k, v + k * (2048 >> 4), kIdescO,
+                         k > 0 ? 1u : first ? 0u : 1u);
+            if (last) mma_commit(o_full(X));
+          }
+          __syncwarp();
+        };
+        auto issue_s = [&](auto half, uint32_t sj) {
+          constexpr int X = decltype(half)::value;
+          if (dead) return;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t k0 = k_desc + (sj & 1) * (S::kTile >> 4);
+#pragma unroll
+            for (int k = 0; k < DIM / 16; ++k) {
+              constexpr uint64_t kXQ = X * (S::kTile >> 4);
+              const uint64_t at = ((k / 4) * kBlock + (k % 4) * 32) >> 4;
+              mma_f16(tmem + 128 * X, q_desc + kXQ + at, k0 + at, kIdescS, k > 0 ? 1u : 0u);
             }
-            if (j >= from[x] && j < to[x]) {  // S_X = Q_X K^T of step j
-              if (!have_k) wait(k_full(sj & 1), sj >> 1);
-              have_k = true;
-              if (!dead) {
-                tc_fence_after();
-                const uint32_t qbase = sbase + S::kQ + x * S::kTile;
-                const uint32_t kbase = sbase + S::kK + (sj & 1) * S::kTile;
+            mma_commit(s_full(X));
+          }
+          __syncwarp();
+        };
+        for (int done = 0; done < run.count; ++tile) {
+          warp_wait(q_full, tile);
+          const int count = dead ? 1 : piece[0];
+          const int from0 = piece[1], to0 = piece[2], from1 = piece[3], to1 = piece[4];
+          for (int j = 0; j <= count; ++j) {
+            const uint32_t sj = step + j, sv = sj - 1;  // run steps of the keys, the values
+            if (j > 0) warp_wait(v_full(sv & 1), sv >> 1);
+            if (j > from0 && j <= to0) issue_o(Const<0>{}, sv, j - 1 == from0, j == to0, n_p0);
+            if (j < count) warp_wait(k_full(sj & 1), sj >> 1);
+            if (j >= from0 && j < to0) issue_s(Const<0>{}, sj);
+            if (j > from1 && j <= to1) issue_o(Const<1>{}, sv, j - 1 == from1, j == to1, n_p1);
+            if (lane == 0 && j > 0 && !dead) mma_commit(v_empty(sv & 1));
+            if (j >= from1 && j < to1) issue_s(Const<1>{}, sj);
+            if (lane == 0 && j < count && !dead) mma_commit(k_empty(sj & 1));
+          }
+          step += count;
+          done += count;
+        }
+        // every MMA and commit has ended before the block does (with a limit, also
+        // after a wait that ran out)
+        volatile int go_on = 0;
+        if (lane == 0) {
+          mma_commit(drain);
+          mbar_wait(drain, 0, &go_on, p.status);
+        }
+        __syncwarp();
+      }
+    } else {
+      // ---------------- converters ----------------
+      // Warps 8..11 keys, 12..15 values; the next step's codes are on their way to
+      // registers while the MMAs use this one's.
+      // Groups of TPL tokens go to the warps in turn; a lane takes 32 codes (16
+      // bytes) of a token, the lanes of a phase of 8 different tokens of 8 (no
+      // bank conflicts).
+      auto converter = [&](auto which) {
+        constexpr bool VALUES = decltype(which)::value == 1;
+        constexpr int WARPS = VALUES ? 3 : 4;
+        constexpr int LPT = DIM / 32, TPL = 32 / LPT, GROUPS = kStep / TPL;
+        constexpr int LOADS = (GROUPS + WARPS - 1) / WARPS, SCALES = VALUES ? 2 : 1;
+        const int cw = warp - (VALUES ? 13 : 8), ctid = cw * 32 + lane, chunk = lane / TPL;
+        const int page_size = (int)p.cache.page_size;
+        const uint32_t page16 = (uint32_t)page_size / 16;
+        const uint8_t* codes_at = p.cache.base + (VALUES ? (int64_t)page_size * (DIM / 2) : 0) +
+                                  chunk * 16 + lane % TPL % 16 * (DIM / 2);
+        const uint8_t* scales_at = p.cache.base + (int64_t)page_size * (DIM + (VALUES ? 2 : 0));
+        // where the loads stand: `ahead` steps into the run; lane l < 8 has the
+        // offsets of the codes and scales of the step's tokens 16 l and on (-1: none)
+        Cursor c;
+        int ahead = 0;
+        int64_t codes_off, scales_off;
+        auto find = [&]() {
+          codes_off = scales_off = -1;
+          const int token = c.t.base + c.off * kStep + lane * 16;
+          if (ahead >= run.count || lane >= 8 || token >= c.t.last) return;
+          const uint32_t group = (uint32_t)token / 16, in_table = p.by_page16(group);
+          const int page = __ldg(p.page_table + (int64_t)c.t.b * p.table_width + in_table);
+          if ((uint32_t)page >= (uint32_t)p.cache.pages) {
+            atomicOr(p.status, kStatusBadIndex);
+            return;
+          }
+          const int64_t block =
+              ((int64_t)page * p.cache.heads + c.head) * kv4_block_bytes(DIM, page_size);
+          const uint32_t inside = (group - in_table * page16) * 16;
+          codes_off = block + inside * (DIM / 2);
+          scales_off = block + inside * 2;
+        };
+        uint4 raw[LOADS];
+        uint32_t raw_s[SCALES];
+        // loads the codes of the step found, and finds the next one
+        auto load = [&]() {
 #pragma unroll
-                for (int k = 0; k < DIM / 16; ++k) {
-                  const uint32_t at = (k / 4) * kBlock + (k % 4) * 32;
-                  mma_f16(tmem + 128 * x, smem_desc_sw128(qbase + at), smem_desc_sw128(kbase + at),
-                          kIdescS, k > 0);
-                }
-                mma_commit(s_full(x));
-              }
+          for (int i = 0; i < LOADS; ++i) {
+            const int first = (cw + WARPS * i) * TPL;  // token of the step
+            const int64_t off = __shfl_sync(0xffffffffu, codes_off, first / 16 % 8);
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (first < kStep && off >= 0)
+              raw[i] = load_once(codes_at + off + first % 16 * (DIM / 2));
+          }
+#pragma unroll
+          for (int i = 0; i < SCALES; ++i) {
+            const int token = ctid + 32 * WARPS * i;
+            const int64_t off = __shfl_sync(0xffffffffu, scales_off, token / 16 % 8);
+            raw_s[i] = 0;
+            if (token < kStep && off >= 0)
+              raw_s[i] = __ldg(reinterpret_cast<const uint16_t*>(scales_at + off) + token % 16);
+          }
+          if (++ahead < run.count && ++c.off == c.t.steps) c.next_tile(p);
+          find();
+        };
+        c.start(p, run);
+        find();
+        load();
+        uint32_t tile = 0;
+        int left = 0;  // (keys) steps of the present tile still to convert
+        float factor = 1.0f;
+        for (int s = 0; s < run.count; ++s) {
+          if (!VALUES && left-- == 0) {
+            wait(q_full, tile++);
+            left = dead ? run.count : piece[0] - 1;
+            factor = *reinterpret_cast<volatile float*>(factor_slot);
+          }
+          const int st = s & 1, use = s >> 1;
+#pragma unroll
+          for (int i = 0; i < SCALES; ++i) {
+            const int token = ctid + 32 * WARPS * i;
+            if (token < kStep)
+              scales[((s % kScaleSlots) * 2 + (VALUES ? 1 : 0)) * kStep + token] =
+                  __uint_as_float(raw_s[i] << 16) * factor;
+          }
+          mbar_arrive(scale_full(s % kScaleSlots));
+          if (use > 0) wait(VALUES ? v_empty(st) : k_empty(st), use - 1);
+          const uint32_t dst = sbase + (VALUES ? S::kV : S::kK) + st * S::kTile;
+#pragma unroll
+          for (int i = 0; i < LOADS; ++i) {
+            const int r = (cw + WARPS * i) * TPL + lane % TPL;
+            if (r >= kStep) continue;
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t w8 = w[k] >> 8;
+              const int at = chunk * 4 + k;
+              st_shared_v4(dst + (at / 8) * kBlock + swizzled(r, at % 8), (int)codes0<false>(w[k]),
+                           (int)codes0<true>(w[k]), (int)codes0<false>(w8), (int)codes0<true>(w8));
             }
           }
-          // (a step that neither half sees is converted all the same: its
-          // barriers are passed on)
-          if (j > 0) {
-            if (!have_v) wait(v_full(sv & 1), sv >> 1);
-            if (!dead) mma_commit(v_empty(sv & 1));
-          }
-          if (j < count) {
-            if (!have_k) wait(k_full(sj & 1), sj >> 1);
-            if (!dead) mma_commit(k_empty(sj & 1));
-          }
+          fence_proxy_async_smem();
+          mbar_arrive(VALUES ? v_full(st) : k_full(st));
+          __syncwarp();
+          load();
         }
-        step += count;
-        done += count;
-        if (done < run.count) c.next_tile(p);
+      };
+      if (run.count > 0) {
+        if (warp < 12) converter(Const<0>{});
+        else converter(Const<1>{});
       }
-      // every MMA and commit has ended before the block does (with a limit, also
-      // after a wait that ran out)
-      volatile int go_on = 0;
-      mma_commit(drain);
-      mbar_wait(drain, 0, &go_on, p.status);
-    }
-  } else if (warp >= 8) {
-    // ---------------- converters ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    // lane -> 32 codes (16 bytes) of a token: LPT lanes a token, tokens whose
-    // low three bits differ across a phase of 8 lanes (no bank conflicts)
-    constexpr int LPT = DIM / 32, TPL = 32 / LPT, LOADS = 32 / TPL;
-    const int cw = warp - 8, ctid = threadIdx.x - 256;
-    const int row0 = cw * 32 + lane % TPL, chunk = lane / TPL;
-    const int page_size = (int)p.cache.page_size;
-    const uint32_t page16 = (uint32_t)page_size / 16;
-    const int64_t block_bytes = kv4_block_bytes(DIM, page_size);
-    Cursor c;
-    if (run.count > 0) c.start(p, run);
-    int tile_steps = 0;
-    // this warp's two groups of 16 tokens: block of the page and token in it
-    auto find = [&](const uint8_t* (&block)[2], int (&inside)[2]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int token = c.t.base + c.off * kStep + cw * 32 + h * 16;
-        block[h] = nullptr;
-        inside[h] = 0;
-        if (token >= c.t.last) continue;
-        const uint32_t group = (uint32_t)token / 16, in_table = p.by_page16(group);
-        const int page = __ldg(p.page_table + (int64_t)c.t.b * p.table_width + in_table);
-        if ((uint32_t)page >= (uint32_t)p.cache.pages) {
-          if (lane == 0) atomicOr(p.status, kStatusBadIndex);
-          continue;
-        }
-        block[h] = p.cache.base + ((int64_t)page * p.cache.heads + c.head) * block_bytes;
-        inside[h] = (int)(group - in_table * page16) * 16;
-      }
-    };
-    uint4 raw_k[LOADS], raw_v[LOADS];
-    uint32_t raw_s = 0;  // scales of token ctid: key, value << 16
-    auto load = [&](const uint8_t* const (&block)[2], const int (&inside)[2]) {
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        const int r = lane % TPL + i * TPL, h = r / 16;  // token of the warp's 32
-        raw_k[i] = raw_v[i] = make_uint4(0, 0, 0, 0);
-        if (block[h] == nullptr) continue;
-        const uint8_t* at = block[h] + (inside[h] + r % 16) * (DIM / 2) + chunk * 16;
-        raw_k[i] = __ldg(reinterpret_cast<const uint4*>(at));
-        raw_v[i] = __ldg(reinterpret_cast<const uint4*>(at + (int64_t)page_size * (DIM / 2)));
-      }
-      raw_s = 0;
-      const uint8_t* b = lane < 16 ? block[0] : block[1];
-      if (b) {
-        const uint16_t* at = reinterpret_cast<const uint16_t*>(b + (int64_t)page_size * DIM) +
-                             (lane < 16 ? inside[0] : inside[1]) + lane % 16;
-        raw_s = (uint32_t)__ldg(at) | (uint32_t)__ldg(at + page_size) << 16;
-      }
-    };
-    auto convert = [&](uint32_t dst, const uint4 (&raw)[LOADS]) {
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        const int r = row0 + i * TPL;
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t w8 = w[k] >> 8;
-          const int at = chunk * 4 + k;
-          st_shared_v4(dst + (at / 8) * kBlock + swizzled(r, at % 8), (int)codes0<false>(w[k]),
-                       (int)codes0<true>(w[k]), (int)codes0<false>(w8), (int)codes0<true>(w8));
-        }
-      }
-    };
-    uint32_t tile = 0;
-    const uint8_t* block[2];
-    int inside[2];
-    if (run.count > 0) {
-      find(block, inside);
-      load(block, inside);
-    }
-    float factor = 0.0f;
-    for (int s = 0; s < run.count; ++s) {
-      if (tile_steps == 0) {  // a new tile: its queries' factor
-        tile_steps = min(c.t.steps - c.off, run.count - s);
-        wait(q_full, tile++);
-        factor = *reinterpret_cast<volatile float*>(factor_slot);
-      }
-      --tile_steps;
-      // on to the next step, and its pages
-      const uint8_t* next_block[2] = {nullptr, nullptr};
-      int next_inside[2] = {0, 0};
-      if (s + 1 < run.count) {
-        if (++c.off == c.t.steps) c.next_tile(p);
-        find(next_block, next_inside);
-      }
-      const int st = s & 1, use = s >> 1;
-      float* sc = scales + (s % kScaleSlots) * 2 * kStep;
-      sc[ctid] = __uint_as_float(raw_s << 16) * factor;
-      sc[kStep + ctid] = __uint_as_float(raw_s & 0xffff0000u);
-      mbar_arrive(scale_full(s % kScaleSlots));
-      if (use > 0) wait(k_empty(st), use - 1);
-      convert(sbase + S::kK + st * S::kTile, raw_k);
-      fence_proxy_async_smem();
-      mbar_arrive(k_full(st));
-      if (use > 0) wait(v_empty(st), use - 1);
-      convert(sbase + S::kV + st * S::kTile, raw_v);
-      fence_proxy_async_smem();
-      mbar_arrive(v_full(st));
-      load(next_block, next_inside);
     }
   } else {
-    // ---------------- softmax: thread = row ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    const int x = warp / 4, r = threadIdx.x;  // row of the 256
+    // ---------------- softmax ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    const int x = warp / 4, r = threadIdx.x;  // half; row of the 256 (queries and results)
+    const int g = lane / 4, c4 = lane % 4;    // scores: rows g + 8 i of the warp's 32, i < 4
     const uint32_t lane_base = (uint32_t)(32 * (warp % 4)) << 16;
     const uint32_t ts = tmem + lane_base + 128 * x, to_ = tmem + lane_base + kColO + 128 * x;
-    Cursor c;
-    if (run.count > 0) c.start(p, run);
+    // What a tile is, is looked up again where it is needed (hidden from the
+    // compiler, which would keep it in registers throughout and spill others).
+    auto hide = [](int v) {
+      asm volatile("" : "+r"(v));
+      return v;
+    };
+    int seq_tile = run.seq_tile, head = run.head, off = run.off;
     uint32_t step = 0, n_s = 0, n_o = 0;
     for (int done = 0; done < run.count;) {
-      const RowTile& t = c.t;
-      const int count = min(t.steps - c.off, run.count - done);
+      int count, from, upto, all_from, all_to, token_base;
+      {
+      const RowTile t = row_tile(p, hide(seq_tile));
+      count = min(t.steps - off, run.count - done);
       const HalfTile h = half_tile(p, t, x);
       const bool live = r < t.rows;
       const int qi = (int)p.by_group((uint32_t)(t.r0 + min(r, t.rows - 1)));
@@ -406,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
       // codes divided by 16.  (Every MMA of the tile before has ended.)
       {
         const T* src = static_cast<const T*>(p.q) + (int64_t)(t.q0 + qi) * p.q_stride +
-                       (int64_t)(c.head * p.group + t.r0 + min(r, t.rows - 1) - qi * p.group) * DIM;
+                       (int64_t)(head * p.group + t.r0 + min(r, t.rows - 1) - qi * p.group) * DIM;
         float most = 0.0f;
 #pragma unroll 4
         for (int i = 0; i < DIM / 8; ++i) {
@@ -427,8 +504,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
         int k2 = 0;
         if (most > 0.0f) k2 = min(max(14 - ((int)(__float_as_uint(most) >> 23) - 127), -103), 126);
         const float up = __uint_as_float((uint32_t)(127 + k2) << 23), up16 = up * 0.0625f;
-        if (r == 0)
+        if (r == 0) {
+          const HalfTile h1 = half_tile(p, t, 1);  // (this thread's is half 0)
+          piece[0] = count;
+          piece[1] = min(max(h.from - off, 0), count);
+          piece[2] = min(max(h.to - off, piece[1]), count);
+          piece[3] = min(max(h1.from - off, 0), count);
+          piece[4] = min(max(h1.to - off, piece[3]), count);
           *factor_slot = __uint_as_float((uint32_t)(127 + 24 - k2) << 23) * (p.scale * kLog2e);
+        }
         const uint32_t dst = sbase + S::kQ + x * S::kTile;
 #pragma unroll 4
         for (int i = 0; i < DIM / 8; ++i) {
@@ -443,17 +527,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
         fence_proxy_async_smem();
         mbar_arrive(q_full);
       }
-      // ---- the steps that this half sees
-      const int from = min(max(h.from - c.off, 0), count);
-      const int upto = min(max(h.to - c.off, from), count);
-      const int seen_to = min(t.last, last_seen(p, t, qi));
-      const int seen_from = max(t.first, first_seen(p, last_seen(p, t, qi)));
-      // tokens that every row of the half sees
+      // ---- the steps that this half sees, and the tokens that all its rows see
+      from = min(max(h.from - off, 0), count);
+      upto = min(max(h.to - off, from), count);
+      token_base = t.base + off * kStep;
       const int hr0 = t.r0 + 128 * x;
-      const int all_to = min(t.last, last_seen(p, t, (int)p.by_group((uint32_t)hr0)));
-      const int all_from = max(t.first, first_seen(p, last_seen(p, t, (int)p.by_group(
-                                            (uint32_t)(hr0 + max(h.rows, 1) - 1)))));
-      float ref = -3.0e38f, m = -3.0e38f, l = 0.0f, wtop = 0.0f;
+      all_to = min(t.last, last_seen(p, t, (int)p.by_group((uint32_t)hr0)));
+      all_from = max(t.first, first_seen(p, last_seen(p, t, (int)p.by_group(
+                                                (uint32_t)(hr0 + max(h.rows, 1) - 1)))));
+      }
+      // (the largest scores and products, which only the careful path reads, are
+      // kept in shared memory)
+      float ref[4], l[4];
+      float* tops = reinterpret_cast<float*>(smem + S::kTops) + threadIdx.x;
+      float *m = tops, *wtop = tops + 4 * 256;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ref[i] = m[i * 256] = -3.0e38f;
+        l[i] = wtop[i * 256] = 0.0f;
+      }
       for (int j = from; j < upto; ++j) {
         const uint32_t slot = (step + j) % kScaleSlots;
         warp_wait(scale_full(slot), (step + j) / kScaleSlots);
@@ -462,119 +554,166 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
         tc_fence_after();
         const float* ks = scales + slot * 2 * kStep;
         const float* vs = ks + kStep;
-        const int token0 = t.base + (c.off + j) * kStep;
+        const int token0 = token_base + j * kStep;
         const bool masked = token0 < all_from || token0 + kStep > all_to;
         bool again = masked;
         if (!masked) {
-          float sv[4][32];
+          uint32_t pw[2][2][16];  // [64 tokens][16 rows]
+          uint64_t nref[4], sum[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, reinterpret_cast<uint32_t(&)[32]>(sv[q]));
-          tmem_ld_wait();
-          uint32_t pw[2][32];
-          const uint64_t nref = pair(-ref, -ref);
-          uint64_t sum0 = 0, sum1 = 0;
+          for (int i = 0; i < 4; ++i) {
+            nref[i] = pair(-ref[i], -ref[i]);
+            sum[i] = 0;
+          }
           __half2 most = __half2half2(__half(0.0f));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {  // four tokens
-            const float* s4 = &sv[i / 8][i % 8 * 4];
-            const ulonglong2 k4 = reinterpret_cast<const ulonglong2*>(ks)[i];
-            const ulonglong2 v4 = reinterpret_cast<const ulonglong2*>(vs)[i];
-            float x0, x1, x2, x3;
-            unpair(fma2(pair(s4[0], s4[1]), k4.x, nref), x0, x1);
-            unpair(fma2(pair(s4[2], s4[3]), k4.y, nref), x2, x3);
-            const uint64_t p0 = pair(ex2(x0), ex2(x1)), p1 = pair(ex2(x2), ex2(x3));
-            sum0 = add2(sum0, p0);
-            sum1 = add2(sum1, p1);
-            float w0, w1, w2, w3;
-            unpair(mul2(p0, v4.x), w0, w1);
-            unpair(mul2(p1, v4.y), w2, w3);
-            const __half2 h0 = __floats2half2_rn(w0, w1), h1 = __floats2half2_rn(w2, w3);
-            most = __hmax2(most, __hmax2(__habs2(h0), __habs2(h1)));
-            pw[i / 16][i % 16 * 2] = *reinterpret_cast<const uint32_t*>(&h0);
-            pw[i / 16][i % 16 * 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+          for (int q = 0; q < 4; ++q) {  // 32 tokens
+            uint32_t sv[2][16];
+            tmem_ld_16x32(ts + 32 * q, sv[0]);
+            tmem_ld_16x32(ts + (16u << 16) + 32 * q, sv[1]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const uint64_t k2 = *reinterpret_cast<const uint64_t*>(ks + 32 * q + 8 * b + 2 * c4);
+              const uint64_t v2 = *reinterpret_cast<const uint64_t*>(vs + 32 * q + 8 * b + 2 * c4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float x0, x1;
+                unpair(fma2(pair(__uint_as_float(sv[i / 2][4 * b + i % 2 * 2]),
+                                 __uint_as_float(sv[i / 2][4 * b + i % 2 * 2 + 1])),
+                            k2, nref[i]),
+                       x0, x1);
+                const uint64_t p2 = pair(ex2(x0), ex2(x1));
+                sum[i] = add2(sum[i], p2);
+                unpair(mul2(p2, v2), x0, x1);
+                const __half2 h = __floats2half2_rn(x0, x1);
+                most = __hmax2(most, __habs2(h));
+                pw[q / 2][i / 2][q % 2 * 8 + 2 * b + i % 2] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+            }
           }
-          float a, b, sum;
-          unpair(add2(sum0, sum1), a, b);
-          sum = a + b;
-          again = sum > kFar || !__hble2(most, __half2half2(__half(32768.0f)));
+          float part[4];
+          again = !__hble2(most, __half2half2(__half(32768.0f)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a, b;
+            unpair(sum[i], a, b);
+            part[i] = a + b;
+            again |= part[i] > kFar;
+          }
           again = __any_sync(0xffffffffu, again);
           if (!again) {
-            l += sum;
-            tmem_st32(ts, pw[0]);
-            tmem_st32(ts + 32, pw[1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[i] += part[i];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) tmem_st_16x32(ts + ((16u * i) << 16) + 32 * q, pw[q][i]);
           }
         }
         if (again) {
-          // masked scores, or weights out of range: with care, 32 tokens at a time
-          float high = m;
-          auto hidden = [&](int token) { return token >= seen_to || token < seen_from; };
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v[32];
-            tmem_ld32(ts + 32 * q, v);
-            tmem_ld_wait();
+          // masked scores, or weights out of range: with care, 64 tokens and 16
+          // rows at a time (rows 2 hh, 2 hh + 1 of the four)
+          const RowTile t = row_tile(p, hide(seq_tile));
+          int sees[4];  // one past the last token that row g + 8 i sees, before clipping
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int n = 32 * q + i;
-              if (!hidden(token0 + n)) high = fmaxf(high, __uint_as_float(v[i]) * ks[n]);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const int row = min(32 * warp + g + 8 * i, t.rows - 1);
+            sees[i] = last_seen(p, t, (int)p.by_group((uint32_t)(t.r0 + row)));
           }
-          float top = wtop * ex2(m - high);
-          const float before = top;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v[32];
-            tmem_ld32(ts + 32 * q, v);
-            tmem_ld_wait();
+          auto hidden = [&](int i, int token) {
+            return token >= min(t.last, sees[i]) || token < max(t.first, first_seen(p, sees[i]));
+          };
+          bool moved = false;
+          float f[4];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int n = 32 * q + i;
-              if (!hidden(token0 + n))
-                top = fmaxf(top, fabsf(ex2(__uint_as_float(v[i]) * ks[n] - high) * vs[n]));
-            }
-          }
-          float next = ref;
-          if (high > m || top > before) {
-            const float lead = fminf(fmaxf(top, kLeastTop), 1.0e30f);
-            next = high - (float)(10 - ((int)(__float_as_uint(lead) >> 23) - 127));
-          }
-          m = high;
-          wtop = top;
-          const float f = ex2(ref - next);
-          const bool moved = next != ref;
-          ref = next;
-          l *= f;
-          // (S of this step was committed after O += P V of the step before)
-          if (j > from && __any_sync(0xffffffffu, moved)) {
+          for (int hh = 0; hh < 2; ++hh) {
+            float high[2] = {m[2 * hh * 256], m[(2 * hh + 1) * 256]}, top[2], before[2];
 #pragma unroll 1
-            for (int q = 0; q < DIM / 32; ++q) {
+            for (int q = 0; q < 2; ++q) {
               uint32_t v[32];
-              tmem_ld32(to_ + 32 * q, v);
+              tmem_ld_16x64(ts + ((16u * hh) << 16) + 64 * q, v);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              tmem_st32(to_ + 32 * q, v);
+              for (int k = 0; k < 32; ++k) {
+                const int n = 64 * q + k / 4 * 8 + 2 * c4 + k % 2, i = k / 2 % 2;
+                if (!hidden(2 * hh + i, token0 + n))
+                  high[i] = fmaxf(high[i], __uint_as_float(v[k]) * ks[n]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 1));
+              high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 2));
+              before[i] = top[i] = wtop[(2 * hh + i) * 256] * ex2(m[(2 * hh + i) * 256] - high[i]);
+            }
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              uint32_t v[32];
+              tmem_ld_16x64(ts + ((16u * hh) << 16) + 64 * q, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const int n = 64 * q + k / 4 * 8 + 2 * c4 + k % 2, i = k / 2 % 2;
+                if (!hidden(2 * hh + i, token0 + n))
+                  top[i] = fmaxf(top[i], fabsf(ex2(__uint_as_float(v[k]) * ks[n] - high[i]) * vs[n]));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+              top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+              float next = ref[2 * hh + i];
+              if (high[i] > m[(2 * hh + i) * 256] || top[i] > before[i]) {
+                const float lead = fminf(fmaxf(top[i], kLeastTop), 1.0e30f);
+                next = high[i] - (float)(kLevel - ((int)(__float_as_uint(lead) >> 23) - 127));
+              }
+              m[(2 * hh + i) * 256] = high[i];
+              wtop[(2 * hh + i) * 256] = top[i];
+              f[2 * hh + i] = ex2(ref[2 * hh + i] - next);
+              moved |= next != ref[2 * hh + i];
+              ref[2 * hh + i] = next;
+              l[2 * hh + i] *= f[2 * hh + i];
+            }
+            // (P overwrites S of these rows and of tokens that are done with)
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              uint32_t v[32], w[16];
+              tmem_ld_16x64(ts + ((16u * hh) << 16) + 64 * q, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const int i = 2 * hh + k / 2 % 2;
+                float w2[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int n = 64 * q + k / 4 * 8 + 2 * c4 + e;
+                  const bool hide = hidden(i, token0 + n);
+                  const float pj =
+                      hide ? 0.0f : ex2(fmaf(__uint_as_float(v[k + e]), ks[n], -ref[i]));
+                  l[i] += pj;
+                  // what a row does not see has weight 0 whatever its scale
+                  w2[e] = hide ? 0.0f : pj * vs[n];
+                }
+                w[k / 2] = pack_f16(w2[0], w2[1]);
+              }
+              tmem_st_16x32(ts + ((16u * hh) << 16) + 32 * q, w);
             }
           }
+          // (S of this step was committed after O += P V of the step before)
+          if (j > from && __any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v[32], w[16];
-            tmem_ld32(ts + 32 * q, v);
-            tmem_ld_wait();
+              for (int q = 0; q < DIM / 64; ++q) {
+                uint32_t v[32];
+                tmem_ld_16x64(to_ + ((16u * hh) << 16) + 64 * q, v);
+                tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float w2[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int n = 32 * q + i + e;
-                const float pj = hidden(token0 + n) ? 0.0f : ex2(fmaf(__uint_as_float(v[i + e]), ks[n], -ref));
-                l += pj;
-                // what a row does not see has weight 0 whatever its scale
-                w2[e] = hidden(token0 + n) ? 0.0f : pj * vs[n];
+                for (int k = 0; k < 32; ++k)
+                  v[k] = __float_as_uint(__uint_as_float(v[k]) * f[2 * hh + k / 2 % 2]);
+                tmem_st_16x64(to_ + ((16u * hh) << 16) + 64 * q, v);
               }
-              w[i / 2] = pack_f16(w2[0], w2[1]);
-            }
-            tmem_st16(ts + 16 * q, w);
           }
         }
         tmem_st_wait();
@@ -582,22 +721,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
         mbar_arrive(p_full(x));
       }
       // ---- the rows' results
-      const bool whole = count == t.steps;
-      const bool none = l == 0.0f;
-      const float inv = none ? 0.0f : 1.0f / l;
-      const float lse = none ? -INFINITY : ref + log2f(l);
+      // (a thread a row again: row `lane` of the warp's 32 is row i = lane / 8 of
+      // the lanes 4 (lane % 8) ..)
+      const RowTile t = row_tile(p, hide(seq_tile));
+      const bool whole = count == t.steps, live = r < t.rows;
+      float l_row = 0.0f, ref_row = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        const float a = __shfl_sync(0xffffffffu, l[i], 4 * (lane % 8));
+        const float b = __shfl_sync(0xffffffffu, ref[i], 4 * (lane % 8));
+        if (lane / 8 == i) {
+          l_row = a;
+          ref_row = b;
+        }
+      }
+      const bool none = l_row == 0.0f;
+      const float inv = none ? 0.0f : 1.0f / l_row;
+      const float lse = none ? -INFINITY : ref_row + log2f(l_row);
       if (upto > from) {
         warp_wait(o_full(x), n_o++);
         tc_fence_after();
       }
-      if (p.joins > 0 && c.off == 0 && (!whole || p.by_tile) && threadIdx.x == 0) {
+      if (p.joins > 0 && off == 0 && (!whole || p.by_tile) && threadIdx.x == 0) {
         const int64_t last = (run.pos + done + t.steps - 1) / run.per;  // the CTA of its last step
-        p.join[p.by_tile ? c.seq_tile * p.cache.heads + c.head : (int)blockIdx.x] =
-            Kv4Join{c.seq_tile, c.head, (int)blockIdx.x, whole ? -1 : (int)last};
+        p.join[p.by_tile ? seq_tile * p.cache.heads + head : (int)blockIdx.x] =
+            Kv4Join{seq_tile, head, (int)blockIdx.x, whole ? -1 : (int)last};
       }
-      const int64_t share = ((int64_t)blockIdx.x * 2 + (c.off == 0)) * p.tile_rows + r;
-      const int64_t at = out_row(p, t, c.head, t.r0 + min(r, t.rows - 1));
-      if (h.rows > 0 && !dead) {
+      const int64_t share = ((int64_t)blockIdx.x * 2 + (off == 0)) * p.tile_rows + r;
+      const int64_t at = out_row(p, t, head, t.r0 + min(r, t.rows - 1));
+      if (t.rows > 128 * x && !dead) {
 #pragma unroll 1
         for (int q = 0; q < DIM / 32; ++q) {
           uint32_t v[32];
@@ -631,7 +785,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
       }
       step += count;
       done += count;
-      if (done < run.count) c.next_tile(p);
+      off = 0;
+      if (done < run.count && ++head == p.cache.heads) {
+        head = 0;
+        do ++seq_tile;
+        while (row_tile(p, hide(seq_tile)).steps == 0);
+      }
     }
   }
   tc_fence_before();
