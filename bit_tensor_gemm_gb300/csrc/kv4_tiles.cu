@@ -52,8 +52,8 @@ struct Smem {
   static constexpr int kK = kQ + 2 * kTile;      // [2] keys
   static constexpr int kV = kK + 2 * kTile;      // [2] values
   static constexpr int kScales = kV + 2 * kTile; // [4][2][128] fp32: keys' x factor, values'
-  static constexpr int kTops = kScales + kScaleSlots * 2 * kStep * 4;  // [2][4][256] fp32
-  static constexpr int kBars = kTops + 2 * 4 * 256 * 4;
+  static constexpr int kState = kScales + kScaleSlots * 2 * kStep * 4;  // [8][256] fp32
+  static constexpr int kBars = kState + 8 * 256 * 4;
   static constexpr int kNumBars = 8 + kScaleSlots + 1 + 7;
   static constexpr int kMisc = kBars + 8 * kNumBars;
   static constexpr int kBytes = kMisc + 96 + 1024;  // slack to align to 1024
@@ -74,21 +74,8 @@ __device__ __forceinline__ uint64_t smem_desc_rows_k(uint32_t addr, uint32_t blo
   return d;
 }
 
-// 16 TMEM lanes x 64 columns: register 4 b + i of lane (g, c) is column 8 b + 2 c +
+// 16 TMEM lanes x 32 columns: register 4 b + i of lane (g, c) is column 8 b + 2 c +
 // i % 2 of TMEM lane g + 8 (i / 2).
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32"
-      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
-      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31},"
-      " [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
-        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
-        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32"
@@ -98,28 +85,36 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16])
         "=r"(v[14]), "=r"(v[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_16x64(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0],"
-      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
-      " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
-          taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
-      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-      "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
-}
-// 16 TMEM lanes x 32 columns of pairs of halves: register 2 b + i of lane (g, c) is
-// column 4 b + c of TMEM lane g + 8 i.
 __device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0],"
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0],"
       " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+// 16 TMEM lanes x 16 columns of pairs of halves: register 2 b + i of lane (g, c) is
+// column 4 b + c of TMEM lane g + 8 i.
+__device__ __forceinline__ void tmem_ld_16x16h(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x16h(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
+// Wait for this thread's TMEM loads; the registers that they fill pass through
+// it, so that nothing uses them before.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[N]) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -146,10 +141,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-template <int N>
+template <bool B>
 struct Const {
-  static constexpr int value = N;
+  static constexpr bool value = B;
 };
+
+constexpr float kNoRef = -3.0e38f;  // the reference of a row that has seen nothing
 
 // 16 bytes that this SM reads once: past the L1, which is small beside this much
 // shared memory.
@@ -205,8 +202,112 @@ __device__ __forceinline__ HalfTile half_tile(const Kv4AttnParams& p, const RowT
   return h;
 }
 
+// The careful form of 32 tokens' weights (chunk q of the step whose S begins at
+// `ts`; warp-uniform call).  state: this thread's ref[4], l[4] in shared memory,
+// 256 floats apart; ks: the chunk's scales of this thread's first columns; seen:
+// the tokens of the step that each of its four rows sees.  Where a reference
+// moves, the sums (`to`, when they hold anything: S of this step was committed
+// after O += P V of the step before) and this step's weights so far follow.
+// A function of its own, so that its registers are not the loop's.
+template <int DIM>
+__device__ __noinline__ void careful_weights(uint32_t ts, uint32_t to_, const float* ks, int q,
+                                             bool sums, uint32_t seen0, uint32_t seen1,
+                                             uint32_t seen2, uint32_t seen3, float* state) {
+  const int c4 = threadIdx.x % 4;
+  float f[4];
+  bool moved = false;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t sv[16], pw[8];
+    tmem_ld_16x32(ts + (half ? 16u << 16 : 0u) + 32 * q, sv);
+    tmem_ld_wait_for(sv);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 2 * half + k;
+      const uint32_t seen = i == 0 ? seen0 : i == 1 ? seen1 : i == 2 ? seen2 : seen3;
+      const int to = (int)(seen >> 16) - 32 * q - 2 * c4, fr = (int)(seen & 0xffffu) - 32 * q - 2 * c4;
+      const float rf = state[i * 256];
+      float high = -INFINITY, top = -INFINITY;  // of t; of log2 |2^t vs|
+      float s8[8];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int token = n / 2 * 8 + n % 2;
+        const bool see = token < to && token >= fr;
+        s8[n] = see ? __uint_as_float(sv[n / 2 * 4 + k * 2 + n % 2]) * ks[token] : -INFINITY;
+        high = fmaxf(high, s8[n]);
+        const float v = fabsf(ks[kStep + token]);
+        if (see && v < INFINITY) top = fmaxf(top, s8[n] + __log2f(v));
+      }
+#pragma unroll
+      for (int d = 1; d < 4; d *= 2) {  // (the four lanes of a row agree)
+        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      }
+      float ref = rf;
+      const float need = fmaxf(fminf(top, 3.0e38f) - kLevel, high - 90.0f);
+      if (rf == kNoRef) {
+        if (high > -INFINITY) ref = need;
+      } else if (top - rf > 14.9f || high - rf > 99.0f) {
+        ref = rf + ceilf(need - rf);
+      }
+      f[i] = rf == kNoRef ? 0.0f : ex2(rf - ref);
+      moved |= rf != kNoRef && ref != rf;
+      float total = 0.0f;
+#pragma unroll
+      for (int n = 0; n < 8; n += 2) {
+        float w2[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int token = n / 2 * 8 + e;
+          const bool see = token < to && token >= fr;
+          const float pj = ex2(s8[n + e] - ref);
+          total += see ? pj : 0.0f;
+          // what a row does not see has weight 0 whatever its scale
+          w2[e] = see ? pj * ks[kStep + token] : 0.0f;
+        }
+        pw[n + k] = pack_f16(w2[0], w2[1]);
+      }
+      state[i * 256] = ref;
+      state[(4 + i) * 256] = state[(4 + i) * 256] * f[i] + total;
+    }
+    tmem_st_16x16h(ts + (half ? 16u << 16 : 0u) + 16 * q, pw);
+  }
+  if (!__any_sync(0xffffffffu, moved)) return;
+  tmem_st_wait();
+  if (sums) {
+#pragma unroll 1
+    for (int n = 0; n < DIM / 16; ++n) {  // 16 rows x 32 columns at a time
+      const uint32_t at = to_ + (n % 2 ? 16u << 16 : 0u) + n / 2 * 32;
+      uint32_t v[16];
+      tmem_ld_16x32(at, v);
+      tmem_ld_wait_for(v);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float fk = k / 2 % 2 ? (n % 2 ? f[3] : f[1]) : (n % 2 ? f[2] : f[0]);
+        v[k] = __float_as_uint(__uint_as_float(v[k]) * fk);
+      }
+      tmem_st_16x32(at, v);
+    }
+  }
+#pragma unroll 1
+  for (int n = 0; n < 2 * q; ++n) {
+    const uint32_t at = ts + (n % 2 ? 16u << 16 : 0u) + n / 2 * 16;
+    uint32_t v[8];
+    tmem_ld_16x16h(at, v);
+    tmem_ld_wait_for(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {  // (in fp32: a factor may be below fp16's range)
+      const float fk = k % 2 ? (n % 2 ? f[3] : f[1]) : (n % 2 ? f[2] : f[0]);
+      const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
+      v[k] = pack_f16(w.x * fk, w.y * fk);
+    }
+    tmem_st_16x16h(at, v);
+  }
+}
+
 template <typename T, int DIM>
-__global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    kv4_tiles_kernel(const __grid_constant__ Kv4AttnParams p) {
   using S = Smem<DIM>;
   constexpr int kBlock = kStep * 128;
   constexpr uint32_t kIdescS = instr_desc(128, kStep);
@@ -275,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
   };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 12) {
       // ---------------- the MMAs ----------------
       // The whole warp walks, lane 0 issues: what it passes stays warp-uniform and
@@ -288,9 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
         uint32_t step = 0, tile = 0;     // of the run: steps so far, tiles so far
         uint32_t n_p0 = 0, n_p1 = 0;     // weights of each half consumed so far
         // O_X += P_X V of run step sv; S_X = Q_X K^T of run step sj
-        auto issue_o = [&](auto half, uint32_t sv, bool first, bool last, uint32_t& n_p) {
-          constexpr int X = decltype(half)::value;
-          warp_wait(p_full(X), n_p++);
+        auto issue_o = [&](int X, uint32_t sv, bool first, bool last) {
+          warp_wait(p_full(X), X ? n_p1++ : n_p0++);
           if (dead) return;
           tc_fence_after();
           if (lane == 0) {
@@ -303,17 +403,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
           }
           __syncwarp();
         };
-        auto issue_s = [&](auto half, uint32_t sj) {
-          constexpr int X = decltype(half)::value;
+        auto issue_s = [&](int X, uint32_t sj) {
           if (dead) return;
           tc_fence_after();
           if (lane == 0) {
-            const uint64_t k0 = k_desc + (sj & 1) * (S::kTile >> 4);
+            const uint64_t q0 = q_desc + X * (S::kTile >> 4), k0 = k_desc + (sj & 1) * (S::kTile >> 4);
 #pragma unroll
             for (int k = 0; k < DIM / 16; ++k) {
-              constexpr uint64_t kXQ = X * (S::kTile >> 4);
               const uint64_t at = ((k / 4) * kBlock + (k % 4) * 32) >> 4;
-              mma_f16(tmem + 128 * X, q_desc + kXQ + at, k0 + at, kIdescS, k > 0 ? 1u : 0u);
+              mma_f16(tmem + 128 * X, q0 + at, k0 + at, kIdescS, k > 0 ? 1u : 0u);
             }
             mma_commit(s_full(X));
           }
@@ -326,12 +424,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
           for (int j = 0; j <= count; ++j) {
             const uint32_t sj = step + j, sv = sj - 1;  // run steps of the keys, the values
             if (j > 0) warp_wait(v_full(sv & 1), sv >> 1);
-            if (j > from0 && j <= to0) issue_o(Const<0>{}, sv, j - 1 == from0, j == to0, n_p0);
-            if (j < count) warp_wait(k_full(sj & 1), sj >> 1);
-            if (j >= from0 && j < to0) issue_s(Const<0>{}, sj);
-            if (j > from1 && j <= to1) issue_o(Const<1>{}, sv, j - 1 == from1, j == to1, n_p1);
-            if (lane == 0 && j > 0 && !dead) mma_commit(v_empty(sv & 1));
-            if (j >= from1 && j < to1) issue_s(Const<1>{}, sj);
+#pragma unroll 1
+            for (int X = 0; X < 2; ++X) {
+              const int from = X ? from1 : from0, to = X ? to1 : to0;
+              if (j > from && j <= to) issue_o(X, sv, j - 1 == from, j == to);
+              if (X == 1 && lane == 0 && j > 0 && !dead) mma_commit(v_empty(sv & 1));
+              if (X == 0 && j < count) warp_wait(k_full(sj & 1), sj >> 1);
+              if (j >= from && j < to) issue_s(X, sj);
+            }
             if (lane == 0 && j < count && !dead) mma_commit(k_empty(sj & 1));
           }
           step += count;
@@ -353,20 +453,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
       // Groups of TPL tokens go to the warps in turn; a lane takes 32 codes (16
       // bytes) of a token, the lanes of a phase of 8 different tokens of 8 (no
       // bank conflicts).
-      auto converter = [&](auto which) {
-        constexpr bool VALUES = decltype(which)::value == 1;
-        constexpr int WARPS = VALUES ? 3 : 4;
+      {
+        const bool values = warp > 12;
+        const int warps = values ? 3 : 4;
         constexpr int LPT = DIM / 32, TPL = 32 / LPT, GROUPS = kStep / TPL;
-        constexpr int LOADS = (GROUPS + WARPS - 1) / WARPS, SCALES = VALUES ? 2 : 1;
-        const int cw = warp - (VALUES ? 13 : 8), ctid = cw * 32 + lane, chunk = lane / TPL;
+        constexpr int LOADS = (GROUPS + 2) / 3, SCALES = 2;
+        const int cw = warp - (values ? 13 : 8), ctid = cw * 32 + lane, chunk = lane / TPL;
         const int page_size = (int)p.cache.page_size;
         const uint32_t page16 = (uint32_t)page_size / 16;
-        const uint8_t* codes_at = p.cache.base + (VALUES ? (int64_t)page_size * (DIM / 2) : 0) +
+        const uint8_t* codes_at = p.cache.base + (values ? (int64_t)page_size * (DIM / 2) : 0) +
                                   chunk * 16 + lane % TPL % 16 * (DIM / 2);
-        const uint8_t* scales_at = p.cache.base + (int64_t)page_size * (DIM + (VALUES ? 2 : 0));
+        const uint8_t* scales_at = p.cache.base + (int64_t)page_size * (DIM + (values ? 2 : 0));
         // where the loads stand: `ahead` steps into the run; lane l < 8 has the
         // offsets of the codes and scales of the step's tokens 16 l and on (-1: none)
-        Cursor c;
+        Cursor c = {};
         int ahead = 0;
         int64_t codes_off, scales_off;
         auto find = [&]() {
@@ -391,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
         auto load = [&]() {
 #pragma unroll
           for (int i = 0; i < LOADS; ++i) {
-            const int first = (cw + WARPS * i) * TPL;  // token of the step
+            const int first = (cw + warps * i) * TPL;  // token of the step
             const int64_t off = __shfl_sync(0xffffffffu, codes_off, first / 16 % 8);
             raw[i] = make_uint4(0, 0, 0, 0);
             if (first < kStep && off >= 0)
@@ -399,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
           }
 #pragma unroll
           for (int i = 0; i < SCALES; ++i) {
-            const int token = ctid + 32 * WARPS * i;
+            const int token = ctid + 32 * warps * i;
             const int64_t off = __shfl_sync(0xffffffffu, scales_off, token / 16 % 8);
             raw_s[i] = 0;
             if (token < kStep && off >= 0)
@@ -408,14 +508,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
           if (++ahead < run.count && ++c.off == c.t.steps) c.next_tile(p);
           find();
         };
-        c.start(p, run);
-        find();
-        load();
+        if (run.count > 0) {
+          c.start(p, run);
+          find();
+          load();
+        }
         uint32_t tile = 0;
         int left = 0;  // (keys) steps of the present tile still to convert
         float factor = 1.0f;
         for (int s = 0; s < run.count; ++s) {
-          if (!VALUES && left-- == 0) {
+          if (!values && left-- == 0) {
             wait(q_full, tile++);
             left = dead ? run.count : piece[0] - 1;
             factor = *reinterpret_cast<volatile float*>(factor_slot);
@@ -423,17 +525,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
           const int st = s & 1, use = s >> 1;
 #pragma unroll
           for (int i = 0; i < SCALES; ++i) {
-            const int token = ctid + 32 * WARPS * i;
+            const int token = ctid + 32 * warps * i;
             if (token < kStep)
-              scales[((s % kScaleSlots) * 2 + (VALUES ? 1 : 0)) * kStep + token] =
+              scales[((s % kScaleSlots) * 2 + (values ? 1 : 0)) * kStep + token] =
                   __uint_as_float(raw_s[i] << 16) * factor;
           }
           mbar_arrive(scale_full(s % kScaleSlots));
-          if (use > 0) wait(VALUES ? v_empty(st) : k_empty(st), use - 1);
-          const uint32_t dst = sbase + (VALUES ? S::kV : S::kK) + st * S::kTile;
+          if (use > 0) wait(values ? v_empty(st) : k_empty(st), use - 1);
+          const uint32_t dst = sbase + (values ? S::kV : S::kK) + st * S::kTile;
 #pragma unroll
           for (int i = 0; i < LOADS; ++i) {
-            const int r = (cw + WARPS * i) * TPL + lane % TPL;
+            const int r = (cw + warps * i) * TPL + lane % TPL;
             if (r >= kStep) continue;
             const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
@@ -445,19 +547,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
             }
           }
           fence_proxy_async_smem();
-          mbar_arrive(VALUES ? v_full(st) : k_full(st));
+          mbar_arrive(values ? v_full(st) : k_full(st));
           __syncwarp();
           load();
         }
-      };
-      if (run.count > 0) {
-        if (warp < 12) converter(Const<0>{});
-        else converter(Const<1>{});
       }
     }
   } else {
     // ---------------- softmax ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     const int x = warp / 4, r = threadIdx.x;  // half; row of the 256 (queries and results)
     const int g = lane / 4, c4 = lane % 4;    // scores: rows g + 8 i of the warp's 32, i < 4
     const uint32_t lane_base = (uint32_t)(32 * (warp % 4)) << 16;
@@ -536,64 +634,97 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
       all_from = max(t.first, first_seen(p, last_seen(p, t, (int)p.by_group(
                                                 (uint32_t)(hr0 + max(h.rows, 1) - 1)))));
       }
-      // (the largest scores and products, which only the careful path reads, are
-      // kept in shared memory)
+      // Per row: weights 2^(t - ref), l their sum.  A weight times a value scale goes
+      // into the value product in fp16; `ref` puts the largest of those at 2^10 when
+      // it is set, and moves (up, by whole binades, so that what is there scales
+      // exactly) when one exceeds 2^15, or a weight 2^100: fp16 then holds them
+      // without loss down to 2^-24 of the largest, whatever scores and scales look
+      // like.  Until a row has seen a token its reference is kNoRef: its first
+      // weight overflows and so sets it.
       float ref[4], l[4];
-      float* tops = reinterpret_cast<float*>(smem + S::kTops) + threadIdx.x;
-      float *m = tops, *wtop = tops + 4 * 256;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        ref[i] = m[i * 256] = -3.0e38f;
-        l[i] = wtop[i * 256] = 0.0f;
+        ref[i] = kNoRef;
+        l[i] = 0.0f;
       }
+      float* state = reinterpret_cast<float*>(smem + S::kState) + threadIdx.x;
       for (int j = from; j < upto; ++j) {
         const uint32_t slot = (step + j) % kScaleSlots;
         warp_wait(scale_full(slot), (step + j) / kScaleSlots);
         warp_wait(s_full(x), n_s++);
         if (dead) break;
         tc_fence_after();
-        const float* ks = scales + slot * 2 * kStep;
-        const float* vs = ks + kStep;
         const int token0 = token_base + j * kStep;
         const bool masked = token0 < all_from || token0 + kStep > all_to;
-        bool again = masked;
-        if (!masked) {
-          uint32_t pw[2][2][16];  // [64 tokens][16 rows]
-          uint64_t nref[4], sum[4];
+        // tokens of the step that row i sees: from the low half, to the high half
+        uint32_t seen[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) seen[i] = (uint32_t)kStep << 16;
+        if (masked) {
+          const RowTile t = row_tile(p, hide(seq_tile));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            nref[i] = pair(-ref[i], -ref[i]);
-            sum[i] = 0;
+            const int row = min(32 * warp + g + 8 * i, t.rows - 1);
+            const int sees = last_seen(p, t, (int)p.by_group((uint32_t)(t.r0 + row)));
+            const int lo = max(t.first, first_seen(p, sees)) - token0;
+            const int hi = min(t.last, sees) - token0;
+            seen[i] = (uint32_t)min(max(lo, 0), kStep) | (uint32_t)min(max(hi, 0), kStep) << 16;
           }
-          __half2 most = __half2half2(__half(0.0f));
+        }
+        // (not unrolled: the loops of all roles have to stay in the SM's instruction
+        // cache; unrolled, a kernel of 1.85 ms waited for instructions half its time)
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {  // 32 tokens; P overwrites S that is done with
+          const float* ks = scales + slot * 2 * kStep + 32 * q + 2 * c4;
+          uint32_t sv[2][16], pw[2][8];
+          tmem_ld_16x32(ts + 32 * q, sv[0]);
+          tmem_ld_16x32(ts + (16u << 16) + 32 * q, sv[1]);
+          tmem_ld_wait_for(sv[0]);
+          tmem_ld_wait_for(sv[1]);
+          uint64_t sum[4];
+          __half2 most[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {  // 32 tokens
-            uint32_t sv[2][16];
-            tmem_ld_16x32(ts + 32 * q, sv[0]);
-            tmem_ld_16x32(ts + (16u << 16) + 32 * q, sv[1]);
-            tmem_ld_wait();
+          for (int i = 0; i < 4; ++i) {
+            sum[i] = 0;
+            most[i] = __half2half2(__half(0.0f));
+          }
+          bool again = false;
+          auto weights = [&](auto with_mask) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-              const uint64_t k2 = *reinterpret_cast<const uint64_t*>(ks + 32 * q + 8 * b + 2 * c4);
-              const uint64_t v2 = *reinterpret_cast<const uint64_t*>(vs + 32 * q + 8 * b + 2 * c4);
+              const uint64_t k2 = *reinterpret_cast<const uint64_t*>(ks + 8 * b);
+              const uint64_t v2 = *reinterpret_cast<const uint64_t*>(ks + kStep + 8 * b);
+              if (with_mask.value) {  // a scale that is not a number may stand in a masked place
+                float a, c;
+                unpair(v2, a, c);
+                again |= !(fabsf(a) < INFINITY) || !(fabsf(c) < INFINITY);
+              }
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float x0, x1;
                 unpair(fma2(pair(__uint_as_float(sv[i / 2][4 * b + i % 2 * 2]),
                                  __uint_as_float(sv[i / 2][4 * b + i % 2 * 2 + 1])),
-                            k2, nref[i]),
+                            k2, pair(-ref[i], -ref[i])),
                        x0, x1);
+                if (with_mask.value) {
+                  const int n = 32 * q + 8 * b + 2 * c4, lo = seen[i] & 0xffffu, hi = seen[i] >> 16;
+                  if (n < lo || n >= hi) x0 = -INFINITY;
+                  if (n + 1 < lo || n + 1 >= hi) x1 = -INFINITY;
+                }
                 const uint64_t p2 = pair(ex2(x0), ex2(x1));
                 sum[i] = add2(sum[i], p2);
                 unpair(mul2(p2, v2), x0, x1);
                 const __half2 h = __floats2half2_rn(x0, x1);
-                most = __hmax2(most, __habs2(h));
-                pw[q / 2][i / 2][q % 2 * 8 + 2 * b + i % 2] = *reinterpret_cast<const uint32_t*>(&h);
+                most[i] = __hmax2(most[i], __habs2(h));
+                pw[i / 2][2 * b + i % 2] = *reinterpret_cast<const uint32_t*>(&h);
               }
             }
-          }
+          };
+          if (masked) weights(Const<true>{});
+          else weights(Const<false>{});
           float part[4];
-          again = !__hble2(most, __half2half2(__half(32768.0f)));
+          again |= !__hble2(__hmax2(__hmax2(most[0], most[1]), __hmax2(most[2], most[3])),
+                            __half2half2(__half(32768.0f)));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float a, b;
@@ -601,120 +732,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
             part[i] = a + b;
             again |= part[i] > kFar;
           }
-          again = __any_sync(0xffffffffu, again);
-          if (!again) {
+          if (__any_sync(0xffffffffu, again)) {
+            // weights out of range, or odd scales beside a mask: once more, with care
 #pragma unroll
-            for (int i = 0; i < 4; ++i) l[i] += part[i];
+            for (int i = 0; i < 4; ++i) {
+              state[i * 256] = ref[i];
+              state[(4 + i) * 256] = l[i];
+            }
+            careful_weights<DIM>(ts, to_, ks, q, j > from, seen[0], seen[1], seen[2], seen[3], state);
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) tmem_st_16x32(ts + ((16u * i) << 16) + 32 * q, pw[q][i]);
+            for (int i = 0; i < 4; ++i) {
+              ref[i] = state[i * 256];
+              l[i] = state[(4 + i) * 256];
+            }
+            continue;
           }
-        }
-        if (again) {
-          // masked scores, or weights out of range: with care, 64 tokens and 16
-          // rows at a time (rows 2 hh, 2 hh + 1 of the four)
-          const RowTile t = row_tile(p, hide(seq_tile));
-          int sees[4];  // one past the last token that row g + 8 i sees, before clipping
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = min(32 * warp + g + 8 * i, t.rows - 1);
-            sees[i] = last_seen(p, t, (int)p.by_group((uint32_t)(t.r0 + row)));
-          }
-          auto hidden = [&](int i, int token) {
-            return token >= min(t.last, sees[i]) || token < max(t.first, first_seen(p, sees[i]));
-          };
-          bool moved = false;
-          float f[4];
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float high[2] = {m[2 * hh * 256], m[(2 * hh + 1) * 256]}, top[2], before[2];
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-              uint32_t v[32];
-              tmem_ld_16x64(ts + ((16u * hh) << 16) + 64 * q, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const int n = 64 * q + k / 4 * 8 + 2 * c4 + k % 2, i = k / 2 % 2;
-                if (!hidden(2 * hh + i, token0 + n))
-                  high[i] = fmaxf(high[i], __uint_as_float(v[k]) * ks[n]);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 1));
-              high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 2));
-              before[i] = top[i] = wtop[(2 * hh + i) * 256] * ex2(m[(2 * hh + i) * 256] - high[i]);
-            }
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-              uint32_t v[32];
-              tmem_ld_16x64(ts + ((16u * hh) << 16) + 64 * q, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const int n = 64 * q + k / 4 * 8 + 2 * c4 + k % 2, i = k / 2 % 2;
-                if (!hidden(2 * hh + i, token0 + n))
-                  top[i] = fmaxf(top[i], fabsf(ex2(__uint_as_float(v[k]) * ks[n] - high[i]) * vs[n]));
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-              top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-              float next = ref[2 * hh + i];
-              if (high[i] > m[(2 * hh + i) * 256] || top[i] > before[i]) {
-                const float lead = fminf(fmaxf(top[i], kLeastTop), 1.0e30f);
-                next = high[i] - (float)(kLevel - ((int)(__float_as_uint(lead) >> 23) - 127));
-              }
-              m[(2 * hh + i) * 256] = high[i];
-              wtop[(2 * hh + i) * 256] = top[i];
-              f[2 * hh + i] = ex2(ref[2 * hh + i] - next);
-              moved |= next != ref[2 * hh + i];
-              ref[2 * hh + i] = next;
-              l[2 * hh + i] *= f[2 * hh + i];
-            }
-            // (P overwrites S of these rows and of tokens that are done with)
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-              uint32_t v[32], w[16];
-              tmem_ld_16x64(ts + ((16u * hh) << 16) + 64 * q, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                const int i = 2 * hh + k / 2 % 2;
-                float w2[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int n = 64 * q + k / 4 * 8 + 2 * c4 + e;
-                  const bool hide = hidden(i, token0 + n);
-                  const float pj =
-                      hide ? 0.0f : ex2(fmaf(__uint_as_float(v[k + e]), ks[n], -ref[i]));
-                  l[i] += pj;
-                  // what a row does not see has weight 0 whatever its scale
-                  w2[e] = hide ? 0.0f : pj * vs[n];
-                }
-                w[k / 2] = pack_f16(w2[0], w2[1]);
-              }
-              tmem_st_16x32(ts + ((16u * hh) << 16) + 32 * q, w);
-            }
-          }
-          // (S of this step was committed after O += P V of the step before)
-          if (j > from && __any_sync(0xffffffffu, moved)) {
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-#pragma unroll 1
-              for (int q = 0; q < DIM / 64; ++q) {
-                uint32_t v[32];
-                tmem_ld_16x64(to_ + ((16u * hh) << 16) + 64 * q, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  v[k] = __float_as_uint(__uint_as_float(v[k]) * f[2 * hh + k / 2 % 2]);
-                tmem_st_16x64(to_ + ((16u * hh) << 16) + 64 * q, v);
-              }
-          }
+          for (int i = 0; i < 4; ++i) l[i] += part[i];
+          tmem_st_16x16h(ts + 16 * q, pw[0]);
+          tmem_st_16x16h(ts + (16u << 16) + 16 * q, pw[1]);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -757,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tiles_kernel(const Kv4AttnPar
           uint32_t v[32];
           if (upto > from) {
             tmem_ld32(to_ + 32 * q, v);
-            tmem_ld_wait();
+            tmem_ld_wait_for(v);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
