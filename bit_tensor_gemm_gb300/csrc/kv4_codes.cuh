@@ -10,7 +10,7 @@ namespace lbg {
 // The reference of a row's weights moves when one exceeds kFar, and is set for
 // a largest product of at least kLeastTop.
 constexpr float kFar = 1.2676506e30f;       // 2^100
-constexpr int kLevel = 10;                   // the largest product is put at 2^10 .. 2^11
+constexpr int kLevel = 11;  // the largest product is put at 2^11
 constexpr float kLeastTop = 8.2718061e-25f;  // 2^-80
 
 // Codes 0 and 4 of a word (HIGH: 1 and 5) as two subnormal halves: (code + 8)

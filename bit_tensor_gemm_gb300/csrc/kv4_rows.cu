@@ -420,9 +420,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
               float next = ref[nt][e];
               // (the eight lanes of a column agree on all of this)
               if (high > m[nt][e] || top > before) {
-                // 2^(high - next) top = 2^kLevel .. 2^(kLevel + 1)
+                // 2^(high - next) top = 2^(kLevel - 1) .. 2^kLevel
                 const float lead = fminf(fmaxf(top, kLeastTop), 1.0e30f);
-                next = high - (float)(kLevel - ((int)(__float_as_uint(lead) >> 23) - 127));
+                next = high - (float)(kLevel - 1 - ((int)(__float_as_uint(lead) >> 23) - 127));
               }
               m[nt][e] = high;
               wtop[nt][e] = top;

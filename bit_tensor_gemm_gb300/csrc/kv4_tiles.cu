@@ -141,9 +141,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-template <bool B>
+template <typename V, V N>
 struct Const {
-  static constexpr bool value = B;
+  static constexpr V value = N;
 };
 
 constexpr float kNoRef = -3.0e38f;  // the reference of a row that has seen nothing
@@ -202,106 +202,97 @@ __device__ __forceinline__ HalfTile half_tile(const Kv4AttnParams& p, const RowT
   return h;
 }
 
-// The careful form of 32 tokens' weights (chunk q of the step whose S begins at
-// `ts`; warp-uniform call).  state: this thread's ref[4], l[4] in shared memory,
-// 256 floats apart; ks: the chunk's scales of this thread's first columns; seen:
-// the tokens of the step that each of its four rows sees.  Where a reference
-// moves, the sums (`to`, when they hold anything: S of this step was committed
-// after O += P V of the step before) and this step's weights so far follow.
-// A function of its own, so that its registers are not the loop's.
+// The careful form of the weights of 32 tokens (chunk q of the step) and two of a
+// thread's rows, 16 TMEM lanes, whose S begins at `ts` (warp-uniform call).
+// state: the rows' ref[2], l[2] in shared memory, 256 floats apart; ks: the
+// chunk's scales of this thread's first columns; seen: the tokens of the step
+// that each row sees (from the low half to the high half), beside `state`.  Where a reference moves, the sums (at `to`, when they hold
+// anything: S of this step was committed after O += P V of the step before) and
+// this step's weights so far follow.  A function of its own, so that its
+// registers are not the loop's.
 template <int DIM>
-__device__ __noinline__ void careful_weights(uint32_t ts, uint32_t to_, const float* ks, int q,
-                                             bool sums, uint32_t seen0, uint32_t seen1,
-                                             uint32_t seen2, uint32_t seen3, float* state) {
+__device__ __noinline__ void careful_weights(uint32_t ts, uint32_t to, const float* ks, int q,
+                                             bool sums, const uint32_t* seen_at,
+                                             float* state) {
   const int c4 = threadIdx.x % 4;
-  float f[4];
+  float f[2];
   bool moved = false;
+  uint32_t sv[16], pw[8];
+  tmem_ld_16x32(ts + 32 * q, sv);
+  tmem_ld_wait_for(sv);
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t sv[16], pw[8];
-    tmem_ld_16x32(ts + (half ? 16u << 16 : 0u) + 32 * q, sv);
-    tmem_ld_wait_for(sv);
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t seen = seen_at[i * 256];
+    const int upto = (int)(seen >> 16) - 32 * q - 2 * c4, from = (int)(seen & 0xffffu) - 32 * q - 2 * c4;
+    const float rf = state[i * 256];
+    float high = -INFINITY, top = -INFINITY;  // of t; of log2 |2^t vs|
+    float s8[8];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int i = 2 * half + k;
-      const uint32_t seen = i == 0 ? seen0 : i == 1 ? seen1 : i == 2 ? seen2 : seen3;
-      const int to = (int)(seen >> 16) - 32 * q - 2 * c4, fr = (int)(seen & 0xffffu) - 32 * q - 2 * c4;
-      const float rf = state[i * 256];
-      float high = -INFINITY, top = -INFINITY;  // of t; of log2 |2^t vs|
-      float s8[8];
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int token = n / 2 * 8 + n % 2;
-        const bool see = token < to && token >= fr;
-        s8[n] = see ? __uint_as_float(sv[n / 2 * 4 + k * 2 + n % 2]) * ks[token] : -INFINITY;
-        high = fmaxf(high, s8[n]);
-        const float v = fabsf(ks[kStep + token]);
-        if (see && v < INFINITY) top = fmaxf(top, s8[n] + __log2f(v));
-      }
-#pragma unroll
-      for (int d = 1; d < 4; d *= 2) {  // (the four lanes of a row agree)
-        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      }
-      float ref = rf;
-      const float need = fmaxf(fminf(top, 3.0e38f) - kLevel, high - 90.0f);
-      if (rf == kNoRef) {
-        if (high > -INFINITY) ref = need;
-      } else if (top - rf > 14.9f || high - rf > 99.0f) {
-        ref = rf + ceilf(need - rf);
-      }
-      f[i] = rf == kNoRef ? 0.0f : ex2(rf - ref);
-      moved |= rf != kNoRef && ref != rf;
-      float total = 0.0f;
-#pragma unroll
-      for (int n = 0; n < 8; n += 2) {
-        float w2[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int token = n / 2 * 8 + e;
-          const bool see = token < to && token >= fr;
-          const float pj = ex2(s8[n + e] - ref);
-          total += see ? pj : 0.0f;
-          // what a row does not see has weight 0 whatever its scale
-          w2[e] = see ? pj * ks[kStep + token] : 0.0f;
-        }
-        pw[n + k] = pack_f16(w2[0], w2[1]);
-      }
-      state[i * 256] = ref;
-      state[(4 + i) * 256] = state[(4 + i) * 256] * f[i] + total;
+    for (int n = 0; n < 8; ++n) {
+      const int token = n / 2 * 8 + n % 2;
+      const bool see = token < upto && token >= from;
+      s8[n] = see ? __uint_as_float(sv[n / 2 * 4 + i * 2 + n % 2]) * ks[token] : -INFINITY;
+      high = fmaxf(high, s8[n]);
+      const float v = fabsf(ks[kStep + token]);
+      if (see && v < INFINITY) top = fmaxf(top, s8[n] + __log2f(v));
     }
-    tmem_st_16x16h(ts + (half ? 16u << 16 : 0u) + 16 * q, pw);
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2) {  // (the four lanes of a row agree)
+      high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
+    float ref = rf;
+    const float need = fmaxf(fminf(top, 3.0e38f) - kLevel, high - 90.0f);
+    if (rf == kNoRef) {
+      if (high > -INFINITY) ref = need;
+    } else if (top - rf > 14.9f || high - rf > 99.0f) {
+      ref = rf + ceilf(need - rf);
+    }
+    f[i] = rf == kNoRef ? 0.0f : ex2(rf - ref);
+    moved |= rf != kNoRef && ref != rf;
+    float total = 0.0f;
+#pragma unroll
+    for (int n = 0; n < 8; n += 2) {
+      float w2[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int token = n / 2 * 8 + e;
+        const bool see = token < upto && token >= from;
+        const float pj = ex2(s8[n + e] - ref);
+        total += see ? pj : 0.0f;
+        // what a row does not see has weight 0 whatever its scale
+        w2[e] = see ? pj * ks[kStep + token] : 0.0f;
+      }
+      pw[n + i] = pack_f16(w2[0], w2[1]);
+    }
+    state[i * 256] = ref;
+    state[(2 + i) * 256] = state[(2 + i) * 256] * f[i] + total;
   }
+  tmem_st_16x16h(ts + 16 * q, pw);
   if (!__any_sync(0xffffffffu, moved)) return;
   tmem_st_wait();
   if (sums) {
 #pragma unroll 1
-    for (int n = 0; n < DIM / 16; ++n) {  // 16 rows x 32 columns at a time
-      const uint32_t at = to_ + (n % 2 ? 16u << 16 : 0u) + n / 2 * 32;
+    for (int n = 0; n < DIM / 32; ++n) {
       uint32_t v[16];
-      tmem_ld_16x32(at, v);
+      tmem_ld_16x32(to + 32 * n, v);
       tmem_ld_wait_for(v);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float fk = k / 2 % 2 ? (n % 2 ? f[3] : f[1]) : (n % 2 ? f[2] : f[0]);
-        v[k] = __float_as_uint(__uint_as_float(v[k]) * fk);
-      }
-      tmem_st_16x32(at, v);
+      for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f[k / 2 % 2]);
+      tmem_st_16x32(to + 32 * n, v);
     }
   }
 #pragma unroll 1
-  for (int n = 0; n < 2 * q; ++n) {
-    const uint32_t at = ts + (n % 2 ? 16u << 16 : 0u) + n / 2 * 16;
+  for (int n = 0; n < q; ++n) {
     uint32_t v[8];
-    tmem_ld_16x16h(at, v);
+    tmem_ld_16x16h(ts + 16 * n, v);
     tmem_ld_wait_for(v);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {  // (in fp32: a factor may be below fp16's range)
-      const float fk = k % 2 ? (n % 2 ? f[3] : f[1]) : (n % 2 ? f[2] : f[0]);
       const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
-      v[k] = pack_f16(w.x * fk, w.y * fk);
+      v[k] = pack_f16(w.x * f[k % 2], w.y * f[k % 2]);
     }
-    tmem_st_16x16h(at, v);
+    tmem_st_16x16h(ts + 16 * n, v);
   }
 }
 
@@ -388,32 +379,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t v_desc = smem_desc_rows_k(sbase + S::kV, kBlock);
         uint32_t step = 0, tile = 0;     // of the run: steps so far, tiles so far
         uint32_t n_p0 = 0, n_p1 = 0;     // weights of each half consumed so far
-        // O_X += P_X V of run step sv; S_X = Q_X K^T of run step sj
-        auto issue_o = [&](int X, uint32_t sv, bool first, bool last) {
-          warp_wait(p_full(X), X ? n_p1++ : n_p0++);
+        // O_X += P_X V of run step sv (`with_o`), S_X = Q_X K^T of run step sj (`with_s`)
+        auto issue = [&](int X, uint32_t sv, bool with_o, bool first, bool last, uint32_t sj,
+                         bool with_s) {
+          if (with_o) warp_wait(p_full(X), X ? n_p1++ : n_p0++);
           if (dead) return;
           tc_fence_after();
           if (lane == 0) {
-            const uint64_t v = v_desc + (sv & 1) * (S::kTile >> 4);
+            if (with_o) {
+              const uint64_t v = v_desc + (sv & 1) * (S::kTile >> 4);
 #pragma unroll
-            for (int k = 0; k < kStep / 16; ++k)
-              mma_f16_ts(tmem + kColO + 128 * X, tmem + 128 * X + 8 * k, v + k * (2048 >> 4), kIdescO,
-                         k > 0 ? 1u : first ? 0u : 1u);
-            if (last) mma_commit(o_full(X));
-          }
-          __syncwarp();
-        };
-        auto issue_s = [&](int X, uint32_t sj) {
-          if (dead) return;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t q0 = q_desc + X * (S::kTile >> 4), k0 = k_desc + (sj & 1) * (S::kTile >> 4);
-#pragma unroll
-            for (int k = 0; k < DIM / 16; ++k) {
-              const uint64_t at = ((k / 4) * kBlock + (k % 4) * 32) >> 4;
-              mma_f16(tmem + 128 * X, q0 + at, k0 + at, kIdescS, k > 0 ? 1u : 0u);
+              for (int k = 0; k < kStep / 16; ++k)
+                mma_f16_ts(tmem + kColO + 128 * X, tmem + 128 * X + 8 * k, v + k * (2048 >> 4),
+                           kIdescO, k > 0 ? 1u : first ? 0u : 1u);
+              if (last) mma_commit(o_full(X));
             }
-            mma_commit(s_full(X));
+            if (with_s) {
+              const uint64_t q0 = q_desc + X * (S::kTile >> 4), k0 = k_desc + (sj & 1) * (S::kTile >> 4);
+#pragma unroll
+              for (int k = 0; k < DIM / 16; ++k) {
+                const uint64_t at = ((k / 4) * kBlock + (k % 4) * 32) >> 4;
+                mma_f16(tmem + 128 * X, q0 + at, k0 + at, kIdescS, k > 0 ? 1u : 0u);
+              }
+              mma_commit(s_full(X));
+            }
+            // (half 1 goes last: both halves have then used the step's values, keys)
+            if (X == 1 && sv != ~0u) mma_commit(v_empty(sv & 1));
+            if (X == 1 && sj != ~0u) mma_commit(k_empty(sj & 1));
           }
           __syncwarp();
         };
@@ -422,17 +414,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int count = dead ? 1 : piece[0];
           const int from0 = piece[1], to0 = piece[2], from1 = piece[3], to1 = piece[4];
           for (int j = 0; j <= count; ++j) {
-            const uint32_t sj = step + j, sv = sj - 1;  // run steps of the keys, the values
+            // run steps of the values and the keys (~0: none)
+            const uint32_t sv = j > 0 ? step + j - 1 : ~0u, sj = j < count ? step + j : ~0u;
             if (j > 0) warp_wait(v_full(sv & 1), sv >> 1);
+            if (j < count) warp_wait(k_full(sj & 1), sj >> 1);
 #pragma unroll 1
             for (int X = 0; X < 2; ++X) {
               const int from = X ? from1 : from0, to = X ? to1 : to0;
-              if (j > from && j <= to) issue_o(X, sv, j - 1 == from, j == to);
-              if (X == 1 && lane == 0 && j > 0 && !dead) mma_commit(v_empty(sv & 1));
-              if (X == 0 && j < count) warp_wait(k_full(sj & 1), sj >> 1);
-              if (j >= from && j < to) issue_s(X, sj);
+              issue(X, sv, j > from && j <= to, j - 1 == from, j == to, sj, j >= from && j < to);
             }
-            if (lane == 0 && j < count && !dead) mma_commit(k_empty(sj & 1));
           }
           step += count;
           done += count;
@@ -648,6 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         l[i] = 0.0f;
       }
       float* state = reinterpret_cast<float*>(smem + S::kState) + threadIdx.x;
+      uint32_t* seen = reinterpret_cast<uint32_t*>(state + 4 * 256);
+      bool was_masked = true;  // (and `seen` to be set)
       for (int j = from; j < upto; ++j) {
         const uint32_t slot = (step + j) % kScaleSlots;
         warp_wait(scale_full(slot), (step + j) / kScaleSlots);
@@ -656,77 +648,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int token0 = token_base + j * kStep;
         const bool masked = token0 < all_from || token0 + kStep > all_to;
-        // tokens of the step that row i sees: from the low half, to the high half
-        uint32_t seen[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) seen[i] = (uint32_t)kStep << 16;
+        // tokens of the step that row i sees
         if (masked) {
           const RowTile t = row_tile(p, hide(seq_tile));
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             const int row = min(32 * warp + g + 8 * i, t.rows - 1);
             const int sees = last_seen(p, t, (int)p.by_group((uint32_t)(t.r0 + row)));
             const int lo = max(t.first, first_seen(p, sees)) - token0;
             const int hi = min(t.last, sees) - token0;
-            seen[i] = (uint32_t)min(max(lo, 0), kStep) | (uint32_t)min(max(hi, 0), kStep) << 16;
+            seen[i * 256] =
+                (uint32_t)min(max(lo, 0), kStep) | (uint32_t)min(max(hi, 0), kStep) << 16;
           }
+          was_masked = true;
+        } else if (was_masked) {
+          was_masked = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) seen[i * 256] = (uint32_t)kStep << 16;
         }
-        // (not unrolled: the loops of all roles have to stay in the SM's instruction
-        // cache; unrolled, a kernel of 1.85 ms waited for instructions half its time)
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {  // 32 tokens; P overwrites S that is done with
-          const float* ks = scales + slot * 2 * kStep + 32 * q + 2 * c4;
-          uint32_t sv[2][16], pw[2][8];
-          tmem_ld_16x32(ts + 32 * q, sv[0]);
-          tmem_ld_16x32(ts + (16u << 16) + 32 * q, sv[1]);
-          tmem_ld_wait_for(sv[0]);
-          tmem_ld_wait_for(sv[1]);
-          uint64_t sum[4];
-          __half2 most[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sum[i] = 0;
-            most[i] = __half2half2(__half(0.0f));
-          }
+        // 32 tokens and 16 TMEM lanes (rows i = 2 HALF, + 1) at a time, the next
+        // lot's scores on their way; P overwrites S that is done with.  (Not
+        // unrolled further: the loops of all roles have to stay in the SM's
+        // instruction cache; unrolled, a kernel of 1.85 ms waited for instructions
+        // half its time.)
+        uint32_t sv[2][16];
+        auto weights = [&](auto half_, auto masked_, int q, const float* ks) {
+          constexpr int HALF = decltype(half_)::value;
+          constexpr bool MASKED = decltype(masked_)::value;
+          uint32_t pw[8];
+          uint64_t sum[2] = {0, 0};
+          __half2 most[2];
           bool again = false;
-          auto weights = [&](auto with_mask) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint64_t k2 = *reinterpret_cast<const uint64_t*>(ks + 8 * b);
-              const uint64_t v2 = *reinterpret_cast<const uint64_t*>(ks + kStep + 8 * b);
-              if (with_mask.value) {  // a scale that is not a number may stand in a masked place
-                float a, c;
-                unpair(v2, a, c);
-                again |= !(fabsf(a) < INFINITY) || !(fabsf(c) < INFINITY);
-              }
+          for (int i = 0; i < 2; ++i) most[i] = __half2half2(__half(0.0f));
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float x0, x1;
-                unpair(fma2(pair(__uint_as_float(sv[i / 2][4 * b + i % 2 * 2]),
-                                 __uint_as_float(sv[i / 2][4 * b + i % 2 * 2 + 1])),
-                            k2, pair(-ref[i], -ref[i])),
-                       x0, x1);
-                if (with_mask.value) {
-                  const int n = 32 * q + 8 * b + 2 * c4, lo = seen[i] & 0xffffu, hi = seen[i] >> 16;
-                  if (n < lo || n >= hi) x0 = -INFINITY;
-                  if (n + 1 < lo || n + 1 >= hi) x1 = -INFINITY;
-                }
-                const uint64_t p2 = pair(ex2(x0), ex2(x1));
-                sum[i] = add2(sum[i], p2);
-                unpair(mul2(p2, v2), x0, x1);
-                const __half2 h = __floats2half2_rn(x0, x1);
-                most[i] = __hmax2(most[i], __habs2(h));
-                pw[i / 2][2 * b + i % 2] = *reinterpret_cast<const uint32_t*>(&h);
-              }
+          for (int b = 0; b < 4; ++b) {
+            const uint64_t k2 = *reinterpret_cast<const uint64_t*>(ks + 8 * b);
+            const uint64_t v2 = *reinterpret_cast<const uint64_t*>(ks + kStep + 8 * b);
+            if (MASKED) {  // a scale that is not a number may stand in a masked place
+              float a, c;
+              unpair(v2, a, c);
+              again |= !(fabsf(a) < INFINITY) || !(fabsf(c) < INFINITY);
             }
-          };
-          if (masked) weights(Const<true>{});
-          else weights(Const<false>{});
-          float part[4];
-          again |= !__hble2(__hmax2(__hmax2(most[0], most[1]), __hmax2(most[2], most[3])),
-                            __half2half2(__half(32768.0f)));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
+              const float rf = ref[2 * HALF + i];
+              float x0, x1;
+              unpair(fma2(pair(__uint_as_float(sv[HALF][4 * b + 2 * i]),
+                               __uint_as_float(sv[HALF][4 * b + 2 * i + 1])),
+                          k2, pair(-rf, -rf)),
+                     x0, x1);
+              if (MASKED) {
+                const uint32_t see = seen[(2 * HALF + i) * 256], lo = see & 0xffffu, hi = see >> 16;
+                const uint32_t n = 32 * q + 8 * b + 2 * c4;
+                if (n < lo || n >= hi) x0 = -INFINITY;
+                if (n + 1 < lo || n + 1 >= hi) x1 = -INFINITY;
+              }
+              const uint64_t p2 = pair(ex2(x0), ex2(x1));
+              sum[i] = add2(sum[i], p2);
+              unpair(mul2(p2, v2), x0, x1);
+              const __half2 h = __floats2half2_rn(x0, x1);
+              most[i] = __hmax2(most[i], __habs2(h));
+              pw[2 * b + i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+          again |= !__hble2(__hmax2(most[0], most[1]), __half2half2(__half(32768.0f)));
+          float part[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
             float a, b;
             unpair(sum[i], a, b);
             part[i] = a + b;
@@ -734,24 +723,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (__any_sync(0xffffffffu, again)) {
             // weights out of range, or odd scales beside a mask: once more, with care
+            tmem_ld_wait_for(sv[1 - HALF]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              state[i * 256] = ref[i];
-              state[(4 + i) * 256] = l[i];
+            for (int i = 0; i < 2; ++i) {
+              state[i * 256] = ref[2 * HALF + i];
+              state[(2 + i) * 256] = l[2 * HALF + i];
             }
-            careful_weights<DIM>(ts, to_, ks, q, j > from, seen[0], seen[1], seen[2], seen[3], state);
+            const uint32_t lanes = HALF ? 16u << 16 : 0u;
+            careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from,
+                                 seen + 2 * HALF * 256, state);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              ref[i] = state[i * 256];
-              l[i] = state[(4 + i) * 256];
+            for (int i = 0; i < 2; ++i) {
+              ref[2 * HALF + i] = state[i * 256];
+              l[2 * HALF + i] = state[(2 + i) * 256];
             }
-            continue;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) l[2 * HALF + i] += part[i];
+            tmem_st_16x16h(ts + (HALF ? 16u << 16 : 0u) + 16 * q, pw);
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) l[i] += part[i];
-          tmem_st_16x16h(ts + 16 * q, pw[0]);
-          tmem_st_16x16h(ts + (16u << 16) + 16 * q, pw[1]);
-        }
+        };
+        auto chunks = [&](auto masked_) {
+          const float* ks = scales + slot * 2 * kStep + 2 * c4;
+          tmem_ld_16x32(ts, sv[0]);
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q, ks += 32) {
+            tmem_ld_wait_for(sv[0]);
+            tmem_ld_16x32(ts + (16u << 16) + 32 * q, sv[1]);
+            weights(Const<int, 0>{}, masked_, q, ks);
+            tmem_ld_wait_for(sv[1]);
+            // (the last time round: some scores once more, not used)
+            tmem_ld_16x32(ts + 32 * min(q + 1, 3), sv[0]);
+            weights(Const<int, 1>{}, masked_, q, ks);
+          }
+          tmem_ld_wait_for(sv[0]);
+        };
+        if (masked) chunks(Const<bool, true>{});
+        else chunks(Const<bool, false>{});
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(p_full(x));
