@@ -58,29 +58,6 @@ size_t norm_rope_scratch(const NormRopeParams& p, int sm_count);
 cudaError_t launch_norm_rope_backward(int dtype, const NormRopeParams& p, int sm_count,
                                       float* partial, int* launches, cudaStream_t s);
 
-// ---- the cache ----------------------------------------------------------------------
-struct Kv4Cache {
-  uint8_t* base = nullptr;
-  int64_t pages = 0, page_size = 0;
-  int heads = 0, dim = 0;
-};
-// Byte offsets inside a head's block of a page.
-__host__ __device__ inline int64_t kv4_block_bytes(int64_t dim, int64_t page_size) {
-  return page_size * (dim + 4);
-}
-
-struct Kv4CopyParams {  // write: K, V -> cache; read: cache -> K, V
-  Kv4Cache cache;
-  int64_t tokens = 0;
-  void *k = nullptr, *v = nullptr;
-  int64_t k_stride = 0, v_stride = 0;
-  const int64_t* slots = nullptr;
-  int* status = nullptr;
-};
-cudaError_t launch_kv4_write(int dtype, const Kv4CopyParams& p, int sm_count, cudaStream_t s);
-cudaError_t launch_kv4_read(int dtype, const Kv4CopyParams& p, int sm_count, cudaStream_t s);
-
-// ---- attention ------------------------------------------------------------------------
 // Division of non-negative 32-bit numbers by a number known at launch, as a
 // multiplication: x / d = (x * mul) >> 32 >> shift, exact for x < 2^31.
 struct FastDiv {
@@ -99,6 +76,32 @@ struct FastDiv {
 #endif
 };
 
+// ---- the cache ----------------------------------------------------------------------
+struct Kv4Cache {
+  uint8_t* base = nullptr;
+  int64_t pages = 0, page_size = 0;
+  int heads = 0, dim = 0;
+};
+// Byte offsets inside a head's block of a page.
+__host__ __device__ inline int64_t kv4_block_bytes(int64_t dim, int64_t page_size) {
+  return page_size * (dim + 4);
+}
+
+struct Kv4CopyParams {  // write: K, V -> cache; read: cache -> K, V
+  Kv4Cache cache;
+  int64_t tokens = 0;
+  void *k = nullptr, *v = nullptr;
+  int64_t k_stride = 0, v_stride = 0;
+  const int64_t* slots = nullptr;
+  int* status = nullptr;
+  // how the launch cuts the vectors
+  int per_block = 1;
+  FastDiv by_chunks, by_page;
+};
+cudaError_t launch_kv4_write(int dtype, const Kv4CopyParams& p, cudaStream_t s);
+cudaError_t launch_kv4_read(int dtype, const Kv4CopyParams& p, cudaStream_t s);
+
+// ---- attention ------------------------------------------------------------------------
 // A call's work is a row of steps: for each sequence, each tile of its query
 // rows and each key-value head, the steps of 128 tokens that the tile sees.
 // A row is a (token, head of the group) pair, token-major.  Every CTA takes an

@@ -250,8 +250,8 @@ static lbgemm_status kv4_copy(bool write, int dtype, int64_t tokens, int64_t hea
   p.v_stride = v_stride;
   p.slots = slots;
   p.status = dev.status;
-  cudaError_t e = write ? launch_kv4_write(dtype, p, dev.sm_count, as_stream(stream))
-                        : launch_kv4_read(dtype, p, dev.sm_count, as_stream(stream));
+  cudaError_t e = write ? launch_kv4_write(dtype, p, as_stream(stream))
+                        : launch_kv4_read(dtype, p, as_stream(stream));
   if (e != cudaSuccess) return report_cuda_error(e, write ? "cache write launch" : "cache read launch");
   count_launches(1);
   return LBGEMM_OK;
