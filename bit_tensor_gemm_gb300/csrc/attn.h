@@ -54,7 +54,7 @@ struct NormRopeParams {
 };
 cudaError_t launch_norm_rope(int dtype, const NormRopeParams& p, int sm_count, cudaStream_t s);
 // partial: scratch of norm_rope_scratch() bytes (unused when no weight is given).
-size_t norm_rope_scratch(const NormRopeParams& p, int sm_count);
+size_t norm_rope_scratch(int dtype, const NormRopeParams& p, int sm_count);
 cudaError_t launch_norm_rope_backward(int dtype, const NormRopeParams& p, int sm_count,
                                       float* partial, int* launches, cudaStream_t s);
 

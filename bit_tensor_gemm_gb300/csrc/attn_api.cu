@@ -194,7 +194,7 @@ lbgemm_status lbgemm_qk_norm_rope_backward(
     p.status = dev.status;
     cudaStream_t s = as_stream(stream);
     int launches = 0;
-    const size_t bytes = norm_rope_scratch(p, dev.sm_count);
+    const size_t bytes = norm_rope_scratch(dtype, p, dev.sm_count);
     cudaError_t e;
     if (bytes == 0) {
       e = launch_norm_rope_backward(dtype, p, dev.sm_count, nullptr, &launches, s);

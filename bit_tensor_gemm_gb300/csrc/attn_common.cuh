@@ -74,7 +74,41 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
   if constexpr (sizeof(T) == 4) reinterpret_cast<uint4*>(p)[1] = r.v[1];
 }
 
+// Four consecutive elements: 8 bytes (16-bit types) or 16 (fp32).
+template <typename T>
+struct Raw4 {
+  uint2 v[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float (&f)[4]) {
+  Raw4<T> r;
+  if constexpr (sizeof(T) == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r.v[0] = make_uint2(v.x, v.y);
+    r.v[1] = make_uint2(v.z, v.w);
+  } else {
+    r.v[0] = *reinterpret_cast<const uint2*>(p);
+  }
+  const T* h = reinterpret_cast<const T*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = to_f32(h[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float (&f)[4]) {
+  Raw4<T> r;
+  T* h = reinterpret_cast<T*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = from_f32<T>(f[i]);
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<uint4*>(p) = make_uint4(r.v[0].x, r.v[0].y, r.v[1].x, r.v[1].y);
+  else
+    *reinterpret_cast<uint2*>(p) = r.v[0];
+}
+
 // ---- two fp32 numbers in one operation ------------------------------------------
+using float2x = uint64_t;
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
