@@ -348,9 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 12) {
       // ---------------- the MMAs ----------------
       // The whole warp walks, lane 0 issues: what it passes stays warp-uniform and
-      // the descriptors of a step are sums of few registers and constants.  (One
-      // thread that computed each descriptor took 2900 cycles to issue the eight
-      // MMAs of O += P V, against 512 to run them.)
+      // the descriptors of a step are sums of few registers and constants.
       if (run.count > 0) {
         const uint64_t q_desc = smem_desc_sw128(sbase + S::kQ), k_desc = smem_desc_sw128(sbase + S::kK);
         const uint64_t v_desc = smem_desc_rows_k(sbase + S::kV, kBlock);
@@ -644,18 +642,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) seen[i * 256] = (uint32_t)kStep << 16;
         }
-        // 32 tokens and 16 TMEM lanes (rows i = 2 HALF, + 1) at a time, the next
-        // lot's scores on their way; P overwrites S that is done with.  (Not
-        // unrolled further: the loops of all roles have to stay in the SM's
-        // instruction cache; unrolled, a kernel of 1.85 ms waited for instructions
-        // half its time.)
-        uint32_t sv[2][16];
-        auto weights = [&](auto half_, auto masked_, int q, const float* ks) {
-          constexpr int HALF = decltype(half_)::value;
+        // 32 tokens and the thread's four rows (rows 2 h, 2 h + 1 in sv[h]) at a time; P
+        // overwrites S that is done with.  (Not unrolled further: the loops of all
+        // roles have to stay in the SM's instruction cache; unrolled, a kernel of
+        // 1.85 ms waited for instructions half its time.  The next lot's scores
+        // loaded ahead gained nothing: the other half's warps fill that time.)
+        auto weights = [&](auto masked_, int q, const float* ks) {
           constexpr bool MASKED = decltype(masked_)::value;
-          uint32_t pw[8];
-          uint64_t sum[2] = {0, 0};
-          uint32_t most[2] = {0, 0};
+          uint32_t sv[2][16], pw[2][8];
+          tmem_ld_16x32(ts + 32 * q, sv[0]);
+          tmem_ld_16x32(ts + (16u << 16) + 32 * q, sv[1]);
+          tmem_ld_wait_for(sv[0]);
+          tmem_ld_wait_for(sv[1]);
+          uint64_t sum[4] = {0, 0, 0, 0};
+          __half2 most = __half2half2(__half(0.0f));
           bool again = false;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
@@ -667,15 +667,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               again |= !(fabsf(a) < INFINITY) || !(fabsf(c) < INFINITY);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float rf = ref[2 * HALF + i];
+            for (int i = 0; i < 4; ++i) {
               float x0, x1;
-              unpair(fma2(pair(__uint_as_float(sv[HALF][4 * b + 2 * i]),
-                               __uint_as_float(sv[HALF][4 * b + 2 * i + 1])),
-                          k2, pair(-rf, -rf)),
+              unpair(fma2(pair(__uint_as_float(sv[i / 2][4 * b + i % 2 * 2]),
+                               __uint_as_float(sv[i / 2][4 * b + i % 2 * 2 + 1])),
+                          k2, pair(-ref[i], -ref[i])),
                      x0, x1);
               if (MASKED) {
-                const uint32_t see = seen[(2 * HALF + i) * 256], lo = see & 0xffffu, hi = see >> 16;
+                const uint32_t see = seen[i * 256], lo = see & 0xffffu, hi = see >> 16;
                 const uint32_t n = 32 * q + 8 * b + 2 * c4;
                 if (n < lo || n >= hi) x0 = -INFINITY;
                 if (n + 1 < lo || n + 1 >= hi) x1 = -INFINITY;
@@ -684,57 +683,48 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum[i] = add2(sum[i], p2);
               unpair(mul2(p2, v2), x0, x1);
               const uint32_t h = pack_f16(x0, x1);
-              // (halves that are not negative order as whole numbers; one that is, or
-              // is no number, counts as out of range)
-              most[i] = __vmaxu2(most[i], h);
-              pw[2 * b + i] = h;
+              most = __hmax2_nan(most, __habs2(*reinterpret_cast<const __half2*>(&h)));
+              pw[i / 2][2 * b + i % 2] = h;
             }
           }
-          again |= __vcmpgtu2(__vmaxu2(most[0], most[1]), 0x78007800u) != 0;  // above 2^15
-          float part[2];
+          again |= !__hble2(most, __half2half2(__half(32768.0f)));  // (or no number)
+          float part[4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < 4; ++i) {
             float a, b;
             unpair(sum[i], a, b);
             part[i] = a + b;
-            again |= part[i] > kFar;
           }
+          again |= fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) > kFar;
           if (__any_sync(0xffffffffu, again)) {
             // weights out of range, or odd scales beside a mask: once more, with care
-            tmem_ld_wait_for(sv[1 - HALF]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              state[i * 256] = ref[2 * HALF + i];
-              state[(2 + i) * 256] = l[2 * HALF + i];
-            }
-            const uint32_t lanes = HALF ? 16u << 16 : 0u;
-            careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from,
-                                 seen + 2 * HALF * 256, state);
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              ref[2 * HALF + i] = state[i * 256];
-              l[2 * HALF + i] = state[(2 + i) * 256];
+              for (int i = 0; i < 2; ++i) {
+                state[i * 256] = ref[2 * h + i];
+                state[(2 + i) * 256] = l[2 * h + i];
+              }
+              const uint32_t lanes = h ? 16u << 16 : 0u;
+              careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from, seen + 2 * h * 256,
+                                   state);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                ref[2 * h + i] = state[i * 256];
+                l[2 * h + i] = state[(2 + i) * 256];
+              }
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) l[2 * HALF + i] += part[i];
-            tmem_st_16x16h(ts + (HALF ? 16u << 16 : 0u) + 16 * q, pw);
+            for (int i = 0; i < 4; ++i) l[i] += part[i];
+            tmem_st_16x16h(ts + 16 * q, pw[0]);
+            tmem_st_16x16h(ts + (16u << 16) + 16 * q, pw[1]);
           }
         };
         auto chunks = [&](auto masked_) {
           const float* ks = scales + slot * 2 * kStep + 2 * c4;
-          tmem_ld_16x32(ts, sv[0]);
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q, ks += 32) {
-            tmem_ld_wait_for(sv[0]);
-            tmem_ld_16x32(ts + (16u << 16) + 32 * q, sv[1]);
-            weights(Const<int, 0>{}, masked_, q, ks);
-            tmem_ld_wait_for(sv[1]);
-            // (the last time round: some scores once more, not used)
-            tmem_ld_16x32(ts + 32 * min(q + 1, 3), sv[0]);
-            weights(Const<int, 1>{}, masked_, q, ks);
-          }
-          tmem_ld_wait_for(sv[0]);
+          for (int q = 0; q < 4; ++q, ks += 32) weights(masked_, q, ks);
         };
         if (masked) chunks(Const<bool, true>{});
         else chunks(Const<bool, false>{});
