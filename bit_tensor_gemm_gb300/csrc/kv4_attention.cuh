@@ -49,8 +49,13 @@ __device__ __forceinline__ RowTile row_tile(const Kv4AttnParams& p, int seq_tile
 }
 
 // This CTA's run of steps: it begins `off` steps into head `head` of sequence
-// tile `seq_tile`; `count` steps (0: none), the first of them being step `pos`
-// of the whole row, which is cut into runs of `per`.
+// tile `seq_tile` and has `count` steps (0: none).
+//
+// A tile costs time beside its steps (its queries, its results), which is
+// counted as `tile_cost` steps in front of its own: the row of steps with
+// these in it is cut into runs of `per`.  `pos` is the place in that row of the
+// run's first step, so that step s of the run, in its n-th tile (from 0), stands
+// at pos + s + n tile_cost.
 struct Run {
   int seq_tile, head, off, count;
   int64_t pos, per;
@@ -59,14 +64,15 @@ struct Run {
 // Threads take equal segments of the sequence tiles, sum their steps, and the
 // one whose segment holds the run's begin looks it up.  THREADS: of the block.
 template <int THREADS>
-__device__ __forceinline__ Run find_run(const Kv4AttnParams& p, int min_steps) {
+__device__ __forceinline__ Run find_run(const Kv4AttnParams& p, int min_steps, int tile_cost) {
   __shared__ int64_t warp_sum[THREADS / 32];
   __shared__ Run run;
   const int tiles = p.batch * p.row_tiles, seg = (tiles + THREADS - 1) / THREADS;
   const int from = min(tiles, (int)threadIdx.x * seg), to = min(tiles, from + seg);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  auto places = [&](int steps) { return steps > 0 ? steps + tile_cost : 0; };
   int64_t mine = 0;
-  for (int i = from; i < to; ++i) mine += row_tile(p, i).steps;
+  for (int i = from; i < to; ++i) mine += places(row_tile(p, i).steps);
   int64_t upto = mine;  // inclusive over the warp, then the block
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -84,25 +90,46 @@ __device__ __forceinline__ Run find_run(const Kv4AttnParams& p, int min_steps) {
   const int64_t heads = p.cache.heads;
   total *= heads;
   const int64_t per = max((int64_t)min_steps, (total + gridDim.x - 1) / (int64_t)gridDim.x);
-  const int64_t pos = per * blockIdx.x;
-  if (pos >= total) {
-    Run none = {0, 0, 0, 0, pos, per};
+  const int64_t begin = per * blockIdx.x;
+  if (begin >= total) {
+    Run none = {0, 0, 0, 0, begin, per};
     return none;
   }
-  int64_t at = (before + upto - mine) * heads;  // steps before this thread's segment
-  if (pos >= at && pos < at + mine * heads) {
-    int i = from, n = 0;
+  int64_t at = (before + upto - mine) * heads;  // places before this thread's segment
+  if (begin >= at && begin < at + mine * heads) {
+    int i = from, n = 0, wide = 0;
     for (; i < to; ++i) {
       n = row_tile(p, i).steps;
-      if (pos < at + n * heads) break;
-      at += n * heads;
+      wide = places(n);
+      if (begin < at + wide * heads) break;
+      at += wide * heads;
     }
     run.seq_tile = i;
-    run.head = (int)((pos - at) / n);
-    run.off = (int)(pos - at - (int64_t)run.head * n);
-    run.count = (int)min(per, total - pos);
-    run.pos = pos;
+    run.head = (int)((begin - at) / wide);
+    at += (int64_t)run.head * wide;
+    run.off = max(0, (int)(begin - at) - tile_cost);
+    run.pos = at + tile_cost + run.off;
     run.per = per;
+    // its steps: what is left of this tile, then whole heads and tiles, then a part
+    const int64_t end = min(begin + per, total);
+    int64_t count = max((int64_t)0, min((int64_t)(n - run.off), end - run.pos));
+    at += wide;
+    for (int64_t left = heads - run.head - 1; at < end;) {
+      if (wide > 0) {
+        const int64_t whole = min(left, (end - at) / wide);
+        count += whole * n;
+        at += whole * wide;
+        if (whole < left) {
+          count += max((int64_t)0, end - at - tile_cost);
+          break;
+        }
+      }
+      if (++i == tiles) break;
+      n = row_tile(p, i).steps;
+      wide = places(n);
+      left = heads;
+    }
+    run.count = (int)count;
   }
   __syncthreads();
   return run;

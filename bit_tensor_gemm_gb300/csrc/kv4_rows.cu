@@ -40,7 +40,8 @@ namespace lbg {
 namespace {
 
 constexpr int kWarps = 4, kStages = 3, kTokens = 32, kStep = kStepTokens;
-constexpr int kMinSteps = 2;  // of a CTA's run
+constexpr int kMinSteps = 3;  // of a CTA's run
+constexpr int kTileCost = 2;  // in steps (see find_run)
 static_assert(kWarps * kTokens == kStep, "a warp's share of a step");
 template <int DIM>
 struct Ring {
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
   fence_barrier_init();
   // the kernel that joins shares may be scheduled once every CTA has begun
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Run run = find_run<kWarps * 32>(p, kMinSteps);  // (with a barrier of the block)
+  const Run run = find_run<kWarps * 32>(p, kMinSteps, kTileCost);  // (with a barrier of the block)
   if (p.joins > 0 && !p.by_tile && threadIdx.x == 0) p.join[blockIdx.x].last_cta = -1;
   if (run.count == 0) return;
 
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
       (uint32_t)(Rg::kCodes + warp * kTokens * (DIM / 2));
 
   bool dead = false;  // a wait ran out: no more waits and sums, but every barrier
-  int seq_tile = run.seq_tile, head = run.head, off = run.off, done = 0;
+  int seq_tile = run.seq_tile, head = run.head, off = run.off, done = 0, tile = 0;
   RowTile t = row_tile(p, seq_tile);
   while (true) {
     const int piece_steps = min(t.steps - off, run.count - done);
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     const bool whole = piece_steps == t.steps;
     const int64_t share = ((int64_t)blockIdx.x * 2 + (off == 0)) * p.tile_rows;
     if (p.joins > 0 && off == 0 && (!whole || p.by_tile) && threadIdx.x == 0) {
-      const int64_t last = (run.pos + done + t.steps - 1) / run.per;  // the CTA of its last step
+      const int64_t last = (run.pos + done + tile * kTileCost + t.steps - 1) / run.per;  // the CTA of its last step
       p.join[p.by_tile ? seq_tile * p.cache.heads + head : (int)blockIdx.x] =
           Kv4Join{seq_tile, head, (int)blockIdx.x, whole ? -1 : (int)last};
     }
@@ -553,6 +554,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     }
     done += piece_steps;
     if (done == run.count) break;
+    ++tile;
     __syncthreads();  // the merge buffers are free again
     off = 0;
     if (++head == p.cache.heads) {

@@ -43,6 +43,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kStep = kStepTokens;
 constexpr int kMinSteps = 4;
+constexpr int kTileCost = 3;  // in steps (see find_run)
 constexpr int kScaleSlots = 4;
 
 template <int DIM>
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
-  const Run run = find_run<kThreads>(p, kMinSteps);  // (with a barrier of the block)
+  const Run run = find_run<kThreads>(p, kMinSteps, kTileCost);  // (with a barrier of the block)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int seq_tile = run.seq_tile, head = run.head, off = run.off;
     uint32_t step = 0, n_s = 0, n_o = 0;
-    for (int done = 0; done < run.count;) {
+    for (int done = 0, tile = 0; done < run.count; ++tile) {
       int count, from, upto, all_from, all_to, token_base;
       {
       const RowTile t = row_tile(p, hide(seq_tile));
@@ -547,11 +548,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         const T* src = static_cast<const T*>(p.q) + (int64_t)(t.q0 + qi) * p.q_stride +
                        (int64_t)(head * p.group + t.r0 + min(r, t.rows - 1) - qi * p.group) * DIM;
+        // (kept for the second use as far as registers go: the L1 beside this much
+        // shared memory keeps little)
+        constexpr int KEEP = 8;
+        Raw8<T> raw[KEEP];
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) raw[i] = load8_raw(src + 8 * i);
         float most = 0.0f;
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < DIM / 8; ++i) {
           float v[8];
-          load8(src + 8 * i, v);
+          unpack8(i < KEEP ? raw[i % KEEP] : load8_raw(src + 8 * i), v);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             if (fabsf(v[k]) < INFINITY) most = fmaxf(most, fabsf(v[k]));
@@ -577,10 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           *factor_slot = __uint_as_float((uint32_t)(127 + 24 - k2) << 23) * (p.scale * kLog2e);
         }
         const uint32_t dst = sbase + S::kQ + x * S::kTile;
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < DIM / 8; ++i) {
           float v[8];
-          load8(src + 8 * i, v);
+          unpack8(i < KEEP ? raw[i % KEEP] : load8_raw(src + 8 * i), v);
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = live ? v[k] * (k & 1 ? up16 : up) : 0.0f;
           st_shared_v4(dst + (i / 8) * kBlock + swizzled(r % 128, i % 8), (int)pack_f16(v[0], v[4]),
@@ -757,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       if (p.joins > 0 && off == 0 && (!whole || p.by_tile) && threadIdx.x == 0) {
-        const int64_t last = (run.pos + done + t.steps - 1) / run.per;  // the CTA of its last step
+        const int64_t last = (run.pos + done + tile * kTileCost + t.steps - 1) / run.per;  // the CTA of its last step
         p.join[p.by_tile ? seq_tile * p.cache.heads + head : (int)blockIdx.x] =
             Kv4Join{seq_tile, head, (int)blockIdx.x, whole ? -1 : (int)last};
       }
