@@ -33,13 +33,17 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnPar
   constexpr int LANES = DIM / 4, TEAMS = kJoinThreads / LANES, PER_ROW = MANY_ROWS ? 1 : TEAMS;
   const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
   const int row = MANY_ROWS ? blockIdx.y * TEAMS + team : blockIdx.y;
+  // (what comes from the call's inputs is looked up before the shares are there;
+  // by tile, one without rows has no record)
+  RowTile t = {};
+  if (p.by_tile) {
+    t = row_tile(p, blockIdx.x / p.cache.heads);
+    if ((MANY_ROWS ? blockIdx.y * TEAMS : row) >= t.rows) return;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (by tile, one without rows has no record: the tile is looked at first)
-  const int first_row = MANY_ROWS ? blockIdx.y * TEAMS : row;
-  if (p.by_tile && first_row >= row_tile(p, blockIdx.x / p.cache.heads).rows) return;
   const Kv4Join j = p.join[blockIdx.x];
   if (j.last_cta < 0) return;
-  const RowTile t = row_tile(p, j.seq_tile);
+  if (!p.by_tile) t = row_tile(p, j.seq_tile);
   const bool live = row < t.rows;
   // share 0 of the tile is its first CTA's share 1, the others' share 0 follow
   const int shares = live ? j.last_cta - j.first_cta + 1 : 0;

@@ -39,7 +39,7 @@
 namespace lbg {
 namespace {
 
-constexpr int kWarps = 4, kStages = 3, kTokens = 32, kStep = kStepTokens;
+constexpr int kWarps = 4, kStages = 4, kTokens = 32, kStep = kStepTokens;
 constexpr int kMinSteps = 3;  // of a CTA's run
 constexpr int kTileCost = 2;  // in steps (see find_run)
 static_assert(kWarps * kTokens == kStep, "a warp's share of a step");
@@ -97,7 +97,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 //           side: four codes each.  MMA tile 2 q + j, row g is channel 32 q +
 //           4 g + 2 j, row g + 8 the one after it.
 template <typename T, int DIM, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     kv4_rows_kernel(const Kv4AttnParams p) {
   constexpr int KW = DIM / 32;   // 32-bit words of a key that a lane holds
   constexpr int MT = DIM / 16;   // MMA tiles of channels
@@ -179,9 +179,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
   if (warp < kStages) {
     if (is_step < run.count) issue();
     // the first step that this warp issues in the loop
-    advance(warp == 0 ? kWarps + 2 : 2);
-  } else {
-    advance(2);
+    advance(kWarps);
   }
 
   const int eg = (g ^ (g >> 1)) & 1;        // e(g)
@@ -287,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
 
     for (int s = done; s < done + piece_steps; ++s) {
       const uint32_t slot = (uint32_t)(s % kStages);
-      if (s + 2 == is_step && !dead) {
+      if (s > 0 && s + 3 == is_step && !dead) {
         const int old = s - 1;  // the step whose slot this is
         if (is_step < run.count) {
           dead = !mbar_wait(empty + 8 * (old % kStages), (uint32_t)(old / kStages) & 1u, &abort_flag,
@@ -597,7 +595,7 @@ cudaError_t launch_typed(const Kv4AttnParams& p, cudaStream_t s) {
 
 }  // namespace
 
-int kv4_rows_per_sm(int tile_rows) { return tile_rows == 8 ? 4 : 3; }
+int kv4_rows_per_sm(int tile_rows) { return tile_rows == 8 ? 3 : 2; }
 
 cudaError_t launch_kv4_rows(int dtype, const Kv4AttnParams& p, cudaStream_t s) {
   return dtype == LBGEMM_BF16 ? launch_typed<__nv_bfloat16>(p, s) : launch_typed<__half>(p, s);
