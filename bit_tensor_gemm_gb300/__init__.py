@@ -2,6 +2,7 @@
 
 The compute path is the CUDA library ``lib/liblbgemm.so`` (C ABI in
 ``include/lbgemm.h``), built in-tree by ``build.build()``; ``lbgemm`` is its
-Python binding and ``synth`` draws seeded synthetic operands.
+Python binding, ``synth`` draws seeded synthetic operands and
+``attention_layer`` runs the attention operators between two linear layers.
 """
-__all__ = ["build", "lbgemm", "synth"]
+__all__ = ["attention_layer", "build", "lbgemm", "synth"]
