@@ -182,14 +182,14 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4CopyParams 
 #pragma unroll
       for (int k = 0; k < 2; ++k) {  // codes 0, 4 and 1, 5; then 2, 6 and 3, 7
         const uint32_t w = k ? word[u] >> 8 : word[u];
-        const uint32_t lo = codes0<false>(w), hi = codes0<true>(w);
+        const uint32_t lo = codes_f16<false>(w), hi = codes_f16<true>(w);
         const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
         const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
         // (the codes' unit first: exact, whatever the scale)
-        x[2 * k] = a.x * 16777216.0f * scale[u];
-        x[2 * k + 4] = a.y * 16777216.0f * scale[u];
-        x[2 * k + 1] = b.x * 1048576.0f * scale[u];
-        x[2 * k + 5] = b.y * 1048576.0f * scale[u];
+        x[2 * k] = a.x * (1.0f / kCodeUnit) * scale[u];
+        x[2 * k + 4] = a.y * (1.0f / kCodeUnit) * scale[u];
+        x[2 * k + 1] = b.x * (1.0f / kCodeUnit) * scale[u];
+        x[2 * k + 5] = b.y * (1.0f / kCodeUnit) * scale[u];
       }
       store8(dst + u * DIM, x);
     }

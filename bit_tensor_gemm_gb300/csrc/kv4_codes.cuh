@@ -13,24 +13,26 @@ constexpr float kFar = 1.2676506e30f;       // 2^100
 constexpr int kLevel = 11;  // the largest product is put at 2^11
 constexpr float kLeastTop = 8.2718061e-25f;  // 2^-80
 
-// Codes 0 and 4 of a word (HIGH: 1 and 5) as two subnormal halves: (code + 8)
-// 2^-24, or 16 times that.  Codes 2, 6 and 3, 7 are those of the word >> 8.
-// One three-input operation, (w & mask) ^ eight: left to the compiler it became
-// two (45.1 -> XX us over 131072 tokens).
+// Codes 0 and 4 of a word (HIGH: 1 and 5) as two halves in units of kCodeUnit;
+// codes 2, 6 and 3, 7 are those of the word >> 8.  One three-input logical
+// operation, (w & mask) ^ eight, makes subnormals (code + 8) 2^-24, or 16 times
+// that (left to the compiler it became two: 45.1 -> 37.8 us over 131072 tokens);
+// a multiply-add brings them to normal numbers and takes the 8 out, exactly.
+// MMAs would take the subnormals exactly too, but line products up by their
+// operands' exponents before they drop digits: a subnormal's leading zeros then
+// cost up to 8 digits of a score (log-sums off by 6.7e-7 of themselves).
+constexpr float kCodeUnit = 1.0f / 512.0f;
 template <bool HIGH>
-__device__ __forceinline__ uint32_t codes8(uint32_t w) {
-  uint32_t d;
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w) {
+  uint32_t c;
   asm("lop3.b32 %0, %1, %2, %3, 0x6A;"
-      : "=r"(d)
+      : "=r"(c)
       : "r"(w), "r"(HIGH ? 0x00F000F0u : 0x000F000Fu), "r"(HIGH ? 0x00800080u : 0x00080008u));
-  return d;
-}
-// The same without the 8: code 2^-24, or 16 times that (exact).
-template <bool HIGH>
-__device__ __forceinline__ uint32_t codes0(uint32_t w) {
-  const uint32_t c = codes8<HIGH>(w), eight = HIGH ? 0x00800080u : 0x00080008u;
-  const __half2 v =
-      __hsub2(*reinterpret_cast<const __half2*>(&c), *reinterpret_cast<const __half2*>(&eight));
+  const uint32_t up = HIGH ? 0x68006800u : 0x78007800u;  // 2^11, 2^15
+  const uint32_t eight = 0xA400A400u;                    // -8 kCodeUnit
+  const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&c),
+                            *reinterpret_cast<const __half2*>(&up),
+                            *reinterpret_cast<const __half2*>(&eight));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 

@@ -199,7 +199,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     const int end = t.last;
     // ---- queries: B fragments, column g of tile nt is row t.r0 + 8 nt + g
     uint32_t q[NT][MT][2];
-    float bias[NT][2];   // -8 sum(q) of columns 2c, 2c + 1, in the accumulators' unit
     int seen_to[NT][2];  // one past the last token that columns 2c, 2c + 1 see
     // The tile's power of two: its largest element goes to 2^14 .. 2^15, so that
     // in fp16 every element keeps its digits down to 2^-28 of that, and scores
@@ -232,29 +231,23 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     int k = 0;
     if (most > 0.0f) k = min(max(14 - ((int)(__float_as_uint(most) >> 23) - 127), -103), 126);
     const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-    // the accumulators' unit, 2^(24 - k), times scale log2(e)
-    const float factor = __uint_as_float((uint32_t)(127 + 24 - k) << 23) * (p.scale * kLog2e);
+    // the accumulators' unit times scale log2(e)
+    const float factor =
+        __uint_as_float((uint32_t)(127 - k) << 23) * (p.scale * kLog2e / kCodeUnit);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const T* x = reinterpret_cast<const T*>(raw[nt]);
-      float sum = 0.0f;
       // channels (d, d + 4) of a word of codes make a register; those of odd
       // codes, whose halves are 16 times larger, are divided by 16
 #pragma unroll
       for (int w = 0; w < KW; ++w)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float f = i % 2 ? up * 0.0625f : up;
-          const __half2 h = __floats2half2_rn(to_f32(x[8 * w + i]) * f, to_f32(x[8 * w + i + 4]) * f);
+          const __half2 h = __floats2half2_rn(to_f32(x[8 * w + i]) * up, to_f32(x[8 * w + i + 4]) * up);
           q[nt][2 * w + i / 2][i % 2] = *reinterpret_cast<const uint32_t*>(&h);
-          const float2 v = __half22float2(h);
-          sum += (v.x + v.y) * (i % 2 ? 16.0f : 1.0f);
         }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        bias[nt][e] = __shfl_sync(0xffffffffu, sum, 4 * (2 * c + e)) * (-8.0f / 16777216.0f);
         seen_to[nt][e] = last_seen(p, t, (int)p.by_group((uint32_t)(t.r0 + 8 * nt + 2 * c + e)));
       }
     }
@@ -319,13 +312,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // codes 0, 1 (with 4, 5), then 2, 3 (with 6, 7)
               const uint32_t wa = i ? ka[w] >> 8 : ka[w], wb = i ? kb[w] >> 8 : kb[w];
-              const uint32_t a0 = codes8<false>(wa), a1 = codes8<false>(wb);
-              const uint32_t a2 = codes8<true>(wa), a3 = codes8<true>(wb);
+              const uint32_t a0 = codes_f16<false>(wa), a1 = codes_f16<false>(wb);
+              const uint32_t a2 = codes_f16<true>(wa), a3 = codes_f16<true>(wb);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 if (w == 0 && i == 0)
-                  mma16816_from(acc[mt][nt], bias[nt][0], bias[nt][1], a0, a1, a2, a3, q[nt][0][0],
-                                q[nt][0][1]);
+                  mma16816_from(acc[mt][nt], 0.0f, 0.0f, a0, a1, a2, a3, q[nt][0][0], q[nt][0][1]);
                 else
                   mma16816(acc[mt][nt], a0, a1, a2, a3, q[nt][2 * w + i][0], q[nt][2 * w + i][1]);
               }
@@ -460,8 +452,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
             for (int i = 0; i < 4; ++i) {  // MMA tile 4 u + i: codes 0, 1, then 2, 3 of a chunk
               const uint32_t x = i & 1 ? v[i & 2] >> 8 : v[i & 2];
               const uint32_t y = i & 1 ? v[(i & 2) + 1] >> 8 : v[(i & 2) + 1];
-              const uint32_t a0 = codes0<false>(x), a1 = codes0<true>(x);
-              const uint32_t a2 = codes0<false>(y), a3 = codes0<true>(y);
+              const uint32_t a0 = codes_f16<false>(x), a1 = codes_f16<true>(x);
+              const uint32_t a2 = codes_f16<false>(y), a3 = codes_f16<true>(y);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma16816(o[4 * u + i][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
@@ -501,11 +493,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
           for (int i = 1; i < kWarps; ++i) all = fmaxf(all, merge_ref[i][r]);
           // the halves' unit: 2^-24, and 2^-20 for odd channels
-          const float f = ex2(ref[nt][e] - all) * 16777216.0f;
+          const float f = ex2(ref[nt][e] - all) * (1.0f / kCodeUnit);
           float2* dst = reinterpret_cast<float2*>(mo + r * ROW + 2 * g);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            float2 v = make_float2(o[i][nt][e] * f, o[i][nt][2 + e] * (f * 0.0625f));
+            float2 v = make_float2(o[i][nt][e] * f, o[i][nt][2 + e] * f);
             if (w > 0) {
               v.x += dst[8 * i].x;
               v.y += dst[8 * i].y;

@@ -508,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) {
               const uint32_t w8 = w[k] >> 8;
               const int at = chunk * 4 + k;
-              st_shared_v4(dst + (at / 8) * kBlock + swizzled(r, at % 8), (int)codes0<false>(w[k]),
-                           (int)codes0<true>(w[k]), (int)codes0<false>(w8), (int)codes0<true>(w8));
+              st_shared_v4(dst + (at / 8) * kBlock + swizzled(r, at % 8), (int)codes_f16<false>(w[k]),
+                           (int)codes_f16<true>(w[k]), (int)codes_f16<false>(w8), (int)codes_f16<true>(w8));
             }
           }
           fence_proxy_async_smem();
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 8; ++i) most = fmaxf(most, most_slots[i]);
         int k2 = 0;
         if (most > 0.0f) k2 = min(max(14 - ((int)(__float_as_uint(most) >> 23) - 127), -103), 126);
-        const float up = __uint_as_float((uint32_t)(127 + k2) << 23), up16 = up * 0.0625f;
+        const float up = __uint_as_float((uint32_t)(127 + k2) << 23);
         if (r == 0) {
           const HalfTile h1 = half_tile(p, t, 1);  // (this thread's is half 0)
           piece[0] = count;
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           piece[2] = min(max(h.to - off, piece[1]), count);
           piece[3] = min(max(h1.from - off, 0), count);
           piece[4] = min(max(h1.to - off, piece[3]), count);
-          *factor_slot = __uint_as_float((uint32_t)(127 + 24 - k2) << 23) * (p.scale * kLog2e);
+          *factor_slot = __uint_as_float((uint32_t)(127 - k2) << 23) * (p.scale * kLog2e / kCodeUnit);
         }
         const uint32_t dst = sbase + S::kQ + x * S::kTile;
 #pragma unroll
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[8];
           unpack8(i < KEEP ? raw[i % KEEP] : load8_raw(src + 8 * i), v);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = live ? v[k] * (k & 1 ? up16 : up) : 0.0f;
+          for (int k = 0; k < 8; ++k) v[k] = live ? v[k] * up : 0.0f;
           st_shared_v4(dst + (i / 8) * kBlock + swizzled(r % 128, i % 8), (int)pack_f16(v[0], v[4]),
                        (int)pack_f16(v[1], v[5]), (int)pack_f16(v[2], v[6]),
                        (int)pack_f16(v[3], v[7]));
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 8; ++k) {
               const int d = k / 2 + (k & 1) * 4;
               ch[d] = none ? 0.0f
-                           : __uint_as_float(v[8 * i + k]) * ((d & 1 ? 1048576.0f : 16777216.0f) * inv);
+                           : __uint_as_float(v[8 * i + k]) * ((1.0f / kCodeUnit) * inv);
             }
             if (!live) continue;
             if (whole) store8(static_cast<T*>(p.o) + at * DIM + 32 * q + 8 * i, ch);
