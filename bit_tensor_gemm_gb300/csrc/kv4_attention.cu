@@ -50,6 +50,20 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnPar
   auto index = [&](int c) -> int64_t {
     return (int64_t)((j.first_cta + c) * 2 + (c == 0)) * p.tile_rows + row;
   };
+  // the first shares, on their way while the largest lse is found
+  constexpr int AHEAD = 2;
+  float4 v_ahead[AHEAD];
+  float lse_ahead[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    const int c = (MANY_ROWS ? 0 : team) + k * PER_ROW;
+    v_ahead[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    lse_ahead[k] = -INFINITY;
+    if (c < shares) {
+      v_ahead[k] = reinterpret_cast<const float4*>(p.share_o + index(c) * DIM)[lane];
+      lse_ahead[k] = p.share_lse[index(c)];
+    }
+  }
   // the largest lse, and whether one is a NaN
   float top = -INFINITY;
   int nan = 0;
@@ -66,18 +80,20 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnPar
   const float ref = top == -INFINITY ? 0.0f : top;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float sum = 0.0f;
-#pragma unroll 4
-  for (int c = MANY_ROWS ? 0 : team; c < shares; c += PER_ROW) {
-    const int64_t at = index(c);
-    const float w = ex2(p.share_lse[at] - ref);
-    const float4 v = reinterpret_cast<const float4*>(p.share_o + at * DIM)[lane];
-    // (a share that the row sees nothing of has o = 0 and weight 0)
+  // (a share that the row sees nothing of has o = 0 and weight 0)
+  auto add = [&](float share_lse, const float4& v) {
+    const float w = ex2(share_lse - ref);
     sum += w;
     acc.x += w * v.x;
     acc.y += w * v.y;
     acc.z += w * v.z;
     acc.w += w * v.w;
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) add(lse_ahead[k], v_ahead[k]);
+#pragma unroll 4
+  for (int c = (MANY_ROWS ? 0 : team) + AHEAD * PER_ROW; c < shares; c += PER_ROW)
+    add(p.share_lse[index(c)], reinterpret_cast<const float4*>(p.share_o + index(c) * DIM)[lane]);
   if constexpr (!MANY_ROWS) {
     __shared__ float4 sh[TEAMS][LANES];
     __shared__ float sum_sh[TEAMS];
