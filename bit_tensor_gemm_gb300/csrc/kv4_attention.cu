@@ -17,9 +17,12 @@
 namespace lbg {
 namespace {
 
-// Rows of a tile (query tokens x heads of a group) up to which the kernel for
-// few rows runs.
-constexpr int64_t kFewRows = 32;
+// Rows of a sequence (query tokens x heads of a group) up to which the kernel
+// for few rows runs: it streams the cache once for every 16 of them (from L2, but
+// for the first), the other works for 256 rows whatever there are.  16 sequences
+// of up to 8192 tokens: 64 rows 79 us with the one, 88 with the other, 96 rows
+// 154 and 96; one sequence of 4096: 64 rows 17.3 and 27.7, 96 rows 22.6 and 28.6.
+constexpr int64_t kFewRows = 64;
 
 // Joins the shares of a tile's row: with share c's o_c and lse_c (log2),
 //   o = sum_c 2^(lse_c - lse) o_c,  lse = log2 sum_c 2^lse_c.
@@ -152,6 +155,7 @@ size_t kv4_attention_plan(Kv4AttnParams* p, int sm_count) {
   const int64_t rows = (int64_t)p->max_q * p->group;
   p->by_group = FastDiv((uint32_t)p->group);
   p->by_page16 = FastDiv((uint32_t)(p->cache.page_size / 16));
+  // (8 rows of those 16 sequences 31 us; 9 to 16, which need twice the MMAs, 49)
   p->tile_rows = rows <= 8 ? 8 : rows <= kFewRows ? 16 : 256;
   p->row_tiles = (int)((rows + p->tile_rows - 1) / p->tile_rows);
   // one wave of CTAs, or fewer where the longest lengths would not fill it

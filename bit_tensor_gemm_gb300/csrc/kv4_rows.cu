@@ -2,32 +2,30 @@
 // step, drafted tokens): tiles of 8 or 16 rows (query tokens x heads of a
 // group), streaming the cache once.
 //
-// Bound by HBM: D + 4 bytes per cached token and head against 4 D flops a
+// The floor is HBM: D + 4 bytes per cached token and head against 4 D flops a
 // row.  What an SM must keep up with at the copy rate is about 24 bytes a
 // cycle, which is 47 codes to turn into floats, so the design keeps the
 // instructions per code low:
 //   - warp MMAs with the cached tokens (keys) or channels (values) as the 16
 //     rows and the query rows as the 8 columns, so 8 rows cost no padding;
-//   - a code becomes an fp16 by one logical operation on two codes at once
-//     (and a shift for every second pair): n = code + 8 in the lowest bits of
-//     a half is the subnormal n 2^-24, in bits 4..7 it is 16 n 2^-24; MMAs take
-//     subnormals exactly.  Logic and shifts issue at half rate, and with 8
-//     floats a register built from exponents (three more of them per 8 codes)
-//     that pipe was the bound: 52 -> 33 us over 131072 tokens.
-//   - the constant 8 is taken out of the key product by starting the
-//     accumulators at -8 sum(q); for values it is subtracted in fp16 (exact),
-//     since there the products add up over thousands of tokens and the
-//     constant would cost digits;
-//   - queries enter as fp16 times a power of two of their row (exact for
-//     elements down to 2^-35 of the row's largest);
-//   - the order of channels in a product is free, so a lane's codes are used
-//     in the order in which they lie in memory;
-//   - the running maximum, and the largest weight seen, move only when a score
-//     or weight exceeds them 2^8 or 2^4 times, so almost no step rescales its
-//     accumulators.
+//   - two codes become two fp16 by a logical operation and a multiply-add (and a
+//     shift for every second pair; kv4_codes.cuh);
+//   - queries enter as fp16 times a power of two of their tile, in the order of
+//     channels in which a lane's codes lie in memory (the order is free);
+//   - the reference of the weights moves only when one leaves fp16's range, so
+//     almost no step rescales its accumulators.
 // A CTA streams 128 tokens a step through a ring of bulk copies; each of its
-// four warps takes 32 of them, with a running maximum and sum of its own until
-// the end.  The warps issue the copies in turn.
+// four warps takes 32 of them, with a reference and sum of its own until the
+// end.  The warps issue the copies in turn.  Three CTAs an SM with four stages
+// (16 rows: two): with four CTAs of three stages, which left 128 registers and
+// spilled, 131072 tokens took 44.4 us, 41.4 so.
+// Measured: one row group over 131072 tokens of 8 heads (138 MB) 41.9 us, 3.3
+// TB/s; 64 sequences of up to 8192 tokens (296 MB) 82 us, 3.6 TB/s.  In there,
+// by clock: 7.4 us until the first tokens are worked on (finding the run, the
+// pages, the queries: all first passes through their instructions), 1.5 us a
+// step of an SM's three CTAs (5.1 TB/s; each instruction waits for the one
+// before it too often for 12 warps to fill the SM: issue 37 %), 1.5 us for the
+// warps' sums, 5 us for the join.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -41,7 +39,10 @@ namespace {
 
 constexpr int kWarps = 4, kStages = 4, kTokens = 32, kStep = kStepTokens;
 constexpr int kMinSteps = 3;  // of a CTA's run
-constexpr int kTileCost = 2;  // in steps (see find_run)
+// in steps (see find_run).  64 sequences of up to 8192 tokens: 97.7 us with 0, 85.8
+// with 1, 81.1 with 2, 81.6 with 3, 82.2 with 4 (and 24 drafts of 5 tokens
+// 19.6, 17.1, 17.8, 18.2, 21.7).
+constexpr int kTileCost = 2;
 static_assert(kWarps * kTokens == kStep, "a warp's share of a step");
 template <int DIM>
 struct Ring {
@@ -59,15 +60,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The same from other accumulators: d = c + a b.
-__device__ __forceinline__ void mma16816_from(float (&d)[4], float c0, float c1, uint32_t a0,
-                                              uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                              uint32_t b1) {
+// The same into new accumulators: d = a b.
+__device__ __forceinline__ void mma16816_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%10, %11, %10, %11};"
+      "{%8, %9}, {%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Four 8 x 8 matrices of halves, transposed: lane l gives the address of row
@@ -237,8 +237,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const T* x = reinterpret_cast<const T*>(raw[nt]);
-      // channels (d, d + 4) of a word of codes make a register; those of odd
-      // codes, whose halves are 16 times larger, are divided by 16
+      // channels (d, d + 4) of a word of codes make a register
 #pragma unroll
       for (int w = 0; w < KW; ++w)
 #pragma unroll
@@ -247,9 +246,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
           q[nt][2 * w + i / 2][i % 2] = *reinterpret_cast<const uint32_t*>(&h);
         }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e)
         seen_to[nt][e] = last_seen(p, t, (int)p.by_group((uint32_t)(t.r0 + 8 * nt + 2 * c + e)));
-      }
     }
     // steps wholly inside [all_from, all_to) need no mask
     const int i_last = (int)p.by_group((uint32_t)(t.r0 + t.rows - 1));
@@ -259,8 +257,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     // Per column: the weights are 2^(t - ref), l their sum, and weight x value
     // scale goes into the value product in fp16.  `ref` is such that the largest
     // of those products so far was 2^10 .. 2^11 when it was set (and moves when
-    // one exceeds 2^15, or a weight 2^100): fp16 then holds them without loss
-    // down to 2^-24 of the largest, whatever scores and scales look like.
+    // one exceeds 2^15, or a weight 2^100): fp16 then holds them with all its digits
+    // down to 2^-24 of the largest, whatever scores and scales look like.  (A
+    // channel in which every larger product has code 0 keeps what lies above
+    // 2^-34 of the row's largest.)
     // m, wtop: the largest score, and the largest product relative to 2^m.
     float o[MT][NT][4], ref[NT][2], l[NT][2], m[NT][2], wtop[NT][2];
 #pragma unroll
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 if (w == 0 && i == 0)
-                  mma16816_from(acc[mt][nt], 0.0f, 0.0f, a0, a1, a2, a3, q[nt][0][0], q[nt][0][1]);
+                  mma16816_new(acc[mt][nt], a0, a1, a2, a3, q[nt][0][0], q[nt][0][1]);
                 else
                   mma16816(acc[mt][nt], a0, a1, a2, a3, q[nt][2 * w + i][0], q[nt][2 * w + i][1]);
               }
@@ -492,7 +492,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
           float all = merge_ref[0][r];
 #pragma unroll
           for (int i = 1; i < kWarps; ++i) all = fmaxf(all, merge_ref[i][r]);
-          // the halves' unit: 2^-24, and 2^-20 for odd channels
           const float f = ex2(ref[nt][e] - all) * (1.0f / kCodeUnit);
           float2* dst = reinterpret_cast<float2*>(mo + r * ROW + 2 * g);
 #pragma unroll

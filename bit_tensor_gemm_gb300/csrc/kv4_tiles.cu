@@ -7,9 +7,7 @@
 //
 //   converters (4 warps for keys, 3 for values)
 //                          codes of a step -> fp16 in shared memory, for S = Q
-//                          K^T and O += P V, each once for both tiles; codes as
-//                          subnormal halves code 2^-24 (every second one 16
-//                          times that), as in kv4_rows.cu
+//                          K^T and O += P V, each once for both tiles
 //   one warp               the MMAs: O_X += P_X V of step j - 1, then S_X = Q_X
 //                          K^T of step j, for X = 0, then 1
 //   softmax (4 warps an X) weights 2^(t - ref) from S_X, times the value scales
@@ -20,11 +18,17 @@
 //                          alone held shared memory for 2048 cycles a step
 //
 // While the tensor cores work for one tile, the other tile's softmax runs.
-// Bound: the MMAs, 4 x 128 x DIM flops per row and step; the converters' and
-// softmax's instructions (about 1.2 a code and 4 a score) must fit beside them,
+// The floor is the MMAs, 4 x 128 x DIM flops per row and step (2150 cycles for
+// DIM = 128); the converters' and softmax's instructions must fit beside them,
 // which is why both scales stay factors of columns, the weights need no maximum
 // (the reference moves only when a product with a value scale leaves fp16's
 // range, as in kv4_rows.cu), and arithmetic goes in pairs (f32x2).
+// Measured: 4096 queries of 32 heads over 16384 tokens (962 GFLOP) 1.01 ms, 0.95
+// PFLOP/s; 7 prompts of up to 1100 tokens, DIM = 64, 138 us.  A step takes 5000
+// cycles: what bounds it is the chain score MMA - weights - value MMA of a half,
+// with one softmax warp of a half on each of the SM's quarters (issue 48 %, MMAs
+// 40 %, exponentials 20 % of their rates); tensor memory is full with two halves'
+// scores and sums, so a third half to fill the gaps has no room.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -38,12 +42,16 @@ namespace {
 
 // Warps 0..3, 4..7 softmax, 8..11 keys, 12 MMAs, 13..15 values.  Launched with
 // 128 registers a thread (512 threads: all of the SM's); the softmax warps then
-// go up to 176 and the others down to 80: 176 + 176 + 80 + 80 = 4 x 128 in each
-// quarter of the register file.
+// go up to 152 and the others down to 104: 152 + 152 + 104 + 104 = 4 x 128 in
+// each quarter of the register file.
 constexpr int kThreads = 512;
 constexpr int kStep = kStepTokens;
 constexpr int kMinSteps = 4;
-constexpr int kTileCost = 3;  // in steps (see find_run)
+// In steps (see find_run).  A tile's queries, its first scores, its results and
+// the wait for its other half take 8 us, three steps: 7 prompts of up to 1100
+// tokens (416 tiles of 2 to 24 steps) 184 us with 0, 167 with 1, 145 with 2, 138
+// with 3.
+constexpr int kTileCost = 3;
 constexpr int kScaleSlots = 4;
 
 template <int DIM>
@@ -543,8 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = r < t.rows;
       const int qi = (int)p.by_group((uint32_t)(t.r0 + min(r, t.rows - 1)));
       // ---- queries to shared memory: fp16 times the tile's power of two (its
-      // largest element goes to 2^14 .. 2^15), in the codes' order, those of odd
-      // codes divided by 16.  (Every MMA of the tile before has ended.)
+      // largest element goes to 2^14 .. 2^15), in the codes' order.  (Every MMA of
+      // the tile before has ended.)
       {
         const T* src = static_cast<const T*>(p.q) + (int64_t)(t.q0 + qi) * p.q_stride +
                        (int64_t)(head * p.group + t.r0 + min(r, t.rows - 1) - qi * p.group) * DIM;
@@ -781,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             // columns 8 i .. of the accumulator are channels 0, 4, 1, 5, 2, 6, 3, 7 of
-            // eight, in units of 2^-24 (2^-20 for odd codes)
+            // eight, in units of kCodeUnit
             float ch[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {

@@ -6,10 +6,13 @@
 //             dw = sum over tokens and heads of g . xhat
 //             dx = rstd * (w . g - xhat * mean(w . g . xhat))
 //
-// A few operations per element against 4 bytes moved (8 for the backward
+// A few operations per element against 4 bytes moved (6 for the backward
 // pass): bound by HBM.  One pass: a head's vector lives in the registers of a
 // few lanes from its load to its store, its sum of squares is a shuffle
 // reduction, and the rotation's partner channel is in the same lane.
+// Measured, bf16, 40 heads of 128 channels: 16384 tokens 60.2 us (5.7 TB/s; a
+// block a few rows, loads into registers: 70.6); 8192 tokens with the backward
+// pass 84.8 us (123), of which the backward pass 52 (252 MB: 4.9 TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -469,7 +472,8 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const GradRowsOf
   if (x == 0 && mine < dim) r.dw[mine] = v;
 }
 
-// Heads of 64, 128 or 256 channels whose pairs fit the register layout.
+// Heads of 64, 128 or 256 channels whose pairs fit the register layout (16384
+// tokens of 40 heads of 128: 60 us so, 355 with the kernel for any size).
 bool in_registers(const NormRopeParams& p) {
   return (p.dim == 64 || p.dim == 128 || p.dim == 256) && p.rot % 8 == 0;
 }
