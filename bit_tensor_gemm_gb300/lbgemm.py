@@ -129,6 +129,8 @@ _lib = None
 def load(path: str | None = None):
     """Open the compiled library (raises if it has not been built)."""
     global _lib
+    if _lib is not None and path is None:  # (set once, under the lock)
+        return _lib
     with _lock:
         if _lib is None or path is not None:
             p = path or LIBRARY
@@ -154,10 +156,11 @@ def exported_symbols():
 def _addr(x) -> int | None:
     if x is None:
         return None
+    data_ptr = getattr(x, "data_ptr", None)
+    if data_ptr is not None:
+        return data_ptr()
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if hasattr(x, "ctypes"):  # numpy array (host memory)
         return x.ctypes.data
     raise TypeError(f"cannot take the address of {type(x).__name__}")
