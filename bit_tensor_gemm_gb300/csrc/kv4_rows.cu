@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
         for (int mt = 0; mt < 2; ++mt) {
           const uint8_t* kp = buf + (warp * kTokens + mt * 16) * (DIM / 2) + c * (DIM / 8);
           uint32_t ka[KW], kb[KW];
+          float odd[NT][4];
           if constexpr (KW == 4) {
             *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(kp + tok_a * (DIM / 2));
             *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(kp + tok_b * (DIM / 2));
@@ -316,12 +317,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
               const uint32_t a2 = codes_f16<true>(wa), a3 = codes_f16<true>(wb);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                if (w == 0 && i == 0)
-                  mma16816_new(acc[mt][nt], a0, a1, a2, a3, q[nt][0][0], q[nt][0][1]);
+                // (two chains of sums: an MMA waits for the one before it in its chain)
+                float(&d)[4] = i ? odd[nt] : acc[mt][nt];
+                if (w == 0)
+                  mma16816_new(d, a0, a1, a2, a3, q[nt][i][0], q[nt][i][1]);
                 else
-                  mma16816(acc[mt][nt], a0, a1, a2, a3, q[nt][2 * w + i][0], q[nt][2 * w + i][1]);
+                  mma16816(d, a0, a1, a2, a3, q[nt][2 * w + i][0], q[nt][2 * w + i][1]);
               }
             }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[mt][nt][r] += odd[nt][r];
           const uint8_t* scales = buf + 2 * Rg::kCodes + (warp * kTokens + mt * 16) * 2 + g * 4;
           const uint32_t ks2 = *reinterpret_cast<const uint32_t*>(scales);
           const uint32_t vs2 = *reinterpret_cast<const uint32_t*>(scales + 2 * kStep);
