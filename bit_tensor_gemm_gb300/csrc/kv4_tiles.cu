@@ -63,7 +63,7 @@ struct Smem {
   static constexpr int kScales = kV + 2 * kTile; // [4][2][128] fp32: keys' x factor, values'
   static constexpr int kState = kScales + kScaleSlots * 2 * kStep * 4;  // [8][256] fp32
   static constexpr int kBars = kState + 8 * 256 * 4;
-  static constexpr int kNumBars = 8 + kScaleSlots + 1 + 7;
+  static constexpr int kNumBars = 8 + kScaleSlots + 1 + 8;
   static constexpr int kMisc = kBars + 8 * kNumBars;
   static constexpr int kBytes = kMisc + 96 + 1024;  // slack to align to 1024
 };
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto s_full = [&](int x) { return q_full + 8u + 8u * x; };
   auto p_full = [&](int x) { return q_full + 24u + 8u * x; };
   auto o_full = [&](int x) { return q_full + 40u + 8u * x; };
-  const uint32_t drain = q_full + 56u;
+  const uint32_t drain = q_full + 56u, taken = q_full + 64u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
   float* factor_slot = reinterpret_cast<float*>(smem + S::kMisc + 8);
@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(scale_full(i), 128 + 96);
     mbar_init(q_full, 256);
+    mbar_init(taken, 128 + 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -397,6 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           warp_wait(q_full, tile);
           const int count = dead ? 1 : piece[0];
           const int from0 = piece[1], to0 = piece[2], from1 = piece[3], to1 = piece[4];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(taken);
           for (int j = 0; j <= count; ++j) {
             // run steps of the values and the keys (~0: none)
             const uint32_t sv = j > 0 ? step + j - 1 : ~0u, sj = j < count ? step + j : ~0u;
@@ -495,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(q_full, tile++);
             left = dead ? run.count : piece[0] - 1;
             factor = *reinterpret_cast<volatile float*>(factor_slot);
+            mbar_arrive(taken);
           }
           const int st = s & 1, use = s >> 1;
 #pragma unroll
@@ -552,8 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qi = (int)p.by_group((uint32_t)(t.r0 + min(r, t.rows - 1)));
       // ---- queries to shared memory: fp16 times the tile's power of two (its
       // largest element goes to 2^14 .. 2^15), in the codes' order.  (Every MMA of
-      // the tile before has ended.)
+      // the tile before has ended.)  The MMAs' warp and the keys' converters have
+      // taken over the tile before: of one that sees nothing this half waited for
+      // nothing, and several in a row would run away from those that walk them.
       {
+        if (tile > 0) warp_wait(taken, tile - 1);
         const T* src = static_cast<const T*>(p.q) + (int64_t)(t.q0 + qi) * p.q_stride +
                        (int64_t)(head * p.group + t.r0 + min(r, t.rows - 1) - qi * p.group) * DIM;
         // (kept for the second use as far as registers go: the L1 beside this much
@@ -631,6 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* state = reinterpret_cast<float*>(smem + S::kState) + threadIdx.x;
       uint32_t* seen = reinterpret_cast<uint32_t*>(state + 4 * 256);
       bool was_masked = true;  // (and `seen` to be set)
+      // The steps before `from` were not waited for: with the first scores there,
+      // every earlier step has its scales, so the barrier of a slot of scales is in
+      // this step's phase or past it, and its parity says which.
+      if (from < upto) warp_wait(s_full(x), n_s);
       for (int j = from; j < upto; ++j) {
         const uint32_t slot = (step + j) % kScaleSlots;
         warp_wait(scale_full(slot), (step + j) / kScaleSlots);
