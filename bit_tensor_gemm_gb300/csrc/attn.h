@@ -135,6 +135,8 @@ struct Kv4AttnParams {
   float* share_o = nullptr;     // [cta][2][tile_rows][dim]
   float* share_lse = nullptr;   // [cta][2][tile_rows]
 };
+// Tiles of rows of a call, those that a shorter sequence leaves empty among them.
+int64_t kv4_attention_tiles(int64_t batch, int64_t max_q, int64_t group);
 // Fills in the cut for this device; the scratch that it needs.
 size_t kv4_attention_plan(Kv4AttnParams* p, int sm_count);
 void kv4_attention_scratch(Kv4AttnParams* p, void* scratch);

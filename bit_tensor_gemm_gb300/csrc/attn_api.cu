@@ -302,6 +302,10 @@ lbgemm_status lbgemm_kv4_attention(int dtype, int64_t batch, int64_t total_q, in
                  (long long)heads_q, (long long)heads_kv);
     if (max_q * heads_q / heads_kv > INT32_MAX)
       return bad(LBGEMM_ERR_INVALID_ARG, "max_q times the heads of a group must be below 2^31");
+    // (the kernels count tiles in 32 bits)
+    if (kv4_attention_tiles(batch, max_q, heads_q / heads_kv) > INT32_MAX)
+      return bad(LBGEMM_ERR_INVALID_ARG, "%lld sequences of up to %lld rows are too many tiles",
+                 (long long)batch, (long long)max_q);
     if (max_kv < 0 || max_kv > (int64_t(1) << 30) || table_width < 0 || table_width > INT32_MAX)
       return bad(LBGEMM_ERR_INVALID_ARG, "max_kv %lld (at most 2^30), table_width %lld",
                  (long long)max_kv, (long long)table_width);

@@ -149,22 +149,28 @@ cudaError_t launch_join(const Kv4AttnParams& p, cudaStream_t s) {
   return p.cache.dim == 64 ? launch_join_dim<T, 64>(p, s) : launch_join_dim<T, 128>(p, s);
 }
 
+// (8 rows of those 16 sequences 31 us; 9 to 16, which need twice the MMAs, 49)
+int tile_rows_of(int64_t rows) { return rows <= 8 ? 8 : rows <= kFewRows ? 16 : 256; }
+
 }  // namespace
+
+int64_t kv4_attention_tiles(int64_t batch, int64_t max_q, int64_t group) {
+  const int64_t rows = max_q * group, tile = tile_rows_of(rows);
+  return batch * ((rows + tile - 1) / tile);
+}
 
 size_t kv4_attention_plan(Kv4AttnParams* p, int sm_count) {
   const int64_t rows = (int64_t)p->max_q * p->group;
   p->by_group = FastDiv((uint32_t)p->group);
   p->by_page16 = FastDiv((uint32_t)(p->cache.page_size / 16));
-  // (8 rows of those 16 sequences 31 us; 9 to 16, which need twice the MMAs, 49)
-  p->tile_rows = rows <= 8 ? 8 : rows <= kFewRows ? 16 : 256;
-  p->row_tiles = (int)((rows + p->tile_rows - 1) / p->tile_rows);
+  p->tile_rows = tile_rows_of(rows);
+  p->row_tiles = (int)kv4_attention_tiles(1, p->max_q, p->group);
   // one wave of CTAs, or fewer where the longest lengths would not fill it
-  const int64_t steps = (int64_t)p->batch * p->row_tiles * p->cache.heads *
-                        (p->max_kv / kStepTokens + 2);
+  const int64_t tiles = kv4_attention_tiles(p->batch, p->max_q, p->group) * p->cache.heads;
+  const int64_t steps = tiles * (p->max_kv / kStepTokens + 2);
   const int per_sm = p->tile_rows == 256 ? 1 : kv4_rows_per_sm(p->tile_rows);
   p->ctas = (int)std::min<int64_t>((int64_t)sm_count * per_sm, steps);
   // (tiles of one step each cannot be cut)
-  const int64_t tiles = (int64_t)p->batch * p->row_tiles * p->cache.heads;
   p->by_tile = tiles <= p->ctas;
   p->joins = p->max_kv <= kStepTokens ? 0 : p->by_tile ? (int)tiles : p->ctas;
   if (p->joins == 0) return 0;

@@ -623,7 +623,9 @@ lbgemm_status lbgemm_kv4_read(int dtype, int64_t tokens, int64_t heads, int64_t 
  * negative position) gets o = 0 and lse = -inf; tokens it does not see have
  * no effect on it, whatever their scales hold.
  * max_q, max_kv: bounds that no sequence's rows and length exceed (they size
- * the launch; table_width * page_size may be larger than max_kv).
+ * the launch; table_width * page_size may be larger than max_kv).  Rows go in
+ * tiles of 256 (of 16 or 8 up to 64 rows a sequence and key-value head): batch
+ * times the tiles of max_q * heads_q / heads_kv rows must be below 2^31.
  * dtype: LBGEMM_BF16 or LBGEMM_F16.  heads_q: a multiple of heads_kv; query
  * heads h * heads_q / heads_kv and the following share key-value head h.
  * O: [total_q, heads_q, head_dim] of dtype; lse: fp32 [total_q, heads_q],
