@@ -48,6 +48,24 @@ __device__ __forceinline__ RowTile row_tile(const Kv4AttnParams& p, int seq_tile
   return t;
 }
 
+// The tile to look at after `seq_tile`: past the sequence when this one, and so
+// all of the sequence that follow, has no rows.  (With one long prompt beside
+// thousands of single tokens nearly all tiles are such.)
+__device__ __forceinline__ int tile_after(const Kv4AttnParams& p, const RowTile& t, int seq_tile) {
+  return t.rows > 0 ? seq_tile + 1 : (t.b + 1) * p.row_tiles;
+}
+
+// The next tile with rows (the caller knows that there is one).
+__device__ __forceinline__ RowTile next_row_tile(const Kv4AttnParams& p, int* seq_tile) {
+  ++*seq_tile;
+  RowTile t = row_tile(p, *seq_tile);
+  while (t.rows == 0) {
+    *seq_tile = tile_after(p, t, *seq_tile);
+    t = row_tile(p, *seq_tile);
+  }
+  return t;
+}
+
 // This CTA's run of steps: it begins `off` steps into head `head` of sequence
 // tile `seq_tile` and has `count` steps (0: none).
 //
@@ -67,12 +85,18 @@ template <int THREADS>
 __device__ __forceinline__ Run find_run(const Kv4AttnParams& p, int min_steps, int tile_cost) {
   __shared__ int64_t warp_sum[THREADS / 32];
   __shared__ Run run;
-  const int tiles = p.batch * p.row_tiles, seg = (tiles + THREADS - 1) / THREADS;
-  const int from = min(tiles, (int)threadIdx.x * seg), to = min(tiles, from + seg);
+  const int tiles = p.batch * p.row_tiles;  // (below 2^31)
+  const int64_t seg = ((int64_t)tiles + THREADS - 1) / THREADS;
+  const int from = (int)min((int64_t)tiles, threadIdx.x * seg);
+  const int to = (int)min((int64_t)tiles, from + seg);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   auto places = [&](int steps) { return steps > 0 ? steps + tile_cost : 0; };
   int64_t mine = 0;
-  for (int i = from; i < to; ++i) mine += places(row_tile(p, i).steps);
+  for (int i = from; i < to;) {
+    const RowTile t = row_tile(p, i);
+    mine += places(t.steps);
+    i = tile_after(p, t, i);
+  }
   int64_t upto = mine;  // inclusive over the warp, then the block
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -97,12 +121,15 @@ __device__ __forceinline__ Run find_run(const Kv4AttnParams& p, int min_steps, i
   }
   int64_t at = (before + upto - mine) * heads;  // places before this thread's segment
   if (begin >= at && begin < at + mine * heads) {
-    int i = from, n = 0, wide = 0;
-    for (; i < to; ++i) {
-      n = row_tile(p, i).steps;
-      wide = places(n);
-      if (begin < at + wide * heads) break;
+    int i = from;
+    RowTile t = row_tile(p, i);
+    int n = t.steps, wide = places(n);
+    while (begin >= at + wide * heads) {
       at += wide * heads;
+      i = tile_after(p, t, i);
+      t = row_tile(p, i);
+      n = t.steps;
+      wide = places(n);
     }
     run.seq_tile = i;
     run.head = (int)((begin - at) / wide);
@@ -124,8 +151,10 @@ __device__ __forceinline__ Run find_run(const Kv4AttnParams& p, int min_steps, i
           break;
         }
       }
-      if (++i == tiles) break;
-      n = row_tile(p, i).steps;
+      i = tile_after(p, t, i);
+      if (i >= tiles) break;
+      t = row_tile(p, i);
+      n = t.steps;
       wide = places(n);
       left = heads;
     }

@@ -153,8 +153,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
       is_off -= is.steps;
       if (++is_head == p.cache.heads) {
         is_head = 0;
-        do is = row_tile(p, ++is_tile);
-        while (is.steps == 0);  // (there is one with steps: the run goes on)
+        is = next_row_tile(p, &is_tile);  // (there is one: the run goes on)
       }
     }
     const int token = is.base + is_off * kStep + stretch_at;
@@ -555,8 +554,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     off = 0;
     if (++head == p.cache.heads) {
       head = 0;
-      do t = row_tile(p, ++seq_tile);
-      while (t.steps == 0);
+      t = next_row_tile(p, &seq_tile);
     }
   }
   if (dead) {  // let the copies in flight land (again with a limit)

@@ -159,8 +159,7 @@ struct Cursor {
     off = 0;
     if (++head == p.cache.heads) {
       head = 0;
-      do t = row_tile(p, ++seq_tile);
-      while (t.steps == 0);
+      t = next_row_tile(p, &seq_tile);
     }
   }
 };
@@ -826,8 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       off = 0;
       if (done < run.count && ++head == p.cache.heads) {
         head = 0;
-        do ++seq_tile;
-        while (row_tile(p, hide(seq_tile)).steps == 0);
+        next_row_tile(p, &seq_tile);
       }
     }
   }

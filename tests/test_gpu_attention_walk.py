@@ -50,3 +50,52 @@ EMPTY = [
 @pytest.mark.parametrize("case", EMPTY)
 def test_tiles_that_see_nothing(case):
     run(case, 300, repeat=40)
+
+
+def event_ms(call, repeat=5):
+    call()
+    times = []
+    for _ in range(repeat):
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        e[0].record()
+        call()
+        e[1].record()
+        e[1].synchronize()
+        times.append(e[0].elapsed_time(e[1]))
+    return sorted(times)[repeat // 2]
+
+
+def test_long_prompt_beside_single_tokens():
+    """One prompt of many rows beside thousands of single tokens: nearly all of the
+    call's tiles of rows are empty, and cost next to nothing (each CTA went through
+    them one by one)."""
+    singles, prompt, hq, dim, page = 2048, 65536, 8, 64, 16
+    rows = np.ones(singles + 1, np.int64)
+    rows[singles // 2] = prompt
+    lens = np.full(singles + 1, 33)
+    cache = A.U.Cache(8, page, 1, dim, np.random.default_rng(4))
+    buf = A.to_torch(cache)
+    table = np.random.default_rng(5).integers(0, 8, (singles + 1, 3))
+    q = A.rand(6, (int(rows.sum()), hq, dim), BF16, 0.8)
+
+    def call(case, q):
+        return A.attend(case, q, buf, 8, table[:len(case[5])], case[6], 0.1)
+
+    both = (BF16, dim, hq, 1, page, rows.tolist(), lens.tolist(), True, 0)
+    alone = (BF16, dim, hq, 1, page, [prompt], [33], True, 0)
+    rest = (BF16, dim, hq, 1, page, [1] * singles, [33] * singles, True, 0)
+    o, lse = call(both, q)
+    L.lbgemm_device_status()
+    # every single token, and the prompt's last rows (the others see nothing)
+    first = int(rows[:singles // 2].sum())
+    keep = np.r_[0:first, first + prompt - 40:int(rows.sum())]
+    small = rows.copy()
+    small[singles // 2] = 40
+    A.check_attention((BF16, dim, hq, 1, page, small.tolist(), lens.tolist(), True, 0), cache, table,
+                      q[keep], o[keep], lse[keep], 0.1)
+    assert (o[first:first + prompt - 40] == 0).all()
+    ms, parts = event_ms(lambda: call(both, q)), (event_ms(lambda: call(alone, q[:prompt])),
+                                                  event_ms(lambda: call(rest, q[:singles])))
+    print(ms, parts)
+    # (the 256-row kernel takes the single tokens too here: a few times their own call)
+    assert ms <= 5 * sum(parts)
