@@ -43,8 +43,15 @@ namespace {
 // Warps 0..3, 4..7 softmax, 8..11 keys, 12 MMAs, 13..15 values.  Launched with
 // 128 registers a thread (512 threads: all of the SM's); the softmax warps then
 // go up to 152 and the others down to 104: 152 + 152 + 104 + 104 = 4 x 128 in
-// each quarter of the register file.
-constexpr int kThreads = 512;
+// each quarter of the register file.  The block has no more than it was launched
+// with, and a warp waits without a limit for what it asks: the launch checks that
+// the compiler did give the kernel 128 (a block of 17 warps once got 96, and
+// waited for ever).
+constexpr int kThreads = 512, kSoftmaxThreads = 256;
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kOtherRegs = 104;
+static_assert(kSoftmaxThreads * kSoftmaxRegs + (kThreads - kSoftmaxThreads) * kOtherRegs <=
+                  kThreads * kLaunchRegs,
+              "the shares of a block's registers");
 constexpr int kStep = kStepTokens;
 constexpr int kMinSteps = 4;
 // In steps (see find_run).  A tile's queries, its first scores, its results and
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 12) {
       // ---------------- the MMAs ----------------
       // The whole warp walks, lane 0 issues: what it passes stays warp-uniform and
@@ -532,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------- softmax ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int x = warp / 4, r = threadIdx.x;  // half; row of the 256 (queries and results)
     const int g = lane / 4, c4 = lane % 4;    // scores: rows g + 8 i of the warp's 32, i < 4
     const uint32_t lane_base = (uint32_t)(32 * (warp % 4)) << 16;
@@ -845,6 +852,10 @@ cudaError_t launch_tile(const Kv4AttnParams& p, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(set.load() >> dev & 1)) {
+    cudaFuncAttributes has = {};
+    e = cudaFuncGetAttributes(&has, kernel);
+    if (e != cudaSuccess) return e;
+    if (has.numRegs < kLaunchRegs) return cudaErrorLaunchOutOfResources;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<DIM>::kBytes);
     if (e != cudaSuccess) return e;
     set |= uint64_t(1) << dev;
