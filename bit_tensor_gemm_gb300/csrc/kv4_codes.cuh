@@ -11,7 +11,12 @@ namespace lbg {
 // a largest product of at least kLeastTop.
 constexpr float kFar = 1.2676506e30f;       // 2^100
 constexpr int kLevel = 11;  // the largest product is put at 2^11
-constexpr float kLeastTop = 8.2718061e-25f;  // 2^-80
+// ... by the reference alone where a row's largest product with a value scale is
+// within 2^-60 .. 2^60 of its largest weight; past that the reference stops, so
+// that weights and their sum stay normal fp32 numbers, and products take a power of
+// two of the row besides, in the careful form of a step only.
+constexpr int kSpan = 60;
+constexpr float kSpanLeast = 8.6736174e-19f, kSpanMost = 1.1529215e18f;  // 2^-60, 2^60
 
 // Codes 0 and 4 of a word (HIGH: 1 and 5) as two halves in units of kCodeUnit;
 // codes 2, 6 and 3, 7 are those of the word >> 8.  One three-input logical

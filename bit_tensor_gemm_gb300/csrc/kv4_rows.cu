@@ -37,6 +37,16 @@
 namespace lbg {
 namespace {
 
+// The power of two that a row's products take besides its reference, from its
+// largest product over its largest weight: 0 within the span.
+__device__ __forceinline__ int top_shift(float top) {
+  const int e = (int)(__float_as_uint(top) >> 23) - 127;
+  return top > 0.0f ? min(max(e, -kSpan), kSpan) - e : 0;
+}
+__device__ __forceinline__ float power_of_two(int e) {  // of a normal number
+  return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
 constexpr int kWarps = 4, kStages = 4, kTokens = 32, kStep = kStepTokens;
 constexpr int kMinSteps = 3;  // of a CTA's run
 // in steps (see find_run).  64 sequences of up to 8192 tokens: 97.7 us with 0, 85.8
@@ -261,6 +271,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     // channel in which every larger product has code 0 keeps what lies above
     // 2^-34 of the row's largest.)
     // m, wtop: the largest score, and the largest product relative to 2^m.
+    // shifts: the columns' top_shift in force, a byte each; where one is not 0,
+    // every step takes the careful form.
+    uint32_t shifts = 0;
+    auto shift_of = [&](int nt, int e) { return (int)(int8_t)(shifts >> 8 * (2 * nt + e)); };
     float o[MT][NT][4], ref[NT][2], l[NT][2], m[NT][2], wtop[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -376,15 +390,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
             }
         }
         // masked scores, or weights out of range: once more, with care
-        bool again = hidden != 0 || !__hble2(most2, __half2half2(__half(32768.0f)));
+        bool again = (hidden | shifts) != 0 || !__hble2(most2, __half2half2(__half(32768.0f)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) again |= part[nt][0] > kFar || part[nt][1] > kFar;
         if (__any_sync(0xffffffffu, again)) {
+          bool far = shifts != 0;  // a row whose products take a power of two besides
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float t4[4], w4[4];  // scores; weights x value scales
+              float t4[4];  // scores
               float high = m[nt][e];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -398,24 +413,22 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
               float top = wtop[nt][e] * ex2(m[nt][e] - high);
               const float before = top;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                // what a row does not see has weight 0 whatever its scale
-                w4[i] = t4[i] == -INFINITY ? 0.0f : ex2(t4[i] - high) * vs[i / 2][i & 1];
-                top = fmaxf(top, fabsf(w4[i]));
-              }
+              for (int i = 0; i < 4; ++i)  // (a NaN is passed over)
+                top = fmaxf(top, fabsf(ex2(t4[i] - high) * vs[i / 2][i & 1]));
 #pragma unroll
               for (int x = 4; x <= 16; x <<= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
               float next = ref[nt][e];
+              const float lead = fminf(fmaxf(top, kSpanLeast), kSpanMost);
+              far |= top != lead && top > 0.0f;
               // (the eight lanes of a column agree on all of this)
               if (high > m[nt][e] || top > before) {
-                // 2^(high - next) top = 2^(kLevel - 1) .. 2^kLevel
-                const float lead = fminf(fmaxf(top, kLeastTop), 1.0e30f);
+                // 2^(high - next) top = 2^(kLevel - 1) .. 2^kLevel, within the span
                 next = high - (float)(kLevel - 1 - ((int)(__float_as_uint(lead) >> 23) - 127));
               }
               m[nt][e] = high;
               wtop[nt][e] = top;
-              const float f = ex2(ref[nt][e] - next), up2 = ex2(high - next);
+              const float f = ex2(ref[nt][e] - next);
               ref[nt][e] = next;
               l[nt][e] *= f;
 #pragma unroll
@@ -426,10 +439,33 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
               part[nt][e] = 0.0f;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                part[nt][e] += ex2(t4[i] - next);
-                acc[i / 2][nt][(i & 1) * 2 + e] = w4[i] * up2;
+                const float w = ex2(t4[i] - next);
+                part[nt][e] += w;
+                // what a row does not see has weight 0 whatever its scale
+                acc[i / 2][nt][(i & 1) * 2 + e] = t4[i] == -INFINITY ? 0.0f : w * vs[i / 2][i & 1];
               }
             }
+          if (__any_sync(0xffffffffu, far)) {
+            uint32_t next_shifts = 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int shift = top_shift(wtop[nt][e]);
+                next_shifts |= (uint32_t)(shift & 255) << 8 * (2 * nt + e);
+                // (o does not grow by this and f together: what was the largest
+                // product is not more now)
+                const float f = power_of_two(min(max(shift - shift_of(nt, e), -126), 126));
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                  o[i][nt][e] *= f;
+                  o[i][nt][2 + e] *= f;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i / 2][nt][(i & 1) * 2 + e] *= power_of_two(shift);
+              }
+            shifts = next_shifts;
+          }
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -498,7 +534,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
           float all = merge_ref[0][r];
 #pragma unroll
           for (int i = 1; i < kWarps; ++i) all = fmaxf(all, merge_ref[i][r]);
-          const float f = ex2(ref[nt][e] - all) * (1.0f / kCodeUnit);
+          const float f =
+              ex2(ref[nt][e] - all) * (1.0f / kCodeUnit) * power_of_two(-shift_of(nt, e));
           float2* dst = reinterpret_cast<float2*>(mo + r * ROW + 2 * g);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {

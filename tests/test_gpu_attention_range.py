@@ -1,0 +1,82 @@
+"""GPU tests of attention over cached values of every size that a bf16 scale can
+hold, within the bounds of attention_tight.py."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import attention_tight as T  # noqa: E402
+import test_gpu_attention as A  # noqa: E402
+from bit_tensor_gemm_gb300 import build as bld  # noqa: E402
+from bit_tensor_gemm_gb300 import lbgemm as L  # noqa: E402
+
+BF16 = L.BF16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    bld.build()
+    L.load()
+
+
+def value_scales(kind, scales, rng):
+    """scales [tokens, heads] of the values, as `kind` has them; and the token that
+    takes most of the weight (None: none does)."""
+    n = len(scales)
+    if kind == "huge":  # values up to 2^127
+        scales[:] = 2.0 ** 124
+    elif kind == "tiny":
+        scales[:] = 1e-36 * np.exp(rng.normal(0, 1, scales.shape))
+    elif kind == "below the normal range":
+        scales[:] = 2.0 ** -130
+    elif kind == "one huge":
+        scales[n // 2] = 2.0 ** 124
+    elif kind == "one tiny with the weight":
+        scales[n // 3] = 1e-36
+        return n // 3
+    elif kind == "all but one tiny":
+        scales[:] = 1e-37
+        scales[n - 2] = 1.0
+    elif kind == "growing":
+        scales[:] = 2.0 ** np.linspace(-125, 124, n)[:, None]
+    elif kind == "falling":
+        scales[:] = 2.0 ** np.linspace(124, -125, n)[:, None]
+    elif kind == "huge, the last ones ordinary with the weight":
+        scales[:n - 1] = 2.0 ** 120
+        return n - 1
+    return None
+
+
+KINDS = ["huge", "tiny", "below the normal range", "one huge", "one tiny with the weight",
+         "all but one tiny", "growing", "falling", "huge, the last ones ordinary with the weight"]
+
+
+def check_kind(kind, rows, dim, length=700):
+    case = (BF16, dim, 4, 2, 16, [rows], [length], True, 0)
+    cache, table, width, pages, q = A.attend_inputs(case, 640, junk=False)
+    rng = np.random.default_rng(12)
+    at = table[0, np.arange(length) // 16], np.arange(length) % 16
+    s = cache.scales[1][at]
+    heavy = value_scales(kind, s, rng)
+    cache.scales[1][at] = A.U.bf16_round(s)
+    if heavy is not None:  # its key is along every query: they get one more channel of one sign
+        q[..., 0] = 4
+        cache.codes[0][..., 0] = 0
+        cache.codes[0][at[0][heavy], at[1][heavy], :, 0] = 7
+        cache.scales[0][at[0][heavy], at[1][heavy]] = 8.0
+    scale = 1 / math.sqrt(dim)
+    o, lse = A.attend(case, q, A.to_torch(cache), pages, table, case[6], scale)
+    L.lbgemm_device_status()
+    ref = T.attention(q, torch.bfloat16, cache, case[6], case[5], table, scale, True, 0)
+    T.check(o, lse, ref)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,dim", [(1, 128), (6, 64), (30, 128)])
+def test_value_scales_few_rows(kind, rows, dim):
+    check_kind(kind, rows, dim)
