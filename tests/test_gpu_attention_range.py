@@ -80,3 +80,40 @@ def check_kind(kind, rows, dim, length=700):
 @pytest.mark.parametrize("rows,dim", [(1, 128), (6, 64), (30, 128)])
 def test_value_scales_few_rows(kind, rows, dim):
     check_kind(kind, rows, dim)
+
+
+@pytest.mark.parametrize("rows", [1, 6, 30])
+def test_shares_of_the_largest_values(rows):
+    """Every value near the largest that a bf16 output holds: so is the result, whose
+    shares a join must not add up past it."""
+    length, dim = 1500, 64
+    case = (BF16, dim, 4, 2, 16, [rows], [length], True, 0)
+    cache, table, width, pages, q = A.attend_inputs(case, 641, junk=False)
+    cache.codes[1][:] = 7
+    cache.scales[1][:] = 2.0 ** 125  # 7 * 2^125 = 2.98e38
+    o, lse = A.attend(case, q, A.to_torch(cache), pages, table, case[6], 0.125)
+    L.lbgemm_device_status()
+    T.check(o, lse, T.attention(q, torch.bfloat16, cache, case[6], case[5], table, 0.125, True, 0))
+
+
+@pytest.mark.parametrize("above", [100, 126, 127, 130, 140, 147])
+@pytest.mark.parametrize("rows", [1, 6, 30])
+def test_shares_far_below_the_largest(rows, above):
+    """One token's weight 2^above times the others' and its values 2^-above theirs:
+    both count, in shares of their own too."""
+    length, dim = 1500, 64
+    case = (BF16, dim, 4, 2, 16, [rows], [length], True, 0)
+    cache, table, width, pages, q = A.attend_inputs(case, 642, junk=False)
+    at = table[0, np.arange(length) // 16], np.arange(length) % 16
+    heavy, scale = length // 3, 0.125
+    q[..., 0] = 4
+    cache.codes[0][..., 0] = 0
+    cache.codes[0][at[0][heavy], at[1][heavy]] = 0
+    cache.codes[0][at[0][heavy], at[1][heavy], :, 0] = 7
+    # 4 * 7 * ks / 8 = above ln 2, within the rounding of ks
+    cache.scales[0][at[0][heavy], at[1][heavy]] = A.U.bf16_round(above * math.log(2) / 3.5)
+    cache.scales[1][at[0][heavy], at[1][heavy]] = max(2.0 ** -above, 2.0 ** -126)
+    cache.codes[1][at[0][heavy], at[1][heavy]] = np.arange(dim) % 2 * 7
+    o, lse = A.attend(case, q, A.to_torch(cache), pages, table, case[6], scale)
+    L.lbgemm_device_status()
+    T.check(o, lse, T.attention(q, torch.bfloat16, cache, case[6], case[5], table, scale, True, 0))
