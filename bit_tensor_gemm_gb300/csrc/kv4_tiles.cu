@@ -68,8 +68,8 @@ struct Smem {
   static constexpr int kK = kQ + 2 * kTile;      // [2] keys
   static constexpr int kV = kK + 2 * kTile;      // [2] values
   static constexpr int kScales = kV + 2 * kTile; // [4][2][128] fp32: keys' x factor, values'
-  static constexpr int kState = kScales + kScaleSlots * 2 * kStep * 4;  // [8][256] fp32
-  static constexpr int kBars = kState + 8 * 256 * 4;
+  static constexpr int kState = kScales + kScaleSlots * 2 * kStep * 4;  // [12][256] fp32
+  static constexpr int kBars = kState + 12 * 256 * 4;
   static constexpr int kNumBars = 8 + kScaleSlots + 1 + 8;
   static constexpr int kMisc = kBars + 8 * kNumBars;
   static constexpr int kBytes = kMisc + 96 + 1024;  // slack to align to 1024
@@ -198,16 +198,19 @@ __device__ __forceinline__ HalfTile half_tile(const Kv4AttnParams& p, const RowT
 // thread's rows, 16 TMEM lanes, whose S begins at `ts` (warp-uniform call).
 // state: the rows' ref[2], l[2] in shared memory, 256 floats apart; ks: the
 // chunk's scales of this thread's first columns; seen: the tokens of the step
-// that each row sees (from the low half to the high half), beside `state`.  Where a reference moves, the sums (at `to`, when they hold
-// anything: S of this step was committed after O += P V of the step before) and
-// this step's weights so far follow.  A function of its own, so that its
-// registers are not the loop's.
+// that each row sees (from the low half to the high half), beside `state`; shifts:
+// the exponents of the powers of two that the rows' products take besides
+// (kSpan), beside it too.  Where a reference or such a power moves, the sums (at
+// `to`, when they hold anything: S of this step was committed after O += P V of
+// the step before) and this step's weights so far follow.  True where a row has
+// such a power.  A function of its own, so that its registers are not the loop's.
 template <int DIM>
-__device__ __noinline__ void careful_weights(uint32_t ts, uint32_t to, const float* ks, int q,
-                                             bool sums, const uint32_t* seen_at,
-                                             float* state) {
+__device__ __noinline__ bool careful_weights(uint32_t ts, uint32_t to, const float* ks, int q,
+                                             bool sums, const uint32_t* seen_at, float* state,
+                                             float* shifts) {
   const int c4 = threadIdx.x % 4;
   float f[2];
+  bool wide = false;
   bool moved = false;
   uint32_t sv[16], pw[8];
   tmem_ld_16x32(ts + 32 * q, sv);
@@ -216,7 +219,8 @@ __device__ __noinline__ void careful_weights(uint32_t ts, uint32_t to, const flo
   for (int i = 0; i < 2; ++i) {
     const uint32_t seen = seen_at[i * 256];
     const int upto = (int)(seen >> 16) - 32 * q - 2 * c4, from = (int)(seen & 0xffffu) - 32 * q - 2 * c4;
-    const float rf = state[i * 256];
+    const float rf = state[i * 256], shift = shifts[i * 256];
+    float sum = state[(2 + i) * 256];  // this lane's columns only
     float high = -INFINITY, top = -INFINITY;  // of t; of log2 |2^t vs|
     float s8[8];
 #pragma unroll
@@ -232,16 +236,30 @@ __device__ __noinline__ void careful_weights(uint32_t ts, uint32_t to, const flo
     for (int d = 1; d < 4; d *= 2) {  // (the four lanes of a row agree)
       high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      sum += __shfl_xor_sync(0xffffffffu, sum, d);
     }
-    float ref = rf;
-    const float need = fmaxf(fminf(top, 3.0e38f) - (rf == kNoRef ? kFirstLevel : kLevel), high - 90.0f);
-    if (rf == kNoRef) {
-      if (high > -INFINITY) ref = need;
-    } else if (top - rf > 14.9f || high - rf > 99.0f) {
-      ref = rf + ceilf(need - rf);
+    float ref = rf, next_shift = shift;
+    if (rf == kNoRef || top - rf + shift > 14.9f) {
+      // The largest product to its level, by the reference as far as kSpan allows
+      // it beside the largest weight (of what is there: at most its sum).
+      const float most = rf == kNoRef ? high : fmaxf(high, rf + __log2f(sum));
+      const float level = rf == kNoRef ? (float)kFirstLevel : (float)kLevel;
+      const float over = fminf(top, 3.0e38f) - most;
+      const float follow = top > -INFINITY ? fminf(fmaxf(over, -(float)kSpan), (float)kSpan) : 0.0f;
+      const float need = follow == over ? top - level : most + follow - level;
+      if (rf != kNoRef) ref = rf + ceilf(need - rf);  // (binades: what is there scales exactly)
+      else if (high > -INFINITY) ref = need;
+      next_shift = follow == over || top == -INFINITY ? 0.0f : fminf(rintf(follow - over), 100.0f);
+    } else if (high - rf > 99.0f) {
+      // weights out of range, products not: these stay where they are
+      ref = rf + ceilf(high - kSpan - rf);
+      next_shift = fminf(shift + (ref - rf), 100.0f);
     }
-    f[i] = rf == kNoRef ? 0.0f : ex2(rf - ref);
-    moved |= rf != kNoRef && ref != rf;
+    const float fl = rf == kNoRef ? 0.0f : ex2(rf - ref);
+    f[i] = rf == kNoRef ? 0.0f : ex2(rf - ref + (next_shift - shift));
+    moved |= rf != kNoRef && (ref != rf || next_shift != shift);
+    wide |= next_shift != 0.0f;
+    const float power = ex2(next_shift);
     float total = 0.0f;
 #pragma unroll
     for (int n = 0; n < 8; n += 2) {
@@ -253,15 +271,16 @@ __device__ __noinline__ void careful_weights(uint32_t ts, uint32_t to, const flo
         const float pj = ex2(s8[n + e] - ref);
         total += see ? pj : 0.0f;
         // what a row does not see has weight 0 whatever its scale
-        w2[e] = see ? pj * ks[kStep + token] : 0.0f;
+        w2[e] = see ? pj * ks[kStep + token] * power : 0.0f;
       }
       pw[n + i] = pack_f16(w2[0], w2[1]);
     }
     state[i * 256] = ref;
-    state[(2 + i) * 256] = state[(2 + i) * 256] * f[i] + total;
+    state[(2 + i) * 256] = state[(2 + i) * 256] * fl + total;
+    shifts[i * 256] = next_shift;
   }
   tmem_st_16x16h(ts + 16 * q, pw);
-  if (!__any_sync(0xffffffffu, moved)) return;
+  if (!__any_sync(0xffffffffu, moved)) return wide;
   tmem_st_wait();
   if (sums) {
 #pragma unroll 1
@@ -286,6 +305,7 @@ __device__ __noinline__ void careful_weights(uint32_t ts, uint32_t to, const flo
     }
     tmem_st_16x16h(ts + 16 * n, v);
   }
+  return wide;
 }
 
 template <typename T, int DIM>
@@ -631,8 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // into the value product in fp16; `ref` puts the largest of the first 32 of
       // those at 2^5, and moves (up, by whole binades, so that what is there scales
       // exactly) when one exceeds 2^15, or a weight 2^100, which then goes to 2^11:
-      // fp16 holds them without loss down to 2^-19 (2^-25 once it has moved) of the
-      // largest.  (2^11 from the start: rows then moved after every other chunk of
+      // fp16 rounds them by 2^-11 of themselves or 2^-30 (2^-36 once it has moved) of the
+      // largest, whichever is more.  (2^11 from the start: rows then moved after every other chunk of
       // the first steps, 1250 us instead of 1099 for 4096 queries over 16384 tokens.)  Until a row has seen a token its reference is kNoRef: its first
       // weight overflows and so sets it.
       float ref[4], l[4];
@@ -643,6 +663,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float* state = reinterpret_cast<float*>(smem + S::kState) + threadIdx.x;
       uint32_t* seen = reinterpret_cast<uint32_t*>(state + 4 * 256);
+      float* shifts = state + 8 * 256;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) shifts[i * 256] = 0.0f;
+      bool wide = false;  // a row's products take a power of two besides
       bool was_masked = true;  // (and `seen` to be set)
       // The steps before `from` were not waited for: with the first scores there,
       // every earlier step has its scales, so the barrier of a slot of scales is in
@@ -688,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait_for(sv[1]);
           uint64_t sum[4] = {0, 0, 0, 0};
           __half2 most = __half2half2(__half(0.0f));
-          bool again = false;
+          bool again = wide;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const uint64_t k2 = *reinterpret_cast<const uint64_t*>(ks + 8 * b);
@@ -730,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           again |= fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) > kFar;
           if (__any_sync(0xffffffffu, again)) {
             // weights out of range, or odd scales beside a mask: once more, with care
+            wide = false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -738,8 +763,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 state[(2 + i) * 256] = l[2 * h + i];
               }
               const uint32_t lanes = h ? 16u << 16 : 0u;
-              careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from, seen + 2 * h * 256,
-                                   state);
+              wide |= careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from,
+                                           seen + 2 * h * 256, state, shifts + 2 * h * 256);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 ref[2 * h + i] = state[i * 256];
@@ -781,6 +806,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ref_row = b;
         }
       }
+      __syncwarp();
+      // (columns are in units of kCodeUnit; first the sum, which brings them into range)
+      const float unit = ex2(-(reinterpret_cast<const float*>(smem + S::kState) + 8 * 256)
+                                  [lane / 8 * 256 + threadIdx.x - lane + 4 * (lane % 8)]) *
+                         (1.0f / kCodeUnit);
       const bool none = l_row == 0.0f;
       const float inv = none ? 0.0f : 1.0f / l_row;
       const float lse = none ? -INFINITY : ref_row + log2f(l_row);
@@ -812,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 8; ++k) {
               const int d = k / 2 + (k & 1) * 4;
               ch[d] = none ? 0.0f
-                           : __uint_as_float(v[8 * i + k]) * ((1.0f / kCodeUnit) * inv);
+                           : __uint_as_float(v[8 * i + k]) * inv * unit;
             }
             if (!live) continue;
             if (whole) store8(static_cast<T*>(p.o) + at * DIM + 32 * q + 8 * i, ch);

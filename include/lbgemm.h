@@ -629,10 +629,10 @@ lbgemm_status lbgemm_kv4_read(int dtype, int64_t tokens, int64_t heads, int64_t 
  * dtype: LBGEMM_BF16 or LBGEMM_F16.  heads_q: a multiple of heads_kv; query
  * heads h * heads_q / heads_kv and the following share key-value head h.
  * O: [total_q, heads_q, head_dim] of dtype; lse: fp32 [total_q, heads_q],
- * natural logarithm, or NULL.  Products of a weight and a value scale are rounded
- * to fp16 relative to a row's largest one (11 bits; what lies below 2^-30 of it
- * may be lost); scores, sums of weights and outputs are fp32.  Scratch for
- * partial results of a cut cache is taken as in lbgemm_run. */
+ * natural logarithm, or NULL.  A product of a weight and a value scale is rounded
+ * to fp16: by 2^-11 of itself or 2^-30 of a row's largest one, whichever is more,
+ * whatever size the scales have; scores, sums of weights and outputs are fp32.
+ * Scratch for partial results of a cut cache is taken as in lbgemm_run. */
 lbgemm_status lbgemm_kv4_attention(int dtype, int64_t batch, int64_t total_q, int64_t max_q,
                                    int64_t heads_q, int64_t heads_kv, int64_t head_dim,
                                    const void* Q, int64_t q_stride, const int32_t* cu_q,

@@ -82,7 +82,13 @@ def test_value_scales_few_rows(kind, rows, dim):
     check_kind(kind, rows, dim)
 
 
-@pytest.mark.parametrize("rows", [1, 6, 30])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,dim", [(90, 64), (400, 128)])
+def test_value_scales_many_rows(kind, rows, dim):
+    check_kind(kind, rows, dim)
+
+
+@pytest.mark.parametrize("rows", [1, 6, 30, 90])
 def test_shares_of_the_largest_values(rows):
     """Every value near the largest that a bf16 output holds: so is the result, whose
     shares a join must not add up past it."""
@@ -97,7 +103,7 @@ def test_shares_of_the_largest_values(rows):
 
 
 @pytest.mark.parametrize("above", [100, 126, 127, 130, 140, 147])
-@pytest.mark.parametrize("rows", [1, 6, 30])
+@pytest.mark.parametrize("rows", [1, 6, 30, 90])
 def test_shares_far_below_the_largest(rows, above):
     """One token's weight 2^above times the others' and its values 2^-above theirs:
     both count, in shares of their own too."""
