@@ -12,11 +12,42 @@ namespace lbg {
 constexpr float kFar = 1.2676506e30f;       // 2^100
 constexpr int kLevel = 11;  // the largest product is put at 2^11
 // ... by the reference alone where a row's largest product with a value scale is
-// within 2^-60 .. 2^60 of its largest weight; past that the reference stops, so
+// within 2^-63 .. 2^63 of its largest weight; past that the reference stops, so
 // that weights and their sum stay normal fp32 numbers, and products take a power of
 // two of the row besides, in the careful form of a step only.
-constexpr int kSpan = 60;
-constexpr float kSpanLeast = 8.6736174e-19f, kSpanMost = 1.1529215e18f;  // 2^-60, 2^60
+constexpr int kSpan = 63;
+constexpr float kSpanLeast = 1.0842022e-19f, kSpanMost = 9.2233720e18f;  // 2^-63, 2^63
+
+__device__ __forceinline__ float power_of_two(int e) {  // of a normal number
+  return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+// Of a warp's numbers, none negative: the largest, the smallest.
+__device__ __forceinline__ float warp_most(float x) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+}
+__device__ __forceinline__ float warp_least(float x) {
+  return __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(x)));
+}
+
+// The exponent of the power of two that brings queries whose largest is `most`
+// to 2^14 .. 2^15 (0 for zeros): -113 .. 126.
+__device__ __forceinline__ int query_power(float most) {
+  return most > 0.0f ? min(14 - ((int)(__float_as_uint(most) >> 23) - 127), 126) : 0;
+}
+// Whether the rows of a tile take powers of their own: the smallest of their
+// largest elements would stay below 1, or the tile's power be too far from 1 to be
+// a factor of the keys' scales.
+__device__ __forceinline__ bool far_queries(float most, float least) {
+  const int k = query_power(most);
+  return k < -64 || least < power_of_two(-k);
+}
+// Then the tile's exponent that goes into that factor, and a row's, at most 126
+// above it (a row whose scores are 2^-126 of another's has scores of 0).
+__device__ __forceinline__ int far_tile_power(float most) { return min(max(query_power(most), -64), 64); }
+__device__ __forceinline__ int far_row_power(float row_most, int tile) {
+  return min(query_power(row_most), tile + 126);
+}
 
 // Codes 0 and 4 of a word (HIGH: 1 and 5) as two halves in units of kCodeUnit;
 // codes 2, 6 and 3, 7 are those of the word >> 8.  One three-input logical

@@ -38,13 +38,10 @@ namespace lbg {
 namespace {
 
 // The power of two that a row's products take besides its reference, from its
-// largest product over its largest weight: 0 within the span.
+// largest product over its largest weight: 0 within the span, -64 .. 63 past it.
 __device__ __forceinline__ int top_shift(float top) {
   const int e = (int)(__float_as_uint(top) >> 23) - 127;
-  return top > 0.0f ? min(max(e, -kSpan), kSpan) - e : 0;
-}
-__device__ __forceinline__ float power_of_two(int e) {  // of a normal number
-  return __uint_as_float((uint32_t)(127 + e) << 23);
+  return top > 0.0f ? min(max(min(max(e, -kSpan), kSpan) - e, -64), 63) : 0;
 }
 
 constexpr int kWarps = 4, kStages = 4, kTokens = 32, kStep = kStepTokens;
@@ -116,7 +113,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
   constexpr int ROW = DIM + 4;  // floats from a row to the next in the merge buffer
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2][kStages];  // full, empty
-  __shared__ float merge_ref[kWarps][R], merge_l[kWarps][R];
+  __shared__ float merge_ref[kWarps][R], merge_l[kWarps][R], row_unit[kWarps][R];
   __shared__ int abort_flag;
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, c = lane % 4;
@@ -210,10 +207,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     uint32_t q[NT][MT][2];
     int seen_to[NT][2];  // one past the last token that columns 2c, 2c + 1 see
     // The tile's power of two: its largest element goes to 2^14 .. 2^15, so that
-    // in fp16 every element keeps its digits down to 2^-28 of that, and scores
-    // are off by at most 2^-39 of the tile's largest.
+    // in fp16 every element keeps its digits down to 2^-28 of that.  Where a row
+    // would stay below 1 by it, or the power is too far from 1 to be a factor of the
+    // keys' scales, every row has its own (own_units): its scores are then brought
+    // to their unit in the careful form of a step.  Either way an element is off by
+    // at most 2^-25 of its row's largest.
     uint32_t raw[NT][DIM / 8];  // DIM / 4 elements of row 8 nt + g: two a word
-    float most = 0.0f;
+    float row_most[NT], most = 0.0f, least = INFINITY;  // least: of rows that are not 0
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = 8 * nt + g;
@@ -229,23 +229,30 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
           reinterpret_cast<uint4*>(raw[nt])[i4] = __ldg(src + i4);
       }
       const T* x = reinterpret_cast<const T*>(raw[nt]);
+      row_most[nt] = 0.0f;
 #pragma unroll
       for (int i = 0; i < DIM / 4; ++i) {
         const float a = fabsf(to_f32(x[i]));
-        if (a < INFINITY) most = fmaxf(most, a);
+        if (a < INFINITY) row_most[nt] = fmaxf(row_most[nt], a);
       }
-    }
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-    int k = 0;
-    if (most > 0.0f) k = min(max(14 - ((int)(__float_as_uint(most) >> 23) - 127), -103), 126);
-    const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-    // the accumulators' unit times scale log2(e)
-    const float factor =
-        __uint_as_float((uint32_t)(127 - k) << 23) * (p.scale * kLog2e / kCodeUnit);
+      for (int x = 2; x >= 1; x >>= 1)
+        row_most[nt] = fmaxf(row_most[nt], __shfl_xor_sync(0xffffffffu, row_most[nt], x));
+      most = fmaxf(most, row_most[nt]);
+      if (row_most[nt] > 0.0f) least = fminf(least, row_most[nt]);
+    }
+    most = warp_most(most);
+    least = warp_least(least);
+    const bool own_units = far_queries(most, least);
+    const int k = own_units ? far_tile_power(most) : query_power(most);
+    // the accumulators' unit (but for the rows' own) times scale log2(e)
+    const float factor = power_of_two(-k) * (p.scale * kLog2e / kCodeUnit);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const T* x = reinterpret_cast<const T*>(raw[nt]);
+      const int k_row = own_units ? far_row_power(row_most[nt], k) : k;
+      const float up = power_of_two(k_row);
+      if (own_units && c == 0) row_unit[warp][8 * nt + g] = power_of_two(k - k_row);
       // channels (d, d + 4) of a word of codes make a register
 #pragma unroll
       for (int w = 0; w < KW; ++w)
@@ -271,10 +278,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     // channel in which every larger product has code 0 keeps what lies above
     // 2^-34 of the row's largest.)
     // m, wtop: the largest score, and the largest product relative to 2^m.
-    // shifts: the columns' top_shift in force, a byte each; where one is not 0,
-    // every step takes the careful form.
-    uint32_t shifts = 0;
-    auto shift_of = [&](int nt, int e) { return (int)(int8_t)(shifts >> 8 * (2 * nt + e)); };
+    // shifts: the columns' top_shift in force, 7 bits each, and own_units; where it
+    // is not 0, every step takes the careful form.
+    constexpr uint32_t kOwnUnits = 1u << 28;
+    uint32_t shifts = own_units ? kOwnUnits : 0;
+    auto shift_of = [&](int nt, int e) { return (int)(shifts << (25 - 7 * (2 * nt + e))) >> 25; };
     float o[MT][NT][4], ref[NT][2], l[NT][2], m[NT][2], wtop[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -394,6 +402,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) again |= part[nt][0] > kFar || part[nt][1] > kFar;
         if (__any_sync(0xffffffffu, again)) {
+          if (shifts & kOwnUnits) {
+            __syncwarp();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float unit = row_unit[warp][8 * nt + 2 * c + e];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  float& s4 = acc[i / 2][nt][(i & 1) * 2 + e];
+                  s4 = s4 * ks[i / 2][i & 1] * unit;
+                }
+              }
+            ks[0][0] = ks[0][1] = ks[1][0] = ks[1][1] = 1.0f;
+          }
           bool far = shifts != 0;  // a row whose products take a power of two besides
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -446,13 +469,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
               }
             }
           if (__any_sync(0xffffffffu, far)) {
-            uint32_t next_shifts = 0;
+            uint32_t next_shifts = shifts & kOwnUnits;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int shift = top_shift(wtop[nt][e]);
-                next_shifts |= (uint32_t)(shift & 255) << 8 * (2 * nt + e);
+                next_shifts |= (uint32_t)(shift & 127) << 7 * (2 * nt + e);
                 // (o does not grow by this and f together: what was the largest
                 // product is not more now)
                 const float f = power_of_two(min(max(shift - shift_of(nt, e), -126), 126));

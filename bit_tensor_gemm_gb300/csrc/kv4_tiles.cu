@@ -69,10 +69,15 @@ struct Smem {
   static constexpr int kV = kK + 2 * kTile;      // [2] values
   static constexpr int kScales = kV + 2 * kTile; // [4][2][128] fp32: keys' x factor, values'
   static constexpr int kState = kScales + kScaleSlots * 2 * kStep * 4;  // [12][256] fp32
-  static constexpr int kBars = kState + 12 * 256 * 4;
+  static constexpr int kUnits = kState + 12 * 256 * 4;  // [256] fp32, and whether they are in use
+  static constexpr int kBars = kUnits + 256 * 4 + 16;
   static constexpr int kNumBars = 8 + kScaleSlots + 1 + 8;
-  static constexpr int kMisc = kBars + 8 * kNumBars;
-  static constexpr int kBytes = kMisc + 96 + 1024;  // slack to align to 1024
+  static constexpr int kMisc = (kBars + 8 * kNumBars + 15) / 16 * 16;
+  static constexpr int kMost = kMisc + 16, kLeast = kMisc + 80;  // [8] fp32 each, read as float4
+  static_assert(kMost % 16 == 0 && kLeast % 16 == 0 && kScales % 16 == 0 && kState % 16 == 0 &&
+                    kUnits % 16 == 0 && kBars % 16 == 0,
+                "wide accesses to shared memory");
+  static constexpr int kBytes = kMisc + 128 + 1024;  // slack to align to 1024
 };
 
 // Chunk j (16 bytes) of row r of a 128-byte-swizzled block of rows of 128 bytes.
@@ -196,21 +201,25 @@ __device__ __forceinline__ HalfTile half_tile(const Kv4AttnParams& p, const RowT
 
 // The careful form of the weights of 32 tokens (chunk q of the step) and two of a
 // thread's rows, 16 TMEM lanes, whose S begins at `ts` (warp-uniform call).
-// state: the rows' ref[2], l[2] in shared memory, 256 floats apart; ks: the
-// chunk's scales of this thread's first columns; seen: the tokens of the step
-// that each row sees (from the low half to the high half), beside `state`; shifts:
-// the exponents of the powers of two that the rows' products take besides
-// (kSpan), beside it too.  Where a reference or such a power moves, the sums (at
-// `to`, when they hold anything: S of this step was committed after O += P V of
-// the step before) and this step's weights so far follow.  True where a row has
-// such a power.  A function of its own, so that its registers are not the loop's.
+// ks: the chunk's scales of this thread's first columns.  state: what shared memory
+// has of this thread's rows (h: rows 2 h, 2 h + 1 of four), in arrays 256 floats
+// apart: [2] ref and [2] l of the two; [4] of all the tokens of the step that the
+// row sees (from the low half to the high half) and [4] the exponents of the powers
+// of two that its products take besides (kSpan); then [256] the tile's rows' own
+// units of the scores, and whether these are in use.  Where a reference or such a
+// power moves, the sums (at `to`, when they hold anything: S of this step was
+// committed after O += P V of the step before) and this step's weights so far
+// follow.  True where the next step needs this form too.  A function of its own, so
+// that its registers are not the loop's.
 template <int DIM>
 __device__ __noinline__ bool careful_weights(uint32_t ts, uint32_t to, const float* ks, int q,
-                                             bool sums, const uint32_t* seen_at, float* state,
-                                             float* shifts) {
+                                             bool sums, float* state, int h) {
   const int c4 = threadIdx.x % 4;
+  const uint32_t* seen_at = reinterpret_cast<const uint32_t*>(state + (4 + 2 * h) * 256);
+  float* shifts = state + (8 + 2 * h) * 256;
+  const float* units = state + 12 * 256 - threadIdx.x % 32 + threadIdx.x % 32 / 4 + 16 * h;
   float f[2];
-  bool wide = false;
+  bool wide = state[13 * 256 - threadIdx.x] != 0.0f;
   bool moved = false;
   uint32_t sv[16], pw[8];
   tmem_ld_16x32(ts + 32 * q, sv);
@@ -219,7 +228,7 @@ __device__ __noinline__ bool careful_weights(uint32_t ts, uint32_t to, const flo
   for (int i = 0; i < 2; ++i) {
     const uint32_t seen = seen_at[i * 256];
     const int upto = (int)(seen >> 16) - 32 * q - 2 * c4, from = (int)(seen & 0xffffu) - 32 * q - 2 * c4;
-    const float rf = state[i * 256], shift = shifts[i * 256];
+    const float rf = state[i * 256], shift = shifts[i * 256], unit = units[i * 8];
     float sum = state[(2 + i) * 256];  // this lane's columns only
     float high = -INFINITY, top = -INFINITY;  // of t; of log2 |2^t vs|
     float s8[8];
@@ -227,7 +236,7 @@ __device__ __noinline__ bool careful_weights(uint32_t ts, uint32_t to, const flo
     for (int n = 0; n < 8; ++n) {
       const int token = n / 2 * 8 + n % 2;
       const bool see = token < upto && token >= from;
-      s8[n] = see ? __uint_as_float(sv[n / 2 * 4 + i * 2 + n % 2]) * ks[token] : -INFINITY;
+      s8[n] = see ? __uint_as_float(sv[n / 2 * 4 + i * 2 + n % 2]) * ks[token] * unit : -INFINITY;
       high = fmaxf(high, s8[n]);
       const float v = fabsf(ks[kStep + token]);
       if (see && v < INFINITY) top = fmaxf(top, s8[n] + __log2f(v));
@@ -334,7 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
   float* factor_slot = reinterpret_cast<float*>(smem + S::kMisc + 8);
-  float* most_slots = reinterpret_cast<float*>(smem + S::kMisc + 16);  // [8]
+  float* most_slots = reinterpret_cast<float*>(smem + S::kMost);
+  float* least_slots = reinterpret_cast<float*>(smem + S::kLeast);
+  float* units = reinterpret_cast<float*>(smem + S::kUnits);
   float* scales = reinterpret_cast<float*>(smem + S::kScales);
   // the present tile, for the MMAs and converters: steps, and those each half sees
   volatile int* piece = reinterpret_cast<volatile int*>(smem + S::kMisc + 48);  // count, from, to, from, to
@@ -581,8 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = r < t.rows;
       const int qi = (int)p.by_group((uint32_t)(t.r0 + min(r, t.rows - 1)));
       // ---- queries to shared memory: fp16 times the tile's power of two (its
-      // largest element goes to 2^14 .. 2^15), in the codes' order.  (Every MMA of
-      // the tile before has ended.)  The MMAs' warp and the keys' converters have
+      // largest element goes to 2^14 .. 2^15), in the codes' order; where a row would
+      // be too small by it, every row its own, and scores are brought to their unit in
+      // the careful form of a step (as in kv4_rows.cu).  (Every MMA of the tile before
+      // has ended.)  The MMAs' warp and the keys' converters have
       // taken over the tile before: of one that sees nothing this half waited for
       // nothing, and several in a row would run away from those that walk them.
       {
@@ -604,17 +617,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 8; ++k)
             if (fabsf(v[k]) < INFINITY) most = fmaxf(most, fabsf(v[k]));
         }
-#pragma unroll
-        for (int i = 16; i >= 1; i >>= 1)
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, i));
+        const float row_most = most;
+        float least = most > 0.0f ? most : INFINITY;  // of rows that are not 0
+        most = warp_most(most);
+        least = warp_least(least);
         asm volatile("bar.sync 1, 256;" ::: "memory");  // (the slots' last readers are done)
-        if (lane == 0) most_slots[warp] = most;
+        if (lane == 0) {
+          most_slots[warp] = most;
+          least_slots[warp] = least;
+        }
         asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < 8; ++i) most = fmaxf(most, most_slots[i]);
-        int k2 = 0;
-        if (most > 0.0f) k2 = min(max(14 - ((int)(__float_as_uint(most) >> 23) - 127), -103), 126);
-        const float up = __uint_as_float((uint32_t)(127 + k2) << 23);
+        for (int i = 0; i < 8; i += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(most_slots + i);
+          const float4 b = *reinterpret_cast<const float4*>(least_slots + i);
+          most = fmaxf(most, fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
+          least = fminf(least, fminf(fminf(b.x, b.y), fminf(b.z, b.w)));
+        }
+        const bool wide = far_queries(most, least);
+        const int k_tile = wide ? far_tile_power(most) : query_power(most);
+        const int k_row = wide ? far_row_power(row_most, k_tile) : k_tile;
+        const float up = power_of_two(k_row);
+        units[r] = power_of_two(k_tile - k_row);
         if (r == 0) {
           const HalfTile h1 = half_tile(p, t, 1);  // (this thread's is half 0)
           piece[0] = count;
@@ -622,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           piece[2] = min(max(h.to - off, piece[1]), count);
           piece[3] = min(max(h1.from - off, 0), count);
           piece[4] = min(max(h1.to - off, piece[3]), count);
-          *factor_slot = __uint_as_float((uint32_t)(127 - k2) << 23) * (p.scale * kLog2e / kCodeUnit);
+          units[256] = wide ? 1.0f : 0.0f;
+          *factor_slot = power_of_two(-k_tile) * (p.scale * kLog2e / kCodeUnit);
         }
         const uint32_t dst = sbase + S::kQ + x * S::kTile;
 #pragma unroll
@@ -666,12 +691,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* shifts = state + 8 * 256;
 #pragma unroll
       for (int i = 0; i < 4; ++i) shifts[i * 256] = 0.0f;
-      bool wide = false;  // a row's products take a power of two besides
       bool was_masked = true;  // (and `seen` to be set)
       // The steps before `from` were not waited for: with the first scores there,
       // every earlier step has its scales, so the barrier of a slot of scales is in
       // this step's phase or past it, and its parity says which.
       if (from < upto) warp_wait(s_full(x), n_s);
+      // every step takes the careful form: rows have units of their own, or products
+      // of a row a power of two besides
+      bool wide = state[13 * 256 - threadIdx.x] != 0.0f;
       for (int j = from; j < upto; ++j) {
         const uint32_t slot = (step + j) % kScaleSlots;
         warp_wait(scale_full(slot), (step + j) / kScaleSlots);
@@ -763,8 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 state[(2 + i) * 256] = l[2 * h + i];
               }
               const uint32_t lanes = h ? 16u << 16 : 0u;
-              wide |= careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from,
-                                           seen + 2 * h * 256, state, shifts + 2 * h * 256);
+              wide |= careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from, state, h);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 ref[2 * h + i] = state[i * 256];

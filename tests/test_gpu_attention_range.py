@@ -123,3 +123,38 @@ def test_shares_far_below_the_largest(rows, above):
     o, lse = A.attend(case, q, A.to_torch(cache), pages, table, case[6], scale)
     L.lbgemm_device_status()
     T.check(o, lse, T.attention(q, torch.bfloat16, cache, case[6], case[5], table, scale, True, 0))
+
+
+def check_queries(case, q, scale, seed):
+    dtype, dim, hq, hk, page, rows, lens, causal, window = case
+    cache, table, width, pages, _ = A.attend_inputs(case, seed)
+    o, lse = A.attend(case, q, A.to_torch(cache), pages, table, lens, scale)
+    L.lbgemm_device_status()
+    used = A.U.Cache(cache.pages, page, hk, dim)
+    used.codes, used.scales = cache.codes, np.nan_to_num(cache.scales, nan=0.0, posinf=0.0)
+    T.check(o, lse, T.attention(q, A.U.DTYPES[dtype], used, lens, rows, table, scale, causal, window))
+
+
+@pytest.mark.parametrize("size", [1e36, 3e37, 1e-36])
+@pytest.mark.parametrize("rows,dim", [([1], 128), ([6, 2], 64), ([30], 64), ([90, 300], 128)])
+def test_query_sizes(rows, dim, size):
+    """Queries near the ends of bf16's range, with a scale that makes ordinary scores."""
+    case = (BF16, dim, 4, 2, 16, rows, [700, 400][:len(rows)], True, 0)
+    q = A.rand(7, (sum(rows), 4, dim), BF16, 1.0) * size
+    check_queries(case, q, 2.0 / math.sqrt(dim) / size, 650)
+
+
+@pytest.mark.parametrize("apart", [2.0 ** 16, 2.0 ** 30, 2.0 ** 45, 2.0 ** 90])
+@pytest.mark.parametrize("rows,dim,hq", [([1], 128, 4), ([6, 2], 64, 4), ([30], 64, 8), ([90, 300], 128, 4)])
+def test_queries_beside_larger_ones(rows, dim, hq, apart):
+    """A row is what it is whatever its neighbours are: rows of ordinary size beside
+    some that are far larger, beside zeros, and rows spread over the whole span."""
+    case = (BF16, dim, hq, 2, 16, rows, [700, 400][:len(rows)], True, 0)
+    q = A.rand(8, (sum(rows), hq, dim), BF16, 1.0)
+    q[0, 1] *= apart
+    q[-1, 2] *= 1 / apart
+    q[-1, 0] = 0
+    if sum(rows) > 30:
+        q[5:20] *= apart ** (torch.rand((15, hq, 1), generator=torch.Generator().manual_seed(9)) - 0.5).bfloat16().cuda()
+        q[23] = 0
+    check_queries(case, q, 1.0 / math.sqrt(dim), 651)
