@@ -164,7 +164,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
       }
     }
     const int token = is.base + is_off * kStep + stretch_at;
-    if (stretch_at >= kStep || token >= is.last) return;
+    // (none of it seen: past the last token, or before a window, where the sequence
+    // may have given its pages back)
+    if (stretch_at >= kStep || token >= is.last || token + stretch <= is.first) return;
     const uint32_t group = (uint32_t)token / 16, in_table = p.by_page16(group);
     const int page = __ldg(p.page_table + (int64_t)is.b * p.table_width + in_table);
     if ((uint32_t)page >= (uint32_t)p.cache.pages) {

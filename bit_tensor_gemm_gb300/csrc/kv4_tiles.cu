@@ -486,7 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto find = [&]() {
           codes_off = scales_off = -1;
           const int token = c.t.base + c.off * kStep + lane * 16;
-          if (ahead >= run.count || lane >= 8 || token >= c.t.last) return;
+          // (no row sees any of it: past the last token, or before a window, where the
+          // sequence may have given its pages back)
+          if (ahead >= run.count || lane >= 8 || token >= c.t.last || token + 16 <= c.t.first) return;
           const uint32_t group = (uint32_t)token / 16, in_table = p.by_page16(group);
           const int page = __ldg(p.page_table + (int64_t)c.t.b * p.table_width + in_table);
           if ((uint32_t)page >= (uint32_t)p.cache.pages) {

@@ -616,7 +616,8 @@ lbgemm_status lbgemm_kv4_read(int dtype, int64_t tokens, int64_t heads, int64_t 
  * cu_q[batch] = total_q) and kv_lens[b] cached tokens (int32), the new
  * tokens' own among them (write them first); cached token j is token j %
  * page_size of page page_table[b * table_width + j / page_size] (int32;
- * entries beyond the length are not read).  With n rows and length L, row i
+ * entries of pages of which no row sees a token, beyond the length or before
+ * every window, are not read).  With n rows and length L, row i
  * stands at position L - n + i.  causal != 0: it sees the tokens up to its
  * position, and with window > 0 only the last `window` of them; causal = 0
  * (window must be 0): all L.  A row that sees nothing (an empty cache, a
