@@ -84,27 +84,35 @@ class AttentionLayer:
 
     def step(self, x, cache, new, stream=None):
         """x: bf16 [tokens, model], the new tokens' hidden states, sequence after
-        sequence; new: what cache.extend() gave for them.  Returns [tokens, model]."""
+        sequence; new: what cache.extend() gave for them.  Returns [tokens, model].
+        stream: as lbgemm takes it; what the step allocates, its result among it, then
+        belongs to that stream (torch hands memory out again in the order of the
+        stream that it belongs to)."""
         import torch  # noqa: PLC0415
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), x.device)
+            with torch.cuda.stream(stream):
+                return self.step(x, cache, new)
         tokens, model = x.shape
         hq, hk, dim = self.heads_q, self.heads_kv, self.dim
         width = (hq + 2 * hk) * dim
         joint = torch.empty((tokens, width), dtype=torch.bfloat16, device=x.device)
-        L.lbgemm_linear_quant(tokens, width, model, x, self.qkv, self.qkv_scale, joint, stream)
+        L.lbgemm_linear_quant(tokens, width, model, x, self.qkv, self.qkv_scale, joint)
         q, k, v = joint[:, :hq * dim], joint[:, hq * dim:(hq + hk) * dim], joint[:, (hq + hk) * dim:]
         L.lbgemm_qk_norm_rope(L.BF16, tokens, hq, hk, dim, q, width, k, width, self.q_norm,
                               self.k_norm, self.eps, self.cosines, self.sines,
                               self.cosines.shape[0], new["positions"], 2 * self.cosines.shape[1],
-                              self.interleaved, q, width, k, width, stream)
+                              self.interleaved, q, width, k, width)
         L.lbgemm_kv4_write(L.BF16, tokens, hk, dim, k, width, v, width, new["slots"], cache.buffer,
-                           cache.pages, cache.page_size, stream)
+                           cache.pages, cache.page_size)
         o = torch.empty((tokens, hq * dim), dtype=torch.bfloat16, device=x.device)
         L.lbgemm_kv4_attention(L.BF16, len(cache.lens), tokens, new["max_q"], hq, hk, dim, q, width,
                                new["cu_q"], cache.buffer, cache.pages, cache.page_size,
                                new["table"], cache.width, new["lens"], new["max_kv"], dim ** -0.5,
-                               True, self.window, o, None, stream)
+                               True, self.window, o, None)
         y = torch.empty((tokens, model), dtype=torch.bfloat16, device=x.device)
-        L.lbgemm_linear_quant(tokens, model, hq * dim, o, self.out, self.out_scale, y, stream)
+        L.lbgemm_linear_quant(tokens, model, hq * dim, o, self.out, self.out_scale, y)
         return y
 
 
