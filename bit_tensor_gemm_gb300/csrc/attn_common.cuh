@@ -60,11 +60,6 @@ __device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&f)[8]) {
 }
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  unpack8(load8_raw(p), f);
-}
-
-template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
   Raw8<T> r;
   T* h = reinterpret_cast<T*>(&r);

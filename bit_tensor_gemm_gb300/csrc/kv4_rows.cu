@@ -132,8 +132,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
 
   // ---- copies.  Step s of the run: one copy per piece (keys, values, two
   // arrays of scales: lane % 4) and stretch of tokens that certainly lie in one
-  // page (lane / 4).  Warp s % 4 issues step s + 2 when it begins step s, into
-  // the slot that step s - 1 leaves.
+  // page (lane / 4).  Warp w issues steps w, w + 4, ...: the first ones at once, step
+  // s + 3 when it begins step s, into the slot that step s - 1 leaves.
+  static_assert(kWarps == kStages, "every warp issues one of the first steps");
   const uint32_t ring = smem_addr(smem);
   const int page_size = (int)p.cache.page_size;
   const int stretch =
@@ -184,11 +185,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     if (is_src) bulk_load(piece_dst + slot * Rg::kBytes, is_src, stretch * row_bytes, bar);
   };
   advance(warp);
-  if (warp < kStages) {
-    if (is_step < run.count) issue();
-    // the first step that this warp issues in the loop
-    advance(kWarps);
-  }
+  if (is_step < run.count) issue();
+  advance(kWarps);  // to the first step that this warp issues in the loop
 
   const int eg = (g ^ (g >> 1)) & 1;        // e(g)
   const int tok_a = 2 * g + eg, tok_b = 2 * g + 1 - eg;
@@ -301,7 +299,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
 
     for (int s = done; s < done + piece_steps; ++s) {
       const uint32_t slot = (uint32_t)(s % kStages);
-      if (s > 0 && s + 3 == is_step && !dead) {
+      if (s > 0 && s + kStages - 1 == is_step && !dead) {
         const int old = s - 1;  // the step whose slot this is
         if (is_step < run.count) {
           dead = !mbar_wait(empty + 8 * (old % kStages), (uint32_t)(old / kStages) & 1u, &abort_flag,

@@ -27,8 +27,9 @@
 // PFLOP/s; 7 prompts of up to 1100 tokens, DIM = 64, 138 us.  A step takes 5000
 // cycles: what bounds it is the chain score MMA - weights - value MMA of a half,
 // with one softmax warp of a half on each of the SM's quarters (issue 48 %, MMAs
-// 40 %, exponentials 20 % of their rates); tensor memory is full with two halves'
-// scores and sums, so a third half to fill the gaps has no room.
+// 40 %, exponentials 20 % of their rates); with 128 channels tensor memory is full
+// with two halves' scores and sums, so a third half to fill the gaps has no room
+// (with 64, a quarter of its columns is free).
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ---------------- converters ----------------
-      // Warps 8..11 keys, 12..15 values; the next step's codes are on their way to
+      // Warps 8..11 keys, 13..15 values; the next step's codes are on their way to
       // registers while the MMAs use this one's.
       // Groups of TPL tokens go to the warps in turn; a lane takes 32 codes (16
       // bytes) of a token, the lanes of a phase of 8 different tokens of 8 (no
