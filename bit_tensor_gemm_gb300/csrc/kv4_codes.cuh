@@ -7,16 +7,20 @@
 
 namespace lbg {
 
-// The reference of a row's weights moves when one exceeds kFar, and is set for
-// a largest product of at least kLeastTop.
-constexpr float kFar = 1.2676506e30f;       // 2^100
-constexpr int kLevel = 11;  // the largest product is put at 2^11
+// The reference of a row's weights moves when one exceeds kFar, or a product of a
+// weight and a value scale fp16's range; then
+constexpr float kFar = 1.2676506e30f;  // 2^100
+constexpr int kLevel = 11;             // the largest product is put at 2^11
 // ... by the reference alone where a row's largest product with a value scale is
-// within 2^-63 .. 2^63 of its largest weight; past that the reference stops, so
-// that weights and their sum stay normal fp32 numbers, and products take a power of
-// two of the row besides, in the careful form of a step only.
-constexpr int kSpan = 63;
-constexpr float kSpanLeast = 1.0842022e-19f, kSpanMost = 9.2233720e18f;  // 2^-63, 2^63
+// within 2^-30 .. 2^30 of its largest weight; past that the reference stops, and
+// products take a power of two of the row besides, in the careful form of a step
+// only.  So weights and sums of one row never stand more than 2^60 apart for their
+// values' sake, wherever they are brought to one reference, and stay normal fp32
+// numbers.  The same where scores are too large (kFarScore) for a reference that is
+// a few binades beside them.
+constexpr int kSpan = 30;
+constexpr float kSpanLeast = 9.3132257e-10f, kSpanMost = 1.0737418e9f;  // 2^-30, 2^30
+constexpr float kFarScore = 4194304.0f;                                  // 2^22: ulps of 1/2
 
 __device__ __forceinline__ float power_of_two(int e) {  // of a normal number
   return __uint_as_float((uint32_t)(127 + e) << 23);

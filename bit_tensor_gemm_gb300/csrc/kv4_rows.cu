@@ -37,11 +37,16 @@
 namespace lbg {
 namespace {
 
-// The power of two that a row's products take besides its reference, from its
-// largest product over its largest weight: 0 within the span, -64 .. 63 past it.
-__device__ __forceinline__ int top_shift(float top) {
-  const int e = (int)(__float_as_uint(top) >> 23) - 127;
-  return top > 0.0f ? min(max(min(max(e, -kSpan), kSpan) - e, -64), 63) : 0;
+// By what power of two a row's largest product is to be multiplied for its level,
+// 2^(kLevel - 1) .. 2^kLevel, where `top` is that product over its largest weight.
+__device__ __forceinline__ int to_level(float top) {
+  return kLevel - 1 - ((int)(__float_as_uint(top) >> 23) - 127);
+}
+// What its products take besides its reference, which is `below` its largest score
+// (of a row within the span to_level, but for scores that are too large to hold
+// it): an even number, -126 .. 126.
+__device__ __forceinline__ int top_shift(float below, float top) {
+  return top > 0.0f ? min(max((to_level(top) - __float2int_rn(below)) & ~1, -126), 126) : 0;
 }
 
 constexpr int kWarps = 4, kStages = 4, kTokens = 32, kStep = kStepTokens;
@@ -278,11 +283,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
     // channel in which every larger product has code 0 keeps what lies above
     // 2^-34 of the row's largest.)
     // m, wtop: the largest score, and the largest product relative to 2^m.
-    // shifts: the columns' top_shift in force, 7 bits each, and own_units; where it
-    // is not 0, every step takes the careful form.
+    // shifts: halves of the columns' top_shift in force, 7 bits each, and own_units;
+    // where it is not 0, every step takes the careful form.
     constexpr uint32_t kOwnUnits = 1u << 28;
     uint32_t shifts = own_units ? kOwnUnits : 0;
-    auto shift_of = [&](int nt, int e) { return (int)(shifts << (25 - 7 * (2 * nt + e))) >> 25; };
+    auto shift_of = [&](int nt, int e) { return (int)(shifts << (25 - 7 * (2 * nt + e))) >> 25 << 1; };
     float o[MT][NT][4], ref[NT][2], l[NT][2], m[NT][2], wtop[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -418,6 +423,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
             ks[0][0] = ks[0][1] = ks[1][0] = ks[1][1] = 1.0f;
           }
           bool far = shifts != 0;  // a row whose products take a power of two besides
+          float down[NT][2];       // by how many binades each row's reference falls
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -433,11 +439,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
               for (int x = 4; x <= 16; x <<= 1)
                 high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, x));
-              float top = wtop[nt][e] * ex2(m[nt][e] - high);
+              // (by square roots of the weights: a weight itself is 0 below 2^-126, its
+              // product with a large scale may yet be the largest)
+              float root = ex2(0.5f * (m[nt][e] - high));
+              float top = wtop[nt][e] * root * root;
               const float before = top;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)  // (a NaN is passed over)
-                top = fmaxf(top, fabsf(ex2(t4[i] - high) * vs[i / 2][i & 1]));
+              for (int i = 0; i < 4; ++i) {  // (a NaN is passed over)
+                root = ex2(0.5f * (t4[i] - high));
+                top = fmaxf(top, fabsf(root * vs[i / 2][i & 1] * root));
+              }
 #pragma unroll
               for (int x = 4; x <= 16; x <<= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -445,20 +456,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
               const float lead = fminf(fmaxf(top, kSpanLeast), kSpanMost);
               far |= top != lead && top > 0.0f;
               // (the eight lanes of a column agree on all of this)
-              if (high > m[nt][e] || top > before) {
-                // 2^(high - next) top = 2^(kLevel - 1) .. 2^kLevel, within the span
-                next = high - (float)(kLevel - 1 - ((int)(__float_as_uint(lead) >> 23) - 127));
-              }
+              if (high > m[nt][e] || top > before) next = high - (float)to_level(lead);
               m[nt][e] = high;
               wtop[nt][e] = top;
-              const float f = ex2(ref[nt][e] - next);
+              down[nt][e] = ref[nt][e] - next;
               ref[nt][e] = next;
-              l[nt][e] *= f;
-#pragma unroll
-              for (int i = 0; i < MT; ++i) {
-                o[i][nt][e] *= f;
-                o[i][nt][2 + e] *= f;
-              }
+              l[nt][e] *= ex2(down[nt][e]);
               part[nt][e] = 0.0f;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -468,27 +471,36 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
                 acc[i / 2][nt][(i & 1) * 2 + e] = t4[i] == -INFINITY ? 0.0f : w * vs[i / 2][i & 1];
               }
             }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) far |= fabsf(m[nt][e]) >= kFarScore && wtop[nt][e] > 0.0f;
           if (__any_sync(0xffffffffu, far)) {
             uint32_t next_shifts = shifts & kOwnUnits;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int shift = top_shift(wtop[nt][e]);
-                next_shifts |= (uint32_t)(shift & 127) << 7 * (2 * nt + e);
-                // (o does not grow by this and f together: what was the largest
-                // product is not more now)
-                const float f = power_of_two(min(max(shift - shift_of(nt, e), -126), 126));
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                  o[i][nt][e] *= f;
-                  o[i][nt][2 + e] *= f;
-                }
+                const int shift = top_shift(m[nt][e] - ref[nt][e], wtop[nt][e]);
+                next_shifts |= (uint32_t)(shift >> 1 & 127) << 7 * (2 * nt + e);
+                // (o hardly grows: what was the largest product is not more now)
+                down[nt][e] = fminf(down[nt][e] + (float)(shift - shift_of(nt, e)), 100.0f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[i / 2][nt][(i & 1) * 2 + e] *= power_of_two(shift);
               }
             shifts = next_shifts;
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float f = ex2(down[nt][e]);
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                o[i][nt][e] *= f;
+                o[i][nt][2 + e] *= f;
+              }
+            }
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -558,7 +570,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
           for (int i = 1; i < kWarps; ++i) all = fmaxf(all, merge_ref[i][r]);
           const float f =
-              ex2(ref[nt][e] - all) * (1.0f / kCodeUnit) * power_of_two(-shift_of(nt, e));
+              ex2(ref[nt][e] - all) * power_of_two(-shift_of(nt, e));
           float2* dst = reinterpret_cast<float2*>(mo + r * ROW + 2 * g);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
@@ -592,7 +604,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 3 : 2)
       const float2 x = *reinterpret_cast<const float2*>(src);
       const float2 y = *reinterpret_cast<const float2*>(src + 16);
       const bool none = sum == 0.0f;
-      const float inv = none ? 0.0f : 1.0f / sum;
+      const float inv = none ? 0.0f : (1.0f / kCodeUnit) / sum;
       const float lse = none ? -INFINITY : all + log2f(sum);
       if (whole) {
         const int64_t at = out_row(p, t, head, t.r0 + r);

@@ -248,22 +248,37 @@ __device__ __noinline__ bool careful_weights(uint32_t ts, uint32_t to, const flo
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       sum += __shfl_xor_sync(0xffffffffu, sum, d);
     }
+    float over = top - high;  // the largest product over the largest weight
+    if (__any_sync(0xffffffffu, fabsf(high) >= kFarScore && top > -INFINITY)) {
+      // (a score of this size drops its scale's logarithm)
+      over = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const float v = fabsf(ks[kStep + n / 2 * 8 + n % 2]);
+        if (v < INFINITY && s8[n] > -INFINITY) over = fmaxf(over, s8[n] - high + __log2f(v));
+      }
+#pragma unroll
+      for (int d = 1; d < 4; d *= 2) over = fmaxf(over, __shfl_xor_sync(0xffffffffu, over, d));
+    }
     float ref = rf, next_shift = shift;
-    if (rf == kNoRef || top - rf + shift > 14.9f) {
+    if (rf == kNoRef || high - rf + over + shift > 14.9f) {
       // The largest product to its level, by the reference as far as kSpan allows
       // it beside the largest weight (of what is there: at most its sum).
       const float most = rf == kNoRef ? high : fmaxf(high, rf + __log2f(sum));
       const float level = rf == kNoRef ? (float)kFirstLevel : (float)kLevel;
-      const float over = fminf(top, 3.0e38f) - most;
-      const float follow = top > -INFINITY ? fminf(fmaxf(over, -(float)kSpan), (float)kSpan) : 0.0f;
-      const float need = follow == over ? top - level : most + follow - level;
-      if (rf != kNoRef) ref = rf + ceilf(need - rf);  // (binades: what is there scales exactly)
-      else if (high > -INFINITY) ref = need;
-      next_shift = follow == over || top == -INFINITY ? 0.0f : fminf(rintf(follow - over), 100.0f);
+      over += high - most;
+      const float follow = over > -INFINITY ? fminf(fmaxf(over, -(float)kSpan), (float)kSpan) : 0.0f;
+      const bool huge = fabsf(most) >= kFarScore;
+      const float need = huge ? most : most + follow - level;
+      if (high > -INFINITY)  // (by binades, where it has moved: what is there scales exactly)
+        ref = huge || rf == kNoRef ? need : rf + ceilf(need - rf);
+      next_shift = over > -INFINITY
+                       ? fminf(fmaxf(rintf(huge ? level - over : follow - over), -126.0f), 100.0f)
+                       : 0.0f;
     } else if (high - rf > 99.0f) {
       // weights out of range, products not: these stay where they are
-      ref = rf + ceilf(high - kSpan - rf);
-      next_shift = fminf(shift + (ref - rf), 100.0f);
+      ref = fabsf(high) >= kFarScore ? high : rf + ceilf(high - kSpan - rf);
+      next_shift = fminf(shift + rintf(ref - rf), 100.0f);
     }
     const float fl = rf == kNoRef ? 0.0f : ex2(rf - ref);
     f[i] = rf == kNoRef ? 0.0f : ex2(rf - ref + (next_shift - shift));
@@ -836,12 +851,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      // (columns are in units of kCodeUnit; first the sum, which brings them into range)
       const float unit = ex2(-(reinterpret_cast<const float*>(smem + S::kState) + 8 * 256)
-                                  [lane / 8 * 256 + threadIdx.x - lane + 4 * (lane % 8)]) *
-                         (1.0f / kCodeUnit);
+                                  [lane / 8 * 256 + threadIdx.x - lane + 4 * (lane % 8)]);
       const bool none = l_row == 0.0f;
-      const float inv = none ? 0.0f : 1.0f / l_row;
+      const float inv = none ? 0.0f : (1.0f / kCodeUnit) / l_row;
       const float lse = none ? -INFINITY : ref_row + log2f(l_row);
       if (upto > from) {
         warp_wait(o_full(x), n_o++);

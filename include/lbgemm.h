@@ -632,7 +632,8 @@ lbgemm_status lbgemm_kv4_read(int dtype, int64_t tokens, int64_t heads, int64_t 
  * O: [total_q, heads_q, head_dim] of dtype; lse: fp32 [total_q, heads_q],
  * natural logarithm, or NULL.  A product of a weight and a value scale is rounded
  * to fp16: by 2^-11 of itself or 2^-30 of a row's largest one, whichever is more,
- * whatever size the scales have; scores, sums of weights and outputs are fp32.
+ * whatever size the scales have; scores, sums of weights and outputs are fp32, and
+ * a weight below 2^-100 of a row's largest may count as 0.
  * Scratch for partial results of a cut cache is taken as in lbgemm_run. */
 lbgemm_status lbgemm_kv4_attention(int dtype, int64_t batch, int64_t total_q, int64_t max_q,
                                    int64_t heads_q, int64_t heads_kv, int64_t head_dim,

@@ -23,9 +23,10 @@ ROUND = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 LEAST = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25}
 
 
-def attention(q, dtype, cache, lens, rows, table, scale, causal, window):
+def attention(q, dtype, cache, lens, rows, table, scale, causal, window, lost=0.0):
     """q [total, heads_q, dim]; cache: attention_util.Cache.  Returns o, lse and
-    what each may be off by, in fp64."""
+    what each may be off by, in fp64; weights below `lost` of a row's largest may
+    count as 0."""
     q = q.double()
     dev, (total, hq, dim) = q.device, q.shape
     hk, page = cache.heads, cache.page
@@ -61,6 +62,8 @@ def attention(q, dtype, cache, lens, rows, table, scale, causal, window):
                 sums = (length / 128 + 60) * 2.0 ** -24
                 e = (ROUND[dtype] * y.abs() + (2.0 ** -11 + 2 * dt + sums) * spread +
                      seen.sum(-1)[:, None] * least + LEAST[dtype])
+                if lost:
+                    e += torch.where(p < lost * p.amax(-1, keepdim=True), p, 0.0) @ v.abs()
                 o[first:first + n, heads] = y.transpose(0, 1)
                 tol[first:first + n, heads] = e.transpose(0, 1)
                 lse[first:first + n, heads] = z[..., 0].T

@@ -158,3 +158,49 @@ def test_queries_beside_larger_ones(rows, dim, hq, apart):
         q[5:20] *= apart ** (torch.rand((15, hq, 1), generator=torch.Generator().manual_seed(9)) - 0.5).bfloat16().cuda()
         q[23] = 0
     check_queries(case, q, 1.0 / math.sqrt(dim), 651)
+
+
+FAR = 2.0 ** -100  # weights below that of a row's largest may count as 0
+SHAPES = [
+    (64, 8, 8, [1] * 30, [66] * 30, True, 0), (64, 14, 2, [8, 6], [280, 260], False, 0),
+    (128, 8, 2, [3] * 20, [35] * 20, True, 0), (64, 12, 3, [90] * 10, [300] * 10, True, 33),
+    (128, 6, 3, [278, 90], [285, 100], True, 0), (64, 32, 8, [146, 299], [12, 40], False, 0),
+    (128, 14, 2, [2, 1, 5], [700, 33, 300], True, 50)]
+
+
+@pytest.mark.parametrize("spread", [40, 80])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("keys", [0, 2])
+def test_value_scales_over_the_whole_range(shape, spread, keys):
+    """Value scales 2^(40 x) and 2^(80 x), x normal, under scores of ordinary and of
+    large size: tokens with tiny weights decide rows, one at a time."""
+    dim, hq, hk, rows, lens, causal, window = shape
+    case = (BF16, dim, hq, hk, 16, rows, lens, causal, window)
+    cache, table, width, pages, q = A.attend_inputs(case, 660, junk=False)
+    rng = np.random.default_rng(spread + keys)
+    cache.scales[1] = A.U.bf16_round(2.0 ** np.clip(rng.normal(0, spread, cache.scales[1].shape), -126, 120))
+    if keys:
+        cache.scales[0] = A.U.bf16_round(2.0 ** rng.normal(0, keys, cache.scales[0].shape))
+    for scale in (0.01, 0.125, 1.0):
+        o, lse = A.attend(case, q, A.to_torch(cache), pages, table, lens, scale)
+        L.lbgemm_device_status()
+        T.check(o, lse, T.attention(q, torch.bfloat16, cache, lens, rows, table, scale, causal, window, FAR))
+
+
+@pytest.mark.parametrize("what", ["keys", "queries", "both"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_scores_past_the_ulp_of_a_binade(shape, what):
+    """Scores from 1e6 to 1e30, where fp32 numbers are more than a binade's exponent
+    apart: one token has a row's weight, and the row is its value."""
+    dim, hq, hk, rows, lens, causal, window = shape
+    case = (BF16, dim, hq, hk, 16, rows, lens, causal, window)
+    cache, table, width, pages, q = A.attend_inputs(case, 661, junk=False)
+    rng = np.random.default_rng(3)
+    if what != "queries":
+        cache.scales[0] = A.U.bf16_round(2.0 ** rng.normal(0, 7, cache.scales[0].shape))
+    if what != "keys":
+        q = q * (2.0 ** torch.from_numpy(np.clip(rng.normal(0, 20, (*q.shape[:2], 1)), -60, 70)).cuda()).bfloat16()
+    for scale in (0.01, -1.0):
+        o, lse = A.attend(case, q, A.to_torch(cache), pages, table, lens, scale)
+        L.lbgemm_device_status()
+        T.check(o, lse, T.attention(q, torch.bfloat16, cache, lens, rows, table, scale, causal, window, FAR))
