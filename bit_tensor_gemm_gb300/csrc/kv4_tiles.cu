@@ -146,6 +146,7 @@ struct Const {
 
 constexpr int kFirstLevel = 5;
 constexpr float kNoRef = -3.0e38f;  // the reference of a row that has seen nothing
+constexpr float kGone = 1000.0f;    // binades after which nothing is left of a weight
 
 // 16 bytes that this SM reads once: past the L1, which is small beside this much
 // shared memory.
@@ -270,14 +271,17 @@ __device__ __noinline__ bool careful_weights(uint32_t ts, uint32_t to, const flo
       const float follow = over > -INFINITY ? fminf(fmaxf(over, -(float)kSpan), (float)kSpan) : 0.0f;
       const bool huge = fabsf(most) >= kFarScore;
       const float need = huge ? most : most + follow - level;
-      if (high > -INFINITY)  // (by binades, where it has moved: what is there scales exactly)
-        ref = huge || rf == kNoRef ? need : rf + ceilf(need - rf);
+      // (by binades, so that what is there scales exactly; not where that is gone)
+      if (high > -INFINITY)
+        ref = huge || rf == kNoRef || need - rf > kGone ? need : rf + ceilf(need - rf);
       next_shift = over > -INFINITY
                        ? fminf(fmaxf(rintf(huge ? level - over : follow - over), -126.0f), 100.0f)
                        : 0.0f;
     } else if (high - rf > 99.0f) {
       // weights out of range, products not: these stay where they are
-      ref = fabsf(high) >= kFarScore ? high : rf + ceilf(high - kSpan - rf);
+      ref = fabsf(high) >= kFarScore ? high
+            : high - rf > kGone      ? high - kSpan
+                                     : rf + ceilf(high - kSpan - rf);
       next_shift = fminf(shift + rintf(ref - rf), 100.0f);
     }
     const float fl = rf == kNoRef ? 0.0f : ex2(rf - ref);

@@ -204,3 +204,31 @@ def test_scores_past_the_ulp_of_a_binade(shape, what):
         o, lse = A.attend(case, q, A.to_torch(cache), pages, table, lens, scale)
         L.lbgemm_device_status()
         T.check(o, lse, T.attention(q, torch.bfloat16, cache, lens, rows, table, scale, causal, window, FAR))
+
+
+@pytest.mark.parametrize("size", [2.0 ** 24, 2.0 ** 27, 2.0 ** 30])
+@pytest.mark.parametrize("rows,dim,first", [([1], 128, 20), ([6, 2], 64, 33), ([90, 300], 128, 1), ([70], 64, 64)])
+def test_lesser_scores_after_huge_negative_ones(rows, dim, first, size):
+    """Rows whose first tokens have scores of some -2 `size`: what comes after them,
+    scores of some thousands, sets the row as if they were not there."""
+    lens = [700, 400][:len(rows)]
+    case = (BF16, dim, 4, 2, 16, rows, lens, True, 0)
+    cache, table, width, pages, q = A.attend_inputs(case, 662, junk=False)
+    j = np.arange(first)
+    q[..., 0] = 4
+    cache.scales[0] = A.U.bf16_round(cache.scales[0] * 1000)
+    for b in range(len(rows)):
+        at = table[b, j // 16], j % 16
+        cache.codes[0][at] = 0
+        cache.codes[0][at[0], at[1], :, 0] = -7
+        cache.scales[0][at] = A.U.bf16_round(size)
+    scale = 1 / math.sqrt(dim)
+    o, lse = A.attend(case, q, A.to_torch(cache), pages, table, lens, scale)
+    L.lbgemm_device_status()
+    # their own tokens' scores do not count in the bounds: nothing is left of them
+    kept = A.U.Cache(cache.pages, 16, 2, dim)
+    kept.codes, kept.scales = cache.codes, cache.scales.copy()
+    for b in range(len(rows)):
+        kept.codes[0][table[b, j // 16], j % 16, :, 0] = -7
+        kept.scales[0][table[b, j // 16], j % 16] = 2.0 ** 14
+    T.check(o, lse, T.attention(q, torch.bfloat16, kept, lens, rows, table, scale, True, 0, FAR))
