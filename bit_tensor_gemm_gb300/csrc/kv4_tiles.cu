@@ -201,38 +201,146 @@ __device__ __forceinline__ HalfTile half_tile(const Kv4AttnParams& p, const RowT
   return h;
 }
 
+// What shared memory has of a softmax thread's four rows beside its registers, in
+// arrays 256 floats apart: [2] ref and [2] l of the two rows at hand; of all four [4]
+// the tokens of the step that the row sees (from the low half to the high half) and
+// [4] the exponents of the powers of two that its products take besides (kSpan);
+// then [256] the tile's rows' own units of the scores, and whether these are in use.
+__device__ __forceinline__ uint32_t row_sees(const float* state, int row) {
+  return reinterpret_cast<const uint32_t*>(state + 4 * 256)[row * 256];
+}
+
+// Where a reference has moved: the sums (at `to`, when they hold anything: S of this
+// step was committed after O += P V of the step before) and this step's weights so
+// far, `q` chunks, times f.
+template <int DIM>
+__device__ __forceinline__ void follow_reference(uint32_t ts, uint32_t to, int q, bool sums,
+                                                 const float (&f)[2]) {
+  tmem_st_wait();
+  if (sums) {
+#pragma unroll 1
+    for (int n = 0; n < DIM / 32; ++n) {
+      uint32_t v[16];
+      tmem_ld_16x32(to + 32 * n, v);
+      tmem_ld_wait_for(v);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f[k / 2 % 2]);
+      tmem_st_16x32(to + 32 * n, v);
+    }
+  }
+#pragma unroll 1
+  for (int n = 0; n < q; ++n) {
+    uint32_t v[8];
+    tmem_ld_16x16h(ts + 16 * n, v);
+    tmem_ld_wait_for(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {  // (in fp32: a factor may be below fp16's range)
+      const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
+      v[k] = pack_f16(w.x * f[k % 2], w.y * f[k % 2]);
+    }
+    tmem_st_16x16h(ts + 16 * n, v);
+  }
+}
+
 // The careful form of the weights of 32 tokens (chunk q of the step) and two of a
-// thread's rows, 16 TMEM lanes, whose S begins at `ts` (warp-uniform call).
-// ks: the chunk's scales of this thread's first columns.  state: what shared memory
-// has of this thread's rows (h: rows 2 h, 2 h + 1 of four), in arrays 256 floats
-// apart: [2] ref and [2] l of the two; [4] of all the tokens of the step that the
-// row sees (from the low half to the high half) and [4] the exponents of the powers
-// of two that its products take besides (kSpan); then [256] the tile's rows' own
-// units of the scores, and whether these are in use.  Where a reference or such a
-// power moves, the sums (at `to`, when they hold anything: S of this step was
-// committed after O += P V of the step before) and this step's weights so far
-// follow.  True where the next step needs this form too.  A function of its own, so
-// that its registers are not the loop's.
+// thread's rows, 2 h and 2 h + 1, 16 TMEM lanes, whose S begins at `ts`
+// (warp-uniform call); ks: the chunk's scales of this thread's first columns.  True,
+// with nothing done, where one of the warp's rows is too far from the ordinary for it
+// (far_weights).  Both are functions of their own, so that their registers are not
+// the loop's, and apart from one another, as every tile begins with this one.
 template <int DIM>
 __device__ __noinline__ bool careful_weights(uint32_t ts, uint32_t to, const float* ks, int q,
                                              bool sums, float* state, int h) {
   const int c4 = threadIdx.x % 4;
-  const uint32_t* seen_at = reinterpret_cast<const uint32_t*>(state + (4 + 2 * h) * 256);
-  float* shifts = state + (8 + 2 * h) * 256;
-  const float* units = state + 12 * 256 - threadIdx.x % 32 + threadIdx.x % 32 / 4 + 16 * h;
-  float f[2];
-  bool wide = state[13 * 256 - threadIdx.x] != 0.0f;
-  bool moved = false;
+  float s8[2][8], ref[2], f[2];
+  bool moved = false, far = state[13 * 256 - threadIdx.x] != 0.0f;
   uint32_t sv[16], pw[8];
   tmem_ld_16x32(ts + 32 * q, sv);
   tmem_ld_wait_for(sv);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t seen = seen_at[i * 256];
+    const uint32_t seen = row_sees(state, 2 * h + i);
+    const int upto = (int)(seen >> 16) - 32 * q - 2 * c4, from = (int)(seen & 0xffffu) - 32 * q - 2 * c4;
+    const float rf = state[i * 256];
+    float high = -INFINITY, top = -INFINITY;  // of t; of log2 |2^t vs|
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const int token = n / 2 * 8 + n % 2;
+      const bool see = token < upto && token >= from;
+      s8[i][n] = see ? __uint_as_float(sv[n / 2 * 4 + i * 2 + n % 2]) * ks[token] : -INFINITY;
+      high = fmaxf(high, s8[i][n]);
+      const float v = fabsf(ks[kStep + token]);
+      if (see && v < INFINITY) top = fmaxf(top, s8[i][n] + __log2f(v));
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2) {  // (the four lanes of a row agree)
+      high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
+    ref[i] = rf;
+    if (high > -INFINITY) {
+      // products past the span of the weights (below it, weights just grow), scores
+      // or a reference too large to be a few binades apart, weights out of range
+      const float over = top - high;
+      far |= !(over <= (float)kSpan && over >= -75.0f) || fabsf(high) >= kFarScore;
+      if (rf == kNoRef) {
+        ref[i] = top - kFirstLevel;
+      } else {
+        far |= fabsf(rf) >= kFarScore || high - rf > 99.0f;
+        if (top - rf > 14.9f) ref[i] = rf + ceilf(top - kLevel - rf);  // (binades: an exact factor)
+      }
+    }
+    far |= state[(8 + 2 * h + i) * 256] != 0.0f;
+    f[i] = rf == kNoRef ? 0.0f : ex2(rf - ref[i]);
+    moved |= rf != kNoRef && ref[i] != rf;
+  }
+  if (__any_sync(0xffffffffu, far)) return true;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float total = 0.0f;
+#pragma unroll
+    for (int n = 0; n < 8; n += 2) {
+      float w2[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float pj = ex2(s8[i][n + e] - ref[i]);
+        const bool see = s8[i][n + e] != -INFINITY;
+        total += see ? pj : 0.0f;
+        // what a row does not see has weight 0 whatever its scale
+        w2[e] = see ? pj * ks[kStep + n / 2 * 8 + e] : 0.0f;
+      }
+      pw[n + i] = pack_f16(w2[0], w2[1]);
+    }
+    state[i * 256] = ref[i];
+    state[(2 + i) * 256] = state[(2 + i) * 256] * f[i] + total;
+  }
+  tmem_st_16x16h(ts + 16 * q, pw);
+  if (__any_sync(0xffffffffu, moved)) follow_reference<DIM>(ts, to, q, sums, f);
+  return false;
+}
+
+// The same for rows of every kind: the largest product goes to its level by the
+// reference as far as kSpan allows it beside the largest weight, past that by a
+// power of two of the row; scores are in units of the rows' own.  True where a row's
+// next step needs this form again.
+template <int DIM>
+__device__ __noinline__ bool far_weights(uint32_t ts, uint32_t to, const float* ks, int q,
+                                         bool sums, float* state, int h) {
+  const int c4 = threadIdx.x % 4;
+  float* shifts = state + (8 + 2 * h) * 256;
+  const float* units = state + 12 * 256 - threadIdx.x % 32 + threadIdx.x % 32 / 4 + 16 * h;
+  float f[2];
+  bool moved = false, wide = state[13 * 256 - threadIdx.x] != 0.0f;
+  uint32_t sv[16], pw[8];
+  tmem_ld_16x32(ts + 32 * q, sv);
+  tmem_ld_wait_for(sv);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t seen = row_sees(state, 2 * h + i);
     const int upto = (int)(seen >> 16) - 32 * q - 2 * c4, from = (int)(seen & 0xffffu) - 32 * q - 2 * c4;
     const float rf = state[i * 256], shift = shifts[i * 256], unit = units[i * 8];
-    float sum = state[(2 + i) * 256];  // this lane's columns only
-    float high = -INFINITY, top = -INFINITY;  // of t; of log2 |2^t vs|
+    float sum = state[(2 + i) * 256];            // this lane's columns only
+    float high = -INFINITY, over = -INFINITY;  // of t; of log2 |2^(t - high) vs|
     float s8[8];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
@@ -240,31 +348,22 @@ __device__ __noinline__ bool careful_weights(uint32_t ts, uint32_t to, const flo
       const bool see = token < upto && token >= from;
       s8[n] = see ? __uint_as_float(sv[n / 2 * 4 + i * 2 + n % 2]) * ks[token] * unit : -INFINITY;
       high = fmaxf(high, s8[n]);
-      const float v = fabsf(ks[kStep + token]);
-      if (see && v < INFINITY) top = fmaxf(top, s8[n] + __log2f(v));
     }
 #pragma unroll
-    for (int d = 1; d < 4; d *= 2) {  // (the four lanes of a row agree)
+    for (int d = 1; d < 4; d *= 2) {
       high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, d));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       sum += __shfl_xor_sync(0xffffffffu, sum, d);
     }
-    float over = top - high;  // the largest product over the largest weight
-    if (__any_sync(0xffffffffu, fabsf(high) >= kFarScore && top > -INFINITY)) {
-      // (a score of this size drops its scale's logarithm)
-      over = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const float v = fabsf(ks[kStep + n / 2 * 8 + n % 2]);
-        if (v < INFINITY && s8[n] > -INFINITY) over = fmaxf(over, s8[n] - high + __log2f(v));
-      }
-#pragma unroll
-      for (int d = 1; d < 4; d *= 2) over = fmaxf(over, __shfl_xor_sync(0xffffffffu, over, d));
+    for (int n = 0; n < 8; ++n) {
+      const float v = fabsf(ks[kStep + n / 2 * 8 + n % 2]);
+      if (v < INFINITY && s8[n] > -INFINITY) over = fmaxf(over, s8[n] - high + __log2f(v));
     }
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2) over = fmaxf(over, __shfl_xor_sync(0xffffffffu, over, d));
     float ref = rf, next_shift = shift;
     if (rf == kNoRef || high - rf + over + shift > 14.9f) {
-      // The largest product to its level, by the reference as far as kSpan allows
-      // it beside the largest weight (of what is there: at most its sum).
+      // (the largest weight of what is there is at most its sum)
       const float most = rf == kNoRef ? high : fmaxf(high, rf + __log2f(sum));
       const float level = rf == kNoRef ? (float)kFirstLevel : (float)kLevel;
       over += high - most;
@@ -295,12 +394,10 @@ __device__ __noinline__ bool careful_weights(uint32_t ts, uint32_t to, const flo
       float w2[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int token = n / 2 * 8 + e;
-        const bool see = token < upto && token >= from;
         const float pj = ex2(s8[n + e] - ref);
+        const bool see = s8[n + e] != -INFINITY;
         total += see ? pj : 0.0f;
-        // what a row does not see has weight 0 whatever its scale
-        w2[e] = see ? pj * ks[kStep + token] * power : 0.0f;
+        w2[e] = see ? pj * ks[kStep + n / 2 * 8 + e] * power : 0.0f;
       }
       pw[n + i] = pack_f16(w2[0], w2[1]);
     }
@@ -309,31 +406,7 @@ __device__ __noinline__ bool careful_weights(uint32_t ts, uint32_t to, const flo
     shifts[i * 256] = next_shift;
   }
   tmem_st_16x16h(ts + 16 * q, pw);
-  if (!__any_sync(0xffffffffu, moved)) return wide;
-  tmem_st_wait();
-  if (sums) {
-#pragma unroll 1
-    for (int n = 0; n < DIM / 32; ++n) {
-      uint32_t v[16];
-      tmem_ld_16x32(to + 32 * n, v);
-      tmem_ld_wait_for(v);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f[k / 2 % 2]);
-      tmem_st_16x32(to + 32 * n, v);
-    }
-  }
-#pragma unroll 1
-  for (int n = 0; n < q; ++n) {
-    uint32_t v[8];
-    tmem_ld_16x16h(ts + 16 * n, v);
-    tmem_ld_wait_for(v);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {  // (in fp32: a factor may be below fp16's range)
-      const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
-      v[k] = pack_f16(w.x * f[k % 2], w.y * f[k % 2]);
-    }
-    tmem_st_16x16h(ts + 16 * n, v);
-  }
+  if (__any_sync(0xffffffffu, moved)) follow_reference<DIM>(ts, to, q, sums, f);
   return wide;
 }
 
@@ -812,7 +885,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 state[(2 + i) * 256] = l[2 * h + i];
               }
               const uint32_t lanes = h ? 16u << 16 : 0u;
-              wide |= careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from, state, h);
+              if (careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from, state, h))
+                wide |= far_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from, state, h);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 ref[2 * h + i] = state[i * 256];
