@@ -20,8 +20,10 @@ namespace {
 // Rows of a sequence (query tokens x heads of a group) up to which the kernel
 // for few rows runs: it streams the cache once for every 16 of them (from L2, but
 // for the first), the other works for 256 rows whatever there are.  16 sequences
-// of up to 8192 tokens: 64 rows 79 us with the one, 88 with the other, 96 rows
-// 154 and 96; one sequence of 4096: 64 rows 17.3 and 27.7, 96 rows 22.6 and 28.6.
+// of up to 8192 tokens: 64 rows 82 us with the one, 92 with the other, 96 rows
+// 162 and 100; one sequence of 4096: 64 rows 17.9 and 29.1, 96 rows 23.8 and 30.0
+// (a single sequence would do better with the first up to 128 rows: the threshold is
+// one that a batch does not lose by).
 constexpr int64_t kFewRows = 64;
 
 // Joins the shares of a tile's row: with share c's o_c and lse_c (log2),
@@ -156,7 +158,7 @@ cudaError_t launch_join(const Kv4AttnParams& p, cudaStream_t s) {
   return p.cache.dim == 64 ? launch_join_dim<T, 64>(p, s) : launch_join_dim<T, 128>(p, s);
 }
 
-// (8 rows of those 16 sequences 31 us; 9 to 16, which need twice the MMAs, 49)
+// (8 rows of those 16 sequences 32 us; 9 to 16, which need twice the MMAs, 50)
 int tile_rows_of(int64_t rows) { return rows <= 8 ? 8 : rows <= kFewRows ? 16 : 256; }
 
 }  // namespace

@@ -19,8 +19,8 @@
 // end.  The warps issue the copies in turn.  Three CTAs an SM with four stages
 // (16 rows: two): with four CTAs of three stages, which left 128 registers and
 // spilled, 131072 tokens took 44.4 us, 41.4 so.
-// Measured: one row group over 131072 tokens of 8 heads (138 MB) 41.9 us, 3.3
-// TB/s; 64 sequences of up to 8192 tokens (296 MB) 82 us, 3.6 TB/s.  In there,
+// Measured: one row group over 131072 tokens of 8 heads (138 MB) 42.8 us, 3.2
+// TB/s; 64 sequences of up to 8192 tokens (296 MB) 83 us, 3.6 TB/s.  In there,
 // by clock: 7.4 us until the first tokens are worked on (finding the run, the
 // pages, the queries: all first passes through their instructions), 1.5 us a
 // step of an SM's three CTAs (5.1 TB/s; each instruction waits for the one

@@ -23,8 +23,8 @@
 // which is why both scales stay factors of columns, the weights need no maximum
 // (the reference moves only when a product with a value scale leaves fp16's
 // range, as in kv4_rows.cu), and arithmetic goes in pairs (f32x2).
-// Measured: 4096 queries of 32 heads over 16384 tokens (962 GFLOP) 1.01 ms, 0.95
-// PFLOP/s; 7 prompts of up to 1100 tokens, DIM = 64, 138 us.  A step takes 5000
+// Measured: 4096 queries of 32 heads over 16384 tokens (962 GFLOP) 1.02 ms, 0.94
+// PFLOP/s; 7 prompts of up to 1100 tokens, DIM = 64, 139 us.  A step takes 5000
 // cycles: what bounds it is the chain score MMA - weights - value MMA of a half,
 // with one softmax warp of a half on each of the SM's quarters (issue 48 %, MMAs
 // 40 %, exponentials 20 % of their rates); with 128 channels tensor memory is full
@@ -772,8 +772,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // those at 2^5, and moves (up, by whole binades, so that what is there scales
       // exactly) when one exceeds 2^15, or a weight 2^100, which then goes to 2^11:
       // fp16 rounds them by 2^-11 of themselves or 2^-30 (2^-36 once it has moved) of the
-      // largest, whichever is more.  (2^11 from the start: rows then moved after every other chunk of
-      // the first steps, 1250 us instead of 1099 for 4096 queries over 16384 tokens.)  Until a row has seen a token its reference is kNoRef: its first
+      // largest, whichever is more.  (2^11 from the start: rows then moved after every
+      // other chunk of the first steps, 1250 us instead of 1099 for 4096 queries over
+      // 16384 tokens.)  Until a row has seen a token its reference is kNoRef: its first
       // weight overflows and so sets it.
       float ref[4], l[4];
 #pragma unroll
