@@ -49,6 +49,8 @@ class PagedCache:
         device arrays: positions and slots of the new tokens, their cu_q, the page
         table and the lengths; and the longest row count and length."""
         rows = np.asarray(rows)
+        if rows.shape != self.lens.shape or (rows < 0).any():
+            raise ValueError("a row count, 0 or more, is needed for every sequence")
         if (self.lens + rows > self.width * self.page_size).any():
             raise ValueError("a sequence outgrows the cache")
         positions, slots = [], []
