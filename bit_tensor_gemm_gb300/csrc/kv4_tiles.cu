@@ -877,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           again |= fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) > kFar;
           if (__any_sync(0xffffffffu, again)) {
             // weights out of range, or odd scales beside a mask: once more, with care
+            const bool odd = __any_sync(0xffffffffu, wide);
             wide = false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -886,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 state[(2 + i) * 256] = l[2 * h + i];
               }
               const uint32_t lanes = h ? 16u << 16 : 0u;
-              if (careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from, state, h))
+              if (odd || careful_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from, state, h))
                 wide |= far_weights<DIM>(ts + lanes, to_ + lanes, ks, q, j > from, state, h);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
