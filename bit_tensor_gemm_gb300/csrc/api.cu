@@ -27,6 +27,7 @@
 #include <vector>
 
 #include "attn.h"
+#include "ffn.h"
 #include "lbgemm.h"
 #include "simt.h"
 #include "tc_params.h"
@@ -160,6 +161,7 @@ struct DeviceState {
   Scratch flush;        // buffer written between timed runs to evict L2
   Scratch quant;        // quantised activations of lbgemm_linear_quant
   Scratch attn;         // partial results of the attention operators
+  Scratch ffn;          // partial results of the feed-forward operators
   std::map<const void*, int> occupancy;
   // lbgemm_run_host's copy streams (host-to-device, device-to-host) and events
   cudaStream_t copy_in = nullptr, copy_out = nullptr;
@@ -2164,6 +2166,15 @@ lbgemm_status attn_scratch_acquire(const CallDevice& dev, size_t bytes, cudaStre
 
 lbgemm_status attn_scratch_release(const CallDevice& dev, cudaStream_t s, void* ptr) {
   return scratch_release(static_cast<DeviceState*>(dev.state)->attn, s, ptr);
+}
+
+lbgemm_status ffn_scratch_acquire(const CallDevice& dev, size_t bytes, cudaStream_t s,
+                                  void** ptr) {
+  return scratch_acquire(static_cast<DeviceState*>(dev.state)->ffn, bytes, s, ptr);
+}
+
+lbgemm_status ffn_scratch_release(const CallDevice& dev, cudaStream_t s, void* ptr) {
+  return scratch_release(static_cast<DeviceState*>(dev.state)->ffn, s, ptr);
 }
 
 void count_launches(int n) { g_launches += n; }

@@ -3,10 +3,9 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <mutex>
 
+#include "api_checks.h"
 #include "attn.h"
 #include "lbgemm.h"
 
@@ -15,27 +14,6 @@ namespace {
 using namespace lbg;
 
 std::mutex g_attn_mu;  // the attention operators' scratch
-
-lbgemm_status bad(lbgemm_status st, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  return report_error(st, buf);
-}
-
-int64_t elem_size(int dtype) { return dtype == LBGEMM_F32 ? 4 : 2; }
-
-bool aligned(const void* p, int64_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-lbgemm_status check_dtype(int dtype, bool f32) {
-  if (dtype == LBGEMM_BF16 || dtype == LBGEMM_F16 || (f32 && dtype == LBGEMM_F32))
-    return LBGEMM_OK;
-  return bad(LBGEMM_ERR_INVALID_ARG, "dtype %d is not taken by this call", dtype);
-}
-
-constexpr int64_t kMaxStride = int64_t(1) << 40;
 
 // A [tokens, heads, dim] tensor given by pointer and token stride.
 lbgemm_status check_tensor(const char* name, const void* p, int64_t stride, int64_t tokens,
@@ -96,8 +74,6 @@ lbgemm_status check_norm_rope(int dtype, int64_t tokens, int64_t heads_q, int64_
   }
   return LBGEMM_OK;
 }
-
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 }  // namespace
 

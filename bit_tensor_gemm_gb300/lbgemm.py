@@ -116,6 +116,18 @@ _SIGNATURES = {
     "lbgemm_kv4_attention": (_i32, [_i32, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp,
                                     _i64, _i64, _vp, _i64, _vp, _i64, _f32, _i32, _i64, _vp, _vp,
                                     _vp]),
+    "lbgemm_w4_quantize": (_i32, [_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                  _i64, _vp]),
+    "lbgemm_w4_linear": (_i32, [_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
+                                _vp]),
+    "lbgemm_moe_route": (_i32, [_i32, _i64, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _vp]),
+    "lbgemm_moe_w4": (_i32, [_i32, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp,
+                             _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "lbgemm_residual_norm": (_i32, [_i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _f32,
+                                    _f32, _vp, _f32, _vp, _i64, _vp, _i64, _vp]),
+    "lbgemm_residual_norm_backward": (_i32, [_i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                             _vp, _i64, _vp, _vp, _i64, _f32, _f32, _vp, _f32,
+                                             _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
     "lbgemm_device_status": (_i32, [_vp]),
     "lbgemm_selftest_timeout": (_i32, [_vp]),
     "lbgemm_last_error": (ctypes.c_char_p, []),
@@ -517,6 +529,57 @@ def lbgemm_kv4_attention(dtype, batch, total_q, max_q, heads_q, heads_kv, head_d
                                        page_size, _addr(page_table), table_width, _addr(kv_lens),
                                        max_kv, scale, int(bool(causal)), window, _addr(O),
                                        _addr(lse), _stream(stream)))
+
+
+def lbgemm_w4_quantize(dtype, N, K, group, W, w_stride, codes, code_stride, scales, scale_stride,
+                       row_scales, row_stride=1, stream=None) -> None:
+    _check(load().lbgemm_w4_quantize(dtype, N, K, group, _addr(W), w_stride, _addr(codes),
+                                     code_stride, _addr(scales), scale_stride, _addr(row_scales),
+                                     row_stride, _stream(stream)))
+
+
+def lbgemm_w4_linear(dtype, M, N, K, group, X, x_stride, codes, scales, row_scales, Y, y_stride,
+                     stream=None) -> None:
+    _check(load().lbgemm_w4_linear(dtype, M, N, K, group, _addr(X), x_stride, _addr(codes),
+                                   _addr(scales), _addr(row_scales), _addr(Y), y_stride,
+                                   _stream(stream)))
+
+
+def lbgemm_moe_route(dtype, tokens, experts, top_k, logits, stride, renormalize, ids, weights,
+                     stream=None) -> None:
+    _check(load().lbgemm_moe_route(dtype, tokens, experts, top_k, _addr(logits), stride,
+                                   int(bool(renormalize)), _addr(ids), _addr(weights),
+                                   _stream(stream)))
+
+
+def lbgemm_moe_w4(dtype, tokens, hidden, inter, experts, top_k, group, X, x_stride, ids, weights,
+                  up_codes, up_scales, up_row_scales, down_codes, down_scales, down_row_scales, Y,
+                  y_stride, stream=None) -> None:
+    _check(load().lbgemm_moe_w4(dtype, tokens, hidden, inter, experts, top_k, group, _addr(X),
+                                x_stride, _addr(ids), _addr(weights), _addr(up_codes),
+                                _addr(up_scales), _addr(up_row_scales), _addr(down_codes),
+                                _addr(down_scales), _addr(down_row_scales), _addr(Y), y_stride,
+                                _stream(stream)))
+
+
+def lbgemm_residual_norm(dtype, tokens, width, X, x_stride, Y, y_stride, w_post, gate, gate_stride,
+                         residual_scale, block_scale, w_next, eps, X_out, x_out_stride, N_out,
+                         n_out_stride, stream=None) -> None:
+    _check(load().lbgemm_residual_norm(dtype, tokens, width, _addr(X), x_stride, _addr(Y), y_stride,
+                                       _addr(w_post), _addr(gate), gate_stride, residual_scale,
+                                       block_scale, _addr(w_next), eps, _addr(X_out), x_out_stride,
+                                       _addr(N_out), n_out_stride, _stream(stream)))
+
+
+def lbgemm_residual_norm_backward(dtype, tokens, width, dX_out, dx_out_stride, dN, dn_stride, X,
+                                  x_stride, Y, y_stride, w_post, gate, gate_stride, residual_scale,
+                                  block_scale, w_next, eps, dX, dx_stride, dY, dy_stride, dgate,
+                                  dgate_stride, dw_post, dw_next, stream=None) -> None:
+    _check(load().lbgemm_residual_norm_backward(
+        dtype, tokens, width, _addr(dX_out), dx_out_stride, _addr(dN), dn_stride, _addr(X),
+        x_stride, _addr(Y), y_stride, _addr(w_post), _addr(gate), gate_stride, residual_scale,
+        block_scale, _addr(w_next), eps, _addr(dX), dx_stride, _addr(dY), dy_stride, _addr(dgate),
+        dgate_stride, _addr(dw_post), _addr(dw_next), _stream(stream)))
 
 
 def lbgemm_device_status(stream=None) -> None:

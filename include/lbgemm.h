@@ -643,6 +643,130 @@ lbgemm_status lbgemm_kv4_attention(int dtype, int64_t batch, int64_t total_q, in
                                    const int32_t* kv_lens, int64_t max_kv, float scale, int causal,
                                    int64_t window, void* O, float* lse, void* stream);
 
+/* ---- the feed-forward half of a block, weights in 4 bits -------------------------
+ * What the rest of a decoder block needs beside the linear layers and attention
+ * above: 16-bit activations times 4-bit weights, a router and a mixture of
+ * experts over such weights, and the norms around a block with its gate and the
+ * residual stream (with their backward pass).
+ *
+ * Conventions of this group: those of the attention group (dtype, pointers,
+ * strides, device status, rounding), a [rows, width] tensor being given by its
+ * pointer and its row stride in elements. */
+
+/* 4-bit weights: rows of K codes, signed numbers of 4 bits, in groups of 32, 64
+ * or 128 (K a multiple of `group`, at most 2^20).  The weight (n, k) is
+ *   code[n][k] * scale[n][k / group] * row_scale[n]
+ * with scales in e4m3 (8 bits) and row scales in fp32.
+ *   codes: K / 2 bytes a row; elements 8w .. 8w + 7 of a row make its little-endian
+ *     32-bit word w: element 8w + 2j in bits 4j .. 4j + 3, element 8w + 2j + 1 in
+ *     bits 16 + 4j .. 16 + 4j + 3, two's complement (two neighbours come out of a
+ *     word by one shift);
+ *   scales: K / group bytes a row; row_scales: one a row.
+ * A code times its scale has at most 7 significant bits and is exact in bf16 and
+ * in fp16, so products with activations are exact in the matrix units.
+ *
+ * lbgemm_w4_quantize makes them from W [N, K] (dtype: any; stride w_stride), in
+ * fp32 steps with IEEE division:
+ *   row_scale = max|w of the row| * (1.0f / 3136)
+ *   scale = e4m3((max|w of the group| * (1.0f / 7)) / row_scale), to nearest even
+ *   code = clamp(round_half_even(w / (scale * row_scale)), -7, 7), 0 where that
+ *          product is 0
+ * A row that holds an infinity or NaN gets a NaN row scale (and codes and scales
+ * of 0).  code_stride, scale_stride: bytes from row to row of the output (codes
+ * in multiples of 16), row_stride: row scales from row to row, so that two
+ * matrices can be interleaved (see lbgemm_moe_w4).  The calls that use weights
+ * take them dense. */
+lbgemm_status lbgemm_w4_quantize(int dtype, int64_t N, int64_t K, int64_t group, const void* W,
+                                 int64_t w_stride, void* codes, int64_t code_stride, void* scales,
+                                 int64_t scale_stride, float* row_scales, int64_t row_stride,
+                                 void* stream);
+
+/* Y[m][n] = sum_k X[m][k] W[n][k], X [M, K], Y [M, N], W in 4 bits as above.
+ * dtype: LBGEMM_BF16 or LBGEMM_F16.  M, N up to 2^30; Y's stride is any from N
+ * on (rows need not be aligned).  Sums are fp32, and the row scale multiplies
+ * them before the one rounding.  A token's result does not depend on the other
+ * tokens of the call, but for the order of its sum, which goes by M.  Scratch for
+ * partial sums is taken as in lbgemm_run. */
+lbgemm_status lbgemm_w4_linear(int dtype, int64_t M, int64_t N, int64_t K, int64_t group,
+                               const void* X, int64_t x_stride, const void* codes,
+                               const void* scales, const float* row_scales, void* Y,
+                               int64_t y_stride, void* stream);
+
+/* The router: for every row of logits [tokens, experts] the top_k largest, in
+ * descending order, the lower expert first among equals.
+ *   ids[t][j]: int32 [tokens, top_k]; weights: fp32 [tokens, top_k]
+ *   weights[t][j] = exp(l_j) / sum exp(l), over the chosen experts where
+ *   `renormalize` is not 0, else over all of the row.
+ * -inf and NaN are never chosen and count as 0 in the sum; places without an expert
+ * get id -1 and weight 0.  +inf counts as the largest finite fp32 number.  dtype:
+ * any; experts 1 .. 1024, top_k 1 .. min(32, experts); logits need no more
+ * alignment than their elements, any stride from `experts` on. */
+lbgemm_status lbgemm_moe_route(int dtype, int64_t tokens, int64_t experts, int64_t top_k,
+                               const void* logits, int64_t stride, int renormalize, int32_t* ids,
+                               float* weights, void* stream);
+
+/* A mixture of experts:
+ *   y_t = sum_j weights[t][j] * Down_e (silu(Gate_e x_t) * (Up_e x_t)),   e = ids[t][j]
+ * with silu(v) = v / (1 + exp(-v)).  X, Y: [tokens, hidden]; ids int32 and weights
+ * fp32 [tokens, top_k] as the router gives them.  An id below 0 adds nothing (a
+ * token without experts gets 0), one of `experts` or more adds nothing and sets
+ * the device status; the same expert may stand twice in a row.
+ *   up: the experts' 4-bit rows [experts][2 * inter], K = hidden: row 2i of an
+ *       expert is row i of its Gate, row 2i + 1 row i of its Up;
+ *   down: [experts][hidden], K = inter.
+ * hidden and inter: multiples of `group`.  dtype: LBGEMM_BF16 or LBGEMM_F16; the
+ * inner vector silu(..) * (..) is rounded to dtype (in fp16 it must stay below
+ * 65520), everything else is summed in fp32 and rounded once.  experts up to
+ * 1024, top_k up to 32, tokens * top_k up to 2^24.  The sum over j runs in the
+ * order of j.  Scratch for the inner vectors is taken as in lbgemm_run. */
+lbgemm_status lbgemm_moe_w4(int dtype, int64_t tokens, int64_t hidden, int64_t inter,
+                            int64_t experts, int64_t top_k, int64_t group, const void* X,
+                            int64_t x_stride, const int32_t* ids, const float* weights,
+                            const void* up_codes, const void* up_scales,
+                            const float* up_row_scales, const void* down_codes,
+                            const void* down_scales, const float* down_row_scales, void* Y,
+                            int64_t y_stride, void* stream);
+
+/* The norms around a block, for every row of X (the residual stream) and Y (the
+ * block's output), [tokens, width]:
+ *   z  = Y * rstd(Y) * w_post       (z = Y where w_post is NULL)
+ *   X_out = residual_scale * X + block_scale * gate * z
+ *   N_out = x' * rstd(x') * w_next  with x' = X_out before its rounding
+ * and rstd(v) = 1 / sqrt(mean(v^2) + eps).  w_post, w_next: [width] of dtype;
+ * w_next and N_out may both be NULL.  gate: NULL (1), one row of dtype for all
+ * tokens (gate_stride 0), or a row for every token (gate_stride >= width).  Y
+ * NULL: no block before (w_post and gate NULL); X_out may then be NULL too, for
+ * the norm alone.  dtype: any; width: a multiple of 8 up to 16384 (8192 in fp32).
+ * Each output may be one of the inputs, with the same stride. */
+lbgemm_status lbgemm_residual_norm(int dtype, int64_t tokens, int64_t width, const void* X,
+                                   int64_t x_stride, const void* Y, int64_t y_stride,
+                                   const void* w_post, const void* gate, int64_t gate_stride,
+                                   float residual_scale, float block_scale, const void* w_next,
+                                   float eps, void* X_out, int64_t x_out_stride, void* N_out,
+                                   int64_t n_out_stride, void* stream);
+
+/* Its backward pass, from the inputs of the forward call and the gradients of
+ * its outputs (dX_out may be NULL: none; dN NULL exactly where w_next is), with
+ * xhat = x' * rstd(x') and yhat = Y * rstd(Y):
+ *   d  = dX_out + rstd(x') * (w_next dN - xhat * mean(w_next dN xhat))
+ *   dX = residual_scale * d,  dz = block_scale * gate * d
+ *   dY = rstd(Y) * (w_post dz - yhat * mean(w_post dz yhat))   (dY = dz where w_post is NULL)
+ *   dw_next = sum over tokens of dN xhat,  dw_post = sum of dz yhat
+ *   dgate = block_scale * z * d: a row of dtype for every token where the gate has
+ *           one, else the sum over tokens, fp32 [width]
+ * dX, dY, dgate rows: dtype; dY NULL exactly where Y is, dgate, dw_post, dw_next
+ * (fp32 [width], written whole, zeros for no tokens) NULL exactly where their
+ * inputs are.  The sums run in a fixed order: the same call gives the same bits.
+ * Each output may be one of the row-by-row inputs, with the same stride.  Scratch
+ * for partial sums is taken as in lbgemm_run. */
+lbgemm_status lbgemm_residual_norm_backward(
+    int dtype, int64_t tokens, int64_t width, const void* dX_out, int64_t dx_out_stride,
+    const void* dN, int64_t dn_stride, const void* X, int64_t x_stride, const void* Y,
+    int64_t y_stride, const void* w_post, const void* gate, int64_t gate_stride,
+    float residual_scale, float block_scale, const void* w_next, float eps, void* dX,
+    int64_t dx_stride, void* dY, int64_t dy_stride, void* dgate, int64_t dgate_stride,
+    float* dw_post, float* dw_next, void* stream);
+
 /* ---- status ------------------------------------------------------------------ */
 
 /* Synchronises `stream`, then returns LBGEMM_ERR_TIMEOUT if any kernel of this
