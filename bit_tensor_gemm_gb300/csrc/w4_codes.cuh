@@ -6,11 +6,17 @@
 // exact numbers; the fp32 scale of a row multiplies its sum.
 //
 // In a word of eight codes element 2j sits in bits 4j .. and 2j + 1 in bits 16 +
-// 4j .., so one shift and one three-input operation give two neighbouring codes
-// as the top mantissa bits of halves between 16 and 32:
-//   ((w << s) & mask) ^ (16.0 with the sign bit of the code turned) = 16 + (code + 8)
-// and one multiply-add with (scale, -24 scale) takes the 24 out, exactly: 24
-// scale has 6 significant bits.
+// 4j .., so a shift and a three-input operation give two neighbouring codes as
+// mantissa bits of a pair of halves:
+//   ((w >> s) & mask) ^ (base with the codes' sign bit turned) = base + unit (code + 8)
+// Logic and shifts run at half the rate of other operations and bound the kernels
+// for few tokens, so shifts are spared:
+//   bf16  code at mantissa bit 3: 16 + (code + 8), and fma(v, s, -24 s) is exact
+//         (24 s has 6 significant bits); pair 0 is taken where it stands, as 128 +
+//         (code + 8), and costs an addition of -136 before the product instead;
+//   fp16  has mantissa bits for two codes where they stand: 1024 + (code + 8) with
+//         an addition of -1032, and 1024 + 16 (code + 8) with fma(v, s / 16, -72 s)
+//         (8 significant bits): one shift for the word.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -31,11 +37,19 @@ struct W4Math;
 
 template <>
 struct W4Math<__nv_bfloat16> {
-  static constexpr int kUp = 3;  // a code's place in 16.0's mantissa
-  static constexpr uint32_t kMask = 0x00780078u, kBase = 0x41c041c0u;
   __device__ static __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+  }
+  __device__ static __forceinline__ uint32_t mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ static __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
   }
   __device__ static __forceinline__ uint32_t twice(float x) {
@@ -46,44 +60,79 @@ struct W4Math<__nv_bfloat16> {
 };
 template <>
 struct W4Math<__half> {
-  static constexpr int kUp = 6;
-  static constexpr uint32_t kMask = 0x03c003c0u, kBase = 0x4e004e00u;
   __device__ static __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
   }
-  __device__ static __forceinline__ uint32_t twice(float x) {
+  __device__ static __forceinline__ uint32_t mul(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(d) : "f"(x));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ static __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
   }
 };
 
-// An e4m3 scale (s, s) and (-24 s, -24 s) as pairs of T.
-struct W4Scale {
+// An e4m3 scale as pairs of T: s, and what the fma above takes beside it (bf16: -24 s;
+// fp16: s / 16 and -72 s).  s / 16 is exact in fp16 (s is a multiple of 2^-9).
+template <typename T>
+struct W4Scale;
+template <>
+struct W4Scale<__nv_bfloat16> {
   uint32_t s, off;
 };
-__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+template <>
+struct W4Scale<__half> {
+  uint32_t s, low, off;
+};
+// Of two bytes, the scales of two rows.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t first, uint32_t second) {
   uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)byte));
-  return __half2float(__ushort_as_half((uint16_t)h));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(first | second << 8)));
+  return h;
 }
-template <typename T>
-__device__ __forceinline__ W4Scale w4_scale(uint32_t byte) {
-  const float s = e4m3_value(byte & 0xffu);
-  return {W4Math<T>::twice(s), W4Math<T>::twice(-24.0f * s)};
+__device__ __forceinline__ void w4_scales(uint32_t first, uint32_t second,
+                                          W4Scale<__nv_bfloat16>& a, W4Scale<__nv_bfloat16>& b) {
+  using M = W4Math<__nv_bfloat16>;
+  const uint32_t h = e4m3_pair(first, second);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  a.s = M::twice(f.x);
+  b.s = M::twice(f.y);
+  a.off = M::mul(a.s, 0xc1c0c1c0u);
+  b.off = M::mul(b.s, 0xc1c0c1c0u);
+}
+__device__ __forceinline__ void w4_scales(uint32_t first, uint32_t second, W4Scale<__half>& a,
+                                          W4Scale<__half>& b) {
+  using M = W4Math<__half>;
+  const uint32_t h = e4m3_pair(first, second);
+  a.s = __byte_perm(h, h, 0x1010);
+  b.s = __byte_perm(h, h, 0x3232);
+  a.low = M::mul(a.s, 0x2c002c00u);
+  b.low = M::mul(b.s, 0x2c002c00u);
+  a.off = M::mul(a.s, 0xd480d480u);
+  b.off = M::mul(b.s, 0xd480d480u);
 }
 
 // Eight weights of a word, as four pairs in order.
-template <typename T>
-__device__ __forceinline__ void w4_word(uint32_t w, const W4Scale& sc, uint32_t (&out)[4]) {
-  using M = W4Math<T>;
+__device__ __forceinline__ void w4_word(uint32_t w, const W4Scale<__nv_bfloat16>& sc,
+                                        uint32_t (&out)[4]) {
+  using M = W4Math<__nv_bfloat16>;
+  out[0] = M::mul(M::add(and_xor(w, 0x000f000fu, 0x43084308u), 0xc308c308u), sc.s);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int up = M::kUp - 4 * j;
-    const uint32_t at = up >= 0 ? w << (up & 31) : w >> (-up & 31);
-    out[j] = M::fma(and_xor(at, M::kMask, M::kBase), sc.s, sc.off);
+  for (int j = 1; j < 4; ++j)
+    out[j] = M::fma(and_xor(w >> (4 * j - 3), 0x00780078u, 0x41c041c0u), sc.s, sc.off);
+}
+__device__ __forceinline__ void w4_word(uint32_t w, const W4Scale<__half>& sc, uint32_t (&out)[4]) {
+  using M = W4Math<__half>;
+#pragma unroll
+  for (int j = 0; j < 4; j += 2) {
+    const uint32_t v = j == 0 ? w : w >> 8;
+    out[j] = M::mul(M::add(and_xor(v, 0x000f000fu, 0x64086408u), 0xe408e408u), sc.s);
+    out[j + 1] = M::fma(and_xor(v, 0x00f000f0u, 0x64806480u), sc.low, sc.off);
   }
 }
 

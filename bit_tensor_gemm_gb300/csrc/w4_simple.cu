@@ -4,6 +4,7 @@
 #include "attn_common.cuh"
 #include "ffn.h"
 #include "w4_codes.cuh"
+#include "w4_kernels.h"
 
 namespace lbg {
 namespace {
@@ -24,8 +25,10 @@ __device__ float row_dot(const T* x, const W4& w, int64_t row, int k, int group)
   for (int o = lane; o < k / 8; o += 32) {
     float f[8];
     unpack8(load8_raw(x + o * 8), f);
+    W4Scale<T> sc, same;
+    w4_scales(scales[o * 8 / group], 0, sc, same);
     uint32_t v[4];
-    w4_word<T>(codes[o], w4_scale<T>(scales[o * 8 / group]), v);
+    w4_word(codes[o], sc, v);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 a = floats<T>(v[j]);
@@ -100,6 +103,7 @@ size_t w4_linear_scratch(W4LinearParams*, int) { return 0; }
 cudaError_t launch_w4_linear(int dtype, const W4LinearParams& p, void*, int sm_count,
                              int* launches, cudaStream_t s) {
   *launches += 1;
+  if (w4_rows_take_linear(p, sm_count)) return launch_w4_rows_linear(dtype, p, sm_count, s);
   if (dtype == LBGEMM_BF16)
     linear_kernel<__nv_bfloat16><<<8 * sm_count, 32 * kWarps, 0, s>>>(p);
   else
@@ -109,6 +113,8 @@ cudaError_t launch_w4_linear(int dtype, const W4LinearParams& p, void*, int sm_c
 size_t moe_w4_scratch(MoeParams* p, int) { return (size_t)p->tokens * p->top_k * p->inter * 2; }
 cudaError_t launch_moe_w4(int dtype, const MoeParams& p, void* scratch, int sm_count,
                           int* launches, cudaStream_t s) {
+  if (w4_rows_take_moe(p, sm_count))
+    return launch_w4_rows_moe(dtype, p, scratch, sm_count, launches, s);
   *launches += 2;
   return dtype == LBGEMM_BF16 ? moe_typed<__nv_bfloat16>(p, scratch, sm_count, s)
                               : moe_typed<__half>(p, scratch, sm_count, s);
