@@ -28,6 +28,7 @@
 
 #include "attn.h"
 #include "ffn.h"
+#include "w4_kernels.h"
 #include "lbgemm.h"
 #include "simt.h"
 #include "tc_params.h"
@@ -2175,6 +2176,23 @@ lbgemm_status ffn_scratch_acquire(const CallDevice& dev, size_t bytes, cudaStrea
 
 lbgemm_status ffn_scratch_release(const CallDevice& dev, cudaStream_t s, void* ptr) {
   return scratch_release(static_cast<DeviceState*>(dev.state)->ffn, s, ptr);
+}
+
+bool encode_map(CUtensorMap* map, int dtype, const void* base, int64_t width, int64_t rows,
+                int64_t stride, int box_width, int box_rows, int swizzle) {
+  const CUtensorMapDataType type = dtype == LBGEMM_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : dtype == LBGEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride};
+  const cuuint32_t box[2] = {(cuuint32_t)box_width, (cuuint32_t)box_rows};
+  const cuuint32_t step[2] = {1, 1};
+  return g_encode &&
+         g_encode(map, type, 2, const_cast<void*>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 void count_launches(int n) { g_launches += n; }

@@ -162,6 +162,9 @@ lbgemm_status lbgemm_w4_linear(int dtype, int64_t M, int64_t N, int64_t K, int64
     if (st != LBGEMM_OK) return st;
     if (M < 0 || M > kMostRows || N < 0 || N > kMostRows)
       return bad(LBGEMM_ERR_INVALID_ARG, "%lld tokens, %lld rows", (long long)M, (long long)N);
+    if (M * N > (int64_t(1) << 45))  // (the kernels count tiles in 32 bits)
+      return bad(LBGEMM_ERR_INVALID_ARG, "%lld tokens by %lld rows are too many tiles",
+                 (long long)M, (long long)N);
     if (M == 0 || N == 0) return LBGEMM_OK;
     st = check_rows("X", X, x_stride, M, K, dtype);
     if (st == LBGEMM_OK) st = check_w4("W", codes, scales, row_scales);

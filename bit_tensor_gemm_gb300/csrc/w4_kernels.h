@@ -1,6 +1,8 @@
 // w4_kernels.h -- the kernels behind the 4-bit products (w4_rows.cu for few
 // tokens) and how a call chooses among them (w4.cu).
 #pragma once
+#include <cuda.h>
+
 #include "ffn.h"
 
 namespace lbg {
@@ -34,5 +36,40 @@ bool w4_rows_take_moe(const MoeParams& m, int sm_count);
 // h: [tokens * top_k][inter] of dtype
 cudaError_t launch_w4_rows_moe(int dtype, const MoeParams& m, void* h, int sm_count, int* launches,
                                cudaStream_t s);
+
+// ---- many tokens --------------------------------------------------------------------------
+constexpr int kTilesMaxExperts = 1024;
+struct W4TilesParams {
+  int64_t n = 0;  // rows of a matrix (of one expert)
+  int k = 0, group = 0;
+  const uint8_t* scales = nullptr;
+  const float* row_scales = nullptr;
+  void* out = nullptr;  // linear: Y, or fp32 [part][m][n]; up: h; down: fp32 [pick][n]
+  int64_t out_stride = 0;
+  int m = 0;  // tokens (linear) or picks
+  int experts = 1;
+  const int *offsets = nullptr, *token_of = nullptr;  // [experts + 1]; [picks]
+  // the cut: blocks of tokens (linear), tiles of rows, slices of k and of a part of it
+  int blocks = 0, row_tiles = 0, slices = 0, parts = 1, part_slices = 0;
+  int* status = nullptr;
+};
+struct MoeSort {
+  const int32_t* ids = nullptr;
+  int picks = 0, top_k = 1, experts = 1, piece = 0, pieces = 0;
+  int *counts = nullptr, *offsets = nullptr, *token_of = nullptr, *pos_of = nullptr;
+  int* status = nullptr;
+};
+size_t w4_tiles_linear_scratch(const W4LinearParams& l, int sm_count);
+cudaError_t launch_w4_tiles_linear(int dtype, const W4LinearParams& l, void* scratch, int sm_count,
+                                   int* launches, cudaStream_t s);
+size_t w4_tiles_moe_scratch(const MoeParams& m);
+cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, int sm_count,
+                                int* launches, cudaStream_t s);
+
+// A 2D tensor map (api.cu): rows of `width` elements of a dtype (or bytes) `stride` bytes
+// apart, boxes of box_width x box_rows, swizzled by 64 or 128 bytes.
+constexpr int LBGEMM_MAP_U8 = -1;
+bool encode_map(CUtensorMap* map, int dtype, const void* base, int64_t width, int64_t rows,
+                int64_t stride, int box_width, int box_rows, int swizzle);
 
 }  // namespace lbg

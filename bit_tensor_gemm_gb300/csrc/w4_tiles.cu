@@ -1,0 +1,775 @@
+// w4_tiles.cu -- products with 4-bit weights for many tokens, on tcgen05: tiles
+// of 128 weight rows by up to 256 tokens.
+//
+//   linear  Y[m][n] = row_scale[n] * sum_k X[m][k] * (code * scale)[n][k]
+//   up      h[pos][i] = silu(gate) * up for the picks (token, expert) in expert order
+//   down    out[pos][n], which combine() adds up by token
+//
+// The weights are the MMA's A operand, read from tensor memory: converter warps
+// turn a slice of 128 codes a row into halves (exactly, w4_codes.cuh), a row a
+// lane, and store them into one of four slots of tensor memory.  Tokens are the B
+// operand, brought by TMA (128-byte swizzle); for `up` row by row through the list
+// of an expert's tokens (tile::gather4), so nothing is copied into expert order
+// first.  So shared memory carries the tokens only once in and once out, and a
+// quarter of the weights' bytes of a product of halves.
+//
+// One persistent CTA an SM, 24 warps: TMA of the codes (0), the MMAs (1), TMA of
+// the tokens (2), read-out (4..7), converters (8..23: two teams that take slices in
+// turn, each two warps to a quarter of the rows).  Tiles of up to 128 tokens have
+// two accumulators, so that a tile is read out beside the next one's MMAs.  A
+// linear layer with few tiles is cut along k and joined by join().
+//
+// Every wait is bounded; on a time-out the CTA winds down (own copies in flight,
+// own MMAs) before tensor memory is freed.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "attn_common.cuh"
+#include "ffn.h"
+#include "ptx.cuh"
+#include "w4_codes.cuh"
+#include "w4_kernels.h"
+
+namespace lbg {
+namespace {
+
+constexpr int kThreads = 24 * 32;
+constexpr int kRows = 128;    // weight rows of a tile
+constexpr int kSlice = 128;   // elements of k of a slice
+constexpr int kSlots = 4;     // slices of converted weights in tensor memory
+constexpr int kSlotCols = kSlice / 2;
+constexpr int kWBytes = kRows * kSlice / 2;
+
+enum Mode { kLinear, kUp, kDown };
+
+template <int BN>
+struct Layout {
+  static constexpr int kXStages = BN == 256 ? 3 : BN == 128 ? 5 : 8;
+  static constexpr int kWStages = BN == 256 ? 3 : BN == 128 ? 6 : 8;
+  static constexpr int kXBytes = BN * kSlice * 2;
+  static constexpr int kAccs = BN == 256 ? 1 : 2;
+  static constexpr int kWOffset = kXStages * kXBytes;
+  static constexpr int kBarOffset = kWOffset + kWStages * kWBytes;
+  // barriers: xfull, xempty, wfull, wempty, afull, aempty, accfull, accempty, done
+  static constexpr int kBars = 2 * (kXStages + kWStages + kSlots + kAccs) + 1;
+  static constexpr int kTmemSlot = kBarOffset + 8 * kBars;
+  static constexpr int kBytes = kTmemSlot + 16 + 1024;
+  static constexpr int kACol = kAccs * BN;  // first column of the slots
+  static_assert(kACol + kSlots * kSlotCols <= 512, "tensor memory");
+  static_assert(kBytes + 4 * (kTilesMaxExperts + 1) + 64 <= 232448, "shared memory");
+};
+
+template <typename T>
+constexpr uint32_t instr(int n) {  // fp32 sums, A and B of T, both K-major, 128 x n
+  const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kRows >> 4) << 24);
+}
+
+__device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, int* status) {
+  volatile int go_on = 0;
+  return mbar_wait(bar, parity, &go_on, status);
+}
+
+// Four rows of a tensor whose box is one row high.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t x, int4 rows) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z),
+      "r"(rows.w), "r"(bar)
+      : "memory");
+}
+
+// A unit of work: a tile of rows by a block of tokens by a part of k.
+struct Unit {
+  int expert, first, count;  // the block's tokens: place of the first, how many
+  int row;                   // first row, in the expert
+  int slice, end, part;      // slices of k
+};
+template <int MODE, int BN>
+struct Units {
+  const W4TilesParams& p;
+  const int* before;  // blocks of tokens before an expert's
+  int u, total, expert = 0;
+  __device__ __forceinline__ Units(const W4TilesParams& q, const int* b) : p(q), before(b) {
+    total = (MODE == kLinear ? p.blocks : before[p.experts]) * p.row_tiles * p.parts;
+    u = blockIdx.x;
+  }
+  __device__ __forceinline__ bool next(Unit& x) {
+    if (u >= total) return false;
+    const int rest = u / p.parts;
+    x.part = u - rest * p.parts;
+    const int block = rest / p.row_tiles;
+    x.row = (rest - block * p.row_tiles) * kRows;
+    x.slice = x.part * p.part_slices;
+    x.end = min(x.slice + p.part_slices, p.slices);
+    if (MODE == kLinear) {
+      x.expert = 0;
+      x.first = block * BN;
+      x.count = min(BN, p.m - x.first);
+    } else {
+      while (before[expert + 1] <= block) ++expert;
+      x.expert = expert;
+      const int skip = (block - before[expert]) * BN, at = p.offsets[expert];
+      x.first = at + skip;
+      x.count = min(BN, p.offsets[expert + 1] - x.first);
+    }
+    u += gridDim.x;
+    return true;
+  }
+};
+
+template <typename T, int MODE, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w,
+                    const __grid_constant__ CUtensorMap map_x, const W4TilesParams p) {
+  using L = Layout<BN>;
+  constexpr int XS = L::kXStages, WS = L::kWStages, ACCS = L::kAccs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  __shared__ int before[MODE == kLinear ? 1 : kTilesMaxExperts + 1];
+  const uint32_t base = smem_addr(smem);
+  const uint32_t bars = base + L::kBarOffset;
+  auto xfull = [&](int i) { return bars + 8u * i; };
+  auto xempty = [&](int i) { return bars + 8u * (XS + i); };
+  auto wfull = [&](int i) { return bars + 8u * (2 * XS + i); };
+  auto wempty = [&](int i) { return bars + 8u * (2 * XS + WS + i); };
+  auto afull = [&](int i) { return bars + 8u * (2 * XS + 2 * WS + i); };
+  auto aempty = [&](int i) { return bars + 8u * (2 * XS + 2 * WS + kSlots + i); };
+  auto accfull = [&](int i) { return bars + 8u * (2 * (XS + WS + kSlots) + i); };
+  auto accempty = [&](int i) { return bars + 8u * (2 * (XS + WS + kSlots) + ACCS + i); };
+  const uint32_t done = bars + 8u * (L::kBars - 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kTmemSlot + 4);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < XS; ++i) mbar_init(xfull(i), 1), mbar_init(xempty(i), 1);
+    for (int i = 0; i < WS; ++i) mbar_init(wfull(i), 1), mbar_init(wempty(i), 8);
+    for (int i = 0; i < kSlots; ++i) mbar_init(afull(i), 8), mbar_init(aempty(i), 1);
+    for (int i = 0; i < ACCS; ++i) mbar_init(accfull(i), 1), mbar_init(accempty(i), 4);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (MODE != kLinear) {
+    for (int e = threadIdx.x; e < p.experts; e += kThreads)
+      before[e + 1] = (p.offsets[e + 1] - p.offsets[e] + BN - 1) / BN;
+    __syncthreads();
+    if (warp == 0) {  // running sums
+      int sum = 0;
+      for (int e0 = 0; e0 < p.experts; e0 += 32) {
+        const int e = e0 + lane;
+        int v = e < p.experts ? before[e + 1] : 0;
+#pragma unroll
+        for (int off = 1; off < 32; off *= 2) {
+          const int x = __shfl_up_sync(0xffffffffu, v, off);
+          if (lane >= off) v += x;
+        }
+        if (e < p.experts) before[e + 1] = sum + v;
+        sum += __shfl_sync(0xffffffffu, v, 31);
+      }
+      if (lane == 0) before[0] = 0;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Units<MODE, BN> units(p, before);
+  Unit x;
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status));
+  };
+
+  if (warp == 0) {
+    // ---- TMA of the codes ----
+    if (lane == 0) {
+      tma_prefetch_desc(&map_w);
+      int stage = 0, parity = 1;
+      int64_t issued = 0;
+      bool ok = true;
+      while (ok && units.next(x))
+        for (int s = x.slice; s < x.end; ++s) {
+          if (!(ok = mbar_wait(wempty(stage), parity, abort_flag, p.status))) break;
+          mbar_arrive_expect_tx(wfull(stage), kWBytes);
+          tma_load_2d(base + L::kWOffset + stage * kWBytes, &map_w, wfull(stage), s * (kSlice / 2),
+                      (int)(x.expert * p.n) + x.row);
+          ++issued;
+          if (++stage == WS) stage = 0, parity ^= 1;
+        }
+      if (!ok)  // wait for the copies still in flight
+        for (int64_t i = min(issued, (int64_t)WS); i > 0; --i) {
+          if (--stage < 0) stage = WS - 1, parity ^= 1;
+          wait_drain(wfull(stage), parity ^ 1, p.status);
+        }
+    }
+  } else if (warp == 2) {
+    // ---- TMA of the tokens: a whole warp for a list of rows, else one lane ----
+    if (MODE == kUp || lane == 0) {
+      if (lane == 0) tma_prefetch_desc(&map_x);
+      int stage = 0, parity = 1;
+      int64_t issued = 0;
+      bool ok = true;
+      constexpr int LISTS = (BN + 127) / 128;  // groups of four rows a lane
+      while (ok && units.next(x)) {
+        int4 rows[LISTS];
+        if (MODE == kUp) {
+#pragma unroll
+          for (int i = 0; i < LISTS; ++i) {  // (past the block: its last token again)
+            const int c = 4 * (lane + 32 * i);
+            const int* list = p.token_of + x.first;
+            rows[i] = make_int4(list[min(c, x.count - 1)], list[min(c + 1, x.count - 1)],
+                                list[min(c + 2, x.count - 1)], list[min(c + 3, x.count - 1)]);
+          }
+        }
+        for (int s = x.slice; s < x.end; ++s) {
+          const bool there = mbar_wait(xempty(stage), parity, abort_flag, p.status);
+          if (!(ok = MODE == kUp ? __all_sync(0xffffffffu, there) : there)) break;
+          const uint32_t dst = base + stage * L::kXBytes;
+          const int boxes = p.k - s * kSlice > 64 ? 2 : 1;  // (none that begins past the row)
+          if (lane == 0) mbar_arrive_expect_tx(xfull(stage), boxes * (L::kXBytes / 2));
+          if (MODE == kUp) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < LISTS; ++i) {
+              const int c = 4 * (lane + 32 * i);
+              if (c < BN) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                  if (b < boxes)
+                    tma_gather4(dst + b * BN * 128 + c * 128, &map_x, xfull(stage),
+                                s * kSlice + 64 * b, rows[i]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              if (b < boxes)
+                tma_load_2d(dst + b * BN * 128, &map_x, xfull(stage), s * kSlice + 64 * b, x.first);
+          }
+          ++issued;
+          if (++stage == XS) stage = 0, parity ^= 1;
+        }
+      }
+      if (!ok && lane == 0)
+        for (int64_t i = min(issued, (int64_t)XS); i > 0; --i) {
+          if (--stage < 0) stage = XS - 1, parity ^= 1;
+          wait_drain(xfull(stage), parity ^ 1, p.status);
+        }
+    }
+  } else if (warp == 1) {
+    // ---- the MMAs ----
+    if (lane == 0) {
+      constexpr uint32_t idesc = instr<T>(BN);
+      int stage = 0, xparity = 0, slot = 0, aparity = 0, acc = 0, cparity = 1;
+      bool ok = true;
+      while (ok && units.next(x)) {
+        if (!(ok = mbar_wait(accempty(acc), cparity, abort_flag, p.status))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * BN;
+        for (int s = x.slice; s < x.end; ++s) {
+          if (!(ok = mbar_wait(xfull(stage), xparity, abort_flag, p.status))) break;
+          if (!(ok = mbar_wait(afull(slot), aparity, abort_flag, p.status))) break;
+          tc_fence_after();
+          const uint64_t desc = smem_desc_sw128(base + stage * L::kXBytes);
+          const uint32_t a = tmem + L::kACol + slot * kSlotCols;
+          const int pieces = min(kSlice, p.k - s * kSlice) / 16;
+#pragma unroll
+          for (int i = 0; i < kSlice / 16; ++i)
+            if (i < pieces)
+              mma_f16_ts(d, a + 8 * i, desc + (i / 4) * (BN * 128 >> 4) + 2 * (i % 4), idesc,
+                         s > x.slice || i > 0 ? 1u : 0u);
+          mma_commit(xempty(stage));
+          mma_commit(aempty(slot));
+          if (++stage == XS) stage = 0, xparity ^= 1;
+          if (++slot == kSlots) slot = 0, aparity ^= 1;
+        }
+        if (!ok) break;
+        mma_commit(accfull(acc));
+        if (++acc == ACCS) acc = 0, cparity ^= 1;
+      }
+      mma_commit(done);  // arrives once every MMA issued above has completed
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---- read-out: lane = row, columns = tokens ----
+    const int quarter = warp & 3;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    int acc = 0, parity = 0;
+    bool ok = true;
+    while (ok && units.next(x)) {
+      const int row = x.row + quarter * 32 + lane;
+      const bool live = row < p.n;
+      const float scale =
+          live ? __ldg(p.row_scales + (int64_t)x.expert * p.n + row) : 0.0f;
+      if (!(ok = wait_warp(accfull(acc), parity))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < BN; c0 += 32) {
+        if (c0 >= x.count) break;
+        uint32_t v[32];
+        tmem_ld32(tmem + lanes + acc * BN + c0, v);
+        tmem_ld_wait();
+        if (MODE == kUp) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            // rows 2i (gate) and 2i + 1 (up) sit in neighbouring lanes: the even one takes
+            // column j, the odd one j + 1
+            const float a = __uint_as_float(v[j]) * scale, b = __uint_as_float(v[j + 1]) * scale;
+            const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+            const float gate = lane & 1 ? other : a, up = lane & 1 ? b : other;
+            const int c = c0 + j + (lane & 1);
+            if (live && c < x.count)
+              static_cast<T*>(p.out)[(int64_t)(x.first + c) * p.out_stride + row / 2] =
+                  from_f32<T>(gate / (1.0f + expf(-gate)) * up);
+          }
+        } else if (MODE == kDown || p.parts > 1) {
+          float* out = static_cast<float*>(p.out) + ((int64_t)x.part * p.m + x.first + c0) * p.n + row;
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c0 + j < x.count)
+                out[(int64_t)j * p.n] = __uint_as_float(v[j]) * scale;
+          }
+        } else {
+          T* out = static_cast<T*>(p.out) + (int64_t)(x.first + c0) * p.out_stride + row;
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c0 + j < x.count)
+                out[j * p.out_stride] = from_f32<T>(__uint_as_float(v[j]) * scale);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(accempty(acc));
+      if (++acc == ACCS) acc = 0, parity ^= 1;
+    }
+  } else if (warp >= 8) {
+    // ---- converters: a row a lane, half a slice a warp, slices in turn by team ----
+    const int quarter = warp & 3, half = (warp - 8) >> 2 & 1, team = (warp - 8) >> 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t scale_row = p.k / p.group;
+    const int shift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
+    int index = 0;  // of the slice among all of this CTA
+    bool ok = true;
+    while (ok && units.next(x)) {
+      const int rows = (int)min((int64_t)kRows, p.n - x.row);
+      const uint8_t* scales =
+          p.scales + ((int64_t)x.expert * p.n + x.row + min(r, rows - 1)) * scale_row;
+      // this team's slices; the scales of its next one are loaded ahead
+      int s = x.slice + ((index ^ team) & 1);
+      const int mine = index + ((index ^ team) & 1);
+      auto scale_at = [&](int slice, int piece) -> uint32_t {  // of 32 elements
+        const int at = slice * kSlice + half * 64 + piece * 32;
+        return at < p.k && slice < x.end ? __ldg(scales + (at >> shift)) : 0;
+      };
+      uint32_t ahead[2] = {scale_at(s, 0), scale_at(s, 1)};
+      for (int i = mine; s < x.end; s += 2, i += 2) {
+        const int stage = i % WS, slot = i % kSlots;
+        W4Scale<T> sc[2];
+        w4_scales(ahead[0], ahead[1], sc[0], sc[1]);
+        ahead[0] = scale_at(s + 2, 0);
+        ahead[1] = scale_at(s + 2, 1);
+        if (!(ok = wait_warp(wfull(stage), (uint32_t)(i / WS) & 1u))) break;
+        // 64-byte swizzle: piece c of row r sits at piece c ^ (r / 2 % 4)
+        const uint8_t* w = smem + L::kWOffset + stage * kWBytes + r * 64;
+        uint32_t words[32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint4 c =
+              *reinterpret_cast<const uint4*>(w + (((2 * half + q) ^ (r >> 1 & 3)) << 4));
+          const uint32_t code[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t o[4];
+            w4_word(code[j], sc[q], o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) words[16 * q + 4 * j + k] = o[k];
+          }
+        }
+        if (!(ok = wait_warp(aempty(slot), ((uint32_t)(i / kSlots) & 1u) ^ 1u))) break;
+        tc_fence_after();
+        tmem_st32(tmem + lanes + L::kACol + slot * kSlotCols + half * 32, words);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(afull(slot));
+          mbar_arrive(wempty(stage));
+        }
+      }
+      index += x.end - x.slice;
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) wait_drain(done, 0, p.status);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int MODE, int BN>
+cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const W4TilesParams& p, int ctas,
+                   bool dependent, cudaStream_t s) {
+  auto kernel = w4_tiles_kernel<T, MODE, BN>;
+  static std::atomic<uint64_t> set{0};  // devices on which the kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  // (more than half of an SM's, so that two CTAs do not share its tensor memory)
+  constexpr int bytes = Layout<BN>::kBytes > 120 * 1024 ? Layout<BN>::kBytes : 120 * 1024;
+  if (!(set.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    set |= uint64_t(1) << dev;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, w, x, p);
+}
+
+template <int MODE, int BN>
+cudaError_t launch(int dtype, const CUtensorMap& w, const CUtensorMap& x, const W4TilesParams& p,
+                   int ctas, bool dependent, cudaStream_t s) {
+  return dtype == LBGEMM_BF16 ? launch<__nv_bfloat16, MODE, BN>(w, x, p, ctas, dependent, s)
+                              : launch<__half, MODE, BN>(w, x, p, ctas, dependent, s);
+}
+
+template <int MODE>
+cudaError_t launch(int dtype, int bn, const CUtensorMap& w, const CUtensorMap& x,
+                   const W4TilesParams& p, int ctas, bool dependent, cudaStream_t s) {
+  if (bn == 32) return launch<MODE, 32>(dtype, w, x, p, ctas, dependent, s);
+  if (bn == 64) return launch<MODE, 64>(dtype, w, x, p, ctas, dependent, s);
+  if (bn == 128) return launch<MODE, 128>(dtype, w, x, p, ctas, dependent, s);
+  return launch<MODE, 256>(dtype, w, x, p, ctas, dependent, s);
+}
+
+// ---- joining the parts of k of a linear layer ---------------------------------------
+// y[m][n] = sum of parts[.][m][n], in order
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ parts, int count,
+                                                   int64_t m, int64_t n, T* y, int64_t y_stride) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t total = m * n;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / n, c = i - row * n;
+    float v = 0.0f;
+    for (int q = 0; q < count; ++q) v += parts[q * total + i];
+    y[row * y_stride + c] = from_f32<T>(v);
+  }
+}
+
+// ---- picks in expert order --------------------------------------------------------------
+// Pieces of the list of picks: a histogram each, then each piece's places from the
+// sums before it.  One piece does both at once.
+constexpr int kSortThreads = 1024;
+__global__ void __launch_bounds__(kSortThreads)
+    count_kernel(const MoeSort q) {
+  __shared__ int counts[kTilesMaxExperts];
+  for (int e = threadIdx.x; e < q.experts; e += kSortThreads) counts[e] = 0;
+  __syncthreads();
+  const int first = blockIdx.x * q.piece, end = min(first + q.piece, q.picks);
+  for (int i = first + threadIdx.x; i < end; i += kSortThreads) {
+    const int e = q.ids[i];
+    if (e >= 0 && e < q.experts) atomicAdd(&counts[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < q.experts; e += kSortThreads)
+    q.counts[blockIdx.x * q.experts + e] = counts[e];
+}
+__global__ void __launch_bounds__(kSortThreads) place_kernel(const MoeSort q) {
+  __shared__ int cursor[kTilesMaxExperts], sums[32];
+  const int first = blockIdx.x * q.piece, end = min(first + q.piece, q.picks);
+  const int e = threadIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  cursor[threadIdx.x] = 0;  // (kSortThreads is kTilesMaxExperts)
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int before = 0, total = 0;  // of expert e: in pieces before this one, in all
+  if (q.pieces == 1) {
+    for (int i = threadIdx.x; i < q.picks; i += kSortThreads) {
+      const int id = q.ids[i];
+      if (id >= 0 && id < q.experts) atomicAdd(&cursor[id], 1);
+    }
+    __syncthreads();
+    total = cursor[e];
+  } else if (e < q.experts) {
+    for (int c = 0; c < q.pieces; ++c) {
+      const int n = q.counts[c * q.experts + e];
+      total += n;
+      if (c < (int)blockIdx.x) before += n;
+    }
+  }
+  int v = total;  // running sum over the experts
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const int x = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += x;
+  }
+  if (lane == 31) sums[warp] = v;
+  __syncthreads();
+  int carry = 0;
+  for (int w = 0; w < warp; ++w) carry += sums[w];
+  v += carry;
+  cursor[e] = v - total + before;
+  if (blockIdx.x == 0 && e < q.experts) {
+    q.offsets[e + 1] = v;
+    if (e == 0) q.offsets[0] = 0;
+  }
+  __syncthreads();
+  // (the order within an expert does not matter: a pick's sums are its own)
+  for (int i = first + threadIdx.x; i < end; i += kSortThreads) {
+    const int id = q.ids[i];
+    int pos = -1;
+    if (id >= 0 && id < q.experts) {
+      pos = atomicAdd(&cursor[id], 1);
+      q.token_of[pos] = i / q.top_k;
+    } else if (id >= q.experts) {
+      atomicOr(q.status, kStatusBadIndex);
+    }
+    q.pos_of[i] = pos;
+  }
+}
+
+// ---- a token's picks added up -------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256)
+    combine_kernel(const float* __restrict__ out, const int* __restrict__ pos_of,
+                   const float* __restrict__ weights, int64_t tokens, int hidden, int top_k, T* y,
+                   int64_t y_stride) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int octets = hidden / 8;
+  const int64_t total = tokens * octets;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / octets;
+    const int c = (int)(i - t * octets) * 8;
+    float v[8] = {};
+    for (int j = 0; j < top_k; ++j) {
+      const int pos = __ldg(pos_of + t * top_k + j);
+      if (pos < 0) continue;
+      const float w = __ldg(weights + t * top_k + j);
+      float f[8];
+      unpack8(load8_raw(out + (int64_t)pos * hidden + c), f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += w * f[k];
+    }
+    store8(y + t * y_stride + c, v);
+  }
+}
+
+template <typename F, typename... A>
+cudaError_t launch_after(F kernel, int64_t blocks, int threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Tokens of a tile for a block of `tokens` on average.
+int width_for(int64_t tokens) {
+  return tokens <= 32 ? 32 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256;
+}
+
+bool maps(int dtype, const W4& w, int64_t rows, int64_t k, const void* x, int64_t x_rows,
+          int64_t x_stride, int box_rows, CUtensorMap* map_w, CUtensorMap* map_x) {
+  return encode_map(map_w, LBGEMM_MAP_U8, w.codes, k / 2, rows, k / 2, kSlice / 2, kRows, 64) &&
+         encode_map(map_x, dtype, x, k, x_rows, x_stride * 2, 64, box_rows, 128);
+}
+
+int64_t round16(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// Where a mixture's scratch lies.
+struct MoeScratch {
+  int64_t h, out, counts, offsets, token_of, pos_of, bytes;
+  int pieces, piece;
+};
+MoeScratch moe_scratch(const MoeParams& m) {
+  MoeScratch z;
+  const int64_t picks = m.tokens * m.top_k;
+  z.piece = (int)std::max<int64_t>(4096, (picks + 63) / 64);
+  z.pieces = (int)((picks + z.piece - 1) / z.piece);
+  z.h = 0;
+  z.out = z.h + round16(picks * m.inter * 2);
+  z.counts = z.out + round16(picks * m.hidden * 4);
+  z.offsets = z.counts + round16((int64_t)z.pieces * m.experts * 4);
+  z.token_of = z.offsets + round16((m.experts + 1) * 4);
+  z.pos_of = z.token_of + round16(picks * 4);
+  z.bytes = z.pos_of + round16(picks * 4);
+  return z;
+}
+
+// Parts of k for a linear layer whose tiles would leave SMs idle.
+void cut_linear(const W4LinearParams& l, int sm_count, int* bn, W4TilesParams* p) {
+  *bn = width_for(l.m);
+  p->blocks = (int)((l.m + *bn - 1) / *bn);
+  p->row_tiles = (int)((l.n + kRows - 1) / kRows);
+  p->slices = (int)((l.k + kSlice - 1) / kSlice);
+  const int64_t tiles = (int64_t)p->blocks * p->row_tiles;
+  p->parts = 1;
+  if (2 * tiles <= sm_count)
+    p->parts = std::max(1, std::min((int)(sm_count / tiles), p->slices / 4));
+  p->part_slices = (p->slices + p->parts - 1) / p->parts;
+  p->parts = (p->slices + p->part_slices - 1) / p->part_slices;
+}
+
+}  // namespace
+
+size_t w4_tiles_linear_scratch(const W4LinearParams& l, int sm_count) {
+  W4TilesParams p;
+  int bn;
+  cut_linear(l, sm_count, &bn, &p);
+  return p.parts > 1 ? (size_t)p.parts * l.m * l.n * sizeof(float) : 0;
+}
+
+cudaError_t launch_w4_tiles_linear(int dtype, const W4LinearParams& l, void* scratch, int sm_count,
+                                   int* launches, cudaStream_t s) {
+  W4TilesParams p;
+  int bn;
+  cut_linear(l, sm_count, &bn, &p);
+  p.n = l.n;
+  p.k = (int)l.k;
+  p.group = l.group;
+  p.scales = l.w.scales;
+  p.row_scales = l.w.row_scales;
+  p.out = p.parts > 1 ? scratch : l.y;
+  p.out_stride = l.y_stride;
+  p.m = (int)l.m;
+  p.status = l.status;
+  CUtensorMap map_w, map_x;
+  if (!maps(dtype, l.w, l.n, l.k, l.x, l.m, l.x_stride, bn, &map_w, &map_x))
+    return cudaErrorInvalidValue;
+  const int64_t units = (int64_t)p.blocks * p.row_tiles * p.parts;
+  cudaError_t e = launch<kLinear>(dtype, bn, map_w, map_x, p,
+                                  (int)std::min<int64_t>(units, sm_count), false, s);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  if (p.parts == 1) return e;
+  const int64_t blocks = std::min<int64_t>((l.m * l.n + 255) / 256, 8 * sm_count);
+  const float* parts = static_cast<const float*>(scratch);
+  if (dtype == LBGEMM_BF16)
+    e = launch_after(join_kernel<__nv_bfloat16>, blocks, 256, s, parts, p.parts, l.m, l.n,
+                     static_cast<__nv_bfloat16*>(l.y), l.y_stride);
+  else
+    e = launch_after(join_kernel<__half>, blocks, 256, s, parts, p.parts, l.m, l.n,
+                     static_cast<__half*>(l.y), l.y_stride);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+size_t w4_tiles_moe_scratch(const MoeParams& m) { return (size_t)moe_scratch(m).bytes; }
+
+cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, int sm_count,
+                                int* launches, cudaStream_t s) {
+  const MoeScratch z = moe_scratch(m);
+  uint8_t* at = static_cast<uint8_t*>(scratch);
+  const int64_t picks = m.tokens * m.top_k;
+  MoeSort q;
+  q.ids = m.ids;
+  q.picks = (int)picks;
+  q.top_k = m.top_k;
+  q.experts = m.experts;
+  q.piece = z.piece;
+  q.pieces = z.pieces;
+  q.counts = reinterpret_cast<int*>(at + z.counts);
+  q.offsets = reinterpret_cast<int*>(at + z.offsets);
+  q.token_of = reinterpret_cast<int*>(at + z.token_of);
+  q.pos_of = reinterpret_cast<int*>(at + z.pos_of);
+  q.status = m.status;
+  cudaError_t e;
+  if (q.pieces > 1) {
+    count_kernel<<<q.pieces, kSortThreads, 0, s>>>(q);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    *launches += 1;
+    e = launch_after(place_kernel, q.pieces, kSortThreads, s, q);
+  } else {
+    place_kernel<<<1, kSortThreads, 0, s>>>(q);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+
+  // Blocks of tokens for the average expert; accumulators are read out beside the
+  // next tile's MMAs up to 128 tokens, which the experts' short k needs.
+  const int bn = std::min(128, width_for((picks + m.experts - 1) / m.experts));
+  W4TilesParams p;
+  p.experts = m.experts;
+  p.offsets = q.offsets;
+  p.token_of = q.token_of;
+  p.group = m.group;
+  p.m = (int)picks;
+  p.parts = 1;
+  p.status = m.status;
+  CUtensorMap map_w, map_x;
+  p.n = 2 * (int64_t)m.inter;
+  p.k = m.hidden;
+  p.row_tiles = (int)((p.n + kRows - 1) / kRows);
+  p.slices = p.part_slices = (p.k + kSlice - 1) / kSlice;
+  p.scales = m.up.scales;
+  p.row_scales = m.up.row_scales;
+  p.out = at + z.h;
+  p.out_stride = m.inter;
+  if (!maps(dtype, m.up, m.experts * p.n, p.k, m.x, m.tokens, m.x_stride, 1, &map_w, &map_x))
+    return cudaErrorInvalidValue;
+  e = launch<kUp>(dtype, bn, map_w, map_x, p, sm_count, true, s);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  p.n = m.hidden;
+  p.k = m.inter;
+  p.row_tiles = (int)((p.n + kRows - 1) / kRows);
+  p.slices = p.part_slices = (p.k + kSlice - 1) / kSlice;
+  p.scales = m.down.scales;
+  p.row_scales = m.down.row_scales;
+  p.out = at + z.out;
+  if (!maps(dtype, m.down, m.experts * p.n, p.k, at + z.h, picks, m.inter, bn, &map_w, &map_x))
+    return cudaErrorInvalidValue;
+  e = launch<kDown>(dtype, bn, map_w, map_x, p, sm_count, true, s);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  const float* out = reinterpret_cast<const float*>(at + z.out);
+  const int64_t blocks = std::min<int64_t>((m.tokens * (m.hidden / 8) + 255) / 256, 16 * sm_count);
+  if (dtype == LBGEMM_BF16)
+    e = launch_after(combine_kernel<__nv_bfloat16>, blocks, 256, s, out, (const int*)q.pos_of,
+                     m.weights, m.tokens, m.hidden, m.top_k, static_cast<__nv_bfloat16*>(m.y),
+                     m.y_stride);
+  else
+    e = launch_after(combine_kernel<__half>, blocks, 256, s, out, (const int*)q.pos_of, m.weights,
+                     m.tokens, m.hidden, m.top_k, static_cast<__half*>(m.y), m.y_stride);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
+}  // namespace lbg
