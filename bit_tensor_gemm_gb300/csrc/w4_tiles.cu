@@ -1,5 +1,5 @@
 // w4_tiles.cu -- products with 4-bit weights for many tokens, on tcgen05: tiles
-// of 128 weight rows by up to 256 tokens.
+// of 128 or 256 weight rows by up to 256 tokens.
 //
 //   linear  Y[m][n] = row_scale[n] * sum_k X[m][k] * (code * scale)[n][k]
 //   up      h[pos][i] = silu(gate) * up for the picks (token, expert) in expert order
@@ -8,19 +8,22 @@
 // The weights are the MMA's A operand, read from tensor memory: converter warps
 // turn a slice of 128 codes a row into halves (exactly, w4_codes.cuh), a row a
 // lane, and store them into one of four slots of tensor memory.  Tokens are the B
-// operand, brought by TMA (128-byte swizzle); for `up` row by row through the list
-// of an expert's tokens (tile::gather4), so nothing is copied into expert order
-// first.  So shared memory carries the tokens only once in and once out, and a
-// quarter of the weights' bytes of a product of halves.
+// operand, brought by TMA (128-byte swizzle).  So shared memory carries a quarter of
+// the weights' bytes of a product of halves, and is bound by the tokens: from 65
+// tokens on a tile is a pair of CTAs' (cta_group::2, 128 weight rows in each), which
+// halves the tokens that each of them brings and reads (a single CTA's tile of 128 x
+// 256 ran 4096 tokens x 11008 x 4096 at 1.16 PFLOP/s, at the rate of its fills).
 //
-// One persistent CTA an SM, 24 warps: TMA of the codes (0), the MMAs (1), TMA of
-// the tokens (2), read-out (4..7), converters (8..23: two teams that take slices in
-// turn, each two warps to a quarter of the rows).  Tiles of up to 128 tokens have
-// two accumulators, so that a tile is read out beside the next one's MMAs.  A
-// linear layer with few tiles is cut along k and joined by join().
+// One persistent CTA an SM, 24 warps: TMA of the codes (0), the MMAs (1, of a pair
+// the even CTA's), TMA of the tokens (2), read-out (4..7), converters (8..23: two
+// teams that take slices in turn, each two warps to a quarter of the rows).  Tiles of
+// up to 128 tokens have two accumulators, so that a tile is read out beside the next
+// one's MMAs.  A linear layer with few tiles is cut along k and joined by join().
 //
-// Every wait is bounded; on a time-out the CTA winds down (own copies in flight,
-// own MMAs) before tensor memory is freed.
+// In a pair the tokens' full barriers, the converters' and the accumulators' empty
+// ones are the even CTA's and count both; the commits of the MMAs go to both.  Every
+// wait is bounded; on a time-out the CTAs wind down (copies in flight, own MMAs)
+// before tensor memory is freed.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -28,6 +31,7 @@
 #include <type_traits>
 
 #include "attn_common.cuh"
+#include "cluster.cuh"
 #include "ffn.h"
 #include "ptx.cuh"
 #include "w4_codes.cuh"
@@ -45,28 +49,33 @@ constexpr int kWBytes = kRows * kSlice / 2;
 
 enum Mode { kLinear, kUp, kDown };
 
-template <int BN>
+// PAIR: the tile's tokens are split between the CTAs.
+template <int BN, bool PAIR>
 struct Layout {
-  static constexpr int kXStages = BN == 256 ? 3 : BN == 128 ? 5 : 8;
-  static constexpr int kWStages = BN == 256 ? 3 : BN == 128 ? 6 : 8;
-  static constexpr int kXBytes = BN * kSlice * 2;
+  static constexpr int kTokens = PAIR ? BN / 2 : BN;  // that a CTA brings
+  static constexpr int kXStages = kTokens == 128 ? 5 : 8;
+  static constexpr int kWStages = kTokens == 128 ? 6 : 8;
+  static constexpr int kXBytes = kTokens * kSlice * 2;
   static constexpr int kAccs = BN == 256 ? 1 : 2;
   static constexpr int kWOffset = kXStages * kXBytes;
   static constexpr int kBarOffset = kWOffset + kWStages * kWBytes;
   // barriers: xfull, xempty, wfull, wempty, afull, aempty, accfull, accempty, done
   static constexpr int kBars = 2 * (kXStages + kWStages + kSlots + kAccs) + 1;
-  static constexpr int kTmemSlot = kBarOffset + 8 * kBars;
-  static constexpr int kBytes = kTmemSlot + 16 + 1024;
+  static constexpr int kPeerIssued = kBarOffset + 8 * kBars;  // int64
+  static constexpr int kTmemSlot = kPeerIssued + 8;
+  static constexpr int kUsed = kTmemSlot + 8 + 1024;
+  // more than half of an SM's, so that no two CTAs share its tensor memory
+  static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
   static constexpr int kACol = kAccs * BN;  // first column of the slots
   static_assert(kACol + kSlots * kSlotCols <= 512, "tensor memory");
   static_assert(kBytes + 4 * (kTilesMaxExperts + 1) + 64 <= 232448, "shared memory");
 };
 
 template <typename T>
-constexpr uint32_t instr(int n) {  // fp32 sums, A and B of T, both K-major, 128 x n
+constexpr uint32_t instr(int m, int n) {  // fp32 sums, A and B of T, both K-major, m x n
   const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
   return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) |
-         ((uint32_t)(kRows >> 4) << 24);
+         ((uint32_t)(m >> 4) << 24);
 }
 
 __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, int* status) {
@@ -74,14 +83,15 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, int* s
   return mbar_wait(bar, parity, &go_on, status);
 }
 
-// Four rows of a tensor whose box is one row high.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int32_t x, int4 rows) {
+// D (+)= A[tmem] . B[smem]^T over the pair: rows 0..127 of A and tokens 0..N/2 of B
+// in the even CTA.
+__device__ __forceinline__ void mma_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z),
-      "r"(rows.w), "r"(bar)
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -91,21 +101,23 @@ struct Unit {
   int row;                   // first row, in the expert
   int slice, end, part;      // slices of k
 };
-template <int MODE, int BN>
+template <int MODE, int BN, bool PAIR>
 struct Units {
   const W4TilesParams& p;
   const int* before;  // blocks of tokens before an expert's
-  int u, total, expert = 0;
+  int u, step, total, rank, expert = 0;
   __device__ __forceinline__ Units(const W4TilesParams& q, const int* b) : p(q), before(b) {
     total = (MODE == kLinear ? p.blocks : before[p.experts]) * p.row_tiles * p.parts;
-    u = blockIdx.x;
+    u = PAIR ? (int)cluster_index() : blockIdx.x;
+    step = PAIR ? (int)cluster_count() : gridDim.x;
+    rank = PAIR ? (int)cluster_rank() : 0;
   }
   __device__ __forceinline__ bool next(Unit& x) {
     if (u >= total) return false;
     const int rest = u / p.parts;
     x.part = u - rest * p.parts;
     const int block = rest / p.row_tiles;
-    x.row = (rest - block * p.row_tiles) * kRows;
+    x.row = (rest - block * p.row_tiles) * (PAIR ? 2 * kRows : kRows) + rank * kRows;
     x.slice = x.part * p.part_slices;
     x.end = min(x.slice + p.part_slices, p.slices);
     if (MODE == kLinear) {
@@ -119,16 +131,16 @@ struct Units {
       x.first = at + skip;
       x.count = min(BN, p.offsets[expert + 1] - x.first);
     }
-    u += gridDim.x;
+    u += step;
     return true;
   }
 };
 
-template <typename T, int MODE, int BN>
+template <typename T, int MODE, int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_x, const W4TilesParams p) {
-  using L = Layout<BN>;
+  using L = Layout<BN, PAIR>;
   constexpr int XS = L::kXStages, WS = L::kWStages, ACCS = L::kAccs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -147,20 +159,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t done = bars + 8u * (L::kBars - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kTmemSlot + 4);
+  volatile int64_t* peer_issued = reinterpret_cast<volatile int64_t*>(smem + L::kPeerIssued);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const bool even = !PAIR || cluster_rank() == 0;
+  constexpr int CTAS = PAIR ? 2 : 1;
+  // an arrival on the even CTA's barrier, and a wait for one that both CTAs arrive on
+  auto arrive_even = [&](uint32_t bar) {
+    if (!PAIR || even)
+      mbar_arrive(bar);
+    else
+      mbar_arrive_cluster(cluster_map(bar, 0));
+  };
+  auto wait_both = [&](uint32_t bar, uint32_t parity) {
+    return PAIR ? mbar_wait_cluster(bar, parity, abort_flag, p.status)
+                : mbar_wait(bar, parity, abort_flag, p.status);
+  };
+  auto commit = [&](uint32_t bar) {
+    if (PAIR)
+      mma_commit_pair(bar);
+    else
+      mma_commit(bar);
+  };
 
   if (threadIdx.x == 0) {
+    *peer_issued = 0;
     for (int i = 0; i < XS; ++i) mbar_init(xfull(i), 1), mbar_init(xempty(i), 1);
     for (int i = 0; i < WS; ++i) mbar_init(wfull(i), 1), mbar_init(wempty(i), 8);
-    for (int i = 0; i < kSlots; ++i) mbar_init(afull(i), 8), mbar_init(aempty(i), 1);
-    for (int i = 0; i < ACCS; ++i) mbar_init(accfull(i), 1), mbar_init(accempty(i), 4);
+    for (int i = 0; i < kSlots; ++i) mbar_init(afull(i), 8 * CTAS), mbar_init(aempty(i), 1);
+    for (int i = 0; i < ACCS; ++i) mbar_init(accfull(i), 1), mbar_init(accempty(i), 4 * CTAS);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_addr(tmem_slot), 512);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(smem_addr(tmem_slot), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_addr(tmem_slot), 512);
+      tmem_relinquish();
+    }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -186,9 +224,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync_all();  // both CTAs' barriers are there before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Units<MODE, BN> units(p, before);
+  Units<MODE, BN, PAIR> units(p, before);
+  int64_t issued = 0;  // copies of tokens
   Unit x;
   auto wait_warp = [&](uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status));
@@ -217,91 +257,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
   } else if (warp == 2) {
-    // ---- TMA of the tokens: a whole warp for a list of rows, else one lane ----
-    if (MODE == kUp || lane == 0) {
-      if (lane == 0) tma_prefetch_desc(&map_x);
+    // ---- TMA of the tokens ----
+    if (lane == 0) {
+      tma_prefetch_desc(&map_x);
       int stage = 0, parity = 1;
-      int64_t issued = 0;
       bool ok = true;
-      constexpr int LISTS = (BN + 127) / 128;  // groups of four rows a lane
-      while (ok && units.next(x)) {
-        int4 rows[LISTS];
-        if (MODE == kUp) {
-#pragma unroll
-          for (int i = 0; i < LISTS; ++i) {  // (past the block: its last token again)
-            const int c = 4 * (lane + 32 * i);
-            const int* list = p.token_of + x.first;
-            rows[i] = make_int4(list[min(c, x.count - 1)], list[min(c + 1, x.count - 1)],
-                                list[min(c + 2, x.count - 1)], list[min(c + 3, x.count - 1)]);
-          }
-        }
+      while (ok && units.next(x))
         for (int s = x.slice; s < x.end; ++s) {
-          const bool there = mbar_wait(xempty(stage), parity, abort_flag, p.status);
-          if (!(ok = MODE == kUp ? __all_sync(0xffffffffu, there) : there)) break;
+          if (!(ok = mbar_wait(xempty(stage), parity, abort_flag, p.status))) break;
           const uint32_t dst = base + stage * L::kXBytes;
-          const int boxes = p.k - s * kSlice > 64 ? 2 : 1;  // (none that begins past the row)
-          if (lane == 0) mbar_arrive_expect_tx(xfull(stage), boxes * (L::kXBytes / 2));
-          if (MODE == kUp) {
-            __syncwarp();
+          const int row = x.first + (even ? 0 : L::kTokens);
 #pragma unroll
-            for (int i = 0; i < LISTS; ++i) {
-              const int c = 4 * (lane + 32 * i);
-              if (c < BN) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                  if (b < boxes)
-                    tma_gather4(dst + b * BN * 128 + c * 128, &map_x, xfull(stage),
-                                s * kSlice + 64 * b, rows[i]);
-              }
+          for (int b = 0; b < 2; ++b) {
+            // (where the second box would begin past the row, any: no MMA reads it)
+            const int k = s * kSlice + 64 * b < p.k ? s * kSlice + 64 * b : 0;
+            if (PAIR) {
+              if (even && b == 0) mbar_arrive_expect_tx(xfull(stage), 2 * L::kXBytes);
+              tma_load_2d_pair(dst + b * L::kTokens * 128, &map_x, cluster_map(xfull(stage), 0), k,
+                               row);
+            } else {
+              if (b == 0) mbar_arrive_expect_tx(xfull(stage), L::kXBytes);
+              tma_load_2d(dst + b * L::kTokens * 128, &map_x, xfull(stage), k, row);
             }
-          } else {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-              if (b < boxes)
-                tma_load_2d(dst + b * BN * 128, &map_x, xfull(stage), s * kSlice + 64 * b, x.first);
           }
           ++issued;
           if (++stage == XS) stage = 0, parity ^= 1;
         }
-      }
-      if (!ok && lane == 0)
+      if (!ok && !PAIR)
         for (int64_t i = min(issued, (int64_t)XS); i > 0; --i) {
           if (--stage < 0) stage = XS - 1, parity ^= 1;
           wait_drain(xfull(stage), parity ^ 1, p.status);
         }
+      if (PAIR && !even)
+        st_cluster_u64(cluster_map(smem_addr((const void*)peer_issued), 0), (uint64_t)issued);
     }
   } else if (warp == 1) {
     // ---- the MMAs ----
-    if (lane == 0) {
-      constexpr uint32_t idesc = instr<T>(BN);
+    if (even && lane == 0) {
+      constexpr uint32_t idesc = instr<T>(kRows * CTAS, BN);
       int stage = 0, xparity = 0, slot = 0, aparity = 0, acc = 0, cparity = 1;
       bool ok = true;
       while (ok && units.next(x)) {
-        if (!(ok = mbar_wait(accempty(acc), cparity, abort_flag, p.status))) break;
+        if (!(ok = wait_both(accempty(acc), cparity))) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
         for (int s = x.slice; s < x.end; ++s) {
           if (!(ok = mbar_wait(xfull(stage), xparity, abort_flag, p.status))) break;
-          if (!(ok = mbar_wait(afull(slot), aparity, abort_flag, p.status))) break;
+          if (!(ok = wait_both(afull(slot), aparity))) break;
           tc_fence_after();
           const uint64_t desc = smem_desc_sw128(base + stage * L::kXBytes);
           const uint32_t a = tmem + L::kACol + slot * kSlotCols;
           const int pieces = min(kSlice, p.k - s * kSlice) / 16;
 #pragma unroll
           for (int i = 0; i < kSlice / 16; ++i)
-            if (i < pieces)
-              mma_f16_ts(d, a + 8 * i, desc + (i / 4) * (BN * 128 >> 4) + 2 * (i % 4), idesc,
-                         s > x.slice || i > 0 ? 1u : 0u);
-          mma_commit(xempty(stage));
-          mma_commit(aempty(slot));
+            if (i < pieces) {
+              const uint64_t b = desc + (i / 4) * (L::kTokens * 128 >> 4) + 2 * (i % 4);
+              const uint32_t more = s > x.slice || i > 0 ? 1u : 0u;
+              if (PAIR)
+                mma_pair_ts(d, a + 8 * i, b, idesc, more);
+              else
+                mma_f16_ts(d, a + 8 * i, b, idesc, more);
+            }
+          commit(xempty(stage));
+          commit(aempty(slot));
           if (++stage == XS) stage = 0, xparity ^= 1;
           if (++slot == kSlots) slot = 0, aparity ^= 1;
         }
         if (!ok) break;
-        mma_commit(accfull(acc));
+        commit(accfull(acc));
         if (++acc == ACCS) acc = 0, cparity ^= 1;
       }
-      mma_commit(done);  // arrives once every MMA issued above has completed
+      commit(done);  // arrives once every MMA issued above has completed
     }
   } else if (warp >= 4 && warp < 8) {
     // ---- read-out: lane = row, columns = tokens ----
@@ -355,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(accempty(acc));
+      if (lane == 0) arrive_even(accempty(acc));
       if (++acc == ACCS) acc = 0, parity ^= 1;
     }
   } else if (warp >= 8) {
@@ -368,9 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int index = 0;  // of the slice among all of this CTA
     bool ok = true;
     while (ok && units.next(x)) {
-      const int rows = (int)min((int64_t)kRows, p.n - x.row);
       const uint8_t* scales =
-          p.scales + ((int64_t)x.expert * p.n + x.row + min(r, rows - 1)) * scale_row;
+          p.scales + ((int64_t)x.expert * p.n + min(x.row + r, (int)p.n - 1)) * scale_row;
       // this team's slices; the scales of its next one are loaded ahead
       int s = x.slice + ((index ^ team) & 1);
       const int mine = index + ((index ^ team) & 1);
@@ -409,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(afull(slot));
+          arrive_even(afull(slot));
           mbar_arrive(wempty(stage));
         }
       }
@@ -418,56 +443,95 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncthreads();
+  if (PAIR) {
+    cluster_sync_all();  // the odd CTA's number of copies has reached the even one
+    if (even && warp == 2 && lane == 0) {
+      // Copies may be in flight only after a time-out, the last XS of the CTA that
+      // issued more: one that the other never issued gets its half armed or completed
+      // here, so that its phase ends when the issued half has landed.
+      const int64_t peer = *peer_issued, most = max(issued, peer);
+      for (int64_t j = max(most - XS, (int64_t)0); j < most; ++j) {
+        const int stage = (int)(j % XS);
+        if (j >= issued)
+          mbar_arrive_expect_tx(xfull(stage), L::kXBytes);
+        else if (j >= peer)
+          mbar_complete_tx(xfull(stage), L::kXBytes);
+        wait_drain(xfull(stage), (uint32_t)(j / XS) & 1u, p.status);
+      }
+    }
+  }
   if (warp == 1) {
     if (lane == 0) wait_drain(done, 0, p.status);
     __syncwarp();
+  }
+  if (PAIR) {
+    tc_fence_before();
+    cluster_sync_all();  // no copy, MMA or arrival targets either CTA any more
+  }
+  if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (PAIR)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
   }
 }
 
+// From this width on a tile is a pair's.
+constexpr int kPairWidth = 128;
+
 template <typename T, int MODE, int BN>
-cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const W4TilesParams& p, int ctas,
-                   bool dependent, cudaStream_t s) {
-  auto kernel = w4_tiles_kernel<T, MODE, BN>;
+cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const W4TilesParams& p,
+                   int64_t units, int sm_count, bool dependent, cudaStream_t s) {
+  constexpr bool PAIR = BN >= kPairWidth;
+  auto kernel = w4_tiles_kernel<T, MODE, BN, PAIR>;
   static std::atomic<uint64_t> set{0};  // devices on which the kernel has its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // (more than half of an SM's, so that two CTAs do not share its tensor memory)
-  constexpr int bytes = Layout<BN>::kBytes > 120 * 1024 ? Layout<BN>::kBytes : 120 * 1024;
+  constexpr int bytes = Layout<BN, PAIR>::kBytes;
   if (!(set.load() >> dev & 1)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     set |= uint64_t(1) << dev;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(PAIR ? 2 * (unsigned)std::min<int64_t>(units, sm_count / 2)
+                          : (unsigned)std::min<int64_t>(units, sm_count));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
+  if (PAIR) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim = {2, 1, 1};
+    ++cfg.numAttrs;
+  }
+  if (dependent) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, w, x, p);
 }
 
 template <int MODE, int BN>
 cudaError_t launch(int dtype, const CUtensorMap& w, const CUtensorMap& x, const W4TilesParams& p,
-                   int ctas, bool dependent, cudaStream_t s) {
-  return dtype == LBGEMM_BF16 ? launch<__nv_bfloat16, MODE, BN>(w, x, p, ctas, dependent, s)
-                              : launch<__half, MODE, BN>(w, x, p, ctas, dependent, s);
+                   int64_t units, int sm_count, bool dependent, cudaStream_t s) {
+  return dtype == LBGEMM_BF16
+             ? launch<__nv_bfloat16, MODE, BN>(w, x, p, units, sm_count, dependent, s)
+             : launch<__half, MODE, BN>(w, x, p, units, sm_count, dependent, s);
 }
 
 template <int MODE>
 cudaError_t launch(int dtype, int bn, const CUtensorMap& w, const CUtensorMap& x,
-                   const W4TilesParams& p, int ctas, bool dependent, cudaStream_t s) {
-  if (bn == 32) return launch<MODE, 32>(dtype, w, x, p, ctas, dependent, s);
-  if (bn == 64) return launch<MODE, 64>(dtype, w, x, p, ctas, dependent, s);
-  if (bn == 128) return launch<MODE, 128>(dtype, w, x, p, ctas, dependent, s);
-  return launch<MODE, 256>(dtype, w, x, p, ctas, dependent, s);
+                   const W4TilesParams& p, int64_t units, int sm_count, bool dependent,
+                   cudaStream_t s) {
+  if (bn == 32) return launch<MODE, 32>(dtype, w, x, p, units, sm_count, dependent, s);
+  if (bn == 64) return launch<MODE, 64>(dtype, w, x, p, units, sm_count, dependent, s);
+  if (bn == 128) return launch<MODE, 128>(dtype, w, x, p, units, sm_count, dependent, s);
+  return launch<MODE, 256>(dtype, w, x, p, units, sm_count, dependent, s);
 }
 
 // ---- joining the parts of k of a linear layer ---------------------------------------
@@ -558,6 +622,26 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const MoeSort q) {
   }
 }
 
+// ---- the picks' tokens in expert order -------------------------------------------------
+// (tile::gather4 reads them where they are, but took 80 cycles for four pieces of 128
+// bytes: 895 us for 24576 picks of 2048 elements against 64 experts)
+__global__ void __launch_bounds__(256)
+    gather_kernel(const uint16_t* __restrict__ x, int64_t x_stride, const int* __restrict__ offsets,
+                  int experts, const int* __restrict__ token_of, int width,
+                  uint16_t* __restrict__ to) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int octets = width / 8, picks = offsets[experts];
+  const int64_t total = (int64_t)picks * octets;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t pos = i / octets;
+    const int c = (int)(i - pos * octets) * 8;
+    *reinterpret_cast<uint4*>(to + pos * width + c) =
+        *reinterpret_cast<const uint4*>(x + token_of[pos] * x_stride + c);
+  }
+}
+
 // ---- a token's picks added up -------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -604,17 +688,23 @@ int width_for(int64_t tokens) {
   return tokens <= 32 ? 32 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256;
 }
 
+int tiles_of(int64_t rows, int width) {
+  const int tile = width >= kPairWidth ? 2 * kRows : kRows;
+  return (int)((rows + tile - 1) / tile);
+}
+
 bool maps(int dtype, const W4& w, int64_t rows, int64_t k, const void* x, int64_t x_rows,
-          int64_t x_stride, int box_rows, CUtensorMap* map_w, CUtensorMap* map_x) {
+          int64_t x_stride, int width, CUtensorMap* map_w, CUtensorMap* map_x) {
   return encode_map(map_w, LBGEMM_MAP_U8, w.codes, k / 2, rows, k / 2, kSlice / 2, kRows, 64) &&
-         encode_map(map_x, dtype, x, k, x_rows, x_stride * 2, 64, box_rows, 128);
+         encode_map(map_x, dtype, x, k, x_rows, x_stride * 2, 64,
+                    width >= kPairWidth ? width / 2 : width, 128);
 }
 
 int64_t round16(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // Where a mixture's scratch lies.
 struct MoeScratch {
-  int64_t h, out, counts, offsets, token_of, pos_of, bytes;
+  int64_t h, x, out, counts, offsets, token_of, pos_of, bytes;
   int pieces, piece;
 };
 MoeScratch moe_scratch(const MoeParams& m) {
@@ -623,7 +713,9 @@ MoeScratch moe_scratch(const MoeParams& m) {
   z.piece = (int)std::max<int64_t>(4096, (picks + 63) / 64);
   z.pieces = (int)((picks + z.piece - 1) / z.piece);
   z.h = 0;
-  z.out = z.h + round16(picks * m.inter * 2);
+  z.x = z.h + round16(picks * m.inter * 2);
+  // (the tokens in expert order are read before the outputs are written)
+  z.out = z.x;
   z.counts = z.out + round16(picks * m.hidden * 4);
   z.offsets = z.counts + round16((int64_t)z.pieces * m.experts * 4);
   z.token_of = z.offsets + round16((m.experts + 1) * 4);
@@ -636,12 +728,13 @@ MoeScratch moe_scratch(const MoeParams& m) {
 void cut_linear(const W4LinearParams& l, int sm_count, int* bn, W4TilesParams* p) {
   *bn = width_for(l.m);
   p->blocks = (int)((l.m + *bn - 1) / *bn);
-  p->row_tiles = (int)((l.n + kRows - 1) / kRows);
+  p->row_tiles = tiles_of(l.n, *bn);
   p->slices = (int)((l.k + kSlice - 1) / kSlice);
   const int64_t tiles = (int64_t)p->blocks * p->row_tiles;
+  const int slots = *bn >= kPairWidth ? sm_count / 2 : sm_count;
   p->parts = 1;
-  if (2 * tiles <= sm_count)
-    p->parts = std::max(1, std::min((int)(sm_count / tiles), p->slices / 4));
+  if (2 * tiles <= slots)
+    p->parts = std::max(1, std::min((int)(slots / tiles), p->slices / 4));
   p->part_slices = (p->slices + p->parts - 1) / p->parts;
   p->parts = (p->slices + p->part_slices - 1) / p->part_slices;
 }
@@ -673,8 +766,7 @@ cudaError_t launch_w4_tiles_linear(int dtype, const W4LinearParams& l, void* scr
   if (!maps(dtype, l.w, l.n, l.k, l.x, l.m, l.x_stride, bn, &map_w, &map_x))
     return cudaErrorInvalidValue;
   const int64_t units = (int64_t)p.blocks * p.row_tiles * p.parts;
-  cudaError_t e = launch<kLinear>(dtype, bn, map_w, map_x, p,
-                                  (int)std::min<int64_t>(units, sm_count), false, s);
+  cudaError_t e = launch<kLinear>(dtype, bn, map_w, map_x, p, units, sm_count, false, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   if (p.parts == 1) return e;
@@ -736,27 +828,34 @@ cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, in
   CUtensorMap map_w, map_x;
   p.n = 2 * (int64_t)m.inter;
   p.k = m.hidden;
-  p.row_tiles = (int)((p.n + kRows - 1) / kRows);
+  p.row_tiles = tiles_of(p.n, bn);
   p.slices = p.part_slices = (p.k + kSlice - 1) / kSlice;
   p.scales = m.up.scales;
   p.row_scales = m.up.row_scales;
   p.out = at + z.h;
   p.out_stride = m.inter;
-  if (!maps(dtype, m.up, m.experts * p.n, p.k, m.x, m.tokens, m.x_stride, 1, &map_w, &map_x))
+  uint16_t* x = reinterpret_cast<uint16_t*>(at + z.x);
+  e = launch_after(gather_kernel, std::min<int64_t>((picks * (m.hidden / 8) + 255) / 256, 16 * sm_count),
+                   256, s, static_cast<const uint16_t*>(m.x), m.x_stride, (const int*)q.offsets,
+                   m.experts, (const int*)q.token_of, m.hidden, x);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  if (!maps(dtype, m.up, m.experts * p.n, p.k, x, picks, m.hidden, bn, &map_w, &map_x))
     return cudaErrorInvalidValue;
-  e = launch<kUp>(dtype, bn, map_w, map_x, p, sm_count, true, s);
+  const int64_t units = INT32_MAX;  // (known on the device only)
+  e = launch<kUp>(dtype, bn, map_w, map_x, p, units, sm_count, true, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   p.n = m.hidden;
   p.k = m.inter;
-  p.row_tiles = (int)((p.n + kRows - 1) / kRows);
+  p.row_tiles = tiles_of(p.n, bn);
   p.slices = p.part_slices = (p.k + kSlice - 1) / kSlice;
   p.scales = m.down.scales;
   p.row_scales = m.down.row_scales;
   p.out = at + z.out;
   if (!maps(dtype, m.down, m.experts * p.n, p.k, at + z.h, picks, m.inter, bn, &map_w, &map_x))
     return cudaErrorInvalidValue;
-  e = launch<kDown>(dtype, bn, map_w, map_x, p, sm_count, true, s);
+  e = launch<kDown>(dtype, bn, map_w, map_x, p, units, sm_count, true, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   const float* out = reinterpret_cast<const float*>(at + z.out);
