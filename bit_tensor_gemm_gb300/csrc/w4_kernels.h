@@ -46,6 +46,7 @@ struct W4TilesParams {
   const float* row_scales = nullptr;
   void* out = nullptr;  // linear: Y, or fp32 [part][m][n]; up: h; down: fp32 [pick][n]
   int64_t out_stride = 0;
+  bool vector = false;  // (linear) Y's rows are 16-byte aligned
   int m = 0;  // tokens (linear) or picks
   int experts = 1;
   const int *offsets = nullptr, *token_of = nullptr;  // [experts + 1]; [picks]

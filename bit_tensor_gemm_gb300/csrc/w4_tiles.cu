@@ -14,11 +14,12 @@
 // halves the tokens that each of them brings and reads (a single CTA's tile of 128 x
 // 256 ran 4096 tokens x 11008 x 4096 at 1.16 PFLOP/s, at the rate of its fills).
 //
-// One persistent CTA an SM, 24 warps: TMA of the codes (0), the MMAs (1, of a pair
-// the even CTA's), TMA of the tokens (2), read-out (4..7), converters (8..23: two
+// One persistent CTA an SM, 28 warps: TMA of the codes (0), the MMAs (1, of a pair
+// the even CTA's), TMA of the tokens (2), read-out (4..11), converters (12..27: two
 // teams that take slices in turn, each two warps to a quarter of the rows).  Tiles of
 // up to 128 tokens have two accumulators, so that a tile is read out beside the next
-// one's MMAs.  A linear layer with few tiles is cut along k and joined by join().
+// one's MMAs.  A reader has a row a lane and turns 32 tokens through shared memory
+// into vectors along the rows.  A linear layer with few tiles is cut along k and joined by join().
 //
 // In a pair the tokens' full barriers, the converters' and the accumulators' empty
 // ones are the even CTA's and count both; the commits of the MMAs go to both.  Every
@@ -40,7 +41,9 @@
 namespace lbg {
 namespace {
 
-constexpr int kThreads = 24 * 32;
+constexpr int kThreads = 28 * 32;
+constexpr int kReaders = 8;          // warps that read accumulators out
+constexpr int kReadBytes = 32 * 80;  // a reader's room to turn 32 tokens of 32 rows: 64 bytes and a pad each
 constexpr int kRows = 128;    // weight rows of a tile
 constexpr int kSlice = 128;   // elements of k of a slice
 constexpr int kSlots = 4;     // slices of converted weights in tensor memory
@@ -54,11 +57,12 @@ template <int BN, bool PAIR>
 struct Layout {
   static constexpr int kTokens = PAIR ? BN / 2 : BN;  // that a CTA brings
   static constexpr int kXStages = kTokens == 128 ? 5 : 8;
-  static constexpr int kWStages = kTokens == 128 ? 6 : 8;
+  static constexpr int kWStages = kTokens == 128 ? 4 : 8;
   static constexpr int kXBytes = kTokens * kSlice * 2;
   static constexpr int kAccs = BN == 256 ? 1 : 2;
   static constexpr int kWOffset = kXStages * kXBytes;
-  static constexpr int kBarOffset = kWOffset + kWStages * kWBytes;
+  static constexpr int kReadOffset = kWOffset + kWStages * kWBytes;
+  static constexpr int kBarOffset = kReadOffset + kReaders * kReadBytes;
   // barriers: xfull, xempty, wfull, wempty, afull, aempty, accfull, accempty, done
   static constexpr int kBars = 2 * (kXStages + kWStages + kSlots + kAccs) + 1;
   static constexpr int kPeerIssued = kBarOffset + 8 * kBars;  // int64
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < XS; ++i) mbar_init(xfull(i), 1), mbar_init(xempty(i), 1);
     for (int i = 0; i < WS; ++i) mbar_init(wfull(i), 1), mbar_init(wempty(i), 8);
     for (int i = 0; i < kSlots; ++i) mbar_init(afull(i), 8 * CTAS), mbar_init(aempty(i), 1);
-    for (int i = 0; i < ACCS; ++i) mbar_init(accfull(i), 1), mbar_init(accempty(i), 4 * CTAS);
+    for (int i = 0; i < ACCS; ++i) mbar_init(accfull(i), 1), mbar_init(accempty(i), kReaders * CTAS);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -329,53 +333,81 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       commit(done);  // arrives once every MMA issued above has completed
     }
-  } else if (warp >= 4 && warp < 8) {
-    // ---- read-out: lane = row, columns = tokens ----
+  } else if (warp >= 4 && warp < 4 + kReaders) {
+    // ---- read-out: lane = row, columns = tokens; the readers of a quarter take 32 in turn ----
     const int quarter = warp & 3;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    uint8_t* turn = smem + L::kReadOffset + (warp - 4) * kReadBytes;
     int acc = 0, parity = 0;
     bool ok = true;
     while (ok && units.next(x)) {
-      const int row = x.row + quarter * 32 + lane;
-      const bool live = row < p.n;
+      const int row0 = x.row + quarter * 32, row = row0 + lane;
       const float scale =
-          live ? __ldg(p.row_scales + (int64_t)x.expert * p.n + row) : 0.0f;
+          row < p.n ? __ldg(p.row_scales + (int64_t)x.expert * p.n + row) : 0.0f;
       if (!(ok = wait_warp(accfull(acc), parity))) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int c0 = 0; c0 < BN; c0 += 32) {
-        if (c0 >= x.count) break;
+      for (int c0 = (warp - 4) / 4 * 32; c0 < min(BN, x.count); c0 += 32 * (kReaders / 4)) {
         uint32_t v[32];
         tmem_ld32(tmem + lanes + acc * BN + c0, v);
         tmem_ld_wait();
-        if (MODE == kUp) {
+        const int64_t first = x.first + c0;
+        const int count = x.count - c0;
+        if (MODE == kDown || p.parts > 1) {
+          float* out = static_cast<float*>(p.out) + ((int64_t)x.part * p.m + first) * p.n + row;
+          if (row < p.n) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
+            for (int j = 0; j < 32; ++j)
+              if (j < count) out[j * p.n] = __uint_as_float(v[j]) * scale;
+          }
+        } else if (MODE == kUp || p.vector) {
+          // BYTES a token of this quarter's rows (up: pairs of rows)
+          constexpr int BYTES = MODE == kUp ? 32 : 64, LANES = BYTES / 16;
+          T* mine = reinterpret_cast<T*>(turn) + (MODE == kUp ? lane / 2 : lane);
+          if (MODE == kUp) {
             // rows 2i (gate) and 2i + 1 (up) sit in neighbouring lanes: the even one takes
-            // column j, the odd one j + 1
-            const float a = __uint_as_float(v[j]) * scale, b = __uint_as_float(v[j + 1]) * scale;
-            const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
-            const float gate = lane & 1 ? other : a, up = lane & 1 ? b : other;
-            const int c = c0 + j + (lane & 1);
-            if (live && c < x.count)
-              static_cast<T*>(p.out)[(int64_t)(x.first + c) * p.out_stride + row / 2] =
-                  from_f32<T>(gate / (1.0f + expf(-gate)) * up);
-          }
-        } else if (MODE == kDown || p.parts > 1) {
-          float* out = static_cast<float*>(p.out) + ((int64_t)x.part * p.m + x.first + c0) * p.n + row;
-          if (live) {
+            // token j, the odd one j + 1
+            float h[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float a = __uint_as_float(v[2 * j]) * scale;
+              const float b = __uint_as_float(v[2 * j + 1]) * scale;
+              const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+              const float gate = lane & 1 ? other : a, up = lane & 1 ? b : other;
+              h[j] = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              mine[(2 * j + (lane & 1)) * (80 / 2)] = from_f32<T>(h[j]);
+          } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (c0 + j < x.count)
-                out[(int64_t)j * p.n] = __uint_as_float(v[j]) * scale;
+              mine[j * (80 / 2)] = from_f32<T>(__uint_as_float(v[j]) * scale);
           }
-        } else {
-          T* out = static_cast<T*>(p.out) + (int64_t)(x.first + c0) * p.out_stride + row;
-          if (live) {
+          __syncwarp();
+          const int piece = lane % LANES;  // 8 elements each
+          const int at = (MODE == kUp ? row0 / 2 : row0) + 8 * piece;
+          const int width = (int)(MODE == kUp ? p.n / 2 : p.n);
+          T* out = static_cast<T*>(p.out) + first * p.out_stride + at;
+#pragma unroll
+          for (int j = lane / LANES; j < 32; j += 32 / LANES) {
+            const uint4 o = *reinterpret_cast<const uint4*>(turn + j * 80 + 16 * piece);
+            if (j < count && at < width) {
+              if (at + 8 <= width) {
+                *reinterpret_cast<uint4*>(out + j * p.out_stride) = o;
+              } else {
+                const T* e = reinterpret_cast<const T*>(&o);
+                for (int i = 0; i < width - at; ++i) out[j * p.out_stride + i] = e[i];
+              }
+            }
+          }
+          __syncwarp();
+        } else {  // rows that are not aligned
+          T* out = static_cast<T*>(p.out) + first * p.out_stride + row;
+          if (row < p.n) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (c0 + j < x.count)
-                out[j * p.out_stride] = from_f32<T>(__uint_as_float(v[j]) * scale);
+              if (j < count) out[j * p.out_stride] = from_f32<T>(__uint_as_float(v[j]) * scale);
           }
         }
       }
@@ -384,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) arrive_even(accempty(acc));
       if (++acc == ACCS) acc = 0, parity ^= 1;
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 4 + kReaders) {
     // ---- converters: a row a lane, half a slice a warp, slices in turn by team ----
-    const int quarter = warp & 3, half = (warp - 8) >> 2 & 1, team = (warp - 8) >> 3;
+    const int quarter = warp & 3, half = warp >> 2 & 1, team = (warp - 4 - kReaders) >> 3;
     const int r = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t scale_row = p.k / p.group;
@@ -760,6 +792,7 @@ cudaError_t launch_w4_tiles_linear(int dtype, const W4LinearParams& l, void* scr
   p.row_scales = l.w.row_scales;
   p.out = p.parts > 1 ? scratch : l.y;
   p.out_stride = l.y_stride;
+  p.vector = l.m == 1 || l.y_stride % 8 == 0;
   p.m = (int)l.m;
   p.status = l.status;
   CUtensorMap map_w, map_x;
