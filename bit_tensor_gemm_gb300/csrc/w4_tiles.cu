@@ -7,7 +7,7 @@
 //
 // The weights are the MMA's A operand, read from tensor memory: converter warps
 // turn a slice of 128 codes a row into halves (exactly, w4_codes.cuh), a row a
-// lane, and store them into one of four slots of tensor memory.  Tokens are the B
+// lane, and store them into a slot of tensor memory.  Tokens are the B
 // operand, brought by TMA (128-byte swizzle).  So shared memory carries a quarter of
 // the weights' bytes of a product of halves, and is bound by the tokens: from 65
 // tokens on a tile is a pair of CTAs' (cta_group::2, 128 weight rows in each), which
@@ -15,14 +15,14 @@
 // 256 ran 4096 tokens x 11008 x 4096 at 1.16 PFLOP/s, at the rate of its fills).
 //
 // One persistent CTA an SM, 28 warps: TMA of the codes (0), the MMAs (1, of a pair
-// the even CTA's), TMA of the tokens (2), read-out (4..11), converters (12..27: two
+// the even CTA's), TMA of the tokens (2) and its relay (3), read-out (4..11), converters (12..27: two
 // teams that take slices in turn, each two warps to a quarter of the rows).  Tiles of
 // up to 128 tokens have two accumulators, so that a tile is read out beside the next
 // one's MMAs.  A reader has a row a lane and turns 32 tokens through shared memory
 // into vectors along the rows.  A linear layer with few tiles is cut along k and joined by join().
 //
-// In a pair the tokens' full barriers, the converters' and the accumulators' empty
-// ones are the even CTA's and count both; the commits of the MMAs go to both.  Every
+// In a pair the full barriers and the accumulators' empty ones are the even CTA's and
+// count both; the commits of the MMAs go to both.  Every
 // wait is bounded; on a time-out the CTAs wind down (copies in flight, own MMAs)
 // before tensor memory is freed.
 #include <cuda_runtime.h>
@@ -46,7 +46,6 @@ constexpr int kReaders = 8;          // warps that read accumulators out
 constexpr int kReadBytes = 32 * 80;  // a reader's room to turn 32 tokens of 32 rows: 64 bytes and a pad each
 constexpr int kRows = 128;    // weight rows of a tile
 constexpr int kSlice = 128;   // elements of k of a slice
-constexpr int kSlots = 4;     // slices of converted weights in tensor memory
 constexpr int kSlotCols = kSlice / 2;
 constexpr int kWBytes = kRows * kSlice / 2;
 
@@ -56,15 +55,16 @@ enum Mode { kLinear, kUp, kDown };
 template <int BN, bool PAIR>
 struct Layout {
   static constexpr int kTokens = PAIR ? BN / 2 : BN;  // that a CTA brings
-  static constexpr int kXStages = kTokens == 128 ? 5 : 8;
-  static constexpr int kWStages = kTokens == 128 ? 4 : 8;
+  // slices of converted weights in tensor memory, and with each a stage of tokens
+  static constexpr int kSlots = BN >= 128 ? 4 : 6;
+  static constexpr int kWStages = kTokens == 128 ? 6 : 8;
   static constexpr int kXBytes = kTokens * kSlice * 2;
   static constexpr int kAccs = BN == 256 ? 1 : 2;
-  static constexpr int kWOffset = kXStages * kXBytes;
+  static constexpr int kWOffset = kSlots * kXBytes;
   static constexpr int kReadOffset = kWOffset + kWStages * kWBytes;
   static constexpr int kBarOffset = kReadOffset + kReaders * kReadBytes;
-  // barriers: xfull, xempty, wfull, wempty, afull, aempty, accfull, accempty, done
-  static constexpr int kBars = 2 * (kXStages + kWStages + kSlots + kAccs) + 1;
+  // barriers: xfull, wfull, wempty, full, empty, accfull, accempty, done
+  static constexpr int kBars = 3 * kSlots + 2 * (kWStages + kAccs) + 1;
   static constexpr int kPeerIssued = kBarOffset + 8 * kBars;  // int64
   static constexpr int kTmemSlot = kPeerIssued + 8;
   static constexpr int kUsed = kTmemSlot + 8 + 1024;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_x, const W4TilesParams p) {
   using L = Layout<BN, PAIR>;
-  constexpr int XS = L::kXStages, WS = L::kWStages, ACCS = L::kAccs;
+  constexpr int SLOTS = L::kSlots, WS = L::kWStages, ACCS = L::kAccs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -153,13 +153,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = smem_addr(smem);
   const uint32_t bars = base + L::kBarOffset;
   auto xfull = [&](int i) { return bars + 8u * i; };
-  auto xempty = [&](int i) { return bars + 8u * (XS + i); };
-  auto wfull = [&](int i) { return bars + 8u * (2 * XS + i); };
-  auto wempty = [&](int i) { return bars + 8u * (2 * XS + WS + i); };
-  auto afull = [&](int i) { return bars + 8u * (2 * XS + 2 * WS + i); };
-  auto aempty = [&](int i) { return bars + 8u * (2 * XS + 2 * WS + kSlots + i); };
-  auto accfull = [&](int i) { return bars + 8u * (2 * (XS + WS + kSlots) + i); };
-  auto accempty = [&](int i) { return bars + 8u * (2 * (XS + WS + kSlots) + ACCS + i); };
+  auto full = [&](int i) { return bars + 8u * (SLOTS + i); };
+  auto empty = [&](int i) { return bars + 8u * (2 * SLOTS + i); };
+  auto wfull = [&](int i) { return bars + 8u * (3 * SLOTS + i); };
+  auto wempty = [&](int i) { return bars + 8u * (3 * SLOTS + WS + i); };
+  auto accfull = [&](int i) { return bars + 8u * (3 * SLOTS + 2 * WS + i); };
+  auto accempty = [&](int i) { return bars + 8u * (3 * SLOTS + 2 * WS + ACCS + i); };
   const uint32_t done = bars + 8u * (L::kBars - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kTmemSlot + 4);
@@ -187,9 +186,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     *peer_issued = 0;
-    for (int i = 0; i < XS; ++i) mbar_init(xfull(i), 1), mbar_init(xempty(i), 1);
     for (int i = 0; i < WS; ++i) mbar_init(wfull(i), 1), mbar_init(wempty(i), 8);
-    for (int i = 0; i < kSlots; ++i) mbar_init(afull(i), 8 * CTAS), mbar_init(aempty(i), 1);
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(xfull(i), 1);
+      mbar_init(full(i), 8 * CTAS + 1);  // the converters, and the tokens' relay
+      mbar_init(empty(i), 1);
+    }
     for (int i = 0; i < ACCS; ++i) mbar_init(accfull(i), 1), mbar_init(accempty(i), kReaders * CTAS);
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       while (ok && units.next(x))
         for (int s = x.slice; s < x.end; ++s) {
-          if (!(ok = mbar_wait(xempty(stage), parity, abort_flag, p.status))) break;
+          if (!(ok = mbar_wait(empty(stage), parity, abort_flag, p.status))) break;
           const uint32_t dst = base + stage * L::kXBytes;
           const int row = x.first + (even ? 0 : L::kTokens);
 #pragma unroll
@@ -285,11 +287,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           ++issued;
-          if (++stage == XS) stage = 0, parity ^= 1;
+          if (++stage == SLOTS) stage = 0, parity ^= 1;
         }
       if (!ok && !PAIR)
-        for (int64_t i = min(issued, (int64_t)XS); i > 0; --i) {
-          if (--stage < 0) stage = XS - 1, parity ^= 1;
+        for (int64_t i = min(issued, (int64_t)SLOTS); i > 0; --i) {
+          if (--stage < 0) stage = SLOTS - 1, parity ^= 1;
           wait_drain(xfull(stage), parity ^ 1, p.status);
         }
       if (PAIR && !even)
@@ -299,17 +301,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- the MMAs ----
     if (even && lane == 0) {
       constexpr uint32_t idesc = instr<T>(kRows * CTAS, BN);
-      int stage = 0, xparity = 0, slot = 0, aparity = 0, acc = 0, cparity = 1;
+      int slot = 0, parity = 0, acc = 0, cparity = 1;
       bool ok = true;
       while (ok && units.next(x)) {
         if (!(ok = wait_both(accempty(acc), cparity))) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
         for (int s = x.slice; s < x.end; ++s) {
-          if (!(ok = mbar_wait(xfull(stage), xparity, abort_flag, p.status))) break;
-          if (!(ok = wait_both(afull(slot), aparity))) break;
+          if (!(ok = wait_both(full(slot), parity))) break;
           tc_fence_after();
-          const uint64_t desc = smem_desc_sw128(base + stage * L::kXBytes);
+          const uint64_t desc = smem_desc_sw128(base + slot * L::kXBytes);
           const uint32_t a = tmem + L::kACol + slot * kSlotCols;
           const int pieces = min(kSlice, p.k - s * kSlice) / 16;
 #pragma unroll
@@ -322,16 +323,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               else
                 mma_f16_ts(d, a + 8 * i, b, idesc, more);
             }
-          commit(xempty(stage));
-          commit(aempty(slot));
-          if (++stage == XS) stage = 0, xparity ^= 1;
-          if (++slot == kSlots) slot = 0, aparity ^= 1;
+          commit(empty(slot));
+          if (++slot == SLOTS) slot = 0, parity ^= 1;
         }
         if (!ok) break;
         commit(accfull(acc));
         if (++acc == ACCS) acc = 0, cparity ^= 1;
       }
       commit(done);  // arrives once every MMA issued above has completed
+    }
+  } else if (warp == 3) {
+    // ---- relay: a slice's tokens are there (one wait less for the MMAs' thread, whose
+    // waits and commits cost it as much as a slice's MMAs take) ----
+    if (even && lane == 0) {
+      int stage = 0, parity = 0;
+      bool ok = true;
+      while (ok && units.next(x))
+        for (int s = x.slice; s < x.end; ++s) {
+          if (!(ok = mbar_wait(xfull(stage), parity, abort_flag, p.status))) break;
+          mbar_arrive(full(stage));
+          if (++stage == SLOTS) stage = 0, parity ^= 1;
+        }
     }
   } else if (warp >= 4 && warp < 4 + kReaders) {
     // ---- read-out: lane = row, columns = tokens; the readers of a quarter take 32 in turn ----
@@ -437,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       uint32_t ahead[2] = {scale_at(s, 0), scale_at(s, 1)};
       for (int i = mine; s < x.end; s += 2, i += 2) {
-        const int stage = i % WS, slot = i % kSlots;
+        const int stage = i % WS, slot = i % SLOTS;
         W4Scale<T> sc[2];
         w4_scales(ahead[0], ahead[1], sc[0], sc[1]);
         ahead[0] = scale_at(s + 2, 0);
@@ -459,14 +471,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) words[16 * q + 4 * j + k] = o[k];
           }
         }
-        if (!(ok = wait_warp(aempty(slot), ((uint32_t)(i / kSlots) & 1u) ^ 1u))) break;
+        if (!(ok = wait_warp(empty(slot), ((uint32_t)(i / SLOTS) & 1u) ^ 1u))) break;
         tc_fence_after();
         tmem_st32(tmem + lanes + L::kACol + slot * kSlotCols + half * 32, words);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          arrive_even(afull(slot));
+          arrive_even(full(slot));
           mbar_arrive(wempty(stage));
         }
       }
@@ -478,17 +490,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (PAIR) {
     cluster_sync_all();  // the odd CTA's number of copies has reached the even one
     if (even && warp == 2 && lane == 0) {
-      // Copies may be in flight only after a time-out, the last XS of the CTA that
+      // Copies may be in flight only after a time-out, the last of the CTA that
       // issued more: one that the other never issued gets its half armed or completed
       // here, so that its phase ends when the issued half has landed.
       const int64_t peer = *peer_issued, most = max(issued, peer);
-      for (int64_t j = max(most - XS, (int64_t)0); j < most; ++j) {
-        const int stage = (int)(j % XS);
+      for (int64_t j = max(most - SLOTS, (int64_t)0); j < most; ++j) {
+        const int stage = (int)(j % SLOTS);
         if (j >= issued)
           mbar_arrive_expect_tx(xfull(stage), L::kXBytes);
         else if (j >= peer)
           mbar_complete_tx(xfull(stage), L::kXBytes);
-        wait_drain(xfull(stage), (uint32_t)(j / XS) & 1u, p.status);
+        wait_drain(xfull(stage), (uint32_t)(j / SLOTS) & 1u, p.status);
       }
     }
   }
