@@ -14,9 +14,9 @@
 // halves the tokens that each of them brings and reads (a single CTA's tile of 128 x
 // 256 ran 4096 tokens x 11008 x 4096 at 1.16 PFLOP/s, at the rate of its fills).
 //
-// One persistent CTA an SM, 28 warps: TMA of the codes (0), the MMAs (1, of a pair
-// the even CTA's), TMA of the tokens (2) and its relay (3), read-out (4..11), converters (12..27: two
-// teams that take slices in turn, each two warps to a quarter of the rows).  Tiles of
+// One persistent CTA an SM: warps for TMA of the codes (0), the MMAs (1, of a pair
+// the even CTA's), TMA of the tokens (2), read-out (4..11), converters (12 on: four
+// teams, of long slices three, that take slices in turn, a warp a quarter of the rows).  Tiles of
 // up to 128 tokens have two accumulators, so that a tile is read out beside the next
 // one's MMAs.  A reader has a row a lane and turns 32 tokens through shared memory
 // into vectors along the rows.  A linear layer with few tiles is cut along k and joined by join().
@@ -41,36 +41,45 @@
 namespace lbg {
 namespace {
 
-constexpr int kThreads = 28 * 32;
 constexpr int kReaders = 8;          // warps that read accumulators out
 constexpr int kReadBytes = 32 * 80;  // a reader's room to turn 32 tokens of 32 rows: 64 bytes and a pad each
 constexpr int kRows = 128;    // weight rows of a tile
-constexpr int kSlice = 128;   // elements of k of a slice
-constexpr int kSlotCols = kSlice / 2;
-constexpr int kWBytes = kRows * kSlice / 2;
 
 enum Mode { kLinear, kUp, kDown };
+
+constexpr int slice_for(int width) { return width <= 64 ? 256 : 128; }
 
 // PAIR: the tile's tokens are split between the CTAs.
 template <int BN, bool PAIR>
 struct Layout {
   static constexpr int kTokens = PAIR ? BN / 2 : BN;  // that a CTA brings
-  // slices of converted weights in tensor memory, and with each a stage of tokens
-  static constexpr int kSlots = BN >= 128 ? 4 : 6;
-  static constexpr int kWStages = kTokens == 128 ? 6 : 8;
+  // Elements of k of a slice.  What a slice costs in waits and commits is as much as
+  // its MMAs take below 128 tokens, so slices are longer there.
+  static constexpr int kSlice = slice_for(BN);
+  static constexpr int kSlotCols = kSlice / 2;
+  static constexpr int kWBytes = kRows * kSlice / 2;
+  static constexpr int kBoxes = kSlice / 64;         // of tokens
+  static constexpr int kSlots = kSlice == 256 ? 3 : 4;  // slices of converted weights
+  static constexpr int kTeams = kSlots;
+  static constexpr int kThreads = 32 * (4 + kReaders + 4 * kTeams);
+  static constexpr int kXStages = BN == 256 ? 4 : BN == 128 ? 8 : BN == 64 ? 3 : 6;
+  static constexpr int kWStages = kSlice == 256 ? 6 : 8;
   static constexpr int kXBytes = kTokens * kSlice * 2;
   static constexpr int kAccs = BN == 256 ? 1 : 2;
-  static constexpr int kWOffset = kSlots * kXBytes;
+  static constexpr int kWOffset = kXStages * kXBytes;
   static constexpr int kReadOffset = kWOffset + kWStages * kWBytes;
   static constexpr int kBarOffset = kReadOffset + kReaders * kReadBytes;
-  // barriers: xfull, wfull, wempty, full, empty, accfull, accempty, done
-  static constexpr int kBars = 3 * kSlots + 2 * (kWStages + kAccs) + 1;
+  // barriers: xfull, xempty, full, empty, wfull, wempty, accfull, accempty, done
+  static constexpr int kBars = 2 * (kXStages + kSlots + kWStages + kAccs) + 1;
   static constexpr int kPeerIssued = kBarOffset + 8 * kBars;  // int64
   static constexpr int kTmemSlot = kPeerIssued + 8;
   static constexpr int kUsed = kTmemSlot + 8 + 1024;
   // more than half of an SM's, so that no two CTAs share its tensor memory
   static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
   static constexpr int kACol = kAccs * BN;  // first column of the slots
+  // A slot and a stage of codes are always the same team's: a team may be a round ahead
+  // of another, and a barrier tells one round from the next only.
+  static_assert(kSlots % kTeams == 0 && kWStages % kTeams == 0, "teams");
   static_assert(kACol + kSlots * kSlotCols <= 512, "tensor memory");
   static_assert(kBytes + 4 * (kTilesMaxExperts + 1) + 64 <= 232448, "shared memory");
 };
@@ -141,11 +150,12 @@ struct Units {
 };
 
 template <typename T, int MODE, int BN, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Layout<BN, PAIR>::kThreads, 1)
     w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_x, const W4TilesParams p) {
   using L = Layout<BN, PAIR>;
-  constexpr int SLOTS = L::kSlots, WS = L::kWStages, ACCS = L::kAccs;
+  constexpr int kSlice = L::kSlice, kSlotCols = L::kSlotCols, kWBytes = L::kWBytes;
+  constexpr int XS = L::kXStages, SLOTS = L::kSlots, WS = L::kWStages, ACCS = L::kAccs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -153,12 +163,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = smem_addr(smem);
   const uint32_t bars = base + L::kBarOffset;
   auto xfull = [&](int i) { return bars + 8u * i; };
-  auto full = [&](int i) { return bars + 8u * (SLOTS + i); };
-  auto empty = [&](int i) { return bars + 8u * (2 * SLOTS + i); };
-  auto wfull = [&](int i) { return bars + 8u * (3 * SLOTS + i); };
-  auto wempty = [&](int i) { return bars + 8u * (3 * SLOTS + WS + i); };
-  auto accfull = [&](int i) { return bars + 8u * (3 * SLOTS + 2 * WS + i); };
-  auto accempty = [&](int i) { return bars + 8u * (3 * SLOTS + 2 * WS + ACCS + i); };
+  auto xempty = [&](int i) { return bars + 8u * (XS + i); };
+  auto full = [&](int i) { return bars + 8u * (2 * XS + i); };
+  auto empty = [&](int i) { return bars + 8u * (2 * XS + SLOTS + i); };
+  auto wfull = [&](int i) { return bars + 8u * (2 * (XS + SLOTS) + i); };
+  auto wempty = [&](int i) { return bars + 8u * (2 * (XS + SLOTS) + WS + i); };
+  auto accfull = [&](int i) { return bars + 8u * (2 * (XS + SLOTS + WS) + i); };
+  auto accempty = [&](int i) { return bars + 8u * (2 * (XS + SLOTS + WS) + ACCS + i); };
   const uint32_t done = bars + 8u * (L::kBars - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kTmemSlot + 4);
@@ -166,16 +177,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const bool even = !PAIR || cluster_rank() == 0;
   constexpr int CTAS = PAIR ? 2 : 1;
-  // an arrival on the even CTA's barrier, and a wait for one that both CTAs arrive on
+  // An arrival on the even CTA's barrier.  What the arrivals of the converters and
+  // readers say is about tensor memory, which tcgen05's own waits and fences order: a
+  // release to the other CTA (0.70 us a slice of 256 tokens with it, 0.58 without) has
+  // nothing to add.
   auto arrive_even = [&](uint32_t bar) {
     if (!PAIR || even)
       mbar_arrive(bar);
     else
-      mbar_arrive_cluster(cluster_map(bar, 0));
-  };
-  auto wait_both = [&](uint32_t bar, uint32_t parity) {
-    return PAIR ? mbar_wait_cluster(bar, parity, abort_flag, p.status)
-                : mbar_wait(bar, parity, abort_flag, p.status);
+      mbar_arrive_cluster_relaxed(cluster_map(bar, 0));
   };
   auto commit = [&](uint32_t bar) {
     if (PAIR)
@@ -186,10 +196,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     *peer_issued = 0;
-    for (int i = 0; i < WS; ++i) mbar_init(wfull(i), 1), mbar_init(wempty(i), 8);
+    for (int i = 0; i < WS; ++i) mbar_init(wfull(i), 1), mbar_init(wempty(i), 4);
+    for (int i = 0; i < XS; ++i) mbar_init(xfull(i), 1), mbar_init(xempty(i), 1);
     for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(xfull(i), 1);
-      mbar_init(full(i), 8 * CTAS + 1);  // the converters, and the tokens' relay
+      mbar_init(full(i), 4 * CTAS);
       mbar_init(empty(i), 1);
     }
     for (int i = 0; i < ACCS; ++i) mbar_init(accfull(i), 1), mbar_init(accempty(i), kReaders * CTAS);
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (MODE != kLinear) {
-    for (int e = threadIdx.x; e < p.experts; e += kThreads)
+    for (int e = threadIdx.x; e < p.experts; e += L::kThreads)
       before[e + 1] = (p.offsets[e + 1] - p.offsets[e] + BN - 1) / BN;
     __syncthreads();
     if (warp == 0) {  // running sums
@@ -270,12 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       while (ok && units.next(x))
         for (int s = x.slice; s < x.end; ++s) {
-          if (!(ok = mbar_wait(empty(stage), parity, abort_flag, p.status))) break;
+          if (!(ok = mbar_wait(xempty(stage), parity, abort_flag, p.status))) break;
           const uint32_t dst = base + stage * L::kXBytes;
           const int row = x.first + (even ? 0 : L::kTokens);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            // (where the second box would begin past the row, any: no MMA reads it)
+          for (int b = 0; b < L::kBoxes; ++b) {
+            // (a box that would begin past the row is any other: no MMA reads it)
             const int k = s * kSlice + 64 * b < p.k ? s * kSlice + 64 * b : 0;
             if (PAIR) {
               if (even && b == 0) mbar_arrive_expect_tx(xfull(stage), 2 * L::kXBytes);
@@ -287,11 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           ++issued;
-          if (++stage == SLOTS) stage = 0, parity ^= 1;
+          if (++stage == XS) stage = 0, parity ^= 1;
         }
       if (!ok && !PAIR)
-        for (int64_t i = min(issued, (int64_t)SLOTS); i > 0; --i) {
-          if (--stage < 0) stage = SLOTS - 1, parity ^= 1;
+        for (int64_t i = min(issued, (int64_t)XS); i > 0; --i) {
+          if (--stage < 0) stage = XS - 1, parity ^= 1;
           wait_drain(xfull(stage), parity ^ 1, p.status);
         }
       if (PAIR && !even)
@@ -301,16 +311,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- the MMAs ----
     if (even && lane == 0) {
       constexpr uint32_t idesc = instr<T>(kRows * CTAS, BN);
-      int slot = 0, parity = 0, acc = 0, cparity = 1;
+      int stage = 0, xparity = 0, slot = 0, parity = 0, acc = 0, cparity = 1;
       bool ok = true;
       while (ok && units.next(x)) {
-        if (!(ok = wait_both(accempty(acc), cparity))) break;
+        if (!(ok = mbar_wait(accempty(acc), cparity, abort_flag, p.status))) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
         for (int s = x.slice; s < x.end; ++s) {
-          if (!(ok = wait_both(full(slot), parity))) break;
+          if (!(ok = mbar_wait(xfull(stage), xparity, abort_flag, p.status))) break;
+          if (!(ok = mbar_wait(full(slot), parity, abort_flag, p.status))) break;
           tc_fence_after();
-          const uint64_t desc = smem_desc_sw128(base + slot * L::kXBytes);
+          const uint64_t desc = smem_desc_sw128(base + stage * L::kXBytes);
           const uint32_t a = tmem + L::kACol + slot * kSlotCols;
           const int pieces = min(kSlice, p.k - s * kSlice) / 16;
 #pragma unroll
@@ -324,6 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_f16_ts(d, a + 8 * i, b, idesc, more);
             }
           commit(empty(slot));
+          commit(xempty(stage));
+          if (++stage == XS) stage = 0, xparity ^= 1;
           if (++slot == SLOTS) slot = 0, parity ^= 1;
         }
         if (!ok) break;
@@ -331,19 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++acc == ACCS) acc = 0, cparity ^= 1;
       }
       commit(done);  // arrives once every MMA issued above has completed
-    }
-  } else if (warp == 3) {
-    // ---- relay: a slice's tokens are there (one wait less for the MMAs' thread, whose
-    // waits and commits cost it as much as a slice's MMAs take) ----
-    if (even && lane == 0) {
-      int stage = 0, parity = 0;
-      bool ok = true;
-      while (ok && units.next(x))
-        for (int s = x.slice; s < x.end; ++s) {
-          if (!(ok = mbar_wait(xfull(stage), parity, abort_flag, p.status))) break;
-          mbar_arrive(full(stage));
-          if (++stage == SLOTS) stage = 0, parity ^= 1;
-        }
     }
   } else if (warp >= 4 && warp < 4 + kReaders) {
     // ---- read-out: lane = row, columns = tokens; the readers of a quarter take 32 in turn ----
@@ -429,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++acc == ACCS) acc = 0, parity ^= 1;
     }
   } else if (warp >= 4 + kReaders) {
-    // ---- converters: a row a lane, half a slice a warp, slices in turn by team ----
-    const int quarter = warp & 3, half = warp >> 2 & 1, team = (warp - 4 - kReaders) >> 3;
+    // ---- converters: a row a lane, slices in turn by team ----
+    const int quarter = warp & 3, team = (warp - 4 - kReaders) >> 2;
     const int r = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t scale_row = p.k / p.group;
@@ -440,40 +440,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && units.next(x)) {
       const uint8_t* scales =
           p.scales + ((int64_t)x.expert * p.n + min(x.row + r, (int)p.n - 1)) * scale_row;
-      // this team's slices; the scales of its next one are loaded ahead
-      int s = x.slice + ((index ^ team) & 1);
-      const int mine = index + ((index ^ team) & 1);
+      const int skip = (team + L::kTeams - index % L::kTeams) % L::kTeams;
+      int s = x.slice + skip;
       auto scale_at = [&](int slice, int piece) -> uint32_t {  // of 32 elements
-        const int at = slice * kSlice + half * 64 + piece * 32;
+        const int at = slice * kSlice + piece * 32;
         return at < p.k && slice < x.end ? __ldg(scales + (at >> shift)) : 0;
       };
-      uint32_t ahead[2] = {scale_at(s, 0), scale_at(s, 1)};
-      for (int i = mine; s < x.end; s += 2, i += 2) {
+      constexpr int PIECES = kSlice / 32;
+      uint32_t ahead[PIECES];
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q) ahead[q] = scale_at(s, q);
+      for (int i = index + skip; s < x.end; s += L::kTeams, i += L::kTeams) {
         const int stage = i % WS, slot = i % SLOTS;
-        W4Scale<T> sc[2];
-        w4_scales(ahead[0], ahead[1], sc[0], sc[1]);
-        ahead[0] = scale_at(s + 2, 0);
-        ahead[1] = scale_at(s + 2, 1);
+        uint32_t bytes[PIECES];
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) bytes[q] = ahead[q];
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) ahead[q] = scale_at(s + L::kTeams, q);
         if (!(ok = wait_warp(wfull(stage), (uint32_t)(i / WS) & 1u))) break;
-        // 64-byte swizzle: piece c of row r sits at piece c ^ (r / 2 % 4)
-        const uint8_t* w = smem + L::kWOffset + stage * kWBytes + r * 64;
-        uint32_t words[32];
+        // 16-byte piece c of row r sits at piece c ^ (r / 2 % 4) of its 64 bytes, or
+        // c ^ (r % 8) of 128: the swizzle by as many bytes
+        const uint8_t* w = smem + L::kWOffset + stage * kWBytes + r * (kSlice / 2);
+        const int turn = kSlice == 128 ? r >> 1 & 3 : r & 7;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint4 c =
-              *reinterpret_cast<const uint4*>(w + (((2 * half + q) ^ (r >> 1 & 3)) << 4));
-          const uint32_t code[4] = {c.x, c.y, c.z, c.w};
+        for (int half = 0; half < kSlice / 64; ++half) {
+          uint32_t words[32];
+          W4Scale<T> sc[2];
+          w4_scales(bytes[2 * half], bytes[2 * half + 1], sc[0], sc[1]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t o[4];
-            w4_word(code[j], sc[q], o);
+          for (int q = 0; q < 2; ++q) {
+            const uint4 c = *reinterpret_cast<const uint4*>(w + (((2 * half + q) ^ turn) << 4));
+            const uint32_t code[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) words[16 * q + 4 * j + k] = o[k];
+            for (int j = 0; j < 4; ++j) {
+              uint32_t o[4];
+              w4_word(code[j], sc[q], o);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) words[16 * q + 4 * j + k] = o[k];
+            }
           }
+          if (half == 0) {
+            if (!(ok = wait_warp(empty(slot), ((uint32_t)(i / SLOTS) & 1u) ^ 1u))) break;
+            tc_fence_after();
+          }
+          tmem_st32(tmem + lanes + L::kACol + slot * kSlotCols + half * 32, words);
         }
-        if (!(ok = wait_warp(empty(slot), ((uint32_t)(i / SLOTS) & 1u) ^ 1u))) break;
-        tc_fence_after();
-        tmem_st32(tmem + lanes + L::kACol + slot * kSlotCols + half * 32, words);
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -494,13 +506,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // issued more: one that the other never issued gets its half armed or completed
       // here, so that its phase ends when the issued half has landed.
       const int64_t peer = *peer_issued, most = max(issued, peer);
-      for (int64_t j = max(most - SLOTS, (int64_t)0); j < most; ++j) {
-        const int stage = (int)(j % SLOTS);
+      for (int64_t j = max(most - XS, (int64_t)0); j < most; ++j) {
+        const int stage = (int)(j % XS);
         if (j >= issued)
           mbar_arrive_expect_tx(xfull(stage), L::kXBytes);
         else if (j >= peer)
           mbar_complete_tx(xfull(stage), L::kXBytes);
-        wait_drain(xfull(stage), (uint32_t)(j / SLOTS) & 1u, p.status);
+        wait_drain(xfull(stage), (uint32_t)(j / XS) & 1u, p.status);
       }
     }
   }
@@ -542,7 +554,7 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const W4TilesPara
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(PAIR ? 2 * (unsigned)std::min<int64_t>(units, sm_count / 2)
                           : (unsigned)std::min<int64_t>(units, sm_count));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Layout<BN, PAIR>::kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -739,7 +751,8 @@ int tiles_of(int64_t rows, int width) {
 
 bool maps(int dtype, const W4& w, int64_t rows, int64_t k, const void* x, int64_t x_rows,
           int64_t x_stride, int width, CUtensorMap* map_w, CUtensorMap* map_x) {
-  return encode_map(map_w, LBGEMM_MAP_U8, w.codes, k / 2, rows, k / 2, kSlice / 2, kRows, 64) &&
+  return encode_map(map_w, LBGEMM_MAP_U8, w.codes, k / 2, rows, k / 2, slice_for(width) / 2, kRows,
+                    slice_for(width) / 2) &&
          encode_map(map_x, dtype, x, k, x_rows, x_stride * 2, 64,
                     width >= kPairWidth ? width / 2 : width, 128);
 }
@@ -773,12 +786,13 @@ void cut_linear(const W4LinearParams& l, int sm_count, int* bn, W4TilesParams* p
   *bn = width_for(l.m);
   p->blocks = (int)((l.m + *bn - 1) / *bn);
   p->row_tiles = tiles_of(l.n, *bn);
-  p->slices = (int)((l.k + kSlice - 1) / kSlice);
+  const int slice = slice_for(*bn);
+  p->slices = (int)((l.k + slice - 1) / slice);
   const int64_t tiles = (int64_t)p->blocks * p->row_tiles;
   const int slots = *bn >= kPairWidth ? sm_count / 2 : sm_count;
   p->parts = 1;
   if (2 * tiles <= slots)
-    p->parts = std::max(1, std::min((int)(slots / tiles), p->slices / 4));
+    p->parts = std::max(1, std::min((int)(slots / tiles), p->slices / (512 / slice)));
   p->part_slices = (p->slices + p->parts - 1) / p->parts;
   p->parts = (p->slices + p->part_slices - 1) / p->part_slices;
 }
@@ -862,6 +876,7 @@ cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, in
   // Blocks of tokens for the average expert; accumulators are read out beside the
   // next tile's MMAs up to 128 tokens, which the experts' short k needs.
   const int bn = std::min(128, width_for((picks + m.experts - 1) / m.experts));
+  const int slice = slice_for(bn);
   W4TilesParams p;
   p.experts = m.experts;
   p.offsets = q.offsets;
@@ -874,7 +889,7 @@ cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, in
   p.n = 2 * (int64_t)m.inter;
   p.k = m.hidden;
   p.row_tiles = tiles_of(p.n, bn);
-  p.slices = p.part_slices = (p.k + kSlice - 1) / kSlice;
+  p.slices = p.part_slices = (p.k + slice - 1) / slice;
   p.scales = m.up.scales;
   p.row_scales = m.up.row_scales;
   p.out = at + z.h;
@@ -894,7 +909,7 @@ cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, in
   p.n = m.hidden;
   p.k = m.inter;
   p.row_tiles = tiles_of(p.n, bn);
-  p.slices = p.part_slices = (p.k + kSlice - 1) / kSlice;
+  p.slices = p.part_slices = (p.k + slice - 1) / slice;
   p.scales = m.down.scales;
   p.row_scales = m.down.row_scales;
   p.out = at + z.out;
