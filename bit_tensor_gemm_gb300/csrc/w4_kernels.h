@@ -44,14 +44,16 @@ struct W4TilesParams {
   int k = 0, group = 0;
   const uint8_t* scales = nullptr;
   const float* row_scales = nullptr;
-  void* out = nullptr;  // linear: Y, or fp32 [part][m][n]; up: h; down: fp32 [pick][n]
+  void* out = nullptr;  // linear: Y; up: h; down: fp32 [pick][n]
   int64_t out_stride = 0;
   bool vector = false;  // (linear) Y's rows are 16-byte aligned
   int m = 0;  // tokens (linear) or picks
   int experts = 1;
   const int *offsets = nullptr, *token_of = nullptr;  // [experts + 1]; [picks]
-  // the cut: blocks of tokens (linear), tiles of rows, slices of k and of a part of it
-  int blocks = 0, row_tiles = 0, slices = 0, parts = 1, part_slices = 0;
+  // The cut: blocks of tokens (linear), tiles of rows, slices of k; tiles that are not cut
+  // along k, parts of the others and a part's slices, and where their shares go.
+  int blocks = 0, row_tiles = 0, slices = 0, whole = 0, parts = 1, part_slices = 0;
+  float* shares = nullptr;  // fp32 [cut tile][part][token][row] of a tile's
   int* status = nullptr;
 };
 struct MoeSort {

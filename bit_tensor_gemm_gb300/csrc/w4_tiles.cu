@@ -108,31 +108,44 @@ __device__ __forceinline__ void mma_pair_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// A unit of work: a tile of rows by a block of tokens by a part of k.
+// A unit of work: a tile of rows by a block of tokens, whole or a part of k of it.
 struct Unit {
   int expert, first, count;  // the block's tokens: place of the first, how many
   int row;                   // first row, in the expert
-  int slice, end, part;      // slices of k
+  int slice, end;            // slices of k
+  int share;                 // of a part: its place among the shares (-1: a whole tile)
 };
+// A linear layer's tiles: `whole` ones, then the rest, each in `parts` parts.
 template <int MODE, int BN, bool PAIR>
 struct Units {
+  static constexpr int kTileRows = PAIR ? 2 * kRows : kRows;
   const W4TilesParams& p;
   const int* before;  // blocks of tokens before an expert's
   int u, step, total, rank, expert = 0;
   __device__ __forceinline__ Units(const W4TilesParams& q, const int* b) : p(q), before(b) {
-    total = (MODE == kLinear ? p.blocks : before[p.experts]) * p.row_tiles * p.parts;
+    if (MODE == kLinear)
+      total = p.whole + (p.blocks * p.row_tiles - p.whole) * p.parts;
+    else
+      total = before[p.experts] * p.row_tiles;
     u = PAIR ? (int)cluster_index() : blockIdx.x;
     step = PAIR ? (int)cluster_count() : gridDim.x;
     rank = PAIR ? (int)cluster_rank() : 0;
   }
   __device__ __forceinline__ bool next(Unit& x) {
     if (u >= total) return false;
-    const int rest = u / p.parts;
-    x.part = u - rest * p.parts;
-    const int block = rest / p.row_tiles;
-    x.row = (rest - block * p.row_tiles) * (PAIR ? 2 * kRows : kRows) + rank * kRows;
-    x.slice = x.part * p.part_slices;
-    x.end = min(x.slice + p.part_slices, p.slices);
+    int tile = u;
+    x.share = -1;
+    x.slice = 0;
+    x.end = p.slices;
+    if (MODE == kLinear && u >= p.whole) {
+      x.share = u - p.whole;
+      tile = x.share / p.parts;
+      x.slice = (x.share - tile * p.parts) * p.part_slices;
+      x.end = min(x.slice + p.part_slices, p.slices);
+      tile += p.whole;
+    }
+    const int block = tile / p.row_tiles;
+    x.row = (tile - block * p.row_tiles) * kTileRows + rank * kRows;
     if (MODE == kLinear) {
       x.expert = 0;
       x.first = block * BN;
@@ -350,32 +363,47 @@ __global__ void __launch_bounds__(Layout<BN, PAIR>::kThreads, 1)
     const int quarter = warp & 3;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     uint8_t* turn = smem + L::kReadOffset + (warp - 4) * kReadBytes;
+    // BYTES a token of this quarter's rows (up: pairs of rows), in 16-byte pieces
+    constexpr int BYTES = MODE == kUp ? 32 : 64, LANES = BYTES / 16;
+    T* const mine = reinterpret_cast<T*>(turn) + (MODE == kUp ? lane / 2 : lane);
+    const int piece = lane % LANES;
+    const int width = (int)(MODE == kUp ? p.n / 2 : p.n);
     int acc = 0, parity = 0;
     bool ok = true;
     while (ok && units.next(x)) {
       const int row0 = x.row + quarter * 32, row = row0 + lane;
       const float scale =
           row < p.n ? __ldg(p.row_scales + (int64_t)x.expert * p.n + row) : 0.0f;
+      const int at = (MODE == kUp ? row0 / 2 : row0) + 8 * piece;
+      const bool shared = MODE == kLinear && x.share >= 0;
+      const bool turned = MODE == kUp || (MODE == kLinear && !shared && p.vector);
+      // the 32 tokens from c0 on, from shared memory to their rows
+      auto put = [&](int c0) {
+        T* out = static_cast<T*>(p.out) + (int64_t)(x.first + c0) * p.out_stride + at;
+#pragma unroll
+        for (int j = lane / LANES; j < 32; j += 32 / LANES) {
+          const uint4 o = *reinterpret_cast<const uint4*>(turn + j * 80 + 16 * piece);
+          if (j < x.count - c0 && at < width) {
+            if (at + 8 <= width) {
+              *reinterpret_cast<uint4*>(out + j * p.out_stride) = o;
+            } else {
+              const T* e = reinterpret_cast<const T*>(&o);
+              for (int i = 0; i < width - at; ++i) out[j * p.out_stride + i] = e[i];
+            }
+          }
+        }
+      };
       if (!(ok = wait_warp(accfull(acc), parity))) break;
       tc_fence_after();
+      int last = -1;  // tokens that are in shared memory
 #pragma unroll 1
       for (int c0 = (warp - 4) / 4 * 32; c0 < min(BN, x.count); c0 += 32 * (kReaders / 4)) {
         uint32_t v[32];
         tmem_ld32(tmem + lanes + acc * BN + c0, v);
+        if (last >= 0) put(last);  // (beside the load)
         tmem_ld_wait();
-        const int64_t first = x.first + c0;
-        const int count = x.count - c0;
-        if (MODE == kDown || p.parts > 1) {
-          float* out = static_cast<float*>(p.out) + ((int64_t)x.part * p.m + first) * p.n + row;
-          if (row < p.n) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < count) out[j * p.n] = __uint_as_float(v[j]) * scale;
-          }
-        } else if (MODE == kUp || p.vector) {
-          // BYTES a token of this quarter's rows (up: pairs of rows)
-          constexpr int BYTES = MODE == kUp ? 32 : 64, LANES = BYTES / 16;
-          T* mine = reinterpret_cast<T*>(turn) + (MODE == kUp ? lane / 2 : lane);
+        if (turned) {
+          __syncwarp();
           if (MODE == kUp) {
             // rows 2i (gate) and 2i + 1 (up) sit in neighbouring lanes: the even one takes
             // token j, the odd one j + 1
@@ -397,29 +425,26 @@ __global__ void __launch_bounds__(Layout<BN, PAIR>::kThreads, 1)
               mine[j * (80 / 2)] = from_f32<T>(__uint_as_float(v[j]) * scale);
           }
           __syncwarp();
-          const int piece = lane % LANES;  // 8 elements each
-          const int at = (MODE == kUp ? row0 / 2 : row0) + 8 * piece;
-          const int width = (int)(MODE == kUp ? p.n / 2 : p.n);
-          T* out = static_cast<T*>(p.out) + first * p.out_stride + at;
-#pragma unroll
-          for (int j = lane / LANES; j < 32; j += 32 / LANES) {
-            const uint4 o = *reinterpret_cast<const uint4*>(turn + j * 80 + 16 * piece);
-            if (j < count && at < width) {
-              if (at + 8 <= width) {
-                *reinterpret_cast<uint4*>(out + j * p.out_stride) = o;
-              } else {
-                const T* e = reinterpret_cast<const T*>(&o);
-                for (int i = 0; i < width - at; ++i) out[j * p.out_stride + i] = e[i];
-              }
-            }
-          }
-          __syncwarp();
-        } else {  // rows that are not aligned
-          T* out = static_cast<T*>(p.out) + first * p.out_stride + row;
+          last = c0;
+        } else if (MODE == kDown || shared) {
+          // down: [pick][n]; a share: [token of the tile][row of the tile]
+          constexpr int TILE = Units<MODE, BN, PAIR>::kTileRows;
+          const int64_t pitch = shared ? TILE : p.n;
+          float* out = static_cast<float*>(shared ? p.shares : p.out) +
+                       (shared ? ((int64_t)x.share * BN + c0) * TILE + row % TILE
+                               : (int64_t)(x.first + c0) * p.n + row);
           if (row < p.n) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (j < count) out[j * p.out_stride] = from_f32<T>(__uint_as_float(v[j]) * scale);
+              if (c0 + j < x.count) out[j * pitch] = __uint_as_float(v[j]) * scale;
+          }
+        } else {  // rows that are not aligned
+          T* out = static_cast<T*>(p.out) + (int64_t)(x.first + c0) * p.out_stride + row;
+          if (row < p.n) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c0 + j < x.count)
+                out[j * p.out_stride] = from_f32<T>(__uint_as_float(v[j]) * scale);
           }
         }
       }
@@ -427,6 +452,8 @@ __global__ void __launch_bounds__(Layout<BN, PAIR>::kThreads, 1)
       __syncwarp();
       if (lane == 0) arrive_even(accempty(acc));
       if (++acc == ACCS) acc = 0, parity ^= 1;
+      if (last >= 0) put(last);  // (beside the next tile's MMAs)
+      __syncwarp();
     }
   } else if (warp >= 4 + kReaders) {
     // ---- converters: a row a lane, slices in turn by team ----
@@ -591,19 +618,23 @@ cudaError_t launch(int dtype, int bn, const CUtensorMap& w, const CUtensorMap& x
 }
 
 // ---- joining the parts of k of a linear layer ---------------------------------------
-// y[m][n] = sum of parts[.][m][n], in order
+// Of the tiles that were cut: y = the sum of their shares, in order.  A block a token
+// of a tile, its threads along the rows.
 template <typename T>
-__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ parts, int count,
-                                                   int64_t m, int64_t n, T* y, int64_t y_stride) {
+__global__ void __launch_bounds__(256)
+    join_kernel(const W4TilesParams p, int width, int tile_rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t total = m * n;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / n, c = i - row * n;
-    float v = 0.0f;
-    for (int q = 0; q < count; ++q) v += parts[q * total + i];
-    y[row * y_stride + c] = from_f32<T>(v);
-  }
+  const int tile = blockIdx.x / width, token = blockIdx.x - tile * width;
+  const int block = (p.whole + tile) / p.row_tiles;
+  const int row = (p.whole + tile - block * p.row_tiles) * tile_rows + threadIdx.x;
+  const int m = block * width + token;
+  if (m >= p.m || row >= p.n) return;
+  const float* share = p.shares + ((int64_t)tile * p.parts * width + token) * tile_rows + threadIdx.x;
+  const int64_t step = (int64_t)width * tile_rows;
+  float v = 0.0f;
+#pragma unroll 4
+  for (int q = 0; q < p.parts; ++q) v += share[q * step];
+  static_cast<T*>(p.out)[m * p.out_stride + row] = from_f32<T>(v);
 }
 
 // ---- picks in expert order --------------------------------------------------------------
@@ -781,20 +812,25 @@ MoeScratch moe_scratch(const MoeParams& m) {
   return z;
 }
 
-// Parts of k for a linear layer whose tiles would leave SMs idle.
+// How a linear layer is cut: tiles that do not make half a wave (of the SMs, or pairs)
+// are cut along k, so that they take one as a whole.  A part has 512 elements at least.
 void cut_linear(const W4LinearParams& l, int sm_count, int* bn, W4TilesParams* p) {
   *bn = width_for(l.m);
   p->blocks = (int)((l.m + *bn - 1) / *bn);
   p->row_tiles = tiles_of(l.n, *bn);
   const int slice = slice_for(*bn);
-  p->slices = (int)((l.k + slice - 1) / slice);
+  p->slices = p->part_slices = (int)((l.k + slice - 1) / slice);
   const int64_t tiles = (int64_t)p->blocks * p->row_tiles;
   const int slots = *bn >= kPairWidth ? sm_count / 2 : sm_count;
+  const int rest = (int)(tiles % slots);
+  p->whole = (int)tiles;
   p->parts = 1;
-  if (2 * tiles <= slots)
-    p->parts = std::max(1, std::min((int)(slots / tiles), p->slices / (512 / slice)));
-  p->part_slices = (p->slices + p->parts - 1) / p->parts;
+  if (rest == 0 || 2 * rest > slots) return;
+  const int parts = std::min(slots / rest, p->slices / (512 / slice));
+  if (parts < 2) return;
+  p->part_slices = (p->slices + parts - 1) / parts;
   p->parts = (p->slices + p->part_slices - 1) / p->part_slices;
+  p->whole = (int)tiles - rest;
 }
 
 }  // namespace
@@ -803,7 +839,8 @@ size_t w4_tiles_linear_scratch(const W4LinearParams& l, int sm_count) {
   W4TilesParams p;
   int bn;
   cut_linear(l, sm_count, &bn, &p);
-  return p.parts > 1 ? (size_t)p.parts * l.m * l.n * sizeof(float) : 0;
+  const size_t shares = ((size_t)p.blocks * p.row_tiles - p.whole) * p.parts;
+  return shares * bn * (bn >= kPairWidth ? 2 * kRows : kRows) * sizeof(float);
 }
 
 cudaError_t launch_w4_tiles_linear(int dtype, const W4LinearParams& l, void* scratch, int sm_count,
@@ -816,27 +853,25 @@ cudaError_t launch_w4_tiles_linear(int dtype, const W4LinearParams& l, void* scr
   p.group = l.group;
   p.scales = l.w.scales;
   p.row_scales = l.w.row_scales;
-  p.out = p.parts > 1 ? scratch : l.y;
+  p.out = l.y;
   p.out_stride = l.y_stride;
   p.vector = l.m == 1 || l.y_stride % 8 == 0;
+  p.shares = static_cast<float*>(scratch);
   p.m = (int)l.m;
   p.status = l.status;
   CUtensorMap map_w, map_x;
   if (!maps(dtype, l.w, l.n, l.k, l.x, l.m, l.x_stride, bn, &map_w, &map_x))
     return cudaErrorInvalidValue;
-  const int64_t units = (int64_t)p.blocks * p.row_tiles * p.parts;
-  cudaError_t e = launch<kLinear>(dtype, bn, map_w, map_x, p, units, sm_count, false, s);
+  const int64_t cut = (int64_t)p.blocks * p.row_tiles - p.whole;
+  cudaError_t e = launch<kLinear>(dtype, bn, map_w, map_x, p, p.whole + cut * p.parts, sm_count,
+                                  false, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
-  if (p.parts == 1) return e;
-  const int64_t blocks = std::min<int64_t>((l.m * l.n + 255) / 256, 8 * sm_count);
-  const float* parts = static_cast<const float*>(scratch);
-  if (dtype == LBGEMM_BF16)
-    e = launch_after(join_kernel<__nv_bfloat16>, blocks, 256, s, parts, p.parts, l.m, l.n,
-                     static_cast<__nv_bfloat16*>(l.y), l.y_stride);
-  else
-    e = launch_after(join_kernel<__half>, blocks, 256, s, parts, p.parts, l.m, l.n,
-                     static_cast<__half*>(l.y), l.y_stride);
+  if (cut == 0) return e;
+  const int rows = bn >= kPairWidth ? 2 * kRows : kRows;
+  e = dtype == LBGEMM_BF16
+          ? launch_after(join_kernel<__nv_bfloat16>, cut * bn, rows, s, p, bn, rows)
+          : launch_after(join_kernel<__half>, cut * bn, rows, s, p, bn, rows);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
@@ -873,9 +908,8 @@ cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, in
   if (e != cudaSuccess) return e;
   *launches += 1;
 
-  // Blocks of tokens for the average expert; accumulators are read out beside the
-  // next tile's MMAs up to 128 tokens, which the experts' short k needs.
-  const int bn = std::min(128, width_for((picks + m.experts - 1) / m.experts));
+  // Blocks of tokens for the average expert.
+  const int bn = width_for((picks + m.experts - 1) / m.experts);
   const int slice = slice_for(bn);
   W4TilesParams p;
   p.experts = m.experts;
@@ -883,13 +917,12 @@ cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, in
   p.token_of = q.token_of;
   p.group = m.group;
   p.m = (int)picks;
-  p.parts = 1;
   p.status = m.status;
   CUtensorMap map_w, map_x;
   p.n = 2 * (int64_t)m.inter;
   p.k = m.hidden;
   p.row_tiles = tiles_of(p.n, bn);
-  p.slices = p.part_slices = (p.k + slice - 1) / slice;
+  p.slices = (p.k + slice - 1) / slice;
   p.scales = m.up.scales;
   p.row_scales = m.up.row_scales;
   p.out = at + z.h;
@@ -909,7 +942,7 @@ cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, in
   p.n = m.hidden;
   p.k = m.inter;
   p.row_tiles = tiles_of(p.n, bn);
-  p.slices = p.part_slices = (p.k + slice - 1) / slice;
+  p.slices = (p.k + slice - 1) / slice;
   p.scales = m.down.scales;
   p.row_scales = m.down.row_scales;
   p.out = at + z.out;
