@@ -28,49 +28,91 @@ namespace {
 
 constexpr int kMaxStages = 4;
 // Blocks an SM is to hold and the shared memory each may take for its ring.
-constexpr int kFwdBlocks = 3, kBwdBlocks = 2;
-constexpr int kFwdRing = 70 * 1024, kBwdRing = 108 * 1024;
+constexpr int kRing = 216 * 1024;
 constexpr int kMostRing = 220 * 1024;  // where one stage alone is more than that
+__host__ __device__ constexpr int blocks_for(int wpr, int vpt, bool back) {
+  return back ? (wpr <= 8 ? 2 : 1) : vpt > 1 ? 1 : wpr <= 8 ? 4 : 2;
+}
 
 struct NormCut {
   int blocks = 0, stages = 0, stage_bytes = 0;
   int groups = 0;  // rows of a stage
 };
 
+// Two numbers; as plain fp32 operations, since the paired ones of this file's other
+// kind cost more in moves here than they save (8192 rows of 4096: 75 against 65 us).
+struct Two {
+  float a, b;
+};
+__device__ __forceinline__ Two two(float a, float b) { return {a, b}; }
+__device__ __forceinline__ Two fma2(Two x, Two y, Two z) {
+  return {fmaf(x.a, y.a, z.a), fmaf(x.b, y.b, z.b)};
+}
+__device__ __forceinline__ Two mul2(Two x, Two y) { return {x.a * y.a, x.b * y.b}; }
+__device__ __forceinline__ Two add2(Two x, Two y) { return {x.a + y.a, x.b + y.b}; }
 template <typename T>
 struct Vec {
-  float2x v[4];
+  Two v[4];
 };
 template <typename T>
-__device__ __forceinline__ Vec<T> load_vec(const T* p) {
+__device__ __forceinline__ Vec<T> vec_of(const Raw8<T>& r) {
   float f[8];
-  unpack8(load8_raw(p), f);
-  return {{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
+  unpack8(r, f);
+  return {{two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7])}};
+}
+template <typename T>
+__device__ __forceinline__ Vec<T> load_vec(const T* p) {
+  return vec_of(load8_raw(p));
+}
+__device__ __forceinline__ uint32_t round2(float lo, float hi, __nv_bfloat16) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t round2(float lo, float hi, __half) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 template <typename T>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T>& x) {
   float f[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) unpair(x.v[i], f[2 * i], f[2 * i + 1]);
-  store8(p, f);
+  for (int i = 0; i < 4; ++i) f[2 * i] = x.v[i].a, f[2 * i + 1] = x.v[i].b;
+  if constexpr (sizeof(T) == 4) {
+    store8(p, f);
+  } else {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(round2(f[0], f[1], T()), round2(f[2], f[3], T()), round2(f[4], f[5], T()),
+                   round2(f[6], f[7], T()));
+  }
 }
-template <typename T>
-__device__ __forceinline__ Vec<T> ones() {
-  const float2x o = pair(1.0f, 1.0f);
-  return {{o, o, o, o}};
-}
-__device__ __forceinline__ float halves(float2x v) {
-  float lo, hi;
-  unpair(v, lo, hi);
-  return lo + hi;
-}
-__device__ __forceinline__ float2x twice(float v) { return pair(v, v); }
+__device__ __forceinline__ float halves(Two v) { return v.a + v.b; }
+__device__ __forceinline__ Two twice(float v) { return two(v, v); }
 
-// Sums of one or two numbers over a row's WPR warps; every thread of the row gets
-// them, in the same order.  `slots`: [2][16] floats of the row, another half for
-// consecutive calls (so one barrier is enough).
+// The WPR warps of a row meet; true where any of them asks to stop.
+template <int WPR>
+__device__ __forceinline__ bool row_meet(int group, bool stop) {
+  if constexpr (WPR == 1) {
+    return __any_sync(0xffffffffu, stop);
+  } else {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(group + 1), "n"(32 * WPR), "r"((int)stop)
+        : "memory");
+    return r != 0;
+  }
+}
+
+// Sums of one or two numbers over a row's warps; every thread of the row gets them, in
+// the same order.  `slots`: [2][16] floats of the row, others for consecutive calls (so
+// one meeting is enough).
 template <int WPR, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float* slots, int warp) {
+__device__ __forceinline__ bool row_sums(float (&v)[N], float* slots, int group, int warp,
+                                         bool stop = false) {
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -79,262 +121,308 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* slots, int warp) 
     if (threadIdx.x % 32 == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) slots[i * 16 + warp] = v[i];
-    __syncthreads();
+  }
+  stop = row_meet<WPR>(group, stop);
+  if constexpr (WPR > 1) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float s = slots[i * 16];
+      v[i] = slots[i * 16 + threadIdx.x % WPR];
 #pragma unroll
-      for (int w = 1; w < WPR; ++w) s += slots[i * 16 + w];
-      v[i] = s;
+      for (int off = WPR / 2; off >= 1; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
     }
   }
+  return stop;
 }
 
-// WPR warps a row, VPT vectors of 8 elements a thread.  The tensors of a stage:
-// x (if any), y, one row of gates each, dx', dn; each [groups][width].
+// WPR warps a row, VPT vectors of 8 elements a thread; the first warp issues the
+// copies (a warp of its own would leave fewer registers to the others).  The tensors of
+// a stage: x, y, a gate for each row, dx', dn, those that are given; each [groups][width].
 template <typename T, int WPR, int VPT, bool BACK>
-__global__ void __launch_bounds__(WPR <= 8 ? 256 : 512)
+__global__ void __launch_bounds__(WPR <= 8 ? 256 : 512, blocks_for(WPR, VPT, BACK))
     residual_norm_kernel(const ResidualNormParams p, const NormCut cut,
                          float* __restrict__ partial) {
   constexpr int THREADS = WPR <= 8 ? 256 : 512;
   constexpr int LANES = 32 * WPR, GROUPS = THREADS / LANES;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ uint64_t bars[kMaxStages];
+  __shared__ uint64_t bars[2 * kMaxStages];
   __shared__ int abort_flag;
-  __shared__ float slots[3][GROUPS][32];
+  __shared__ float slots[4][GROUPS][32];
   const int group = threadIdx.x / LANES, at = threadIdx.x % LANES, warp = at / 32;
   const int width = p.width, vectors = width / 8;
   const int row_bytes = width * (int)sizeof(T);
   const bool own_gate = p.gate && p.gate_stride != 0;
   const float inv = 1.0f / (float)width;
 
-  // which tensors a stage holds, and where
-  const void* src[5];
-  int64_t stride[5];
-  int held = 0, at_x = -1, at_y = -1, at_gate = -1, at_dx = -1, at_dn = -1;
-  auto hold = [&](const void* q, int64_t s, int& where) {
-    if (!q) return;
-    src[held] = q;
-    stride[held] = s;
-    where = held++;
-  };
-  hold(p.x, p.x_stride, at_x);
-  hold(p.y, p.y_stride, at_y);
-  if (own_gate) hold(p.gate, p.gate_stride, at_gate);
-  if (BACK) hold(p.dx_out, p.dx_out_stride, at_dx);
-  if (BACK) hold(p.dn, p.dn_stride, at_dn);
+  // the tensors of a stage, in order
+  const int at_x = 0, at_y = p.y ? 1 : -1;
+  int held = p.y ? 2 : 1;
+  const int at_gate = own_gate ? held++ : -1;
+  const int at_dx = BACK && p.dx_out ? held++ : -1;
+  const int at_dn = BACK && p.dn ? held++ : -1;
 
   const int64_t steps_all = (p.tokens + GROUPS - 1) / GROUPS;
   const int64_t step0 = blockIdx.x, stride_steps = gridDim.x;
+  const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages;
   if (threadIdx.x < cut.stages) {
-    mbar_init(smem_addr(bars) + 8 * threadIdx.x, 1);
+    mbar_init(full + 8 * threadIdx.x, 1);
+    mbar_init(empty + 8 * threadIdx.x, THREADS / 32);
     fence_barrier_init();
   }
   if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
+
   auto issue = [&](int64_t step, int slot) {  // by the first warp
     const int rows = (int)min((int64_t)GROUPS, p.tokens - step * GROUPS);
-    const uint32_t bar = smem_addr(bars) + 8 * slot;
-    const uint32_t dst = smem_addr(ring) + slot * cut.stage_bytes;
+    const uint32_t bar = full + 8 * slot, dst = smem_addr(ring) + slot * cut.stage_bytes;
     if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, (uint32_t)(rows * held * row_bytes));
     __syncwarp();
-    for (int i = threadIdx.x; i < rows * held; i += 32) {
-      const int t = i / rows, r = i - t * rows;
-      const void* base = src[0];
-      int64_t st = stride[0];
-#pragma unroll
-      for (int k = 1; k < 5; ++k)
-        if (k < held && t == k) base = src[k], st = stride[k];
-      bulk_load(dst + (t * GROUPS + r) * row_bytes,
-                static_cast<const T*>(base) + (step * GROUPS + r) * st, row_bytes, bar);
+    for (int i = threadIdx.x; i < held * GROUPS; i += 32) {
+      const int t = i / GROUPS, r = i % GROUPS;
+      const void* from = p.x;
+      int64_t stride = p.x_stride;
+      if (t == at_y) from = p.y, stride = p.y_stride;
+      if (t == at_gate) from = p.gate, stride = p.gate_stride;
+      if (t == at_dx) from = p.dx_out, stride = p.dx_out_stride;
+      if (t == at_dn) from = p.dn, stride = p.dn_stride;
+      if (r < rows)
+        bulk_load(dst + i * row_bytes, static_cast<const T*>(from) + (step * GROUPS + r) * stride,
+                  row_bytes, bar);
     }
+  };
+  // The copy into a slot that all warps are to have read by now; `use`: how often the
+  // slot has been filled before.
+  auto refill = [&](int64_t step, int slot, int use) {
+    if (threadIdx.x >= 32 || step >= steps_all) return;
+    if (__all_sync(0xffffffffu, mbar_wait(empty + 8 * slot, (use - 1) & 1, &abort_flag, p.status)))
+      issue(step, slot);
   };
   if (threadIdx.x < 32)
     for (int s = 0; s < cut.stages; ++s)
       if (step0 + s * stride_steps < steps_all) issue(step0 + s * stride_steps, s);
 
+  // weights of this thread's columns, as they are in memory
+  Raw8<T> w_post[VPT], w_next[VPT], w_gate[VPT];
+  const bool one_gate = p.gate && !own_gate, next = p.next != nullptr, post = p.post != nullptr;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = min(at + j * LANES, vectors - 1);
+    if (post) w_post[j] = load8_raw(static_cast<const T*>(p.post) + v * 8);
+    if (next) w_next[j] = load8_raw(static_cast<const T*>(p.next) + v * 8);
+    if (one_gate) w_gate[j] = load8_raw(static_cast<const T*>(p.gate) + v * 8);
+  }
   Vec<T> sum_post[BACK ? VPT : 1], sum_next[BACK ? VPT : 1], sum_gate[BACK ? VPT : 1];
   if (BACK) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) sum_post[j] = sum_next[j] = sum_gate[j] = {{0, 0, 0, 0}};
+    for (int j = 0; j < VPT; ++j) sum_post[j] = sum_next[j] = sum_gate[j] = {};
   }
-  const T* post = static_cast<const T*>(p.post);
-  const T* next = static_cast<const T*>(p.next);
-  const float2x a2 = twice(p.a), b2 = twice(p.b);
+  const Two a2 = twice(p.a), b2 = twice(p.b);
+  // With one vector a thread, what a row's later passes need stays in registers; with
+  // more it is taken from the stage again.
+  constexpr bool KEEP = VPT == 1;
 
-  int slot = 0, parity = 0;
+  int slot = 0, use = 0;  // the slot of a row, and how often it has been used before
+  bool odd = false;
   for (int64_t step = step0; step < steps_all; step += stride_steps) {
-    // every warp leaves together where the copies do not come
-    const bool ok = mbar_wait(smem_addr(bars) + 8 * slot, parity, &abort_flag, p.status);
-    if (!__syncthreads_and(ok)) break;
+    // (where the copies do not come, the warps of a row leave together below)
+    bool stop = !mbar_wait(full + 8 * slot, use & 1, &abort_flag, p.status);
     const int64_t row = step * GROUPS + group;
-    const bool live = row < p.tokens;  // (a row past the end computes what is there, stores nothing)
-    const uint8_t* stage = ring + slot * cut.stage_bytes + group * row_bytes;
-    auto part = [&](int which, int v) {
-      return load_vec(reinterpret_cast<const T*>(stage + which * GROUPS * row_bytes) + v * 8);
+    // (a row past the end computes what is there, stores nothing)
+    const bool live = GROUPS == 1 || row < p.tokens;
+    const T* stage = reinterpret_cast<const T*>(ring + slot * cut.stage_bytes + group * row_bytes);
+    auto part = [&](int which, int j) {
+      return load_vec(stage + (which * GROUPS * width + (at + j * LANES) * 8));
     };
-    auto gates = [&](int v) {
-      return own_gate ? part(at_gate, v)
-                      : p.gate ? load_vec(static_cast<const T*>(p.gate) + v * 8) : ones<T>();
-    };
+    auto on = [&](int j) { return at + j * LANES < vectors; };
+
+    // ---- rstd(Y) ----
+    Vec<T> y[VPT];  // KEEP: Y, then Y rstd(Y)
     float r1 = 1.0f;
-    if (post) {
-      float2x s = 0;
+    if (at_y >= 0) {
+      Two s = {0, 0};
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int v = at + j * LANES;
-        if (v < vectors) {
-          const Vec<T> y = part(at_y, v);
+        if (!on(j)) continue;
+        y[j] = part(at_y, j);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s = fma2(y.v[i], y.v[i], s);
-        }
+        for (int i = 0; i < 4; ++i) s = fma2(y[j].v[i], y[j].v[i], s);
       }
-      float t[1] = {halves(s)};
-      row_sums<WPR>(t, slots[0][group], warp);
-      r1 = rsqrtf(t[0] * inv + p.eps);
-    }
-    const float2x r1x = twice(r1);
-    // x' of a vector; yhat and what the gate multiplies on the way
-    auto stream = [&](int v, Vec<T>& yhat, Vec<T>& z, Vec<T>& g) {
-      Vec<T> x = at_x >= 0 ? part(at_x, v) : Vec<T>{{0, 0, 0, 0}};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x.v[i] = mul2(x.v[i], a2);
-      if (at_y < 0) return x;
-      yhat = part(at_y, v);
-      z = yhat;
       if (post) {
-        const Vec<T> w = load_vec(post + v * 8);
+        float t[1] = {halves(s)};
+        // (a forward pass without a second norm meets once a row: places in turn)
+        stop = row_sums<WPR>(t, slots[odd ? 3 : 0][group], group, warp, stop);
+        odd = !odd;
+        r1 = rsqrtf(t[0] * inv + p.eps);
+      }
+    }
+    if (!post) stop = row_meet<WPR>(group, stop);
+    if (stop) break;
+    // the slot of the row before, for the row `stages` after that one
+    if (cut.stages > 1 && step > step0)
+      refill(step + (cut.stages - 1) * stride_steps, slot == 0 ? cut.stages - 1 : slot - 1,
+             slot == 0 ? use : use + 1);
+
+    // ---- x', its rstd, mean(next dn xhat) ----
+    const Two r1x = twice(r1);
+    Vec<T> z[VPT], g[VPT], kept[VPT], dn[VPT];  // z; b gate; x'; dn
+    // y = Y rstd(Y), z and b gate of a vector; Y again where it was not kept
+    auto block = [&](int j) {
+      if (!KEEP) y[j] = part(at_y, j);
+      z[j] = y[j];
+      if (post) {
+        const Vec<T> w = vec_of(w_post[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          yhat.v[i] = mul2(yhat.v[i], r1x);
-          z.v[i] = mul2(yhat.v[i], w.v[i]);
+          y[j].v[i] = mul2(y[j].v[i], r1x);
+          z[j].v[i] = mul2(y[j].v[i], w.v[i]);
         }
       }
-      g = gates(v);
+      if (p.gate) {
+        g[j] = own_gate ? part(at_gate, j) : vec_of(w_gate[j]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        g.v[i] = mul2(g.v[i], b2);
-        x.v[i] = fma2(g.v[i], z.v[i], x.v[i]);
+        for (int i = 0; i < 4; ++i) g[j].v[i] = mul2(g[j].v[i], b2);
+      } else {
+        g[j] = {{b2, b2, b2, b2}};
       }
-      return x;
     };
-    float2x s = 0, dot = 0;
-    Vec<T> yhat, z, g;
-    Vec<T> kept[VPT];  // x'
+    Two s = {0, 0}, dot = {0, 0};
+    T* const to_x = !BACK && p.x_out ? static_cast<T*>(p.x_out) + row * p.x_out_stride : nullptr;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int v = at + j * LANES;
-      if (v >= vectors) continue;
-      kept[j] = stream(v, yhat, z, g);
+      if (!on(j)) continue;
+      kept[j] = part(at_x, j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kept[j].v[i] = mul2(kept[j].v[i], a2);
+      if (at_y >= 0) {
+        block(j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kept[j].v[i] = fma2(g[j].v[i], z[j].v[i], kept[j].v[i]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = fma2(kept[j].v[i], kept[j].v[i], s);
       if (BACK && next) {
-        const Vec<T> w = load_vec(next + v * 8), dn = part(at_dn, v);
+        const Vec<T> w = vec_of(w_next[j]);
+        dn[j] = part(at_dn, j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dot = fma2(mul2(w.v[i], dn.v[i]), kept[j].v[i], dot);
+        for (int i = 0; i < 4; ++i) dot = fma2(mul2(w.v[i], dn[j].v[i]), kept[j].v[i], dot);
       }
-      if (!BACK && p.x_out && live)
-        store_vec(static_cast<T*>(p.x_out) + row * p.x_out_stride + v * 8, kept[j]);
+      if (to_x && live) store_vec(to_x + (at + j * LANES) * 8, kept[j]);
     }
     float r2 = 0.0f, mean2 = 0.0f;
     if (next) {
-      float t[2] = {halves(s), halves(dot)};
-      row_sums<WPR>(t, slots[1][group], warp);
-      r2 = rsqrtf(t[0] * inv + p.eps);
-      mean2 = r2 * (t[1] * inv);  // mean(next dn xhat)
+      if constexpr (BACK) {
+        float t[2] = {halves(s), halves(dot)};
+        row_sums<WPR>(t, slots[1][group], group, warp);
+        r2 = rsqrtf(t[0] * inv + p.eps);
+        mean2 = r2 * (t[1] * inv);  // mean(next dn xhat)
+      } else {
+        float t[1] = {halves(s)};
+        row_sums<WPR>(t, slots[1][group], group, warp);
+        r2 = rsqrtf(t[0] * inv + p.eps);
+      }
     }
-    const float2x r2x = twice(r2);
-    if (!BACK) {
+    const Two r2x = twice(r2);
+
+    if constexpr (!BACK) {
+      // ---- n ----
       if (next) {
+        T* const to = static_cast<T*>(p.n_out) + row * p.n_out_stride;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-          const int v = at + j * LANES;
-          if (v >= vectors) continue;
-          const Vec<T> w = load_vec(next + v * 8);
+          if (!on(j)) continue;
+          const Vec<T> w = vec_of(w_next[j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) kept[j].v[i] = mul2(mul2(kept[j].v[i], r2x), w.v[i]);
-          if (live) store_vec(static_cast<T*>(p.n_out) + row * p.n_out_stride + v * 8, kept[j]);
+          if (live) store_vec(to + (at + j * LANES) * 8, kept[j]);
         }
       }
     } else {
-      const float2x m2 = twice(-mean2);
-      float2x dot1 = 0;
-      Vec<T> wdz[VPT];  // post dz
+      // ---- d, dx, dgate, dz ----
+      const Two m2 = twice(-mean2);
+      Two dot1 = {0, 0};
+      T* const to_x = static_cast<T*>(p.dx) + row * p.dx_stride;
+      T* const to_y = static_cast<T*>(p.dy) + row * p.dy_stride;
+      T* const to_gate = static_cast<T*>(p.dgate) + (own_gate ? row * p.dgate_stride : 0);
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int v = at + j * LANES;
-        if (v >= vectors) continue;
-        stream(v, yhat, z, g);
-        Vec<T> d = at_dx >= 0 ? part(at_dx, v) : Vec<T>{{0, 0, 0, 0}};
+        if (!on(j)) continue;
+        const int c = (at + j * LANES) * 8;
+        Vec<T> d = at_dx >= 0 ? part(at_dx, j) : Vec<T>{};
         if (next) {
-          const Vec<T> w = load_vec(next + v * 8), dn = part(at_dn, v);
+          const Vec<T> w = vec_of(w_next[j]);
+          if (!KEEP) dn[j] = part(at_dn, j);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2x xhat = mul2(kept[j].v[i], r2x);
-            if (live) sum_next[j].v[i] = fma2(dn.v[i], xhat, sum_next[j].v[i]);
-            d.v[i] = fma2(r2x, fma2(xhat, m2, mul2(w.v[i], dn.v[i])), d.v[i]);
+            const Two xhat = mul2(kept[j].v[i], r2x);
+            if (live) sum_next[j].v[i] = fma2(dn[j].v[i], xhat, sum_next[j].v[i]);
+            d.v[i] = fma2(r2x, fma2(xhat, m2, mul2(w.v[i], dn[j].v[i])), d.v[i]);
           }
         }
-        if (p.dx && live) {
+        if (live) {
           Vec<T> dx;
 #pragma unroll
           for (int i = 0; i < 4; ++i) dx.v[i] = mul2(d.v[i], a2);
-          store_vec(static_cast<T*>(p.dx) + row * p.dx_stride + v * 8, dx);
+          store_vec(to_x + c, dx);
         }
         if (at_y < 0) continue;
-        if (p.dgate) {
+        if (!KEEP) block(j);
+        if (p.gate) {
           Vec<T> dg;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dg.v[i] = mul2(mul2(d.v[i], b2), z.v[i]);
+          for (int i = 0; i < 4; ++i) dg.v[i] = mul2(mul2(d.v[i], b2), z[j].v[i]);
           if (own_gate) {
-            if (live) store_vec(static_cast<T*>(p.dgate) + row * p.dgate_stride + v * 8, dg);
+            if (live) store_vec(to_gate + c, dg);
           } else if (live) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum_gate[j].v[i] = add2(sum_gate[j].v[i], dg.v[i]);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d.v[i] = mul2(d.v[i], g.v[i]);  // (the gate times b)
+        for (int i = 0; i < 4; ++i) d.v[i] = mul2(d.v[i], g[j].v[i]);  // dz
         if (post) {
-          const Vec<T> w = load_vec(post + v * 8);
+          const Vec<T> w = vec_of(w_post[j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (live) sum_post[j].v[i] = fma2(d.v[i], yhat.v[i], sum_post[j].v[i]);
-            wdz[j].v[i] = mul2(w.v[i], d.v[i]);
-            dot1 = fma2(wdz[j].v[i], yhat.v[i], dot1);
+            if (live) sum_post[j].v[i] = fma2(d.v[i], y[j].v[i], sum_post[j].v[i]);
+            kept[j].v[i] = mul2(w.v[i], d.v[i]);  // (x' has done its part)
+            dot1 = fma2(kept[j].v[i], y[j].v[i], dot1);
           }
         } else if (live) {
-          store_vec(static_cast<T*>(p.dy) + row * p.dy_stride + v * 8, d);
+          store_vec(to_y + c, d);
         }
       }
+      // ---- dy ----
       if (post) {
         float t[1] = {halves(dot1)};
-        row_sums<WPR>(t, slots[2][group], warp);
-        const float2x m1 = twice(-t[0] * inv);
+        row_sums<WPR>(t, slots[2][group], group, warp);
+        const Two m1 = twice(-t[0] * inv);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-          const int v = at + j * LANES;
-          if (v >= vectors) continue;
-          Vec<T> y = part(at_y, v);
+          if (!on(j)) continue;
+          if (!KEEP) {
+            y[j] = part(at_y, j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[j].v[i] = mul2(y[j].v[i], r1x);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            y.v[i] = mul2(r1x, fma2(mul2(y.v[i], r1x), m1, wdz[j].v[i]));
-          if (live) store_vec(static_cast<T*>(p.dy) + row * p.dy_stride + v * 8, y);
+            y[j].v[i] = mul2(r1x, fma2(y[j].v[i], m1, kept[j].v[i]));
+          if (live) store_vec(to_y + (at + j * LANES) * 8, y[j]);
         }
       }
     }
-    // the stage is read: copy the row that comes `stages` steps later over it
-    __syncthreads();
-    const int64_t later = step + cut.stages * stride_steps;
-    if (threadIdx.x < 32 && later < steps_all) issue(later, slot);
-    if (++slot == cut.stages) slot = 0, parity ^= 1;
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(empty + 8 * slot);
+    if (cut.stages == 1) refill(step + stride_steps, 0, use + 1);
+    if (++slot == cut.stages) slot = 0, ++use;
   }
-  if (abort_flag) {  // let the copies in flight land (again with a limit)
+  if (abort_flag) {
+    // Let the copies in flight land (again with a limit): those of the slots from this
+    // row's on.
     volatile int go_on = 0;
     if (threadIdx.x == 0)
       for (int i = 0; i < cut.stages; ++i) {
-        mbar_wait(smem_addr(bars) + 8 * slot, parity, &go_on, p.status, kWaitLimitNs / 8);
-        if (++slot == cut.stages) slot = 0, parity ^= 1;
+        mbar_wait(full + 8 * slot, use & 1, &go_on, p.status, kWaitLimitNs / 8);
+        if (++slot == cut.stages) slot = 0, ++use;
       }
     return;
   }
@@ -349,7 +437,7 @@ __global__ void __launch_bounds__(WPR <= 8 ? 256 : 512)
       auto put = [&](int which, const Vec<T>& x) {
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) unpair(x.v[i], f[2 * i], f[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) f[2 * i] = x.v[i].a, f[2 * i + 1] = x.v[i].b;
         store8<float>(mine + (int64_t)which * width + v * 8, f);
       };
       if (p.dpost) put(0, sum_post[j]);
@@ -364,52 +452,63 @@ __global__ void __launch_bounds__(WPR <= 8 ? 256 : 512)
 struct SumOut {
   float* out[3];
 };
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(256)
     residual_norm_sums_kernel(const float* __restrict__ partial, int rows, int width,
                               const SumOut to) {
-  __shared__ float sh[32][33];
+  __shared__ float4 sh[32][8];
   float* out = blockIdx.y == 0 ? to.out[0] : blockIdx.y == 1 ? to.out[1] : to.out[2];
   if (!out) return;
-  const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-  const int c = blockIdx.x * 32 + x;
-  float v = 0.0f;
-  for (int b = y; b < rows; b += 8 * 32) {
-    float part[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      part[i] = c < width && b + 32 * i < rows
-                    ? partial[((int64_t)(b + 32 * i) * 3 + blockIdx.y) * width + c]
-                    : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v += part[i];
+  const int x = threadIdx.x % 8, y = threadIdx.x / 8;
+  const int c = blockIdx.x * 32 + 4 * x;
+  float4 v = make_float4(0, 0, 0, 0);
+  if (c < width) {
+    const float* from = partial + (int64_t)blockIdx.y * width + c;
+#pragma unroll 5
+    for (int b = y; b < rows; b += 32) {
+      const float4 q = *reinterpret_cast<const float4*>(from + (int64_t)b * 3 * width);
+      v.x += q.x;
+      v.y += q.y;
+      v.z += q.z;
+      v.w += q.w;
+    }
   }
   sh[y][x] = v;
-  __syncthreads();
-  v = sh[x][y];
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  const int mine = blockIdx.x * 32 + y;
-  if (x == 0 && mine < width) out[mine] = v;
+  for (int half = 16; half >= 1; half /= 2) {
+    __syncthreads();
+    if (y < half) {
+      const float4 q = sh[y + half][x];
+      v.x += q.x;
+      v.y += q.y;
+      v.z += q.z;
+      v.w += q.w;
+      sh[y][x] = v;
+    }
+  }
+  if (y == 0 && c < width) *reinterpret_cast<float4*>(out + c) = v;
 }
 
-int warps_per_row(int width) {
+// Warps and vectors a thread for a row.
+struct Shape {
+  int wpr, vpt;
+};
+Shape shape_of(int width) {
   const int vectors = width / 8;
-  for (int w = 1; w < 16; w *= 2)
-    if (vectors <= 32 * w) return w;
-  return 16;
+  for (int w = 1; w <= 16; w *= 2)
+    if (vectors <= 32 * w) return {w, 1};
+  return {16, vectors <= 1024 ? 2 : 4};
 }
 
 NormCut cut_of(int dtype, const ResidualNormParams& p, bool back, int sm_count) {
   NormCut cut;
-  const int wpr = warps_per_row(p.width);
-  cut.groups = wpr <= 8 ? 8 / wpr : 1;
+  const Shape shape = shape_of(p.width);
+  cut.groups = shape.wpr <= 8 ? 8 / shape.wpr : 1;
   const int held = (p.x != nullptr) + (p.y != nullptr) + (p.gate && p.gate_stride != 0) +
                    (back && p.dx_out) + (back && p.dn);
   const int64_t steps = (p.tokens + cut.groups - 1) / cut.groups;
   cut.stage_bytes = cut.groups * p.width * (dtype == LBGEMM_F32 ? 4 : 2) * std::max(held, 1);
-  const int per_sm = back ? kBwdBlocks : kFwdBlocks;
+  const int per_sm = blocks_for(shape.wpr, shape.vpt, back);
   cut.blocks = (int)std::min<int64_t>(steps, (int64_t)sm_count * per_sm);
-  cut.stages = std::min(kMaxStages, (back ? kBwdRing : kFwdRing) / cut.stage_bytes);
+  cut.stages = std::min(kMaxStages, kRing / per_sm / cut.stage_bytes);
   if (cut.stages < 2) cut.stages = std::max(1, std::min(2, kMostRing / cut.stage_bytes));
   if (cut.blocks > 0)
     cut.stages = (int)std::min<int64_t>(cut.stages, (steps + cut.blocks - 1) / cut.blocks);
@@ -436,15 +535,16 @@ cudaError_t launch(const ResidualNormParams& p, const NormCut& cut, float* parti
 template <typename T, bool BACK>
 cudaError_t launch_typed(const ResidualNormParams& p, const NormCut& cut, float* partial,
                          cudaStream_t s) {
-  switch (warps_per_row(p.width)) {
+  const Shape shape = shape_of(p.width);
+  switch (shape.wpr) {
     case 1: return launch<T, 1, 1, BACK>(p, cut, partial, s);
     case 2: return launch<T, 2, 1, BACK>(p, cut, partial, s);
     case 4: return launch<T, 4, 1, BACK>(p, cut, partial, s);
     case 8: return launch<T, 8, 1, BACK>(p, cut, partial, s);
     default: break;
   }
-  if (p.width <= 4096) return launch<T, 16, 1, BACK>(p, cut, partial, s);
-  if (p.width <= 8192) return launch<T, 16, 2, BACK>(p, cut, partial, s);
+  if (shape.vpt == 1) return launch<T, 16, 1, BACK>(p, cut, partial, s);
+  if (shape.vpt == 2) return launch<T, 16, 2, BACK>(p, cut, partial, s);
   if constexpr (sizeof(T) == 2) return launch<T, 16, 4, BACK>(p, cut, partial, s);
   return cudaErrorInvalidValue;
 }
@@ -484,7 +584,7 @@ cudaError_t launch_residual_norm_backward(int dtype, const ResidualNormParams& p
   }
   if (!sums(p)) return cudaSuccess;
   SumOut to = {{p.dpost, p.dnext, p.gate_stride == 0 ? static_cast<float*>(p.dgate) : nullptr}};
-  residual_norm_sums_kernel<<<dim3((p.width + 31) / 32, 3), 1024, 0, s>>>(
+  residual_norm_sums_kernel<<<dim3((p.width + 31) / 32, 3), 256, 0, s>>>(
       partial, cut.blocks * cut.groups, p.width, to);
   *launches += 1;
   return cudaGetLastError();
