@@ -9,7 +9,7 @@ namespace lbg {
 
 // ---- few tokens -------------------------------------------------------------------------
 constexpr int kRowsMaxPicks = 512, kRowsMaxExperts = 1024;
-constexpr int kRowsMaxValues = 12 * 1024;  // floats that a CTA keeps of the picks' outputs
+constexpr int kRowsMaxValues = 6 * 1024;  // floats that a CTA keeps of the picks' outputs
 struct W4RowsParams {
   int64_t n = 0;  // rows of a matrix (of one expert)
   int k = 0, group = 0;
@@ -24,10 +24,8 @@ struct W4RowsParams {
   const float* weights = nullptr;
   int* status = nullptr;
   // How the launch cuts the call: rows a CTA (rows_more CTAs have one more), pieces of
-  // k and their steps, tiles of a round, steps that codes are copied ahead; columns as
-  // a power of two; and where things lie in shared memory.
+  // k and their steps, tiles of a round, steps that codes are copied ahead; and where things lie in shared memory.
   int rows_each = 0, rows_more = 0, chunks = 1, steps = 1, batch = 1, depth = 2;
-  int log_columns = 0;
   int at_shares = 0, at_values = 0, at_tokens = 0, bytes = 0;
 };
 bool w4_rows_take_linear(const W4LinearParams& l, int sm_count);

@@ -199,7 +199,8 @@ struct Run {
   }
 };
 
-// Warps of a CTA: with 16 columns the registers hold 16.
+// Warps of a CTA: 24, or the 16 that 16 columns leave registers for.  (Two CTAs of 12
+// an SM measured the same within 5 %.)
 __host__ __device__ constexpr int warps_for(int nb) { return nb == 1 ? 24 : 16; }
 
 template <typename T, int MODE, int NB, bool STAGED>
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(32 * warps_for(NB), 1) w4_rows_kernel(const W4
   const int g = lane / 4, t = lane % 4;
   const int k = p.k;
 
+  if (MODE == kUp) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (MODE != kLinear) sort_picks(p, COLS, picks, counts);
   auto columns_of = [&](int segment) { return MODE == kLinear ? p.picks : picks.count[segment]; };
   auto pick_of = [&](int segment, int column) {
@@ -502,46 +504,47 @@ __global__ void __launch_bounds__(32 * warps_for(NB), 1) w4_rows_kernel(const W4
       const int longer = more * (each + 1);
       return q < longer ? q / (each + 1) : more + (q - longer) / each;
     };
-    // columns by a power of two, rows (up: pairs of rows) by 16 (8), tiles
-    const int log_cols = MODE == kLinear ? p.log_columns : (NB == 1 ? 3 : 4);
+    // a warp a tile, its lanes along the rows (up: pairs of rows) of a column, then the next
     constexpr int log_rows = MODE == kUp ? 3 : 4;
-    for (int i = threadIdx.x; i < count << (log_rows + log_cols); i += kThreads) {
-      const int which = i >> (log_rows + log_cols), col = i & ((1 << log_cols) - 1);
-      const int r = (i >> log_cols & ((1 << log_rows) - 1)) * (MODE == kUp ? 2 : 1);
+    for (int which = warp; which < count; which += kWarps) {
       int segment, row, rows;
       run.tile(first_tile + which, segment, row, rows);
-      if (col >= columns_of(segment) || r >= rows) continue;
-      const int pick = pick_of(segment, col);
-      const float* scales = p.w.row_scales + first_row_of(segment) + row + r;
-      const float scale0 = __ldg(scales), scale1 = MODE == kUp ? __ldg(scales + 1) : 0.0f;
+      const int cols = columns_of(segment);
       const int w0 = warp_of(which * steps), w1 = warp_of((which + 1) * steps - 1);
-      const float* s = shares + (which + w0) * SHARE + r * COLS + col;
-      float v = 0.0f, u = 0.0f;
-      for (int w = w0; w <= w1; ++w, s += SHARE) {
-        v += s[0];
-        if (MODE == kUp) u += s[COLS];
-      }
-      if (MODE == kUp) {
-        v *= scale0;
-        u *= scale1;
-        static_cast<T*>(p.y)[pick * p.y_stride + (row + r) / 2] =
-            from_f32<T>(v / (1.0f + expf(-v)) * u);
-      } else if (MODE == kDown) {
-        values[(row - run.first_row + r) * p.picks + pick] = v * scale0;
-      } else {
-        // (the same thread meets an output in every piece of k)
-        float* sum = values + (row - run.first_row + r) * COLS + col;
-        if (at.chunk > 0) v += *sum;
-        if (at.chunk + 1 < p.chunks)
-          *sum = v;
-        else
-          static_cast<T*>(p.y)[pick * p.y_stride + row + r] = from_f32<T>(v * scale0);
+      const float* scales = p.w.row_scales + first_row_of(segment) + row;
+      for (int i = lane; i < cols << log_rows; i += 32) {
+        const int col = i >> log_rows;
+        const int r = (i & ((1 << log_rows) - 1)) * (MODE == kUp ? 2 : 1);
+        if (r >= rows) continue;
+        const int pick = pick_of(segment, col);
+        const float scale0 = __ldg(scales + r), scale1 = MODE == kUp ? __ldg(scales + r + 1) : 0.0f;
+        const float* s = shares + (which + w0) * SHARE + r * COLS + col;
+        float v = 0.0f, u = 0.0f;
+        for (int w = w0; w <= w1; ++w, s += SHARE) {
+          v += s[0];
+          if (MODE == kUp) u += s[COLS];
+        }
+        if (MODE == kUp) {
+          v *= scale0;
+          u *= scale1;
+          static_cast<T*>(p.y)[pick * p.y_stride + (row + r) / 2] =
+              from_f32<T>(v / (1.0f + expf(-v)) * u);
+        } else if (MODE == kDown) {
+          values[(row - run.first_row + r) * p.picks + pick] = v * scale0;
+        } else {
+          // (the same lane meets an output in every piece of k)
+          float* sum = values + (row - run.first_row + r) * COLS + col;
+          if (at.chunk > 0) v += *sum;
+          if (at.chunk + 1 < p.chunks)
+            *sum = v;
+          else
+            static_cast<T*>(p.y)[pick * p.y_stride + row + r] = from_f32<T>(v * scale0);
+        }
       }
     }
     next_round(at);
     if (at.round < rounds) __syncthreads();  // (the shares' places are used again)
   }
-  if (MODE == kUp) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (MODE == kDown) {
     __syncthreads();
     const int tokens = p.picks / p.top_k;
@@ -561,9 +564,12 @@ __global__ void __launch_bounds__(32 * warps_for(NB), 1) w4_rows_kernel(const W4
 constexpr int kStatic = sizeof(Picks) + 4 * (kRowsMaxExperts + 1) + 256;
 constexpr int kStaticLinear = 512;
 
-// Fills in the cut of a linear layer; false where it does not fit.
+// Fills in the cut of a linear layer; false where it does not fit (in pieces of k of 16
+// steps at least: fewer are too many rounds).
 bool cut_linear(W4RowsParams& p, int ctas) {
   const int nb = p.picks > 8 ? 2 : 1, warps = warps_for(nb);
+  p.rows_each = (int)(p.n / ctas);
+  p.rows_more = (int)(p.n % ctas);
   const int rows = p.rows_each + (p.rows_more > 0), tiles = (rows + 15) / 16;
   p.batch = std::min(tiles, 48 / nb);
   const int shares = (p.batch + warps) * nb * 512;
@@ -572,7 +578,7 @@ bool cut_linear(W4RowsParams& p, int ctas) {
   const int room = kSmem - kStaticLinear - 2 * warps * kSlotBytes - shares;
   int64_t most = (room / p.picks - 64) / (kStep * 2);
   if (most < steps) most = ((room - sums) / p.picks - 64) / (kStep * 2);
-  if (most < std::min(steps, warps)) return false;  // (too many rounds)
+  if (most < std::min(steps, 16)) return false;
   p.chunks = (int)((steps + most - 1) / most);
   p.steps = (steps + p.chunks - 1) / p.chunks;
   const int held = p.chunks > 1 ? (int)(sums + 15) / 16 * 16 : 0;
@@ -597,7 +603,7 @@ bool cut_experts(W4RowsParams& p, int nb, int vectors, int values) {
   const int room = kSmem - kStatic - shares - held;
   const bool staged = tokens <= room - 2 * warps * kSlotBytes;
   p.depth = std::min<int>(kMaxDepth, (int)((room - (staged ? tokens : 0)) / (warps * kSlotBytes)));
-  if (!staged) p.depth = std::min(p.depth, 64 / warps);  // (L1 is what is left)
+  if (!staged) p.depth = 2;  // (L1 is what is left)
   p.at_shares = p.depth * warps * kSlotBytes;
   p.at_values = p.at_shares + shares;
   p.at_tokens = p.at_values + held;
@@ -646,42 +652,39 @@ cudaError_t launch_any(int dtype, const W4RowsParams& p, int nb, bool staged, in
                               : launch_mode<__half, MODE>(p, nb, staged, ctas, s);
 }
 
-W4RowsParams linear_params(const W4LinearParams& l, int ctas) {
-  W4RowsParams p;
-  p.n = l.n;
-  p.k = (int)l.k;
-  p.group = l.group;
-  p.x = l.x;
-  p.x_stride = l.x_stride;
-  p.w = l.w;
-  p.y = l.y;
-  p.y_stride = l.y_stride;
-  p.picks = (int)l.m;
-  p.status = l.status;
-  p.rows_each = (int)(l.n / ctas);
-  p.rows_more = (int)(l.n % ctas);
-  while (1 << p.log_columns < l.m) ++p.log_columns;
-  return p;
-}
-
 int ctas_for(int64_t rows, int sm_count) {  // no CTA without a row
   return (int)std::min<int64_t>(sm_count, rows);
+}
+
+bool linear_params(const W4LinearParams& l, int sm_count, W4RowsParams* p, int* ctas) {
+  if (l.m > 16) return false;
+  p->n = l.n;
+  p->k = (int)l.k;
+  p->group = l.group;
+  p->x = l.x;
+  p->x_stride = l.x_stride;
+  p->w = l.w;
+  p->y = l.y;
+  p->y_stride = l.y_stride;
+  p->picks = (int)l.m;
+  p->status = l.status;
+  *ctas = ctas_for(l.n, sm_count);
+  return cut_linear(*p, *ctas);
 }
 
 }  // namespace
 
 bool w4_rows_take_linear(const W4LinearParams& l, int sm_count) {
-  if (l.m > 16) return false;
-  const int ctas = ctas_for(l.n, sm_count);
-  W4RowsParams p = linear_params(l, ctas);
-  return cut_linear(p, ctas);
+  W4RowsParams p;
+  int ctas;
+  return linear_params(l, sm_count, &p, &ctas);
 }
 
 cudaError_t launch_w4_rows_linear(int dtype, const W4LinearParams& l, int sm_count,
                                   cudaStream_t s) {
-  const int ctas = ctas_for(l.n, sm_count);
-  W4RowsParams p = linear_params(l, ctas);
-  cut_linear(p, ctas);
+  W4RowsParams p;
+  int ctas;
+  if (!linear_params(l, sm_count, &p, &ctas)) return cudaErrorInvalidValue;
   return launch_any<kLinear>(dtype, p, l.m > 8 ? 2 : 1, true, ctas, s);
 }
 
