@@ -16,12 +16,15 @@ using namespace lbg;
 
 std::mutex g_ffn_mu;  // the feed-forward operators' scratch
 
+// Strides in elements.  (Tensor maps hold fewer than 2^40 bytes.)
+constexpr int64_t kMostStride = int64_t(1) << 38;
+
 // Rows of `width` elements given by pointer and stride.
 lbgemm_status check_rows(const char* name, const void* p, int64_t stride, int64_t rows,
                          int64_t width, int dtype) {
   if (rows == 0) return LBGEMM_OK;
   if (!p) return bad(LBGEMM_ERR_INVALID_ARG, "%s is a null pointer", name);
-  if (stride > kMaxStride || (rows > 1 && stride < width))
+  if (stride > kMostStride || (rows > 1 && stride < width))
     return bad(LBGEMM_ERR_INVALID_ARG, "%s: row stride %lld does not hold %lld elements", name,
                (long long)stride, (long long)width);
   if (!aligned(p, 16) || (rows > 1 && stride * elem_size(dtype) % 16))
