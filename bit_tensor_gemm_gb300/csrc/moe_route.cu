@@ -63,19 +63,18 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParam
   }
   // lane j keeps the j-th choice
   int id = -1;
-  float w = 0.0f;
+  uint32_t chosen = 0;
   for (int j = 0; j < p.top_k; ++j) {
     const uint32_t most = __reduce_max_sync(0xffffffffu, best);
     if (most == 0) break;
     uint32_t at = 0xffffffffu;
+    if (best == most) {
 #pragma unroll
-    for (int i = PER - 1; i >= 0; --i)
-      if (key[i] == most) at = 32 * i + lane;
-    at = __reduce_min_sync(0xffffffffu, at);
-    if (lane == j) {
-      id = (int)at;
-      w = expf(number_of(most) - top);
+      for (int i = PER - 1; i >= 0; --i)
+        if (key[i] == most) at = 32 * i + lane;
     }
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (lane == j) id = (int)at, chosen = most;
     if (lane == (at & 31)) {
       best = 0;
 #pragma unroll
@@ -85,6 +84,7 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParam
       }
     }
   }
+  float w = chosen ? expf(number_of(chosen) - top) : 0.0f;
   if (p.renormalize) {
     all = w;
 #pragma unroll

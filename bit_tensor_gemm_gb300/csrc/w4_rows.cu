@@ -49,7 +49,7 @@ namespace {
 constexpr int kStep = 256;
 constexpr int kSlotBytes = 2048;  // a warp's codes of a step
 constexpr int kMaxDepth = 6;
-constexpr int kSmem = 227 * 1024;
+constexpr int kSmem = 227 * 1024;  // of an SM; kSmem / 2 - 512 of one of two CTAs
 
 enum Mode { kLinear, kUp, kDown };
 
@@ -122,6 +122,35 @@ __device__ __forceinline__ void copies_done(int behind) {  // all but the last `
 // Sorts the picks by expert (all threads of the CTA; `counts`: kRowsMaxExperts + 1).
 __device__ void sort_picks(const W4RowsParams& p, int columns, Picks& picks, int* counts) {
   const int total = p.picks;
+  if (total <= 32) {  // a warp settles it in registers, in the order of first appearance
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      const int e = lane < total ? p.ids[lane] : -1;
+      if (e >= p.experts) atomicOr(p.status, kStatusBadIndex);
+      const bool live = e >= 0 && e < p.experts;
+      const uint32_t same = __match_any_sync(0xffffffffu, live ? e : -1);
+      const int leader = __ffs(same) - 1;
+      const int n = live && leader == lane ? __popc(same) : 0;
+      const int parts = (n + columns - 1) / columns;
+      int a = n, b = parts;  // running sums: picks and segments
+#pragma unroll
+      for (int off = 1; off < 32; off *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, a, off), y = __shfl_up_sync(0xffffffffu, b, off);
+        if (lane >= off) a += x, b += y;
+      }
+      const int first = a - n, at = __shfl_sync(0xffffffffu, first, leader);
+      if (live) picks.pick[at + __popc(same & ((1u << lane) - 1))] = (short)lane;
+      for (int q = 0; q < parts; ++q) {
+        const int seg = b - parts + q;
+        picks.expert[seg] = (short)e;
+        picks.first[seg] = (short)(first + q * columns);
+        picks.count[seg] = (short)min(n - q * columns, columns);
+      }
+      if (lane == 31) picks.segments = b;
+    }
+    __syncthreads();
+    return;
+  }
   for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) counts[e] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < total; i += blockDim.x) {
@@ -199,13 +228,16 @@ struct Run {
   }
 };
 
-// Warps of a CTA: 24, or the 16 that 16 columns leave registers for.  (Two CTAs of 12
-// an SM measured the same within 5 %.)
+// kWarps: 24, or the 16 that 16 columns leave registers for.  A mixture of few picks
+// takes 12 and half of the shared memory, so that the CTAs of `down` stand beside those
+// of `up`: they look up their picks and copy their first codes while `up` runs.
 __host__ __device__ constexpr int warps_for(int nb) { return nb == 1 ? 24 : 16; }
+constexpr int kFewWarps = 12, kFewPicks = 16;
 
-template <typename T, int MODE, int NB, bool STAGED>
-__global__ void __launch_bounds__(32 * warps_for(NB), 1) w4_rows_kernel(const W4RowsParams p) {
-  constexpr int kWarps = warps_for(NB), kThreads = 32 * kWarps;
+template <typename T, int MODE, int NB, bool STAGED, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
+    w4_rows_kernel(const W4RowsParams p) {
+  constexpr int kThreads = 32 * kWarps;
   constexpr int COLS = 8 * NB, SHARE = 16 * COLS;  // columns; numbers of a tile
   extern __shared__ __align__(128) uint8_t smem[];
   float* shares = reinterpret_cast<float*>(smem + p.at_shares);  // [batch + kWarps][SHARE]
@@ -593,14 +625,14 @@ bool cut_linear(W4RowsParams& p, int ctas) {
 }
 
 // ... and of a pass over the experts: staged where two slots of the ring are left.
-bool cut_experts(W4RowsParams& p, int nb, int vectors, int values) {
-  const int warps = warps_for(nb);
-  p.batch = 48 / nb;
+bool cut_experts(W4RowsParams& p, int nb, int warps, int vectors, int values) {
+  const int smem = warps == kFewWarps ? kSmem / 2 - 512 : kSmem;
+  p.batch = warps == kFewWarps ? 24 : 48 / nb;
   const int shares = (p.batch + warps) * nb * 512;
   p.steps = (p.k + kStep - 1) / kStep;
   const int64_t tokens = (int64_t)vectors * (p.steps * kStep * 2 + 64);
   const int held = (values * 4 + 15) / 16 * 16;
-  const int room = kSmem - kStatic - shares - held;
+  const int room = smem - kStatic - shares - held;
   const bool staged = tokens <= room - 2 * warps * kSlotBytes;
   p.depth = std::min<int>(kMaxDepth, (int)((room - (staged ? tokens : 0)) / (warps * kSlotBytes)));
   if (!staged) p.depth = 2;  // (L1 is what is left)
@@ -611,9 +643,9 @@ bool cut_experts(W4RowsParams& p, int nb, int vectors, int values) {
   return staged;
 }
 
-template <typename T, int MODE, int NB, bool STAGED>
+template <typename T, int MODE, int NB, bool STAGED, int WARPS = warps_for(NB)>
 cudaError_t launch(const W4RowsParams& p, int ctas, cudaStream_t s) {
-  auto kernel = w4_rows_kernel<T, MODE, NB, STAGED>;
+  auto kernel = w4_rows_kernel<T, MODE, NB, STAGED, WARPS>;
   static std::atomic<uint64_t> set{0};  // devices on which the kernel has its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -626,7 +658,7 @@ cudaError_t launch(const W4RowsParams& p, int ctas, cudaStream_t s) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(32 * warps_for(NB));
+  cfg.blockDim = dim3(32 * WARPS);
   cfg.dynamicSmemBytes = p.bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -638,18 +670,24 @@ cudaError_t launch(const W4RowsParams& p, int ctas, cudaStream_t s) {
 }
 
 template <typename T, int MODE>
-cudaError_t launch_mode(const W4RowsParams& p, int nb, bool staged, int ctas, cudaStream_t s) {
-  if constexpr (MODE != kLinear)
+cudaError_t launch_mode(const W4RowsParams& p, int nb, int warps, bool staged, int ctas,
+                        cudaStream_t s) {
+  if constexpr (MODE != kLinear) {
+    if (warps == kFewWarps)
+      return staged ? launch<T, MODE, 1, true, kFewWarps>(p, ctas, s)
+                    : launch<T, MODE, 1, false, kFewWarps>(p, ctas, s);
     if (!staged)
       return nb == 1 ? launch<T, MODE, 1, false>(p, ctas, s) : launch<T, MODE, 2, false>(p, ctas, s);
+  }
   return nb == 1 ? launch<T, MODE, 1, true>(p, ctas, s) : launch<T, MODE, 2, true>(p, ctas, s);
 }
 
 template <int MODE>
-cudaError_t launch_any(int dtype, const W4RowsParams& p, int nb, bool staged, int ctas,
+cudaError_t launch_any(int dtype, const W4RowsParams& p, int nb, int warps, bool staged, int ctas,
                        cudaStream_t s) {
-  return dtype == LBGEMM_BF16 ? launch_mode<__nv_bfloat16, MODE>(p, nb, staged, ctas, s)
-                              : launch_mode<__half, MODE>(p, nb, staged, ctas, s);
+  return dtype == LBGEMM_BF16
+             ? launch_mode<__nv_bfloat16, MODE>(p, nb, warps, staged, ctas, s)
+             : launch_mode<__half, MODE>(p, nb, warps, staged, ctas, s);
 }
 
 int ctas_for(int64_t rows, int sm_count) {  // no CTA without a row
@@ -685,7 +723,8 @@ cudaError_t launch_w4_rows_linear(int dtype, const W4LinearParams& l, int sm_cou
   W4RowsParams p;
   int ctas;
   if (!linear_params(l, sm_count, &p, &ctas)) return cudaErrorInvalidValue;
-  return launch_any<kLinear>(dtype, p, l.m > 8 ? 2 : 1, true, ctas, s);
+  const int nb = l.m > 8 ? 2 : 1;
+  return launch_any<kLinear>(dtype, p, nb, warps_for(nb), true, ctas, s);
 }
 
 bool w4_rows_take_moe(const MoeParams& m, int sm_count) {
@@ -714,9 +753,11 @@ cudaError_t launch_w4_rows_moe(int dtype, const MoeParams& m, void* h, int sm_co
   p.weights = m.weights;
   p.status = m.status;
   // Columns that one pass over an expert's rows serves.
-  const int nb = p.picks > 4 * m.experts ? 2 : 1;
-  bool staged = cut_experts(p, nb, (int)m.tokens, 0);
-  cudaError_t e = launch_any<kUp>(dtype, p, nb, staged, sm_count, s);
+  const bool few = p.picks <= kFewPicks;
+  const int nb = !few && p.picks > 4 * m.experts ? 2 : 1;
+  const int warps = few ? kFewWarps : warps_for(nb);
+  bool staged = cut_experts(p, nb, warps, (int)m.tokens, 0);
+  cudaError_t e = launch_any<kUp>(dtype, p, nb, warps, staged, sm_count, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   p.n = m.hidden;
@@ -729,8 +770,8 @@ cudaError_t launch_w4_rows_moe(int dtype, const MoeParams& m, void* h, int sm_co
   const int ctas = ctas_for(m.hidden, sm_count);
   p.rows_each = m.hidden / ctas;
   p.rows_more = m.hidden % ctas;
-  staged = cut_experts(p, nb, p.picks, (p.rows_each + (p.rows_more > 0)) * p.picks);
-  e = launch_any<kDown>(dtype, p, nb, staged, ctas, s);
+  staged = cut_experts(p, nb, warps, p.picks, (p.rows_each + (p.rows_more > 0)) * p.picks);
+  e = launch_any<kDown>(dtype, p, nb, warps, staged, ctas, s);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
