@@ -34,9 +34,14 @@ __host__ __device__ constexpr int blocks_for(int wpr, int vpt, bool back) {
   return back ? (wpr <= 8 ? 2 : 1) : vpt > 1 ? 1 : wpr <= 8 ? 4 : 2;
 }
 
+// Warps and vectors a thread of a row, and rows that are taken at once.
+struct Shape {
+  int wpr, vpt, rows;
+};
 struct NormCut {
+  Shape shape = {};
   int blocks = 0, stages = 0, stage_bytes = 0;
-  int groups = 0;  // rows of a stage
+  int groups = 0;  // of rows, beside one another in a block
 };
 
 // Two numbers; as plain fp32 operations, since the paired ones of this file's other
@@ -134,19 +139,20 @@ __device__ __forceinline__ bool row_sums(float (&v)[N], float* slots, int group,
   return stop;
 }
 
-// WPR warps a row, VPT vectors of 8 elements a thread; the first warp issues the
+// WPR warps a row, VPT vectors of 8 elements a thread, ROWS rows at once (a meeting of
+// the warps costs the same for one and two); the first warp issues the
 // copies (a warp of its own would leave fewer registers to the others).  The tensors of
-// a stage: x, y, a gate for each row, dx', dn, those that are given; each [groups][width].
-template <typename T, int WPR, int VPT, bool BACK>
+// a stage: x, y, a gate for each row, dx', dn, those that are given; each [rows][width].
+template <typename T, int WPR, int VPT, int ROWS, bool BACK>
 __global__ void __launch_bounds__(WPR <= 8 ? 256 : 512, blocks_for(WPR, VPT, BACK))
     residual_norm_kernel(const ResidualNormParams p, const NormCut cut,
                          float* __restrict__ partial) {
   constexpr int THREADS = WPR <= 8 ? 256 : 512;
-  constexpr int LANES = 32 * WPR, GROUPS = THREADS / LANES;
+  constexpr int LANES = 32 * WPR, GROUPS = THREADS / LANES, HELD = GROUPS * ROWS;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t bars[2 * kMaxStages];
   __shared__ int abort_flag;
-  __shared__ float slots[4][GROUPS][32];
+  __shared__ float slots[4][GROUPS][ROWS * 32];
   const int group = threadIdx.x / LANES, at = threadIdx.x % LANES, warp = at / 32;
   const int width = p.width, vectors = width / 8;
   const int row_bytes = width * (int)sizeof(T);
@@ -160,7 +166,7 @@ __global__ void __launch_bounds__(WPR <= 8 ? 256 : 512, blocks_for(WPR, VPT, BAC
   const int at_dx = BACK && p.dx_out ? held++ : -1;
   const int at_dn = BACK && p.dn ? held++ : -1;
 
-  const int64_t steps_all = (p.tokens + GROUPS - 1) / GROUPS;
+  const int64_t steps_all = (p.tokens + HELD - 1) / HELD;
   const int64_t step0 = blockIdx.x, stride_steps = gridDim.x;
   const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages;
   if (threadIdx.x < cut.stages) {
@@ -172,12 +178,12 @@ __global__ void __launch_bounds__(WPR <= 8 ? 256 : 512, blocks_for(WPR, VPT, BAC
   __syncthreads();
 
   auto issue = [&](int64_t step, int slot) {  // by the first warp
-    const int rows = (int)min((int64_t)GROUPS, p.tokens - step * GROUPS);
+    const int rows = (int)min((int64_t)HELD, p.tokens - step * HELD);
     const uint32_t bar = full + 8 * slot, dst = smem_addr(ring) + slot * cut.stage_bytes;
     if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, (uint32_t)(rows * held * row_bytes));
     __syncwarp();
-    for (int i = threadIdx.x; i < held * GROUPS; i += 32) {
-      const int t = i / GROUPS, r = i % GROUPS;
+    for (int i = threadIdx.x; i < held * HELD; i += 32) {
+      const int t = i / HELD, r = i % HELD;
       const void* from = p.x;
       int64_t stride = p.x_stride;
       if (t == at_y) from = p.y, stride = p.y_stride;
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(WPR <= 8 ? 256 : 512, blocks_for(WPR, VPT, BAC
       if (t == at_dx) from = p.dx_out, stride = p.dx_out_stride;
       if (t == at_dn) from = p.dn, stride = p.dn_stride;
       if (r < rows)
-        bulk_load(dst + i * row_bytes, static_cast<const T*>(from) + (step * GROUPS + r) * stride,
+        bulk_load(dst + i * row_bytes, static_cast<const T*>(from) + (step * HELD + r) * stride,
                   row_bytes, bar);
     }
   };
@@ -216,197 +222,212 @@ __global__ void __launch_bounds__(WPR <= 8 ? 256 : 512, blocks_for(WPR, VPT, BAC
     for (int j = 0; j < VPT; ++j) sum_post[j] = sum_next[j] = sum_gate[j] = {};
   }
   const Two a2 = twice(p.a), b2 = twice(p.b);
-  // With one vector a thread, what a row's later passes need stays in registers; with
-  // more it is taken from the stage again.
-  constexpr bool KEEP = VPT == 1;
+  // Vector q is vector q % VPT of row q / VPT.  With one a thread, what a row's later
+  // passes need stays in registers; with more it is taken from the stage again.
+  constexpr int Q = ROWS * VPT;
+  constexpr bool KEEP = Q == 1;
 
   int slot = 0, use = 0;  // the slot of a row, and how often it has been used before
   bool odd = false;
   for (int64_t step = step0; step < steps_all; step += stride_steps) {
     // (where the copies do not come, the warps of a row leave together below)
     bool stop = !mbar_wait(full + 8 * slot, use & 1, &abort_flag, p.status);
-    const int64_t row = step * GROUPS + group;
+    const int64_t row = step * HELD + group * ROWS;
     // (a row past the end computes what is there, stores nothing)
-    const bool live = GROUPS == 1 || row < p.tokens;
-    const T* stage = reinterpret_cast<const T*>(ring + slot * cut.stage_bytes + group * row_bytes);
-    auto part = [&](int which, int j) {
-      return load_vec(stage + (which * GROUPS * width + (at + j * LANES) * 8));
+    auto live = [&](int q) { return HELD == 1 || row + q / VPT < p.tokens; };
+    const T* stage =
+        reinterpret_cast<const T*>(ring + slot * cut.stage_bytes + group * ROWS * row_bytes);
+    auto column = [&](int q) { return (at + q % VPT * LANES) * 8; };
+    auto part = [&](int which, int q) {
+      return load_vec(stage + ((which * HELD + q / VPT) * width + column(q)));
     };
-    auto on = [&](int j) { return at + j * LANES < vectors; };
+    auto on = [&](int q) { return at + q % VPT * LANES < vectors; };
 
     // ---- rstd(Y) ----
-    Vec<T> y[VPT];  // KEEP: Y, then Y rstd(Y)
-    float r1 = 1.0f;
+    Vec<T> y[Q];  // KEEP: Y, then Y rstd(Y)
+    float r1[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) r1[r] = 1.0f;
     if (at_y >= 0) {
-      Two s = {0, 0};
+      Two s[ROWS] = {};
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        if (!on(j)) continue;
-        y[j] = part(at_y, j);
+      for (int q = 0; q < Q; ++q) {
+        if (!on(q)) continue;
+        y[q] = part(at_y, q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s = fma2(y[j].v[i], y[j].v[i], s);
+        for (int i = 0; i < 4; ++i) s[q / VPT] = fma2(y[q].v[i], y[q].v[i], s[q / VPT]);
       }
       if (post) {
-        float t[1] = {halves(s)};
+        float t[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) t[r] = halves(s[r]);
         // (a forward pass without a second norm meets once a row: places in turn)
         stop = row_sums<WPR>(t, slots[odd ? 3 : 0][group], group, warp, stop);
         odd = !odd;
-        r1 = rsqrtf(t[0] * inv + p.eps);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) r1[r] = rsqrtf(t[r] * inv + p.eps);
       }
     }
     if (!post) stop = row_meet<WPR>(group, stop);
     if (stop) break;
-    // the slot of the row before, for the row `stages` after that one
+    // the slot of the rows before, for those `stages` steps after them
     if (cut.stages > 1 && step > step0)
       refill(step + (cut.stages - 1) * stride_steps, slot == 0 ? cut.stages - 1 : slot - 1,
              slot == 0 ? use : use + 1);
 
     // ---- x', its rstd, mean(next dn xhat) ----
-    const Two r1x = twice(r1);
-    Vec<T> z[VPT], g[VPT], kept[VPT], dn[VPT];  // z; b gate; x'; dn
+    Vec<T> z[Q], g[Q], kept[Q], dn[Q];  // z; b gate; x'; dn
     // y = Y rstd(Y), z and b gate of a vector; Y again where it was not kept
-    auto block = [&](int j) {
-      if (!KEEP) y[j] = part(at_y, j);
-      z[j] = y[j];
+    auto block = [&](int q) {
+      if (!KEEP) y[q] = part(at_y, q);
+      z[q] = y[q];
       if (post) {
-        const Vec<T> w = vec_of(w_post[j]);
+        const Two r = twice(r1[q / VPT]);
+        const Vec<T> w = vec_of(w_post[q % VPT]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          y[j].v[i] = mul2(y[j].v[i], r1x);
-          z[j].v[i] = mul2(y[j].v[i], w.v[i]);
+          y[q].v[i] = mul2(y[q].v[i], r);
+          z[q].v[i] = mul2(y[q].v[i], w.v[i]);
         }
       }
       if (p.gate) {
-        g[j] = own_gate ? part(at_gate, j) : vec_of(w_gate[j]);
+        g[q] = own_gate ? part(at_gate, q) : vec_of(w_gate[q % VPT]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) g[j].v[i] = mul2(g[j].v[i], b2);
+        for (int i = 0; i < 4; ++i) g[q].v[i] = mul2(g[q].v[i], b2);
       } else {
-        g[j] = {{b2, b2, b2, b2}};
+        g[q] = {{b2, b2, b2, b2}};
       }
     };
-    Two s = {0, 0}, dot = {0, 0};
+    Two s[ROWS] = {}, dot[ROWS] = {};
     T* const to_x = !BACK && p.x_out ? static_cast<T*>(p.x_out) + row * p.x_out_stride : nullptr;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (!on(j)) continue;
-      kept[j] = part(at_x, j);
+    for (int q = 0; q < Q; ++q) {
+      if (!on(q)) continue;
+      kept[q] = part(at_x, q);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) kept[j].v[i] = mul2(kept[j].v[i], a2);
+      for (int i = 0; i < 4; ++i) kept[q].v[i] = mul2(kept[q].v[i], a2);
       if (at_y >= 0) {
-        block(j);
+        block(q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kept[j].v[i] = fma2(g[j].v[i], z[j].v[i], kept[j].v[i]);
+        for (int i = 0; i < 4; ++i) kept[q].v[i] = fma2(g[q].v[i], z[q].v[i], kept[q].v[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s = fma2(kept[j].v[i], kept[j].v[i], s);
+      for (int i = 0; i < 4; ++i) s[q / VPT] = fma2(kept[q].v[i], kept[q].v[i], s[q / VPT]);
       if (BACK && next) {
-        const Vec<T> w = vec_of(w_next[j]);
-        dn[j] = part(at_dn, j);
+        const Vec<T> w = vec_of(w_next[q % VPT]);
+        dn[q] = part(at_dn, q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dot = fma2(mul2(w.v[i], dn[j].v[i]), kept[j].v[i], dot);
+        for (int i = 0; i < 4; ++i)
+          dot[q / VPT] = fma2(mul2(w.v[i], dn[q].v[i]), kept[q].v[i], dot[q / VPT]);
       }
-      if (to_x && live) store_vec(to_x + (at + j * LANES) * 8, kept[j]);
+      if (to_x && live(q)) store_vec(to_x + q / VPT * p.x_out_stride + column(q), kept[q]);
     }
-    float r2 = 0.0f, mean2 = 0.0f;
+    float r2[ROWS], mean2[ROWS];  // mean2: mean(next dn xhat)
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) r2[r] = mean2[r] = 0.0f;
     if (next) {
-      if constexpr (BACK) {
-        float t[2] = {halves(s), halves(dot)};
-        row_sums<WPR>(t, slots[1][group], group, warp);
-        r2 = rsqrtf(t[0] * inv + p.eps);
-        mean2 = r2 * (t[1] * inv);  // mean(next dn xhat)
-      } else {
-        float t[1] = {halves(s)};
-        row_sums<WPR>(t, slots[1][group], group, warp);
-        r2 = rsqrtf(t[0] * inv + p.eps);
+      constexpr int N = BACK ? 2 * ROWS : ROWS;
+      float t[N];
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        t[r] = halves(s[r]);
+        if (BACK) t[N - ROWS + r] = halves(dot[r]);
+      }
+      row_sums<WPR>(t, slots[1][group], group, warp);
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        r2[r] = rsqrtf(t[r] * inv + p.eps);
+        mean2[r] = r2[r] * (t[N - ROWS + r] * inv);
       }
     }
-    const Two r2x = twice(r2);
 
     if constexpr (!BACK) {
       // ---- n ----
       if (next) {
         T* const to = static_cast<T*>(p.n_out) + row * p.n_out_stride;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          if (!on(j)) continue;
-          const Vec<T> w = vec_of(w_next[j]);
+        for (int q = 0; q < Q; ++q) {
+          if (!on(q)) continue;
+          const Two r = twice(r2[q / VPT]);
+          const Vec<T> w = vec_of(w_next[q % VPT]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) kept[j].v[i] = mul2(mul2(kept[j].v[i], r2x), w.v[i]);
-          if (live) store_vec(to + (at + j * LANES) * 8, kept[j]);
+          for (int i = 0; i < 4; ++i) kept[q].v[i] = mul2(mul2(kept[q].v[i], r), w.v[i]);
+          if (live(q)) store_vec(to + q / VPT * p.n_out_stride + column(q), kept[q]);
         }
       }
     } else {
       // ---- d, dx, dgate, dz ----
-      const Two m2 = twice(-mean2);
-      Two dot1 = {0, 0};
-      T* const to_x = static_cast<T*>(p.dx) + row * p.dx_stride;
-      T* const to_y = static_cast<T*>(p.dy) + row * p.dy_stride;
+      Two dot1[ROWS] = {};
+      T* const to_dx = static_cast<T*>(p.dx) + row * p.dx_stride;
+      T* const to_dy = static_cast<T*>(p.dy) + row * p.dy_stride;
       T* const to_gate = static_cast<T*>(p.dgate) + (own_gate ? row * p.dgate_stride : 0);
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        if (!on(j)) continue;
-        const int c = (at + j * LANES) * 8;
-        Vec<T> d = at_dx >= 0 ? part(at_dx, j) : Vec<T>{};
+      for (int q = 0; q < Q; ++q) {
+        if (!on(q)) continue;
+        const int j = q % VPT;
+        Vec<T> d = at_dx >= 0 ? part(at_dx, q) : Vec<T>{};
         if (next) {
+          const Two r = twice(r2[q / VPT]), m = twice(-mean2[q / VPT]);
           const Vec<T> w = vec_of(w_next[j]);
-          if (!KEEP) dn[j] = part(at_dn, j);
+          if (!KEEP) dn[q] = part(at_dn, q);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const Two xhat = mul2(kept[j].v[i], r2x);
-            if (live) sum_next[j].v[i] = fma2(dn[j].v[i], xhat, sum_next[j].v[i]);
-            d.v[i] = fma2(r2x, fma2(xhat, m2, mul2(w.v[i], dn[j].v[i])), d.v[i]);
+            const Two xhat = mul2(kept[q].v[i], r);
+            if (live(q)) sum_next[j].v[i] = fma2(dn[q].v[i], xhat, sum_next[j].v[i]);
+            d.v[i] = fma2(r, fma2(xhat, m, mul2(w.v[i], dn[q].v[i])), d.v[i]);
           }
         }
-        if (live) {
+        if (live(q)) {
           Vec<T> dx;
 #pragma unroll
           for (int i = 0; i < 4; ++i) dx.v[i] = mul2(d.v[i], a2);
-          store_vec(to_x + c, dx);
+          store_vec(to_dx + q / VPT * p.dx_stride + column(q), dx);
         }
         if (at_y < 0) continue;
-        if (!KEEP) block(j);
+        if (!KEEP) block(q);
         if (p.gate) {
           Vec<T> dg;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dg.v[i] = mul2(mul2(d.v[i], b2), z[j].v[i]);
+          for (int i = 0; i < 4; ++i) dg.v[i] = mul2(mul2(d.v[i], b2), z[q].v[i]);
           if (own_gate) {
-            if (live) store_vec(to_gate + c, dg);
-          } else if (live) {
+            if (live(q)) store_vec(to_gate + q / VPT * p.dgate_stride + column(q), dg);
+          } else if (live(q)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum_gate[j].v[i] = add2(sum_gate[j].v[i], dg.v[i]);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d.v[i] = mul2(d.v[i], g[j].v[i]);  // dz
+        for (int i = 0; i < 4; ++i) d.v[i] = mul2(d.v[i], g[q].v[i]);  // dz
         if (post) {
           const Vec<T> w = vec_of(w_post[j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (live) sum_post[j].v[i] = fma2(d.v[i], y[j].v[i], sum_post[j].v[i]);
-            kept[j].v[i] = mul2(w.v[i], d.v[i]);  // (x' has done its part)
-            dot1 = fma2(kept[j].v[i], y[j].v[i], dot1);
+            if (live(q)) sum_post[j].v[i] = fma2(d.v[i], y[q].v[i], sum_post[j].v[i]);
+            kept[q].v[i] = mul2(w.v[i], d.v[i]);  // (x' has done its part)
+            dot1[q / VPT] = fma2(kept[q].v[i], y[q].v[i], dot1[q / VPT]);
           }
-        } else if (live) {
-          store_vec(to_y + c, d);
+        } else if (live(q)) {
+          store_vec(to_dy + q / VPT * p.dy_stride + column(q), d);
         }
       }
       // ---- dy ----
       if (post) {
-        float t[1] = {halves(dot1)};
+        float t[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) t[r] = halves(dot1[r]);
         row_sums<WPR>(t, slots[2][group], group, warp);
-        const Two m1 = twice(-t[0] * inv);
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          if (!on(j)) continue;
+        for (int q = 0; q < Q; ++q) {
+          if (!on(q)) continue;
+          const Two r = twice(r1[q / VPT]), m = twice(-t[q / VPT] * inv);
           if (!KEEP) {
-            y[j] = part(at_y, j);
+            y[q] = part(at_y, q);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[j].v[i] = mul2(y[j].v[i], r1x);
+            for (int i = 0; i < 4; ++i) y[q].v[i] = mul2(y[q].v[i], r);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            y[j].v[i] = mul2(r1x, fma2(y[j].v[i], m1, kept[j].v[i]));
-          if (live) store_vec(to_y + (at + j * LANES) * 8, y[j]);
+          for (int i = 0; i < 4; ++i) y[q].v[i] = mul2(r, fma2(y[q].v[i], m, kept[q].v[i]));
+          if (live(q)) store_vec(to_dy + q / VPT * p.dy_stride + column(q), y[q]);
         }
       }
     }
@@ -487,38 +508,38 @@ __global__ void __launch_bounds__(256)
   if (y == 0 && c < width) *reinterpret_cast<float4*>(out + c) = v;
 }
 
-// Warps and vectors a thread for a row.
-struct Shape {
-  int wpr, vpt;
-};
-Shape shape_of(int width) {
-  const int vectors = width / 8;
+Shape shape_of(const ResidualNormParams& p, int sm_count) {
+  const int vectors = p.width / 8;
+  // two rows at once where every SM has several
+  const int rows = p.tokens >= 8 * (int64_t)sm_count ? 2 : 1;
   for (int w = 1; w <= 16; w *= 2)
-    if (vectors <= 32 * w) return {w, 1};
-  return {16, vectors <= 1024 ? 2 : 4};
+    if (vectors <= 32 * w) return {w, 1, w >= 8 ? rows : 1};
+  return {16, vectors <= 1024 ? 2 : 4, 1};
 }
 
 NormCut cut_of(int dtype, const ResidualNormParams& p, bool back, int sm_count) {
   NormCut cut;
-  const Shape shape = shape_of(p.width);
+  const Shape shape = shape_of(p, sm_count);
   cut.groups = shape.wpr <= 8 ? 8 / shape.wpr : 1;
+  const int rows = cut.groups * shape.rows;
   const int held = (p.x != nullptr) + (p.y != nullptr) + (p.gate && p.gate_stride != 0) +
                    (back && p.dx_out) + (back && p.dn);
-  const int64_t steps = (p.tokens + cut.groups - 1) / cut.groups;
-  cut.stage_bytes = cut.groups * p.width * (dtype == LBGEMM_F32 ? 4 : 2) * std::max(held, 1);
+  const int64_t steps = (p.tokens + rows - 1) / rows;
+  cut.stage_bytes = rows * p.width * (dtype == LBGEMM_F32 ? 4 : 2) * std::max(held, 1);
   const int per_sm = blocks_for(shape.wpr, shape.vpt, back);
   cut.blocks = (int)std::min<int64_t>(steps, (int64_t)sm_count * per_sm);
   cut.stages = std::min(kMaxStages, kRing / per_sm / cut.stage_bytes);
   if (cut.stages < 2) cut.stages = std::max(1, std::min(2, kMostRing / cut.stage_bytes));
   if (cut.blocks > 0)
     cut.stages = (int)std::min<int64_t>(cut.stages, (steps + cut.blocks - 1) / cut.blocks);
+  cut.shape = shape;
   return cut;
 }
 
-template <typename T, int WPR, int VPT, bool BACK>
+template <typename T, int WPR, int VPT, int ROWS, bool BACK>
 cudaError_t launch(const ResidualNormParams& p, const NormCut& cut, float* partial,
                    cudaStream_t s) {
-  auto kernel = residual_norm_kernel<T, WPR, VPT, BACK>;
+  auto kernel = residual_norm_kernel<T, WPR, VPT, ROWS, BACK>;
   static std::atomic<uint64_t> set{0};  // devices on which the kernel has its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -535,17 +556,21 @@ cudaError_t launch(const ResidualNormParams& p, const NormCut& cut, float* parti
 template <typename T, bool BACK>
 cudaError_t launch_typed(const ResidualNormParams& p, const NormCut& cut, float* partial,
                          cudaStream_t s) {
-  const Shape shape = shape_of(p.width);
+  const Shape& shape = cut.shape;
   switch (shape.wpr) {
-    case 1: return launch<T, 1, 1, BACK>(p, cut, partial, s);
-    case 2: return launch<T, 2, 1, BACK>(p, cut, partial, s);
-    case 4: return launch<T, 4, 1, BACK>(p, cut, partial, s);
-    case 8: return launch<T, 8, 1, BACK>(p, cut, partial, s);
+    case 1: return launch<T, 1, 1, 1, BACK>(p, cut, partial, s);
+    case 2: return launch<T, 2, 1, 1, BACK>(p, cut, partial, s);
+    case 4: return launch<T, 4, 1, 1, BACK>(p, cut, partial, s);
+    case 8:
+      return shape.rows == 2 ? launch<T, 8, 1, 2, BACK>(p, cut, partial, s)
+                             : launch<T, 8, 1, 1, BACK>(p, cut, partial, s);
     default: break;
   }
-  if (shape.vpt == 1) return launch<T, 16, 1, BACK>(p, cut, partial, s);
-  if (shape.vpt == 2) return launch<T, 16, 2, BACK>(p, cut, partial, s);
-  if constexpr (sizeof(T) == 2) return launch<T, 16, 4, BACK>(p, cut, partial, s);
+  if (shape.vpt == 1)
+    return shape.rows == 2 ? launch<T, 16, 1, 2, BACK>(p, cut, partial, s)
+                           : launch<T, 16, 1, 1, BACK>(p, cut, partial, s);
+  if (shape.vpt == 2) return launch<T, 16, 2, 1, BACK>(p, cut, partial, s);
+  if constexpr (sizeof(T) == 2) return launch<T, 16, 4, 1, BACK>(p, cut, partial, s);
   return cudaErrorInvalidValue;
 }
 
