@@ -8,15 +8,16 @@
 namespace lbg {
 
 size_t w4_linear_scratch(W4LinearParams* p, int sm_count) {
-  return w4_rows_take_linear(*p, sm_count) ? 0 : w4_tiles_linear_scratch(*p, sm_count);
+  size_t bytes = 0;
+  return w4_rows_take_linear(*p, sm_count, &bytes) ? bytes : w4_tiles_linear_scratch(*p, sm_count);
 }
 
 cudaError_t launch_w4_linear(int dtype, const W4LinearParams& p, void* scratch, int sm_count,
                              int* launches, cudaStream_t s) {
-  if (!w4_rows_take_linear(p, sm_count))
-    return launch_w4_tiles_linear(dtype, p, scratch, sm_count, launches, s);
-  *launches += 1;
-  return launch_w4_rows_linear(dtype, p, sm_count, s);
+  size_t bytes = 0;
+  return w4_rows_take_linear(p, sm_count, &bytes)
+             ? launch_w4_rows_linear(dtype, p, scratch, sm_count, launches, s)
+             : launch_w4_tiles_linear(dtype, p, scratch, sm_count, launches, s);
 }
 
 size_t moe_w4_scratch(MoeParams* p, int sm_count) {

@@ -25,8 +25,9 @@
 // have are computed from others' data and not stored.
 //
 // Tokens are laid out in shared memory first (STAGED), in the order in which lanes
-// read them; the linear layer does it in pieces of k where they do not fit, the
-// experts read them through L1 then, at 2 conflicts a column and load.
+// read them.  Where they do not fit, the linear layer gives parts of k to CTAs of their
+// own (whose sums a second kernel adds), or takes k in pieces; the experts read them
+// through L1 then, at 2 conflicts a column and load.
 //
 // A tile's shares of the warps that met it are added in shared memory, in the
 // order of the warps, at the end of the run (of a round of it, where it has more
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
   const int g = lane / 4, t = lane % 4;
   const int k = p.k;
 
-  if (MODE == kUp) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (MODE != kDown) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (MODE != kLinear) sort_picks(p, COLS, picks, counts);
   auto columns_of = [&](int segment) { return MODE == kLinear ? p.picks : picks.count[segment]; };
   auto pick_of = [&](int segment, int column) {
@@ -263,7 +264,11 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
 
   // ---- the run ----
   Run<MODE> run;
-  const int cta = blockIdx.x, n = (int)p.n;
+  const int n = (int)p.n;
+  // (linear: CTAs by parts of k, then by rows)
+  const int part = MODE == kLinear ? blockIdx.x / p.row_ctas : 0;
+  const int cta = MODE == kLinear ? blockIdx.x - part * p.row_ctas : blockIdx.x;
+  const int first_step = part * p.steps;  // (one piece of k where there are parts)
   int own_rows = 0;
   if (MODE != kUp) {
     own_rows = p.rows_each + (cta < p.rows_more);
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       code_ptr[i] = p.w.codes + (uint64_t)r[i] * code_row + 16 * t +
-                    128 * (ahead.chunk * steps + ahead.j);
+                    128 * (first_step + ahead.chunk * steps + ahead.j);
   };
   aim_codes();
   const uint32_t ring = smem_addr(smem) + warp * p.depth * kSlotBytes + lane * 16;
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
   const uint32_t ring_end = ring + p.depth * kSlotBytes;
   auto copy_codes = [&] {
     if (ahead.left > 0) {
-      const int step = ahead.chunk * steps + ahead.j;
+      const int step = first_step + ahead.chunk * steps + ahead.j;
       if (step < whole) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -393,14 +398,14 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       scale_ptr[i] = p.w.scales + (uint64_t)r[i] * scale_row +
-                     ((8 * (scaled.chunk * steps + scaled.j) + t) >> shift);
+                     ((8 * (first_step + scaled.chunk * steps + scaled.j) + t) >> shift);
       if (t == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w.row_scales + r[i]));
     }
   };
   aim_scales();
   auto load_scales = [&] {
     if (scaled.left == 0) return;
-    const int step = scaled.chunk * steps + scaled.j;
+    const int step = first_step + scaled.chunk * steps + scaled.j;
     if (step < whole) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -443,7 +448,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
       const int pieces = steps * 32, vectors = MODE == kUp ? p.picks / p.top_k : p.picks;
       for (int v = warp; v < vectors; v += kWarps)
         for (int o = lane; o < pieces; o += 32) {
-          const int at_k = at.chunk * steps * kStep + 8 * o;
+          const int at_k = (first_step + at.chunk * steps) * kStep + 8 * o;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (at_k < k)
             x = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + v * p.x_stride + at_k);
@@ -569,6 +574,8 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
           if (at.chunk > 0) v += *sum;
           if (at.chunk + 1 < p.chunks)
             *sum = v;
+          else if (p.parts > 1)
+            p.part_sums[((int64_t)part * p.picks + pick) * n + row + r] = v * scale0;
           else
             static_cast<T*>(p.y)[pick * p.y_stride + row + r] = from_f32<T>(v * scale0);
         }
@@ -592,25 +599,49 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
   }
 }
 
+// y[m][n] = the sum of the parts of k, in order.
+template <typename T>
+__global__ void __launch_bounds__(256) rows_join_kernel(const W4RowsParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t total = p.picks * p.n;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / p.n, c = i - m * p.n;
+    float v = 0.0f;
+    for (int q = 0; q < p.parts; ++q) v += p.part_sums[q * total + i];
+    static_cast<T*>(p.y)[m * p.y_stride + c] = from_f32<T>(v);
+  }
+}
+
 // ---- how a launch lays out its shared memory -------------------------------------------
 constexpr int kStatic = sizeof(Picks) + 4 * (kRowsMaxExperts + 1) + 256;
 constexpr int kStaticLinear = 512;
 
-// Fills in the cut of a linear layer; false where it does not fit (in pieces of k of 16
-// steps at least: fewer are too many rounds).
-bool cut_linear(W4RowsParams& p, int ctas) {
-  const int nb = p.picks > 8 ? 2 : 1, warps = warps_for(nb);
-  p.rows_each = (int)(p.n / ctas);
-  p.rows_more = (int)(p.n % ctas);
+// Blocks of 8 columns for so many tokens.
+int blocks_of(int tokens) { return tokens <= 8 ? 1 : 2; }
+
+// Fills in the cut of a linear layer into parts of k, each of its own CTAs; false where
+// it does not fit.  A part's tokens are staged at once; only one part may take several
+// pieces (of 16 steps at least: fewer are too many rounds).
+bool cut_linear(W4RowsParams& p, int parts, int sm_count) {
+  const int nb = blocks_of(p.picks), warps = warps_for(nb);
+  p.parts = parts;
+  p.row_ctas = (int)std::min<int64_t>(sm_count / parts, p.n);
+  p.rows_each = (int)(p.n / p.row_ctas);
+  p.rows_more = (int)(p.n % p.row_ctas);
   const int rows = p.rows_each + (p.rows_more > 0), tiles = (rows + 15) / 16;
   p.batch = std::min(tiles, 48 / nb);
   const int shares = (p.batch + warps) * nb * 512;
-  const int steps = (p.k + kStep - 1) / kStep;
+  const int all_steps = (p.k + kStep - 1) / kStep, steps = (all_steps + parts - 1) / parts;
+  if (parts > 1 && (steps < 4 || (parts - 1) * steps >= all_steps)) return false;
   const int64_t sums = (int64_t)rows * 8 * nb * 4;
   const int room = kSmem - kStaticLinear - 2 * warps * kSlotBytes - shares;
   int64_t most = (room / p.picks - 64) / (kStep * 2);
-  if (most < steps) most = ((room - sums) / p.picks - 64) / (kStep * 2);
-  if (most < std::min(steps, 16)) return false;
+  if (most < steps) {
+    if (parts > 1) return false;
+    most = ((room - sums) / p.picks - 64) / (kStep * 2);
+    if (most < 16) return false;
+  }
   p.chunks = (int)((steps + most - 1) / most);
   p.steps = (steps + p.chunks - 1) / p.chunks;
   const int held = p.chunks > 1 ? (int)(sums + 15) / 16 * 16 : 0;
@@ -694,7 +725,10 @@ int ctas_for(int64_t rows, int sm_count) {  // no CTA without a row
   return (int)std::min<int64_t>(sm_count, rows);
 }
 
-bool linear_params(const W4LinearParams& l, int sm_count, W4RowsParams* p, int* ctas) {
+// The cut of a linear layer of up to 16 tokens (32 columns measured 31 us where the tiles
+// of w4_tiles.cu take 20: the parts of k come to too many): the fewest parts of k whose tokens fit
+// shared memory at once, else one part in pieces.
+bool linear_params(const W4LinearParams& l, int sm_count, W4RowsParams* p) {
   if (l.m > 16) return false;
   p->n = l.n;
   p->k = (int)l.k;
@@ -706,25 +740,43 @@ bool linear_params(const W4LinearParams& l, int sm_count, W4RowsParams* p, int* 
   p->y_stride = l.y_stride;
   p->picks = (int)l.m;
   p->status = l.status;
-  *ctas = ctas_for(l.n, sm_count);
-  return cut_linear(*p, *ctas);
+  for (int parts = 1; parts <= 8; ++parts)
+    if (cut_linear(*p, parts, sm_count) && p->chunks == 1) return true;
+  return cut_linear(*p, 1, sm_count);
 }
 
 }  // namespace
 
-bool w4_rows_take_linear(const W4LinearParams& l, int sm_count) {
+bool w4_rows_take_linear(const W4LinearParams& l, int sm_count, size_t* scratch) {
   W4RowsParams p;
-  int ctas;
-  return linear_params(l, sm_count, &p, &ctas);
+  if (!linear_params(l, sm_count, &p)) return false;
+  *scratch = p.parts > 1 ? (size_t)p.parts * l.m * l.n * sizeof(float) : 0;
+  return true;
 }
 
-cudaError_t launch_w4_rows_linear(int dtype, const W4LinearParams& l, int sm_count,
-                                  cudaStream_t s) {
+cudaError_t launch_w4_rows_linear(int dtype, const W4LinearParams& l, void* scratch, int sm_count,
+                                  int* launches, cudaStream_t s) {
   W4RowsParams p;
-  int ctas;
-  if (!linear_params(l, sm_count, &p, &ctas)) return cudaErrorInvalidValue;
-  const int nb = l.m > 8 ? 2 : 1;
-  return launch_any<kLinear>(dtype, p, nb, warps_for(nb), true, ctas, s);
+  if (!linear_params(l, sm_count, &p)) return cudaErrorInvalidValue;
+  p.part_sums = static_cast<float*>(scratch);
+  const int nb = blocks_of(p.picks);
+  cudaError_t e = launch_any<kLinear>(dtype, p, nb, warps_for(nb), true, p.parts * p.row_ctas, s);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  if (p.parts == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((l.m * l.n + 255) / 256, 8 * sm_count));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = dtype == LBGEMM_BF16 ? cudaLaunchKernelEx(&cfg, rows_join_kernel<__nv_bfloat16>, p)
+                           : cudaLaunchKernelEx(&cfg, rows_join_kernel<__half>, p);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
 }
 
 bool w4_rows_take_moe(const MoeParams& m, int sm_count) {
