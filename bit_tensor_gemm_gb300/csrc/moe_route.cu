@@ -5,9 +5,11 @@
 //   chosen experts or over all.
 //
 // A warp a token: the logits sit in registers as sortable 32-bit keys, and each
-// of the top_k rounds is two warp reductions (the largest key; the lowest expert
-// that has it), so ties are settled by value and index and by nothing else.
-// Bound by the launch up to thousands of tokens.
+// of the top_k rounds takes the largest by warp reductions, so ties are settled by
+// value and index and by nothing else.  A 16-bit logit leaves room for the expert in
+// its key's low bits, and one reduction a round finds both; of fp32 logits a second
+// one finds the lowest expert that has the largest key.  Bound by the launch up to
+// thousands of tokens, then by logic operations.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -20,19 +22,33 @@ namespace {
 
 constexpr int kWarps = 4;
 
-// A key that orders as the numbers do (0: never chosen).  NaN and -inf are never
-// chosen, +inf counts as the largest finite number, -0 as 0.
-__device__ __forceinline__ float usable(float x) {
-  if (!(x > -INFINITY)) return -INFINITY;
-  return fminf(x, FLT_MAX) + 0.0f;
+// Low bits of a key that the type's numbers leave free: it has 8 exponent bits and
+// T's mantissa bits.
+template <typename T>
+constexpr int kFree = 0;
+template <>
+constexpr int kFree<__nv_bfloat16> = 16;
+template <>
+constexpr int kFree<__half> = 13;
+
+// A key that orders as the numbers do (0: never chosen), the lower expert first among
+// equals where there is room.  NaN and -inf are never chosen, +inf counts as the largest
+// finite fp32 number (which no 16-bit number is, so there its key is inf's own), -0 as 0.
+template <typename T>
+__device__ __forceinline__ uint32_t key_of(T logit, int expert) {
+  constexpr uint32_t low = (1u << kFree<T>) - 1;
+  float x = to_f32(logit);
+  if (!(x > -INFINITY)) return 0;
+  if (low == 0) x = fminf(x, FLT_MAX);
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  const uint32_t key = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return low ? (key & ~low) | (low - expert) : key;
 }
-__device__ __forceinline__ uint32_t key_of(float x) {
-  if (x == -INFINITY) return 0;
-  const uint32_t u = __float_as_uint(x);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
+template <typename T>
 __device__ __forceinline__ float number_of(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+  constexpr uint32_t low = (1u << kFree<T>) - 1;
+  return fminf(__uint_as_float(key & 0x80000000u ? key & 0x7fffffffu & ~low : ~(key | low)),
+               FLT_MAX);
 }
 
 // PER: experts a lane holds, expert 32 i + lane in place i.
@@ -46,18 +62,18 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParam
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = 32 * i + lane;
-    key[i] = e < p.experts ? key_of(usable(to_f32(row[e]))) : 0;
+    key[i] = e < p.experts ? key_of(row[e], e) : 0;
   }
   uint32_t best = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) best = max(best, key[i]);
   const uint32_t first = __reduce_max_sync(0xffffffffu, best);
-  const float top = number_of(first);
+  const float top = number_of<T>(first);
   float all = 0.0f;
   if (!p.renormalize) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (key[i]) all += expf(number_of(key[i]) - top);
+      if (key[i]) all += expf(number_of<T>(key[i]) - top);
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
   }
@@ -68,12 +84,17 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParam
     const uint32_t most = __reduce_max_sync(0xffffffffu, best);
     if (most == 0) break;
     uint32_t at = 0xffffffffu;
-    if (best == most) {
+    if (kFree<T> > 0) {
+      constexpr uint32_t low = (1u << kFree<T>) - 1;
+      at = low - (most & low);
+    } else {
+      if (best == most) {
 #pragma unroll
-      for (int i = PER - 1; i >= 0; --i)
-        if (key[i] == most) at = 32 * i + lane;
+        for (int i = PER - 1; i >= 0; --i)
+          if (key[i] == most) at = 32 * i + lane;
+      }
+      at = __reduce_min_sync(0xffffffffu, at);
     }
-    at = __reduce_min_sync(0xffffffffu, at);
     if (lane == j) id = (int)at, chosen = most;
     if (lane == (at & 31)) {
       best = 0;
@@ -84,7 +105,7 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParam
       }
     }
   }
-  float w = chosen ? expf(number_of(chosen) - top) : 0.0f;
+  float w = chosen ? expf(number_of<T>(chosen) - top) : 0.0f;
   if (p.renormalize) {
     all = w;
 #pragma unroll

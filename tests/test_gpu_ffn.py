@@ -201,6 +201,27 @@ def test_route_odd_logits(renormalize):
     check_route(2, l, 40, 4, renormalize)
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("experts", [40, 1024])
+def test_route_odd_logits_of_16_bits(dtype, experts):
+    """A key holds the expert too: the largest and smallest numbers, signs, subnormals."""
+    t = U.DTYPES[dtype]
+    inf, nan, most = float("inf"), float("nan"), torch.finfo(t).max
+    tiny = torch.finfo(t).smallest_normal * torch.finfo(t).eps
+    l = torch.zeros((9, experts), device="cuda").to(t)
+    l[0], l[1] = -inf, nan
+    l[2, :-2] = -inf
+    l[3, 5], l[3, 11], l[3, 3] = most, inf, most
+    l[4, ::2] = -0.0
+    l[5, 7], l[5, 9], l[5, 3] = nan, 2.0, -inf
+    l[6, 1::2], l[6, 20] = -tiny, tiny
+    l[7] = -most
+    l[7, -1] = -most * (1 - torch.finfo(t).eps)
+    l[8, :-3], l[8, -1] = inf, -1.0
+    for top, renormalize in ((4, True), (32, False)):
+        check_route(dtype, l, experts, top, renormalize)
+
+
 # ---- experts ----------------------------------------------------------------------------------
 
 
