@@ -33,15 +33,16 @@ constexpr int kRing = 216 * 1024;
 // a stage and the weights that are not among them)
 __host__ __device__ constexpr int most_ring(int vpt) { return (vpt > 1 ? 224 : 220) * 1024; }
 __host__ __device__ constexpr int blocks_for(int wpr, int vpt, bool back) {
-  return back ? (wpr <= 8 ? 2 : 1) : vpt > 1 ? 1 : wpr <= 8 ? 4 : 2;
+  return back ? (wpr <= 8 ? 2 : 1) : vpt > 1 ? (wpr == 12 ? 2 : 1) : wpr <= 8 ? 4 : 2;
 }
+__host__ __device__ constexpr int threads_for(int wpr) { return wpr <= 8 ? 256 : 32 * wpr; }
 
 // Warps and vectors a thread of a row, and rows that are taken at once.
 struct Shape {
   int wpr, vpt, rows;
 };
 // A backward pass with several vectors a thread keeps the weights in shared memory: its
-// sums take the registers (8192 x 5120: 336 us with spills, 205 without).
+// sums take the registers (8192 x 8192: 416 us with spills, 238 without).
 __host__ __device__ constexpr bool weights_aside(int vpt, bool back) { return back && vpt > 1; }
 struct NormCut {
   Shape shape = {};
@@ -141,9 +142,12 @@ __device__ __forceinline__ bool row_sums(float (&v)[N], float* slots, int group,
   if constexpr (WPR > 1) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      v[i] = slots[i * 16 + threadIdx.x % WPR];
+      constexpr int PLACES = WPR == 12 ? 16 : WPR;
+      const int place = threadIdx.x % PLACES;
+      v[i] = place < WPR ? slots[i * 16 + place] : 0.0f;
 #pragma unroll
-      for (int off = WPR / 2; off >= 1; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+      for (int off = PLACES / 2; off >= 1; off >>= 1)
+        v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
     }
   }
   return stop;
@@ -154,10 +158,10 @@ __device__ __forceinline__ bool row_sums(float (&v)[N], float* slots, int group,
 // copies (a warp of its own would leave fewer registers to the others).  The tensors of
 // a stage: x, y, a gate for each row, dx', dn, those that are given; each [rows][width].
 template <typename T, int WPR, int VPT, int ROWS, bool BACK>
-__global__ void __launch_bounds__(WPR <= 8 ? 256 : 512, blocks_for(WPR, VPT, BACK))
+__global__ void __launch_bounds__(threads_for(WPR), blocks_for(WPR, VPT, BACK))
     residual_norm_kernel(const ResidualNormParams p, const NormCut cut,
                          float* __restrict__ partial) {
-  constexpr int THREADS = WPR <= 8 ? 256 : 512;
+  constexpr int THREADS = threads_for(WPR);
   constexpr int LANES = 32 * WPR, GROUPS = THREADS / LANES, HELD = GROUPS * ROWS;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t bars[2 * kMaxStages];
@@ -540,18 +544,25 @@ __global__ void __launch_bounds__(256)
   if (y == 0 && c < width) *reinterpret_cast<float4*>(out + c) = v;
 }
 
-Shape shape_of(const ResidualNormParams& p, int sm_count) {
+Shape shape_of(int dtype, const ResidualNormParams& p, int sm_count, bool back) {
   const int vectors = p.width / 8;
-  // two rows at once where every SM has several
-  const int rows = p.tokens >= 8 * (int64_t)sm_count ? 2 : 1;
+  // Where every SM has several rows: two at once, or (backward, wide rows) two vectors a
+  // thread and two blocks an SM (8192 x 4096: 124 us, two rows at once 131; 300 x 4096:
+  // 15.0 against 12.5 of one row at once).
+  const bool many = p.tokens >= 8 * (int64_t)sm_count;
+  if (back && many && vectors > 256 && vectors <= 512) return {8, 2, 1};
+  const int rows = many ? 2 : 1;
   for (int w = 1; w <= 16; w *= 2)
     if (vectors <= 32 * w) return {w, 1, w >= 8 ? rows : 1};
+  // (8192 x 5120: forward 84 us, with 16 warps 93, backward 181 against 205; forward of
+  // fp32 spills so, 4096 x 6144: 75 against 69)
+  if (vectors <= 768 && (back || dtype != LBGEMM_F32)) return {12, 2, 1};
   return {16, vectors <= 1024 ? 2 : 4, 1};
 }
 
 NormCut cut_of(int dtype, const ResidualNormParams& p, bool back, int sm_count) {
   NormCut cut;
-  const Shape shape = shape_of(p, sm_count);
+  const Shape shape = shape_of(dtype, p, sm_count, back);
   cut.groups = shape.wpr <= 8 ? 8 / shape.wpr : 1;
   const int rows = cut.groups * shape.rows;
   const int held = (p.x != nullptr) + (p.y != nullptr) + (p.gate && p.gate_stride != 0) +
@@ -588,7 +599,7 @@ cudaError_t launch(const ResidualNormParams& p, const NormCut& cut, float* parti
     if (e != cudaSuccess) return e;
     set |= uint64_t(1) << dev;
   }
-  kernel<<<cut.blocks, WPR <= 8 ? 256 : 512, cut.stages * cut.stage_bytes + cut.aside_bytes, s>>>(
+  kernel<<<cut.blocks, threads_for(WPR), cut.stages * cut.stage_bytes + cut.aside_bytes, s>>>(
       p, cut, partial);
   return cudaGetLastError();
 }
@@ -602,13 +613,20 @@ cudaError_t launch_typed(const ResidualNormParams& p, const NormCut& cut, float*
     case 2: return launch<T, 2, 1, 1, BACK>(p, cut, partial, s);
     case 4: return launch<T, 4, 1, 1, BACK>(p, cut, partial, s);
     case 8:
+      if constexpr (BACK)
+        if (shape.vpt == 2) return launch<T, 8, 2, 1, BACK>(p, cut, partial, s);
       return shape.rows == 2 ? launch<T, 8, 1, 2, BACK>(p, cut, partial, s)
                              : launch<T, 8, 1, 1, BACK>(p, cut, partial, s);
+    case 12:
+      if constexpr (BACK || sizeof(T) == 2) return launch<T, 12, 2, 1, BACK>(p, cut, partial, s);
+      return cudaErrorInvalidValue;
     default: break;
   }
-  if (shape.vpt == 1)
-    return shape.rows == 2 ? launch<T, 16, 1, 2, BACK>(p, cut, partial, s)
-                           : launch<T, 16, 1, 1, BACK>(p, cut, partial, s);
+  if (shape.vpt == 1) {
+    if constexpr (!BACK)
+      if (shape.rows == 2) return launch<T, 16, 1, 2, BACK>(p, cut, partial, s);
+    return launch<T, 16, 1, 1, BACK>(p, cut, partial, s);
+  }
   if (shape.vpt == 2) return launch<T, 16, 2, 1, BACK>(p, cut, partial, s);
   if constexpr (sizeof(T) == 2) return launch<T, 16, 4, 1, BACK>(p, cut, partial, s);
   return cudaErrorInvalidValue;

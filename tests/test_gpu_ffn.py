@@ -359,6 +359,10 @@ NORMS = [  # dtype, tokens, width, post, gate, next, pad, a, b
     (0, 40, 16384, True, "token", True, 0, 1.0, 1.0), (2, 19, 8192, True, "token", True, 0, 1.0, 1.0),
     (0, 1500, 512, True, "token", False, 0, 0.0, 1.0), (1, 5, 1024, False, "none", False, 0, 1.0, 1.0),
     (2, 3001, 128, True, "channel", True, 0, 1.0, 1.0), (0, 2000, 6144, True, "channel", True, 0, 1.0, 1.0),
+    (1, 1300, 2064, True, "token", True, 8, 1.0, 1.0), (0, 1700, 4096, True, "channel", True, 0, 1.0, 0.5),
+    (2, 1301, 4088, True, "token", True, 0, 1.0, 1.0), (2, 150, 5128, True, "channel", True, 4, 1.0, 1.0),
+    (2, 35, 8192, True, "channel", True, 0, 1.0, 1.0), (0, 160, 7176, False, "token", True, 0, 1.0, 1.0),
+    (0, 30, 12296, True, "channel", True, 8, 1.0, 1.0), (1, 155, 16384, True, "token", False, 0, 1.0, 1.0),
 ]
 EPS = 1e-5
 
