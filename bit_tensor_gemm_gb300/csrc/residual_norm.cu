@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(threads_for(WPR), blocks_for(WPR, VPT, BACK))
     if (cut.stages == 1) refill(step + stride_steps, 0, use + 1);
     if (++slot == cut.stages) slot = 0, ++use;
   }
-  if (abort_flag) {
+  if (__syncthreads_or(abort_flag)) {
     // Let the copies in flight land (again with a limit): those of the slots from this
     // row's on.
     volatile int go_on = 0;
@@ -485,22 +485,35 @@ __global__ void __launch_bounds__(threads_for(WPR), blocks_for(WPR, VPT, BACK))
   }
   if constexpr (BACK) {
     if (!partial) return;
-    // the row of sums of this block and group: post, next, gate
-    float* mine = partial + ((int64_t)blockIdx.x * GROUPS + group) * 3 * width;
+    // the row of sums of this block: post, next, gate.  Several groups add theirs in shared
+    // memory, in order (the ring is theirs now: a stage holds two rows a group at least, so
+    // its bytes are a row of fp32 sums for each).
+    float* mine = partial + (int64_t)blockIdx.x * 3 * width;
+    float* const joined = reinterpret_cast<float*>(ring);
+    auto put = [&](int which, const Vec<T>* sum) {
+      if constexpr (GROUPS > 1) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = at + j * LANES;
-      if (v >= vectors) continue;
-      auto put = [&](int which, const Vec<T>& x) {
+      for (int j = 0; j < VPT; ++j) {
+        const int v = at + j * LANES;
+        if (v >= vectors) continue;
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[2 * i] = x.v[i].a, f[2 * i + 1] = x.v[i].b;
-        store8<float>(mine + (int64_t)which * width + v * 8, f);
-      };
-      if (p.dpost) put(0, sum_post[j]);
-      if (p.dnext) put(1, sum_next[j]);
-      if (p.dgate && !own_gate) put(2, sum_gate[j]);
-    }
+        for (int i = 0; i < 4; ++i) f[2 * i] = sum[j].v[i].a, f[2 * i + 1] = sum[j].v[i].b;
+        store8<float>((GROUPS > 1 ? joined + group * width : mine + which * width) + v * 8, f);
+      }
+      if constexpr (GROUPS > 1) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < width; c += THREADS) {
+          float f = joined[c];
+#pragma unroll
+          for (int g = 1; g < GROUPS; ++g) f += joined[g * width + c];
+          mine[which * width + c] = f;
+        }
+      }
+    };
+    if (p.dpost) put(0, sum_post);
+    if (p.dnext) put(1, sum_next);
+    if (p.dgate && !own_gate) put(2, sum_gate);
   }
 }
 
@@ -654,7 +667,7 @@ cudaError_t launch_residual_norm(int dtype, const ResidualNormParams& p, int sm_
 size_t residual_norm_scratch(int dtype, const ResidualNormParams& p, int sm_count) {
   if (!sums(p)) return 0;
   const NormCut cut = cut_of(dtype, p, true, sm_count);
-  return (size_t)std::max(1, cut.blocks * cut.groups) * 3 * p.width * sizeof(float);
+  return (size_t)std::max(1, cut.blocks) * 3 * p.width * sizeof(float);
 }
 
 cudaError_t launch_residual_norm_backward(int dtype, const ResidualNormParams& p, int sm_count,
@@ -668,7 +681,7 @@ cudaError_t launch_residual_norm_backward(int dtype, const ResidualNormParams& p
   if (!sums(p)) return cudaSuccess;
   SumOut to = {{p.dpost, p.dnext, p.gate_stride == 0 ? static_cast<float*>(p.dgate) : nullptr}};
   residual_norm_sums_kernel<<<dim3((p.width + 31) / 32, 3), 256, 0, s>>>(
-      partial, cut.blocks * cut.groups, p.width, to);
+      partial, cut.blocks, p.width, to);
   *launches += 1;
   return cudaGetLastError();
 }
