@@ -47,7 +47,6 @@ __host__ __device__ constexpr bool weights_aside(int vpt, bool back) { return ba
 struct NormCut {
   Shape shape = {};
   int blocks = 0, stages = 0, stage_bytes = 0, aside_bytes = 0;
-  int groups = 0;  // of rows, beside one another in a block
 };
 
 // Two numbers; as plain fp32 operations, since the paired ones of this file's other
@@ -557,45 +556,57 @@ __global__ void __launch_bounds__(256)
   if (y == 0 && c < width) *reinterpret_cast<float4*>(out + c) = v;
 }
 
-Shape shape_of(int dtype, const ResidualNormParams& p, int sm_count, bool back) {
-  const int vectors = p.width / 8;
-  // Where every SM has several rows: two at once, or (backward, wide rows) two vectors a
-  // thread and two blocks an SM (8192 x 4096: 124 us, two rows at once 131; 300 x 4096:
-  // 15.0 against 12.5 of one row at once).
-  const bool many = p.tokens >= 8 * (int64_t)sm_count;
-  if (back && many && vectors > 256 && vectors <= 512) return {8, 2, 1};
-  const int rows = many ? 2 : 1;
-  for (int w = 1; w <= 16; w *= 2)
-    if (vectors <= 32 * w) return {w, 1, w >= 8 ? rows : 1};
-  // (8192 x 5120: forward 84 us, with 16 warps 93, backward 181 against 205; forward of
-  // fp32 spills so, 4096 x 6144: 75 against 69)
-  if (vectors <= 768 && (back || dtype != LBGEMM_F32)) return {12, 2, 1};
-  return {16, vectors <= 1024 ? 2 : 4, 1};
-}
+int groups_of(int wpr) { return wpr <= 8 ? 8 / wpr : 1; }
 
-NormCut cut_of(int dtype, const ResidualNormParams& p, bool back, int sm_count) {
+// How a call is cut with a shape; `roomy` tells whether two stages fit a block's share of
+// an SM.
+NormCut cut_with(const Shape& shape, int dtype, const ResidualNormParams& p, bool back,
+                 int sm_count, bool* roomy) {
   NormCut cut;
-  const Shape shape = shape_of(dtype, p, sm_count, back);
-  cut.groups = shape.wpr <= 8 ? 8 / shape.wpr : 1;
-  const int rows = cut.groups * shape.rows;
+  cut.shape = shape;
+  const int row_bytes = p.width * (dtype == LBGEMM_F32 ? 4 : 2);
+  const int rows = groups_of(shape.wpr) * shape.rows;
   const int held = (p.x != nullptr) + (p.y != nullptr) + (p.gate && p.gate_stride != 0) +
                    (back && p.dx_out) + (back && p.dn);
   const int64_t steps = (p.tokens + rows - 1) / rows;
-  cut.stage_bytes = rows * p.width * (dtype == LBGEMM_F32 ? 4 : 2) * std::max(held, 1);
-  const int per_sm = blocks_for(shape.wpr, shape.vpt, back);
-  cut.blocks = (int)std::min<int64_t>(steps, (int64_t)sm_count * per_sm);
-  cut.aside_bytes = 0;
+  cut.stage_bytes = rows * row_bytes * std::max(held, 1);
   if (weights_aside(shape.vpt, back))
     cut.aside_bytes = ((p.post != nullptr) + (p.next != nullptr) +
-                       (p.gate && p.gate_stride == 0)) * p.width * (dtype == LBGEMM_F32 ? 4 : 2);
+                       (p.gate && p.gate_stride == 0)) * row_bytes;
+  const int per_sm = blocks_for(shape.wpr, shape.vpt, back);
+  cut.blocks = (int)std::min<int64_t>(steps, (int64_t)sm_count * per_sm);
   cut.stages = std::min(kMaxStages, (kRing / per_sm - cut.aside_bytes) / cut.stage_bytes);
+  *roomy = cut.stages >= 2;
   if (cut.stages < 2)
     cut.stages = std::max(
         1, std::min(2, (most_ring(shape.vpt) - cut.aside_bytes) / cut.stage_bytes));
   if (cut.blocks > 0)
     cut.stages = (int)std::min<int64_t>(cut.stages, (steps + cut.blocks - 1) / cut.blocks);
-  cut.shape = shape;
   return cut;
+}
+
+NormCut cut_of(int dtype, const ResidualNormParams& p, bool back, int sm_count) {
+  const int vectors = p.width / 8;
+  int wpr = 1;
+  while (wpr < 16 && vectors > 32 * wpr) wpr *= 2;
+  bool roomy = false;
+  // Where every group has several rows and two stages of them fit: two rows at once, or
+  // (backward, wide rows) two vectors a thread and two blocks an SM.  8192 x 4096 backward:
+  // 124 us, two rows at once 131, one 145; 65536 x 512: 55 and 142 us with two rows, 71 and
+  // 159 with one; with a single stage 2048 x 1000 of fp32 takes 33 us backward, not 17.
+  if (vectors <= 512 && p.tokens >= 8 * (int64_t)groups_of(wpr) * sm_count) {
+    const Shape shape = back && wpr == 16 ? Shape{8, 2, 1} : Shape{wpr, 1, 2};
+    const NormCut cut = cut_with(shape, dtype, p, back, sm_count, &roomy);
+    if (roomy) return cut;
+  }
+  Shape shape = {wpr, 1, 1};
+  // (8192 x 5120: forward 84 us, with 16 warps 93, backward 181 against 205; forward of
+  // fp32 spills so, 4096 x 6144: 75 against 69)
+  if (vectors > 512)
+    shape = vectors <= 768 && (back || dtype != LBGEMM_F32)
+                ? Shape{12, 2, 1}
+                : Shape{16, vectors <= 1024 ? 2 : 4, 1};
+  return cut_with(shape, dtype, p, back, sm_count, &roomy);
 }
 
 template <typename T, int WPR, int VPT, int ROWS, bool BACK>
@@ -621,6 +632,17 @@ template <typename T, bool BACK>
 cudaError_t launch_typed(const ResidualNormParams& p, const NormCut& cut, float* partial,
                          cudaStream_t s) {
   const Shape& shape = cut.shape;
+  if (shape.rows == 2) {
+    switch (shape.wpr) {
+      case 1: return launch<T, 1, 1, 2, BACK>(p, cut, partial, s);
+      case 2: return launch<T, 2, 1, 2, BACK>(p, cut, partial, s);
+      case 4: return launch<T, 4, 1, 2, BACK>(p, cut, partial, s);
+      case 8: return launch<T, 8, 1, 2, BACK>(p, cut, partial, s);
+      default: break;
+    }
+    if constexpr (!BACK) return launch<T, 16, 1, 2, BACK>(p, cut, partial, s);
+    return cudaErrorInvalidValue;
+  }
   switch (shape.wpr) {
     case 1: return launch<T, 1, 1, 1, BACK>(p, cut, partial, s);
     case 2: return launch<T, 2, 1, 1, BACK>(p, cut, partial, s);
@@ -628,18 +650,13 @@ cudaError_t launch_typed(const ResidualNormParams& p, const NormCut& cut, float*
     case 8:
       if constexpr (BACK)
         if (shape.vpt == 2) return launch<T, 8, 2, 1, BACK>(p, cut, partial, s);
-      return shape.rows == 2 ? launch<T, 8, 1, 2, BACK>(p, cut, partial, s)
-                             : launch<T, 8, 1, 1, BACK>(p, cut, partial, s);
+      return launch<T, 8, 1, 1, BACK>(p, cut, partial, s);
     case 12:
       if constexpr (BACK || sizeof(T) == 2) return launch<T, 12, 2, 1, BACK>(p, cut, partial, s);
       return cudaErrorInvalidValue;
     default: break;
   }
-  if (shape.vpt == 1) {
-    if constexpr (!BACK)
-      if (shape.rows == 2) return launch<T, 16, 1, 2, BACK>(p, cut, partial, s);
-    return launch<T, 16, 1, 1, BACK>(p, cut, partial, s);
-  }
+  if (shape.vpt == 1) return launch<T, 16, 1, 1, BACK>(p, cut, partial, s);
   if (shape.vpt == 2) return launch<T, 16, 2, 1, BACK>(p, cut, partial, s);
   if constexpr (sizeof(T) == 2) return launch<T, 16, 4, 1, BACK>(p, cut, partial, s);
   return cudaErrorInvalidValue;

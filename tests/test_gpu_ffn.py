@@ -363,6 +363,8 @@ NORMS = [  # dtype, tokens, width, post, gate, next, pad, a, b
     (2, 1301, 4088, True, "token", True, 0, 1.0, 1.0), (2, 150, 5128, True, "channel", True, 4, 1.0, 1.0),
     (2, 35, 8192, True, "channel", True, 0, 1.0, 1.0), (0, 160, 7176, False, "token", True, 0, 1.0, 1.0),
     (0, 30, 12296, True, "channel", True, 8, 1.0, 1.0), (1, 155, 16384, True, "token", False, 0, 1.0, 1.0),
+    (0, 9803, 136, True, "channel", True, 8, 1.0, 1.0), (1, 4999, 504, True, "token", True, 0, 1.0, 1.0),
+    (0, 2501, 1016, True, "channel", True, 0, 1.0, 0.5), (2, 9777, 72, False, "none", True, 0, 1.0, 1.0),
 ]
 EPS = 1e-5
 
