@@ -234,6 +234,9 @@ struct Run {
 // of `up`: they look up their picks and copy their first codes while `up` runs.
 __host__ __device__ constexpr int warps_for(int nb) { return nb == 1 ? 24 : 16; }
 constexpr int kFewWarps = 12, kFewPicks = 16;
+// Tiles of 8 columns in a round (24 tokens to 64 experts, 49 and 58 tiles a CTA: 68.3 us,
+// 69.7 with room for 48; no gain from 80).
+constexpr int kShares = 64;
 
 template <typename T, int MODE, int NB, bool STAGED, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
@@ -298,8 +301,9 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
 
   // ---- rounds: pieces of k by batches of tiles ----
   const int steps = p.steps;  // of a tile in a piece
-  const int TB = p.batch;     // tiles of a round
-  const int batches = (run.tiles + TB - 1) / TB;
+  // tiles of a round: as many in each, as few rounds as there is room for
+  const int batches = (run.tiles + p.batch - 1) / p.batch;
+  const int TB = batches > 1 ? (run.tiles + batches - 1) / batches : run.tiles;
   const int rounds = batches * p.chunks;
 
   // A place in this warp's part of a round.
@@ -630,7 +634,7 @@ bool cut_linear(W4RowsParams& p, int parts, int sm_count) {
   p.rows_each = (int)(p.n / p.row_ctas);
   p.rows_more = (int)(p.n % p.row_ctas);
   const int rows = p.rows_each + (p.rows_more > 0), tiles = (rows + 15) / 16;
-  p.batch = std::min(tiles, 48 / nb);
+  p.batch = std::min(tiles, kShares / nb);
   const int shares = (p.batch + warps) * nb * 512;
   const int all_steps = (p.k + kStep - 1) / kStep, steps = (all_steps + parts - 1) / parts;
   if (parts > 1 && (steps < 4 || (parts - 1) * steps >= all_steps)) return false;
@@ -658,7 +662,7 @@ bool cut_linear(W4RowsParams& p, int parts, int sm_count) {
 // ... and of a pass over the experts: staged where two slots of the ring are left.
 bool cut_experts(W4RowsParams& p, int nb, int warps, int vectors, int values) {
   const int smem = warps == kFewWarps ? kSmem / 2 - 512 : kSmem;
-  p.batch = warps == kFewWarps ? 24 : 48 / nb;
+  p.batch = warps == kFewWarps ? 24 : kShares / nb;
   const int shares = (p.batch + warps) * nb * 512;
   p.steps = (p.k + kStep - 1) / kStep;
   const int64_t tokens = (int64_t)vectors * (p.steps * kStep * 2 + 64);
