@@ -660,10 +660,10 @@ bool cut_linear(W4RowsParams& p, int parts, int sm_count) {
 }
 
 // ... and of a pass over the experts: staged where two slots of the ring are left.
-bool cut_experts(W4RowsParams& p, int nb, int warps, int vectors, int values) {
+bool cut_experts(W4RowsParams& p, int warps, int vectors, int values) {
   const int smem = warps == kFewWarps ? kSmem / 2 - 512 : kSmem;
-  p.batch = warps == kFewWarps ? 24 : kShares / nb;
-  const int shares = (p.batch + warps) * nb * 512;
+  p.batch = warps == kFewWarps ? 24 : kShares;
+  const int shares = (p.batch + warps) * 512;
   p.steps = (p.k + kStep - 1) / kStep;
   const int64_t tokens = (int64_t)vectors * (p.steps * kStep * 2 + 64);
   const int held = (values * 4 + 15) / 16 * 16;
@@ -711,10 +711,10 @@ cudaError_t launch_mode(const W4RowsParams& p, int nb, int warps, bool staged, i
     if (warps == kFewWarps)
       return staged ? launch<T, MODE, 1, true, kFewWarps>(p, ctas, s)
                     : launch<T, MODE, 1, false, kFewWarps>(p, ctas, s);
-    if (!staged)
-      return nb == 1 ? launch<T, MODE, 1, false>(p, ctas, s) : launch<T, MODE, 2, false>(p, ctas, s);
+    return staged ? launch<T, MODE, 1, true>(p, ctas, s) : launch<T, MODE, 1, false>(p, ctas, s);
+  } else {
+    return nb == 1 ? launch<T, MODE, 1, true>(p, ctas, s) : launch<T, MODE, 2, true>(p, ctas, s);
   }
-  return nb == 1 ? launch<T, MODE, 1, true>(p, ctas, s) : launch<T, MODE, 2, true>(p, ctas, s);
 }
 
 template <int MODE>
@@ -783,11 +783,18 @@ cudaError_t launch_w4_rows_linear(int dtype, const W4LinearParams& l, void* scra
   return e;
 }
 
+// An expert's weights stream once for every 8 of its picks; 16 columns a pass were no
+// faster (40 tokens, 6 of 64 experts of 2048 / 1024: 90 against 86 us).  Tiles cost some 20
+// us more for few picks, but no more for many.  Measured, rows against tiles: 64 tokens, 6
+// of 64 experts (384 picks): 104 and 113 us; 2 of 8 experts of 4096 / 2048, 64 and 96 picks:
+// 61 and 67, 76 and 67; of 2048 / 1024, 64 and 128 picks: 25 and 29, 35 and 29; one expert
+// of it, 24 picks: 15 and 27.
 bool w4_rows_take_moe(const MoeParams& m, int sm_count) {
   const int64_t picks = m.tokens * m.top_k;
   const int ctas = ctas_for(m.hidden, sm_count);
   // (runs are counted in 32 bits)
-  return picks <= kRowsMaxPicks && (m.hidden + ctas - 1) / ctas * picks <= kRowsMaxValues &&
+  return picks <= 6 * (int64_t)m.experts + 40 && picks <= kRowsMaxPicks &&
+         (m.hidden + ctas - 1) / ctas * picks <= kRowsMaxValues &&
          picks * std::max<int64_t>(2 * (int64_t)m.inter, m.hidden) < INT32_MAX;
 }
 
@@ -808,12 +815,9 @@ cudaError_t launch_w4_rows_moe(int dtype, const MoeParams& m, void* h, int sm_co
   p.ids = m.ids;
   p.weights = m.weights;
   p.status = m.status;
-  // Columns that one pass over an expert's rows serves.
-  const bool few = p.picks <= kFewPicks;
-  const int nb = !few && p.picks > 4 * m.experts ? 2 : 1;
-  const int warps = few ? kFewWarps : warps_for(nb);
-  bool staged = cut_experts(p, nb, warps, (int)m.tokens, 0);
-  cudaError_t e = launch_any<kUp>(dtype, p, nb, warps, staged, sm_count, s);
+  const int warps = p.picks <= kFewPicks ? kFewWarps : warps_for(1);
+  bool staged = cut_experts(p, warps, (int)m.tokens, 0);
+  cudaError_t e = launch_any<kUp>(dtype, p, 1, warps, staged, sm_count, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   p.n = m.hidden;
@@ -826,8 +830,8 @@ cudaError_t launch_w4_rows_moe(int dtype, const MoeParams& m, void* h, int sm_co
   const int ctas = ctas_for(m.hidden, sm_count);
   p.rows_each = m.hidden / ctas;
   p.rows_more = m.hidden % ctas;
-  staged = cut_experts(p, nb, warps, p.picks, (p.rows_each + (p.rows_more > 0)) * p.picks);
-  e = launch_any<kDown>(dtype, p, nb, warps, staged, ctas, s);
+  staged = cut_experts(p, warps, p.picks, (p.rows_each + (p.rows_more > 0)) * p.picks);
+  e = launch_any<kDown>(dtype, p, 1, warps, staged, ctas, s);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
