@@ -91,6 +91,15 @@ constexpr uint32_t instr(int m, int n) {  // fp32 sums, A and B of T, both K-maj
          ((uint32_t)(m >> 4) << 24);
 }
 
+// True in one lane of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, int* status) {
   volatile int go_on = 0;
   return mbar_wait(bar, parity, &go_on, status);
@@ -321,42 +330,52 @@ __global__ void __launch_bounds__(Layout<BN, PAIR>::kThreads, 1)
         st_cluster_u64(cluster_map(smem_addr((const void*)peer_issued), 0), (uint64_t)issued);
     }
   } else if (warp == 1) {
-    // ---- the MMAs ----
-    if (even && lane == 0) {
+    // ---- the MMAs: the warp keeps step, so that what an MMA takes is the same in all its
+    // lanes, and one lane issues them ----
+    if (even) {
       constexpr uint32_t idesc = instr<T>(kRows * CTAS, BN);
+      constexpr int PIECES = kSlice / 16;
+      const bool one = elect_one();
       int stage = 0, xparity = 0, slot = 0, parity = 0, acc = 0, cparity = 1;
       bool ok = true;
       while (ok && units.next(x)) {
-        if (!(ok = mbar_wait(accempty(acc), cparity, abort_flag, p.status))) break;
+        if (!(ok = wait_warp(accempty(acc), cparity))) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
         for (int s = x.slice; s < x.end; ++s) {
-          if (!(ok = mbar_wait(xfull(stage), xparity, abort_flag, p.status))) break;
-          if (!(ok = mbar_wait(full(slot), parity, abort_flag, p.status))) break;
+          if (!(ok = wait_warp(xfull(stage), xparity))) break;
+          if (!(ok = wait_warp(full(slot), parity))) break;
           tc_fence_after();
           const uint64_t desc = smem_desc_sw128(base + stage * L::kXBytes);
           const uint32_t a = tmem + L::kACol + slot * kSlotCols;
           const int pieces = min(kSlice, p.k - s * kSlice) / 16;
+          auto piece = [&](int i, uint32_t more) {
+            const uint64_t b = desc + (i / 4) * (L::kTokens * 128 >> 4) + 2 * (i % 4);
+            if (PAIR)
+              mma_pair_ts(d, a + 8 * i, b, idesc, more);
+            else
+              mma_f16_ts(d, a + 8 * i, b, idesc, more);
+          };
+          if (one) {
+            piece(0, s > x.slice ? 1u : 0u);
+            if (pieces == PIECES) {
 #pragma unroll
-          for (int i = 0; i < kSlice / 16; ++i)
-            if (i < pieces) {
-              const uint64_t b = desc + (i / 4) * (L::kTokens * 128 >> 4) + 2 * (i % 4);
-              const uint32_t more = s > x.slice || i > 0 ? 1u : 0u;
-              if (PAIR)
-                mma_pair_ts(d, a + 8 * i, b, idesc, more);
-              else
-                mma_f16_ts(d, a + 8 * i, b, idesc, more);
+              for (int i = 1; i < PIECES; ++i) piece(i, 1u);
+            } else {
+              for (int i = 1; i < pieces; ++i) piece(i, 1u);
             }
-          commit(empty(slot));
-          commit(xempty(stage));
+            commit(empty(slot));
+            commit(xempty(stage));
+          }
+          __syncwarp();
           if (++stage == XS) stage = 0, xparity ^= 1;
           if (++slot == SLOTS) slot = 0, parity ^= 1;
         }
         if (!ok) break;
-        commit(accfull(acc));
+        if (one) commit(accfull(acc));
         if (++acc == ACCS) acc = 0, cparity ^= 1;
       }
-      commit(done);  // arrives once every MMA issued above has completed
+      if (one) commit(done);  // arrives once every MMA issued above has completed
     }
   } else if (warp >= 4 && warp < 4 + kReaders) {
     // ---- read-out: lane = row, columns = tokens; the readers of a quarter take 32 in turn ----
