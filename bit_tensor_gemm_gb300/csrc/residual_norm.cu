@@ -14,6 +14,11 @@
 // shared memory, a few rows ahead, so that the bytes in flight do not depend on
 // registers; x' is computed anew from x and y in the backward pass, in fp32, so
 // nothing but the inputs is kept for it.
+//
+// Measured, bf16, every output: 8192 rows of 4096 in 55 us forward (4.9 TB/s; issue slots
+// three quarters full, as a word of two numbers takes some ten instructions an operand) and
+// 124 backward (3.3 TB/s, at 126 registers a thread); of 8192 in 104 and 238; 8192 x 4096 of
+// fp32 in 97 and 160 (5.5 and 5.0 TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>

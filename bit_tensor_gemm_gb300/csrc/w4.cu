@@ -1,22 +1,20 @@
 // w4.cu -- which kernel a call with 4-bit weights takes.
 //
-// Up to 16 tokens of a linear layer (8 for long rows, see w4_rows.cu) and up to 512
-// picks of a mixture stream the weights through warp MMAs; more run on tcgen05.
+// Few tokens (up to 8 of a linear layer, two or three picks an expert: the rules stand in
+// w4_rows.cu) stream the weights through warp MMAs; more run on tcgen05.
 #include "ffn.h"
 #include "w4_kernels.h"
 
 namespace lbg {
 
 size_t w4_linear_scratch(W4LinearParams* p, int sm_count) {
-  size_t bytes = 0;
-  return w4_rows_take_linear(*p, sm_count, &bytes) ? bytes : w4_tiles_linear_scratch(*p, sm_count);
+  return w4_rows_take_linear(*p, sm_count) ? 0 : w4_tiles_linear_scratch(*p, sm_count);
 }
 
 cudaError_t launch_w4_linear(int dtype, const W4LinearParams& p, void* scratch, int sm_count,
                              int* launches, cudaStream_t s) {
-  size_t bytes = 0;
-  return w4_rows_take_linear(p, sm_count, &bytes)
-             ? launch_w4_rows_linear(dtype, p, scratch, sm_count, launches, s)
+  return w4_rows_take_linear(p, sm_count)
+             ? launch_w4_rows_linear(dtype, p, sm_count, launches, s)
              : launch_w4_tiles_linear(dtype, p, scratch, sm_count, launches, s);
 }
 

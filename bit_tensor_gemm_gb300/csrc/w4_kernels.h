@@ -23,17 +23,15 @@ struct W4RowsParams {
   const int32_t* ids = nullptr;
   const float* weights = nullptr;
   int* status = nullptr;
-  // How the launch cuts the call: rows a CTA (rows_more CTAs have one more), pieces of
-  // k and their steps, tiles of a round, steps that codes are copied ahead; and where things lie in shared memory.
-  int rows_each = 0, rows_more = 0, chunks = 1, steps = 1, batch = 1, depth = 2;
-  // (linear) parts of k, the CTAs of each, and the parts' sums: fp32 [part][token][n]
-  int parts = 1, row_ctas = 1;
-  float* part_sums = nullptr;
+  // How the launch cuts the call: rows a CTA (rows_more CTAs have one more), steps of a
+  // row, tiles of a round at most, steps that codes are copied ahead; and where things lie
+  // in shared memory.
+  int rows_each = 0, rows_more = 0, steps = 1, batch = 1, depth = 2;
   int at_shares = 0, at_values = 0, at_tokens = 0, bytes = 0;
 };
-bool w4_rows_take_linear(const W4LinearParams& l, int sm_count, size_t* scratch);
-cudaError_t launch_w4_rows_linear(int dtype, const W4LinearParams& l, void* scratch, int sm_count,
-                                  int* launches, cudaStream_t s);
+bool w4_rows_take_linear(const W4LinearParams& l, int sm_count);
+cudaError_t launch_w4_rows_linear(int dtype, const W4LinearParams& l, int sm_count, int* launches,
+                                  cudaStream_t s);
 bool w4_rows_take_moe(const MoeParams& m, int sm_count);
 // h: [tokens * top_k][inter] of dtype
 cudaError_t launch_w4_rows_moe(int dtype, const MoeParams& m, void* h, int sm_count, int* launches,

@@ -1,5 +1,5 @@
 // w4_rows.cu -- products with 4-bit weights for few tokens: the weights stream
-// through warp MMAs once for 8 or 16 columns (tokens).
+// through warp MMAs once for 8 columns (tokens).
 //
 //   linear  Y[m][n] = row_scale[n] * sum_k X[m][k] * (code * scale)[n][k]
 //   up      h[pick][i] = silu(gate) * up, for every pick (token, expert)
@@ -8,9 +8,12 @@
 // Bound by the weights' stream from HBM (about 0.53 bytes a weight), and close
 // behind it by issue slots: a word of eight codes takes twelve operations to
 // become halves (w4_codes.cuh).  So the codes go to the MMA's 16-row side, which
-// has no row to spare, and the tokens to its 8-column side.
+// has no row to spare, and the tokens to its 8-column side.  Measured: 1 token x 128000 x
+// 4096 in 63 us (4.2 TB/s), x 11008 x 4096 in 10.7 (4 of them launch, staging and the last
+// sums); 24 tokens, 6 of 64 experts of 2048 / 1024, in 68 us (2.8 TB/s; logic operations
+// half of the time).
 //
-// A CTA an SM, 24 warps (16 for 16 columns).  CTAs take equal runs of weight rows: of the rows of all
+// A CTA an SM, 24 warps.  CTAs take equal runs of weight rows: of the rows of all
 // experts with a pick one after the other (linear, up), or, so that a token's
 // picks are joined within a CTA, the same rows of every such expert (down).  A run
 // goes in tiles of up to 16 rows and steps of 256 elements, tile by tile, and every
@@ -25,9 +28,8 @@
 // have are computed from others' data and not stored.
 //
 // Tokens are laid out in shared memory first (STAGED), in the order in which lanes
-// read them.  Where they do not fit, the linear layer gives parts of k to CTAs of their
-// own (whose sums a second kernel adds), or takes k in pieces; the experts read them
-// through L1 then, at 2 conflicts a column and load.
+// read them.  Where they do not fit, the experts read them through L1, at 2 conflicts a
+// load; a linear layer goes to w4_tiles.cu.
 //
 // A tile's shares of the warps that met it are added in shared memory, in the
 // order of the warps, at the end of the run (of a round of it, where it has more
@@ -54,7 +56,7 @@ constexpr int kSmem = 227 * 1024;  // of an SM; kSmem / 2 - 512 of one of two CT
 
 enum Mode { kLinear, kUp, kDown };
 
-// What a CTA knows of the picks: experts with a pick ("segments", of up to 8 NB
+// What a CTA knows of the picks: experts with a pick ("segments", of up to 8
 // picks each), and the picks in their order.
 struct Picks {
   int segments;
@@ -229,20 +231,19 @@ struct Run {
   }
 };
 
-// kWarps: 24, or the 16 that 16 columns leave registers for.  A mixture of few picks
-// takes 12 and half of the shared memory, so that the CTAs of `down` stand beside those
-// of `up`: they look up their picks and copy their first codes while `up` runs.
-__host__ __device__ constexpr int warps_for(int nb) { return nb == 1 ? 24 : 16; }
-constexpr int kFewWarps = 12, kFewPicks = 16;
+// kWarps: 24, as many as registers allow.  A mixture of few picks takes 12 and half of the
+// shared memory, so that the CTAs of `down` stand beside those of `up`: they look up their
+// picks and copy their first codes while `up` runs (1 token, 6 experts: 17.4 -> 14.9 us).
+constexpr int kAllWarps = 24, kFewWarps = 12, kFewPicks = 16;
 // Tiles of 8 columns in a round (24 tokens to 64 experts, 49 and 58 tiles a CTA: 68.3 us,
 // 69.7 with room for 48; no gain from 80).
 constexpr int kShares = 64;
 
-template <typename T, int MODE, int NB, bool STAGED, int kWarps>
+template <typename T, int MODE, bool STAGED, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
     w4_rows_kernel(const W4RowsParams p) {
   constexpr int kThreads = 32 * kWarps;
-  constexpr int COLS = 8 * NB, SHARE = 16 * COLS;  // columns; numbers of a tile
+  constexpr int COLS = 8, SHARE = 16 * COLS;  // columns; numbers of a tile
   extern __shared__ __align__(128) uint8_t smem[];
   float* shares = reinterpret_cast<float*>(smem + p.at_shares);  // [batch + kWarps][SHARE]
   // down: the picks' outputs [rows][picks]; linear: sums between pieces of k [rows][COLS]
@@ -268,10 +269,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
   // ---- the run ----
   Run<MODE> run;
   const int n = (int)p.n;
-  // (linear: CTAs by parts of k, then by rows)
-  const int part = MODE == kLinear ? blockIdx.x / p.row_ctas : 0;
-  const int cta = MODE == kLinear ? blockIdx.x - part * p.row_ctas : blockIdx.x;
-  const int first_step = part * p.steps;  // (one piece of k where there are parts)
+  const int cta = blockIdx.x;
   int own_rows = 0;
   if (MODE != kUp) {
     own_rows = p.rows_each + (cta < p.rows_more);
@@ -299,30 +297,27 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
     }
   }
 
-  // ---- rounds: pieces of k by batches of tiles ----
-  const int steps = p.steps;  // of a tile in a piece
+  // ---- rounds ----
+  const int steps = p.steps;  // of a tile
   // tiles of a round: as many in each, as few rounds as there is room for
-  const int batches = (run.tiles + p.batch - 1) / p.batch;
-  const int TB = batches > 1 ? (run.tiles + batches - 1) / batches : run.tiles;
-  const int rounds = batches * p.chunks;
+  const int rounds = (run.tiles + p.batch - 1) / p.batch;
+  const int TB = rounds > 1 ? (run.tiles + rounds - 1) / rounds : run.tiles;
 
   // A place in this warp's part of a round.
   struct Place {
-    int round, chunk, batch, tile, j, left;
+    int round, tile, j, left;
   };
   auto begin = [&](Place& x) {
-    const int total = min(TB, run.tiles - x.batch * TB) * steps;
+    const int total = min(TB, run.tiles - x.round * TB) * steps;
     const int each = total / kWarps, more = total - each * kWarps;
     const int first = warp * each + min(warp, more);
     x.left = each + (warp < more);
     x.tile = first / steps;
     x.j = first - x.tile * steps;
-    x.tile += x.batch * TB;
+    x.tile += x.round * TB;
   };
   auto next_round = [&](Place& x) {
-    ++x.round;
-    if (++x.batch == batches) x.batch = 0, ++x.chunk;
-    if (x.round < rounds) begin(x);
+    if (++x.round < rounds) begin(x);
   };
   // On from a place without steps left to one that has some (or the end).
   auto settle = [&](Place& x) {
@@ -343,7 +338,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
 
   // ---- codes, `depth` steps ahead ----
   const uint32_t code_row = k / 2, scale_row = k / p.group;
-  Place ahead = {0, 0, 0, 0, 0, 0};
+  Place ahead = {0, 0, 0, 0};
   if (rounds > 0) begin(ahead);
   Place at = ahead;  // (every warp goes through every round)
   settle(ahead);
@@ -356,7 +351,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       code_ptr[i] = p.w.codes + (uint64_t)r[i] * code_row + 16 * t +
-                    128 * (first_step + ahead.chunk * steps + ahead.j);
+                    128 * ahead.j;
   };
   aim_codes();
   const uint32_t ring = smem_addr(smem) + warp * p.depth * kSlotBytes + lane * 16;
@@ -364,7 +359,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
   const uint32_t ring_end = ring + p.depth * kSlotBytes;
   auto copy_codes = [&] {
     if (ahead.left > 0) {
-      const int step = first_step + ahead.chunk * steps + ahead.j;
+      const int step = ahead.j;
       if (step < whole) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -402,14 +397,14 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       scale_ptr[i] = p.w.scales + (uint64_t)r[i] * scale_row +
-                     ((8 * (first_step + scaled.chunk * steps + scaled.j) + t) >> shift);
+                     ((8 * scaled.j + t) >> shift);
       if (t == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w.row_scales + r[i]));
     }
   };
   aim_scales();
   auto load_scales = [&] {
     if (scaled.left == 0) return;
-    const int step = first_step + scaled.chunk * steps + scaled.j;
+    const int step = scaled.j;
     if (step < whole) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -438,21 +433,21 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
   // (weights and picks are older than the launch before this one; h is not)
   if (MODE == kDown) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  float acc[NB][4];
-  // This lane's columns: in memory, or staged: vector v of a piece at v * pitch, its
+  float acc[4];
+  // This lane's column: in memory, or staged: vector v of a piece at v * pitch, its
   // 16 bytes in the order that lanes read them, so that 8 lanes of neighbouring
   // vectors meet no conflict: [half step][word][t].
-  const T* column[NB];
-  const uint8_t* line[NB];
+  const T* column = nullptr;
+  const uint8_t* line = nullptr;
   const int pitch = steps * 512 + 64;
   uint32_t from = ring;
 
   while (at.round < rounds) {
-    if (STAGED && at.batch == 0) {
+    if (STAGED && at.round == 0) {
       const int pieces = steps * 32, vectors = MODE == kUp ? p.picks / p.top_k : p.picks;
       for (int v = warp; v < vectors; v += kWarps)
         for (int o = lane; o < pieces; o += 32) {
-          const int at_k = (first_step + at.chunk * steps) * kStep + 8 * o;
+          const int at_k = 8 * o;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (at_k < k)
             x = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + v * p.x_stride + at_k);
@@ -466,16 +461,15 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
       int segment = 0, row, rows;
       if (MODE != kLinear) run.tile(at.tile, segment, row, rows);
       const int most = columns_of(segment) - 1;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int pick = pick_of(segment, min(8 * b + g, most));
+      {
+        const int pick = pick_of(segment, min(g, most));
         const int v = MODE == kUp ? pick / p.top_k : pick;
         if (STAGED)
-          line[b] = staged + v * pitch + 16 * t + at.j * 512;
+          line = staged + v * pitch + 16 * t + at.j * 512;
         else
-          column[b] = static_cast<const T*>(p.x) + v * p.x_stride + 32 * t + at.j * kStep;
-        acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0.0f;
+          column = static_cast<const T*>(p.x) + v * p.x_stride + 32 * t + at.j * kStep;
       }
+      acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
       const int stop = min(steps, at.j + at.left);
       at.left -= stop - at.j;
       for (; at.j < stop; ++at.j) {
@@ -488,58 +482,45 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
         for (int h = 0; h < 2; ++h) {
           const uint4 cl = load_shared(from + 2 * h * 512);
           const uint4 ch = load_shared(from + (2 * h + 1) * 512);
-          uint4 x[NB][4];
+          uint4 x[4];
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              if (STAGED)
-                x[b][w] = *reinterpret_cast<const uint4*>(line[b] + h * 256 + w * 64);
-              else if (at.j < whole || left_of(at.j) > 128 * h)
-                x[b][w] = *reinterpret_cast<const uint4*>(column[b] + 128 * h + 8 * w);
-              else
-                x[b][w] = make_uint4(0, 0, 0, 0);
-            }
+          for (int w = 0; w < 4; ++w) {
+            if (STAGED)
+              x[w] = *reinterpret_cast<const uint4*>(line + h * 256 + w * 64);
+            else if (at.j < whole || left_of(at.j) > 128 * h)
+              x[w] = *reinterpret_cast<const uint4*>(column + 128 * h + 8 * w);
+            else
+              x[w] = make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t a[4], c[4];
             w4_word(w == 0 ? cl.x : w == 1 ? cl.y : w == 2 ? cl.z : cl.w, lo[h], a);
             w4_word(w == 0 ? ch.x : w == 1 ? ch.y : w == 2 ? ch.z : ch.w, hi[h], c);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              mma<T>(acc[b], a[0], c[0], a[1], c[1], x[b][w].x, x[b][w].y);
-              mma<T>(acc[b], a[2], c[2], a[3], c[3], x[b][w].z, x[b][w].w);
-            }
+            mma<T>(acc, a[0], c[0], a[1], c[1], x[w].x, x[w].y);
+            mma<T>(acc, a[2], c[2], a[3], c[3], x[w].z, x[w].w);
           }
         }
         // (each lane has read its own bytes of the slot: the next copy may land on it)
         copy_codes();
         from += kSlotBytes;
         if (from == ring_end) from = ring;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          if (STAGED)
-            line[b] += 512;
-          else
-            column[b] += kStep;
-        }
+        if (STAGED)
+          line += 512;
+        else
+          column += kStep;
       }
       // This warp's share of the tile: in place tile + warp, which no other share of the
       // round has (along the row of steps one of both grows).
-      float* s = shares + (at.tile - at.batch * TB + warp) * SHARE;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        *reinterpret_cast<float2*>(s + g * COLS + 8 * b + 2 * t) =
-            make_float2(acc[b][0], acc[b][1]);
-        *reinterpret_cast<float2*>(s + (g + 8) * COLS + 8 * b + 2 * t) =
-            make_float2(acc[b][2], acc[b][3]);
-      }
+      float* s = shares + (at.tile - at.round * TB + warp) * SHARE;
+      *reinterpret_cast<float2*>(s + g * COLS + 2 * t) = make_float2(acc[0], acc[1]);
+      *reinterpret_cast<float2*>(s + (g + 8) * COLS + 2 * t) = make_float2(acc[2], acc[3]);
       if (at.j == steps) at.j = 0, ++at.tile;
     }
     __syncthreads();
 
     // ---- the round's sums ----
-    const int first_tile = at.batch * TB, count = min(TB, run.tiles - first_tile);
+    const int first_tile = at.round * TB, count = min(TB, run.tiles - first_tile);
     const int each = count * steps / kWarps, more = count * steps - each * kWarps;
     auto warp_of = [&](int q) {  // whose step q of the round is
       const int longer = more * (each + 1);
@@ -573,15 +554,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
         } else if (MODE == kDown) {
           values[(row - run.first_row + r) * p.picks + pick] = v * scale0;
         } else {
-          // (the same lane meets an output in every piece of k)
-          float* sum = values + (row - run.first_row + r) * COLS + col;
-          if (at.chunk > 0) v += *sum;
-          if (at.chunk + 1 < p.chunks)
-            *sum = v;
-          else if (p.parts > 1)
-            p.part_sums[((int64_t)part * p.picks + pick) * n + row + r] = v * scale0;
-          else
-            static_cast<T*>(p.y)[pick * p.y_stride + row + r] = from_f32<T>(v * scale0);
+          static_cast<T*>(p.y)[pick * p.y_stride + row + r] = from_f32<T>(v * scale0);
         }
       }
     }
@@ -603,59 +576,30 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
   }
 }
 
-// y[m][n] = the sum of the parts of k, in order.
-template <typename T>
-__global__ void __launch_bounds__(256) rows_join_kernel(const W4RowsParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t total = p.picks * p.n;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / p.n, c = i - m * p.n;
-    float v = 0.0f;
-    for (int q = 0; q < p.parts; ++q) v += p.part_sums[q * total + i];
-    static_cast<T*>(p.y)[m * p.y_stride + c] = from_f32<T>(v);
-  }
-}
-
 // ---- how a launch lays out its shared memory -------------------------------------------
 constexpr int kStatic = sizeof(Picks) + 4 * (kRowsMaxExperts + 1) + 256;
 constexpr int kStaticLinear = 512;
 
-// Blocks of 8 columns for so many tokens.
-int blocks_of(int tokens) { return tokens <= 8 ? 1 : 2; }
+int ctas_for(int64_t rows, int sm_count) {  // no CTA without a row
+  return (int)std::min<int64_t>(sm_count, rows);
+}
 
-// Fills in the cut of a linear layer into parts of k, each of its own CTAs; false where
-// it does not fit.  A part's tokens are staged at once; only one part may take several
-// pieces (of 16 steps at least: fewer are too many rounds).
-bool cut_linear(W4RowsParams& p, int parts, int sm_count) {
-  const int nb = blocks_of(p.picks), warps = warps_for(nb);
-  p.parts = parts;
-  p.row_ctas = (int)std::min<int64_t>(sm_count / parts, p.n);
-  p.rows_each = (int)(p.n / p.row_ctas);
-  p.rows_more = (int)(p.n % p.row_ctas);
+// Fills in the cut of a linear layer; false where its tokens do not fit.
+bool cut_linear(W4RowsParams& p, int sm_count) {
+  const int ctas = ctas_for(p.n, sm_count);
+  p.rows_each = (int)(p.n / ctas);
+  p.rows_more = (int)(p.n % ctas);
   const int rows = p.rows_each + (p.rows_more > 0), tiles = (rows + 15) / 16;
-  p.batch = std::min(tiles, kShares / nb);
-  const int shares = (p.batch + warps) * nb * 512;
-  const int all_steps = (p.k + kStep - 1) / kStep, steps = (all_steps + parts - 1) / parts;
-  if (parts > 1 && (steps < 4 || (parts - 1) * steps >= all_steps)) return false;
-  const int64_t sums = (int64_t)rows * 8 * nb * 4;
-  const int room = kSmem - kStaticLinear - 2 * warps * kSlotBytes - shares;
-  int64_t most = (room / p.picks - 64) / (kStep * 2);
-  if (most < steps) {
-    if (parts > 1) return false;
-    most = ((room - sums) / p.picks - 64) / (kStep * 2);
-    if (most < 16) return false;
-  }
-  p.chunks = (int)((steps + most - 1) / most);
-  p.steps = (steps + p.chunks - 1) / p.chunks;
-  const int held = p.chunks > 1 ? (int)(sums + 15) / 16 * 16 : 0;
-  const int tokens = p.picks * (p.steps * kStep * 2 + 64);
-  const int left = kSmem - kStaticLinear - shares - held - tokens;
-  p.depth = std::min(kMaxDepth, left / (warps * kSlotBytes));
-  p.at_shares = p.depth * warps * kSlotBytes;
-  p.at_values = p.at_shares + shares;
-  p.at_tokens = p.at_values + held;
-  p.bytes = p.at_tokens + tokens;
+  p.batch = std::min(tiles, kShares);
+  p.steps = (p.k + kStep - 1) / kStep;
+  const int shares = (p.batch + kAllWarps) * 512;
+  const int64_t tokens = (int64_t)p.picks * (p.steps * kStep * 2 + 64);
+  const int64_t left = kSmem - kStaticLinear - shares - tokens;
+  if (left < 2 * kAllWarps * kSlotBytes) return false;
+  p.depth = (int)std::min<int64_t>(kMaxDepth, left / (kAllWarps * kSlotBytes));
+  p.at_shares = p.depth * kAllWarps * kSlotBytes;
+  p.at_tokens = p.at_shares + shares;
+  p.bytes = p.at_tokens + (int)tokens;
   return true;
 }
 
@@ -678,9 +622,9 @@ bool cut_experts(W4RowsParams& p, int warps, int vectors, int values) {
   return staged;
 }
 
-template <typename T, int MODE, int NB, bool STAGED, int WARPS = warps_for(NB)>
+template <typename T, int MODE, bool STAGED, int WARPS = kAllWarps>
 cudaError_t launch(const W4RowsParams& p, int ctas, cudaStream_t s) {
-  auto kernel = w4_rows_kernel<T, MODE, NB, STAGED, WARPS>;
+  auto kernel = w4_rows_kernel<T, MODE, STAGED, WARPS>;
   static std::atomic<uint64_t> set{0};  // devices on which the kernel has its shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -705,35 +649,34 @@ cudaError_t launch(const W4RowsParams& p, int ctas, cudaStream_t s) {
 }
 
 template <typename T, int MODE>
-cudaError_t launch_mode(const W4RowsParams& p, int nb, int warps, bool staged, int ctas,
-                        cudaStream_t s) {
-  if constexpr (MODE != kLinear) {
-    if (warps == kFewWarps)
-      return staged ? launch<T, MODE, 1, true, kFewWarps>(p, ctas, s)
-                    : launch<T, MODE, 1, false, kFewWarps>(p, ctas, s);
-    return staged ? launch<T, MODE, 1, true>(p, ctas, s) : launch<T, MODE, 1, false>(p, ctas, s);
+cudaError_t launch_mode(const W4RowsParams& p, int warps, bool staged, int ctas, cudaStream_t s) {
+  if constexpr (MODE == kLinear) {
+    return launch<T, MODE, true>(p, ctas, s);
   } else {
-    return nb == 1 ? launch<T, MODE, 1, true>(p, ctas, s) : launch<T, MODE, 2, true>(p, ctas, s);
+    if (warps == kFewWarps)
+      return staged ? launch<T, MODE, true, kFewWarps>(p, ctas, s)
+                    : launch<T, MODE, false, kFewWarps>(p, ctas, s);
+    return staged ? launch<T, MODE, true>(p, ctas, s) : launch<T, MODE, false>(p, ctas, s);
   }
 }
 
 template <int MODE>
-cudaError_t launch_any(int dtype, const W4RowsParams& p, int nb, int warps, bool staged, int ctas,
+cudaError_t launch_any(int dtype, const W4RowsParams& p, int warps, bool staged, int ctas,
                        cudaStream_t s) {
-  return dtype == LBGEMM_BF16
-             ? launch_mode<__nv_bfloat16, MODE>(p, nb, warps, staged, ctas, s)
-             : launch_mode<__half, MODE>(p, nb, warps, staged, ctas, s);
+  return dtype == LBGEMM_BF16 ? launch_mode<__nv_bfloat16, MODE>(p, warps, staged, ctas, s)
+                              : launch_mode<__half, MODE>(p, warps, staged, ctas, s);
 }
 
-int ctas_for(int64_t rows, int sm_count) {  // no CTA without a row
-  return (int)std::min<int64_t>(sm_count, rows);
-}
+}  // namespace
 
-// The cut of a linear layer of up to 16 tokens (32 columns measured 31 us where the tiles
-// of w4_tiles.cu take 20: the parts of k come to too many): the fewest parts of k whose tokens fit
-// shared memory at once, else one part in pieces.
-bool linear_params(const W4LinearParams& l, int sm_count, W4RowsParams* p) {
-  if (l.m > 16) return false;
+// Up to 8 tokens, where they fit shared memory beside the ring, and rows of up to 8192
+// (a launch has some 4 us before and after its stream here, tiles 6; but tiles cut k for
+// themselves and stream as fast).  Measured, rows against tiles: 1, 4 and 8 tokens x 11008 x
+// 4096: 10.9, 11.2, 12.1 and 12.6 us; x 4096 x 11008: 13.3, 13.7, 15.0 and 11.9; 1 x 128000
+// x 4096: 66 and 94; 8 x 19456 x 8192 (k in parts): 28 and 24; 1 x 1024 x 1024: 4.5 and 6.3.
+// Two blocks of 8 columns a pass: 12 x 4096 x 11008 16.5 us, tiles 12.2.
+static bool linear_params(const W4LinearParams& l, int sm_count, W4RowsParams* p) {
+  if (l.m > 8 || l.k > 8192) return false;
   p->n = l.n;
   p->k = (int)l.k;
   p->group = l.group;
@@ -744,56 +687,34 @@ bool linear_params(const W4LinearParams& l, int sm_count, W4RowsParams* p) {
   p->y_stride = l.y_stride;
   p->picks = (int)l.m;
   p->status = l.status;
-  for (int parts = 1; parts <= 8; ++parts)
-    if (cut_linear(*p, parts, sm_count) && p->chunks == 1) return true;
-  return cut_linear(*p, 1, sm_count);
+  return cut_linear(*p, sm_count);
 }
 
-}  // namespace
-
-bool w4_rows_take_linear(const W4LinearParams& l, int sm_count, size_t* scratch) {
+bool w4_rows_take_linear(const W4LinearParams& l, int sm_count) {
   W4RowsParams p;
-  if (!linear_params(l, sm_count, &p)) return false;
-  *scratch = p.parts > 1 ? (size_t)p.parts * l.m * l.n * sizeof(float) : 0;
-  return true;
+  return linear_params(l, sm_count, &p);
 }
 
-cudaError_t launch_w4_rows_linear(int dtype, const W4LinearParams& l, void* scratch, int sm_count,
-                                  int* launches, cudaStream_t s) {
+cudaError_t launch_w4_rows_linear(int dtype, const W4LinearParams& l, int sm_count, int* launches,
+                                  cudaStream_t s) {
   W4RowsParams p;
   if (!linear_params(l, sm_count, &p)) return cudaErrorInvalidValue;
-  p.part_sums = static_cast<float*>(scratch);
-  const int nb = blocks_of(p.picks);
-  cudaError_t e = launch_any<kLinear>(dtype, p, nb, warps_for(nb), true, p.parts * p.row_ctas, s);
-  if (e != cudaSuccess) return e;
-  *launches += 1;
-  if (p.parts == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>((l.m * l.n + 255) / 256, 8 * sm_count));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = dtype == LBGEMM_BF16 ? cudaLaunchKernelEx(&cfg, rows_join_kernel<__nv_bfloat16>, p)
-                           : cudaLaunchKernelEx(&cfg, rows_join_kernel<__half>, p);
+  const cudaError_t e =
+      launch_any<kLinear>(dtype, p, kAllWarps, true, ctas_for(p.n, sm_count), s);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }
 
 // An expert's weights stream once for every 8 of its picks; 16 columns a pass were no
-// faster (40 tokens, 6 of 64 experts of 2048 / 1024: 90 against 86 us).  Tiles cost some 20
-// us more for few picks, but no more for many.  Measured, rows against tiles: 64 tokens, 6
-// of 64 experts (384 picks): 104 and 113 us; 2 of 8 experts of 4096 / 2048, 64 and 96 picks:
-// 61 and 67, 76 and 67; of 2048 / 1024, 64 and 128 picks: 25 and 29, 35 and 29; one expert
-// of it, 24 picks: 15 and 27.
+// faster (40 tokens, 6 of 64 experts of 2048 / 1024: 90 against 86 us).  Tiles cost more for
+// few picks, but no more for many.  Measured, rows against tiles: 24, 32 and 64 tokens, 6 of
+// 64 experts: 72, 80, 104 and 77 us; 16 and 32, 2 of 8 experts of 4096 / 2048: 43, 61 and
+// 45; 32, 2 of 8 of 2048 / 1024: 24 and 23; 24 to one of those: 15 and 21.
 bool w4_rows_take_moe(const MoeParams& m, int sm_count) {
   const int64_t picks = m.tokens * m.top_k;
   const int ctas = ctas_for(m.hidden, sm_count);
   // (runs are counted in 32 bits)
-  return picks <= 6 * (int64_t)m.experts + 40 && picks <= kRowsMaxPicks &&
+  return picks <= 2 * (int64_t)m.experts + 32 && picks <= kRowsMaxPicks &&
          (m.hidden + ctas - 1) / ctas * picks <= kRowsMaxValues &&
          picks * std::max<int64_t>(2 * (int64_t)m.inter, m.hidden) < INT32_MAX;
 }
@@ -815,9 +736,9 @@ cudaError_t launch_w4_rows_moe(int dtype, const MoeParams& m, void* h, int sm_co
   p.ids = m.ids;
   p.weights = m.weights;
   p.status = m.status;
-  const int warps = p.picks <= kFewPicks ? kFewWarps : warps_for(1);
+  const int warps = p.picks <= kFewPicks ? kFewWarps : kAllWarps;
   bool staged = cut_experts(p, warps, (int)m.tokens, 0);
-  cudaError_t e = launch_any<kUp>(dtype, p, 1, warps, staged, sm_count, s);
+  cudaError_t e = launch_any<kUp>(dtype, p, warps, staged, sm_count, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   p.n = m.hidden;
@@ -831,7 +752,7 @@ cudaError_t launch_w4_rows_moe(int dtype, const MoeParams& m, void* h, int sm_co
   p.rows_each = m.hidden / ctas;
   p.rows_more = m.hidden % ctas;
   staged = cut_experts(p, warps, p.picks, (p.rows_each + (p.rows_more > 0)) * p.picks);
-  e = launch_any<kDown>(dtype, p, 1, warps, staged, ctas, s);
+  e = launch_any<kDown>(dtype, p, warps, staged, ctas, s);
   if (e == cudaSuccess) *launches += 1;
   return e;
 }

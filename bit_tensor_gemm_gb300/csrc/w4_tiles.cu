@@ -11,15 +11,24 @@
 // operand, brought by TMA (128-byte swizzle).  So shared memory carries a quarter of
 // the weights' bytes of a product of halves, and is bound by the tokens: from 65
 // tokens on a tile is a pair of CTAs' (cta_group::2, 128 weight rows in each), which
-// halves the tokens that each of them brings and reads (a single CTA's tile of 128 x
-// 256 ran 4096 tokens x 11008 x 4096 at 1.16 PFLOP/s, at the rate of its fills).
+// halves the tokens that each of them brings and reads (4096 tokens x 11008 x 4096: 317 us
+// with single CTAs of 128 x 256, at the rate of their fills, 258 with pairs).
 //
 // One persistent CTA an SM: warps for TMA of the codes (0), the MMAs (1, of a pair
 // the even CTA's), TMA of the tokens (2), read-out (4..11), converters (12 on: four
-// teams, of long slices three, that take slices in turn, a warp a quarter of the rows).  Tiles of
+// teams, of long slices three, that take slices in turn, a warp a quarter of the rows).
+// The MMAs' warp goes through its loop with all lanes: operands that are the same in a
+// warp stay in uniform registers, and an MMA is issued every 46 cycles; with one lane in
+// the loop it was 99, and up to 128 tokens were bound by that.  Tiles of
 // up to 128 tokens have two accumulators, so that a tile is read out beside the next
 // one's MMAs.  A reader has a row a lane and turns 32 tokens through shared memory
 // into vectors along the rows.  A linear layer with few tiles is cut along k and joined by join().
+//
+// Measured: 4096 tokens x 11008 x 4096 in 217 us (1.70 PFLOP/s, what a plain product of
+// 16-bit numbers reaches being 1.90), 64 x 19456 x 8192 in 25 us (3.4 TB/s of weights), 12 x
+// 4096 x 11008 in 12.5; 4096 tokens, 6 of 64 experts of 2048 / 1024, in 367 us (0.83
+// PFLOP/s: 1.9 blocks of tokens an expert, three quarters full; 67 us of sorting, gathering
+// and joining).
 //
 // In a pair the full barriers and the accumulators' empty ones are the even CTA's and
 // count both; the commits of the MMAs go to both.  Every
@@ -85,7 +94,7 @@ struct Layout {
 };
 
 template <typename T>
-constexpr uint32_t instr(int m, int n) {  // fp32 sums, A and B of T, both K-major, m x n
+__host__ __device__ constexpr uint32_t instr(int m, int n) {  // fp32 sums, A and B of T, both K-major, m x n
   const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
   return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
@@ -120,6 +129,9 @@ __device__ __forceinline__ void mma_pair_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 // A unit of work: a tile of rows by a block of tokens, whole or a part of k of it.
 struct Unit {
   int expert, first, count;  // the block's tokens: place of the first, how many
+  // Tokens that the MMAs take: whole thirty-twos for a pair (4096 tokens, 6 of 64 experts:
+  // 367 us, 383 with whole blocks).
+  int width;
   int row;                   // first row, in the expert
   int slice, end;            // slices of k
   int share;                 // of a part: its place among the shares (-1: a whole tile)
@@ -166,6 +178,7 @@ struct Units {
       x.first = at + skip;
       x.count = min(BN, p.offsets[expert + 1] - x.first);
     }
+    x.width = PAIR ? min(BN, (x.count + 31) / 32 * 32) : BN;
     u += step;
     return true;
   }
@@ -304,7 +317,7 @@ __global__ void __launch_bounds__(Layout<BN, PAIR>::kThreads, 1)
         for (int s = x.slice; s < x.end; ++s) {
           if (!(ok = mbar_wait(xempty(stage), parity, abort_flag, p.status))) break;
           const uint32_t dst = base + stage * L::kXBytes;
-          const int row = x.first + (even ? 0 : L::kTokens);
+          const int row = x.first + (even ? 0 : x.width / 2);
 #pragma unroll
           for (int b = 0; b < L::kBoxes; ++b) {
             // (a box that would begin past the row is any other: no MMA reads it)
@@ -333,7 +346,6 @@ __global__ void __launch_bounds__(Layout<BN, PAIR>::kThreads, 1)
     // ---- the MMAs: the warp keeps step, so that what an MMA takes is the same in all its
     // lanes, and one lane issues them ----
     if (even) {
-      constexpr uint32_t idesc = instr<T>(kRows * CTAS, BN);
       constexpr int PIECES = kSlice / 16;
       const bool one = elect_one();
       int stage = 0, xparity = 0, slot = 0, parity = 0, acc = 0, cparity = 1;
@@ -341,6 +353,7 @@ __global__ void __launch_bounds__(Layout<BN, PAIR>::kThreads, 1)
       while (ok && units.next(x)) {
         if (!(ok = wait_warp(accempty(acc), cparity))) break;
         tc_fence_after();
+        const uint32_t idesc = instr<T>(kRows * CTAS, x.width);
         const uint32_t d = tmem + acc * BN;
         for (int s = x.slice; s < x.end; ++s) {
           if (!(ok = wait_warp(xfull(stage), xparity))) break;
@@ -879,7 +892,8 @@ cudaError_t launch_w4_tiles_linear(int dtype, const W4LinearParams& l, void* scr
   p.m = (int)l.m;
   p.status = l.status;
   CUtensorMap map_w, map_x;
-  if (!maps(dtype, l.w, l.n, l.k, l.x, l.m, l.x_stride, bn, &map_w, &map_x))
+  // (a single row's stride may be anything)
+  if (!maps(dtype, l.w, l.n, l.k, l.x, l.m, l.m > 1 ? l.x_stride : l.k, bn, &map_w, &map_x))
     return cudaErrorInvalidValue;
   const int64_t cut = (int64_t)p.blocks * p.row_tiles - p.whole;
   cudaError_t e = launch<kLinear>(dtype, bn, map_w, map_x, p, p.whole + cut * p.parts, sm_count,

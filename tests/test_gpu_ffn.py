@@ -150,6 +150,34 @@ def test_linear_keeps_to_its_inputs():
         assert (~torch.isfinite(y[bad])).all() and torch.isfinite(y[~bad]).all()
 
 
+@pytest.mark.parametrize("k", [4096, 8192, 8320, 11008])
+def test_linear_one_token_of_any_stride(k):
+    """A single row's strides are not looked at, whichever kernel takes it."""
+    rng = np.random.default_rng(k)
+    x, w = rows(rng, 1, k, 0), U.Weights(rng, 203, k, 64)
+    y, again = (torch.empty((1, 203), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    L.lbgemm_w4_linear(0, 1, 203, k, 64, x, k, *w.tensors(), y, 203)
+    L.lbgemm_w4_linear(0, 1, 203, k, 64, x, 3, *w.tensors(), again, 1)
+    L.lbgemm_device_status()
+    want, size = x.double() @ w.dense().T, x.double().abs() @ w.dense().abs().T
+    assert ((y.double() - want).abs() <= U.ROUND[0] * want.abs() + SUM(k) * size).all()
+    assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("m", [7, 8, 9, 16, 31, 33, 64, 65, 95, 97, 128, 129, 161, 224, 255, 257, 290, 513])
+def test_linear_around_the_widths_of_tiles(m):
+    """Blocks of tokens that a kernel fills, and one more; every token on its own."""
+    rng = np.random.default_rng(m)
+    n, k, group = 270, 544, 32
+    x, w = rows(rng, m, k, 1), U.Weights(rng, n, k, group)
+    y, untouched = framed(m, n, n + 2, 1)
+    L.lbgemm_w4_linear(1, m, n, k, group, x, k, *w.tensors(), y, n + 2)
+    L.lbgemm_device_status()
+    want, size = x.double() @ w.dense().T, x.double().abs() @ w.dense().abs().T
+    assert ((y.double() - want).abs() <= U.ROUND[1] * want.abs() + SUM(k) * size + 2.0 ** -25).all()
+    assert untouched()
+
+
 # ---- the router ----------------------------------------------------------------------------
 
 
