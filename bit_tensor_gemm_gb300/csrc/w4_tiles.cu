@@ -26,9 +26,8 @@
 //
 // Measured: 4096 tokens x 11008 x 4096 in 217 us (1.70 PFLOP/s, what a plain product of
 // 16-bit numbers reaches being 1.90), 64 x 19456 x 8192 in 25 us (3.4 TB/s of weights), 12 x
-// 4096 x 11008 in 12.5; 4096 tokens, 6 of 64 experts of 2048 / 1024, in 367 us (0.83
-// PFLOP/s: 1.9 blocks of tokens an expert, three quarters full; 67 us of sorting, gathering
-// and joining).
+// 4096 x 11008 in 12.5; 4096 tokens, 6 of 64 experts of 2048 / 1024, in 348 us (0.87
+// PFLOP/s: blocks of tokens three quarters full; 67 us of sorting, gathering and joining).
 //
 // In a pair the full barriers and the accumulators' empty ones are the even CTA's and
 // count both; the commits of the MMAs go to both.  Every
@@ -972,16 +971,22 @@ cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, in
   e = launch<kUp>(dtype, bn, map_w, map_x, p, units, sm_count, true, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
+  // Tiles with few slices spend their time on the fp32 rows that they write: blocks of 128
+  // have a second accumulator for the next tile (64 experts of 2048 / 1024: 348 us, 366 with
+  // 256; 8 of 4096 / 2048: 348 and 361; of 2048 / 4096: 335 and 320).
+  const int down_bn = m.inter <= 2048 ? std::min(bn, 128) : bn;
+  const int down_slice = slice_for(down_bn);
   p.n = m.hidden;
   p.k = m.inter;
-  p.row_tiles = tiles_of(p.n, bn);
-  p.slices = (p.k + slice - 1) / slice;
+  p.row_tiles = tiles_of(p.n, down_bn);
+  p.slices = (p.k + down_slice - 1) / down_slice;
   p.scales = m.down.scales;
   p.row_scales = m.down.row_scales;
   p.out = at + z.out;
-  if (!maps(dtype, m.down, m.experts * p.n, p.k, at + z.h, picks, m.inter, bn, &map_w, &map_x))
+  if (!maps(dtype, m.down, m.experts * p.n, p.k, at + z.h, picks, m.inter, down_bn, &map_w,
+            &map_x))
     return cudaErrorInvalidValue;
-  e = launch<kDown>(dtype, bn, map_w, map_x, p, units, sm_count, true, s);
+  e = launch<kDown>(dtype, down_bn, map_w, map_x, p, units, sm_count, true, s);
   if (e != cudaSuccess) return e;
   *launches += 1;
   const float* out = reinterpret_cast<const float*>(at + z.out);
