@@ -165,6 +165,46 @@ def test_graphs_share_nothing(tokens):
     assert all(torch.equal(a, b) for a, b in zip(got, made[0][1]))
 
 
+def test_layers_cut_along_k_at_once():
+    """Layers of a few tiles, whose parts of k lie in scratch: on two streams at the same
+    time and from two graphs in turn, the bits of a call alone."""
+    made, want = [], []
+    for seed, tokens, k in ((1, 1, 11008), (2, 12, 8192), (3, 45, 4096), (4, 100, 6144)):
+        rng = np.random.default_rng(seed)
+        x, w = F.rows(rng, tokens, k, 0), U.Weights(rng, 300, k, 128).tensors()
+        y = torch.zeros((tokens, 304), dtype=torch.bfloat16, device="cuda")
+        made.append((lambda stream=None, a=(tokens, k, x, w, y): L.lbgemm_w4_linear(
+            0, a[0], 300, a[1], 128, a[2], a[1], *a[3], a[4], 304, stream), y))
+        made[-1][0]()
+        want.append(y.clone())
+
+    def check():
+        L.lbgemm_device_status()
+        for (_, y), z in zip(made, want):
+            assert torch.equal(y, z)
+            y.zero_()
+        torch.cuda.synchronize()
+
+    check()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for i, (run, _) in enumerate(made):
+            run(streams[i % 2].cuda_stream)
+    torch.cuda.synchronize()
+    check()
+    graphs = []
+    for half in (made[:2], made[2:]):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for run, _ in half:
+                run(torch.cuda.current_stream().cuda_stream)
+    for order in ((0, 1), (1, 0, 1)):
+        for i in order:
+            graphs[i].replay()
+        made[0][0]()
+        check()
+
+
 def test_streams_and_threads():
     """Calls of several sizes from two threads on two streams, sharing the scratch."""
     sizes = [3, 40, 330, 17]
