@@ -256,7 +256,7 @@ lbgemm_status lbgemm_moe_w4(int dtype, int64_t tokens, int64_t hidden, int64_t i
     if (experts < 1 || experts > 1024 || top_k < 1 || top_k > 32)
       return bad(LBGEMM_ERR_INVALID_ARG, "%lld choices among %lld experts (up to 32, up to 1024)",
                  (long long)top_k, (long long)experts);
-    if (tokens < 0 || tokens * top_k > (int64_t(1) << 24))
+    if (tokens < 0 || tokens > (int64_t(1) << 24) / top_k)
       return bad(LBGEMM_ERR_INVALID_ARG, "%lld tokens of %lld choices (up to 2^24 together)",
                  (long long)tokens, (long long)top_k);
     if (experts * std::max(2 * inter, hidden) > kMostRows)
