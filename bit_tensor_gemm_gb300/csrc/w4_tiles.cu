@@ -740,13 +740,16 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const MoeSort q) {
   }
 }
 
+// (In this kernel and combine_kernel only the call's own inputs are __restrict__ or read by
+// __ldg.  A dependent may be resident while the launch before it still writes, and what is
+// loaded as constant for a kernel's whole life could be loaded before its wait.)
+
 // ---- the picks' tokens in expert order -------------------------------------------------
 // (tile::gather4 reads them where they are, but took 80 cycles for four pieces of 128
 // bytes: 895 us for 24576 picks of 2048 elements against 64 experts)
 __global__ void __launch_bounds__(256)
-    gather_kernel(const uint16_t* __restrict__ x, int64_t x_stride, const int* __restrict__ offsets,
-                  int experts, const int* __restrict__ token_of, int width,
-                  uint16_t* __restrict__ to) {
+    gather_kernel(const uint16_t* __restrict__ x, int64_t x_stride, const int* offsets,
+                  int experts, const int* token_of, int width, uint16_t* to) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int octets = width / 8, picks = offsets[experts];
@@ -763,9 +766,8 @@ __global__ void __launch_bounds__(256)
 // ---- a token's picks added up -------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(256)
-    combine_kernel(const float* __restrict__ out, const int* __restrict__ pos_of,
-                   const float* __restrict__ weights, int64_t tokens, int hidden, int top_k, T* y,
-                   int64_t y_stride) {
+    combine_kernel(const float* out, const int* pos_of, const float* __restrict__ weights,
+                   int64_t tokens, int hidden, int top_k, T* y, int64_t y_stride) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int octets = hidden / 8;
   const int64_t total = tokens * octets;
@@ -775,7 +777,7 @@ __global__ void __launch_bounds__(256)
     const int c = (int)(i - t * octets) * 8;
     float v[8] = {};
     for (int j = 0; j < top_k; ++j) {
-      const int pos = __ldg(pos_of + t * top_k + j);
+      const int pos = pos_of[t * top_k + j];
       if (pos < 0) continue;
       const float w = __ldg(weights + t * top_k + j);
       float f[8];

@@ -1,8 +1,12 @@
 """Feed-forward operators at the limits of their arguments, on the host.  No GPU needed."""
+import os
+import re
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
+from bit_tensor_gemm_gb300 import build as bld  # noqa: E402
 from bit_tensor_gemm_gb300 import lbgemm as L  # noqa: E402
 from test_ffn_host import BAD, _lib, moe, refused  # noqa: E402,F401
 
@@ -23,3 +27,35 @@ def test_moe_takes_the_most_picks():
         with pytest.raises(L.LbgemmError) as e:
             moe(tokens=tokens, top=top, experts=64)
         assert e.value.status != BAD
+
+
+# ---- what a dependent launch may take for constant ---------------------------------------
+
+
+def kernels(name):
+    """(name, parameters, body) of a source file's kernels."""
+    with open(os.path.join(bld.CSRC, name)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    for m in re.finditer(r"__global__ void (?:__launch_bounds__\([^{;]*?\)\s*)?(\w+)\(([^{;]*)\)\s*\{", text):
+        end = text.find("\n}", m.end())
+        yield m.group(1), m.group(2), text[m.end():end]
+
+
+# What is older than the whole chain of launches of a call: its own inputs.
+INPUTS = {"x", "weights", "scales", "row_scales", "scale_ptr"}
+
+
+@pytest.mark.parametrize("name", ["w4_tiles.cu", "w4_rows.cu"])
+def test_dependents_take_inputs_only_for_constant(name):
+    """A kernel that waits for the launch before it may stand on the GPU while that launch
+    writes: only inputs of the call are __restrict__ or loaded by __ldg in it."""
+    waiting = 0
+    for kernel, parameters, body in kernels(name):
+        if "griddepcontrol.wait" not in body:
+            continue
+        waiting += 1
+        for p in re.findall(r"__restrict__\s+(\w+)", parameters):
+            assert p in INPUTS, f"{kernel}: {p}"
+        for p in re.findall(r"__ldg\(\s*([\w.]+)", body):
+            assert p.split(".")[-1] in INPUTS, f"{kernel}: {p}"
+    assert waiting == {"w4_tiles.cu": 5, "w4_rows.cu": 1}[name]
