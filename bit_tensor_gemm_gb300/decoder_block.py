@@ -28,6 +28,17 @@ from .attention_layer import PagedCache, random_layer
 _KINDS = {"torch.bfloat16": L.BF16, "torch.float16": L.F16, "torch.float32": L.F32}
 
 
+def _rows(name, x, width, kinds, device):
+    """The library's number for the type of x, rows of `width` elements side by side.
+    (It sees addresses and strides only, so what a tensor is gets checked here.)"""
+    kind = _KINDS.get(str(x.dtype))
+    if kind not in kinds or x.dim() != 2 or x.shape[1] != width or x.stride(1) != 1 or \
+            x.device != device:
+        raise ValueError(f"{name}: rows of {width} elements side by side are needed on {device}, not "
+                         f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
+    return kind
+
+
 class Weights4:
     """4-bit weights [rows, k] with a scale for every `group` elements and row."""
 
@@ -40,10 +51,11 @@ class Weights4:
 
     def store(self, w, first=0, step=1):
         """Quantises w [n, k] into the rows first, first + step, ..."""
+        kind = _rows("weights", w, self.k, (L.BF16, L.F16, L.F32), self.codes.device)
         n, k = w.shape
-        if k != self.k or first < 0 or step < 1 or (n and first + (n - 1) * step >= self.rows):
+        if first < 0 or step < 1 or (n and first + (n - 1) * step >= self.rows):
             raise ValueError("these rows are not among the weights")
-        L.lbgemm_w4_quantize(_KINDS[str(w.dtype)], n, k, self.group, w, w.stride(0),
+        L.lbgemm_w4_quantize(kind, n, k, self.group, w, w.stride(0),
                              self.codes[first:], step * k // 2, self.scales[first:],
                              step * (k // self.group), self.row_scales[first:], step)
         return self
@@ -58,6 +70,9 @@ class Experts:
 
     def __init__(self, router, gate, up, down, top_k, group=64):
         experts, inter, hidden = gate.shape
+        if up.shape != gate.shape or down.shape != (experts, hidden, inter) or \
+                router.shape != (experts, hidden):
+            raise ValueError("router, gate, up and down are not of the same experts")
         self.experts, self.inter, self.hidden, self.top_k, self.group = experts, inter, hidden, top_k, group
         self.router = Weights4(experts, hidden, group, gate.device).store(router)
         self.up = Weights4(experts * 2 * inter, hidden, group, gate.device)
@@ -68,8 +83,8 @@ class Experts:
     def step(self, x):
         """x: bf16 or fp16 [tokens, hidden]; on torch's current stream."""
         import torch  # noqa: PLC0415
+        kind = _rows("x", x, self.hidden, (L.BF16, L.F16), self.up.codes.device)
         tokens, hidden = x.shape
-        kind = _KINDS[str(x.dtype)]
         logits = torch.empty((tokens, self.experts), dtype=x.dtype, device=x.device)
         L.lbgemm_w4_linear(kind, tokens, self.experts, hidden, self.group, x, x.stride(0),
                            *self.router.tensors(), logits, self.experts)
@@ -89,6 +104,11 @@ class DecoderBlock:
     experts and after them (the second and last may be None)."""
 
     def __init__(self, attention, experts, norms, residual_scale=1.0, block_scale=1.0, eps=1e-6):
+        if len(norms) != 4 or norms[0] is None or norms[2] is None:
+            raise ValueError("norms: four, the first and third of them not None")
+        for w in norms:
+            if w is not None:
+                _rows("norm weights", w[None], experts.hidden, (L.BF16,), norms[0].device)
         self.attention, self.experts, self.norms = attention, experts, norms
         self.residual_scale, self.block_scale, self.eps = residual_scale, block_scale, eps
 
@@ -96,15 +116,17 @@ class DecoderBlock:
         """x: bf16 [tokens, model]; new: what cache.extend() gave for them; on torch's
         current stream.  Returns the residual stream after the block."""
         import torch  # noqa: PLC0415
+        _rows("x", x, self.experts.hidden, (L.BF16,), self.norms[0].device)
         tokens, model = x.shape
-        n, x1, n1, x2 = (torch.empty_like(x) for _ in range(4))
+        n, x1, n1, x2 = (torch.empty((tokens, model), dtype=x.dtype, device=x.device)
+                         for _ in range(4))
         before, after, before_experts, after_experts = self.norms
         a, b, eps = self.residual_scale, self.block_scale, self.eps
-        L.lbgemm_residual_norm(L.BF16, tokens, model, x, model, None, 0, None, None, 0, 1.0, 1.0,
-                               before, eps, None, 0, n, model)
+        L.lbgemm_residual_norm(L.BF16, tokens, model, x, x.stride(0), None, 0, None, None, 0,
+                               1.0, 1.0, before, eps, None, 0, n, model)
         y = self.attention.step(n, cache, new)
-        L.lbgemm_residual_norm(L.BF16, tokens, model, x, model, y, model, after, None, 0, a, b,
-                               before_experts, eps, x1, model, n1, model)
+        L.lbgemm_residual_norm(L.BF16, tokens, model, x, x.stride(0), y, model, after, None, 0,
+                               a, b, before_experts, eps, x1, model, n1, model)
         y = self.experts.step(n1)
         L.lbgemm_residual_norm(L.BF16, tokens, model, x1, model, y, model, after_experts, None, 0, a,
                                b, None, eps, x2, model, None, 0)
