@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
           v *= scale0;
           u *= scale1;
           static_cast<T*>(p.y)[pick * p.y_stride + (row + r) / 2] =
-              from_f32<T>(v / (1.0f + expf(-v)) * u);
+              from_f32<T>(silu_times(v, u));
         } else if (MODE == kDown) {
           values[(row - run.first_row + r) * p.picks + pick] = v * scale0;
         } else {

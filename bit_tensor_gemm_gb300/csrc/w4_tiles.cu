@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(Layout<BN, PAIR>::kThreads, 1)
               const float b = __uint_as_float(v[2 * j + 1]) * scale;
               const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
               const float gate = lane & 1 ? other : a, up = lane & 1 ? b : other;
-              h[j] = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+              h[j] = silu_times(gate, up);
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j)

@@ -1,0 +1,49 @@
+"""GPU tests of the feed-forward operators at the limits of their ranges and rules."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import ffn_util as U  # noqa: E402
+from bit_tensor_gemm_gb300 import build as bld  # noqa: E402
+from bit_tensor_gemm_gb300 import lbgemm as L  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    bld.build()
+    L.load()
+
+
+# ---- silu(gate) * up over the range of its factors -------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("tokens", [1, 40, 300])
+def test_moe_gates_of_every_size(dtype, tokens):
+    """Gates far below 0 with an up that makes an ordinary number of it, one channel each:
+    gate, up and the second product are exact, so what is left is silu's own error (an
+    exponential of |gate| / 2, squared: up to 2^-16 at the far end) and the rounding."""
+    gate = np.array([-170, -130, -104, -103, -100, -95, -92, -90, -89.5, -89, -88.75, -88.5, -88.25, -88, -87.75,
+                     -87.5, -87.25, -87, -80, -40, -17, -5, -1, -0.125, 0, 0.25, 1, 9, 30, 88, 89, 1000], np.float32)
+    silu = gate.astype(np.float64) / (1 + np.exp(-gate.astype(np.float64)))
+    up = np.minimum(1.375 / np.maximum(np.abs(silu), 1e-60), 3e38).astype(np.float32)
+    size, eye = 32, np.eye(32, dtype=np.int64)
+    ups, down = (U.Weights(np.random.default_rng(1), n, size, 32) for n in (2 * size, size))
+    ups.codes[:], ups.scales[:], down.codes[:], down.scales[:], down.row[:] = 0, 0x38, eye, 0x38, 1
+    ups.codes[:, 0] = 1
+    ups.row[::2], ups.row[1::2] = gate, up
+    x = torch.zeros((tokens, size), dtype=U.DTYPES[dtype], device="cuda")
+    x[:, 0] = 1
+    ids = torch.zeros((tokens, 1), dtype=torch.int32, device="cuda")
+    y = torch.empty_like(x)
+    L.lbgemm_moe_w4(dtype, tokens, size, size, 1, 1, 32, x, size, ids, torch.ones((tokens, 1), device="cuda"),
+                    *ups.tensors(), *down.tensors(), y, size)
+    L.lbgemm_device_status()
+    want = silu * up.astype(np.float64)
+    tol = (U.ROUND[dtype] + 2.0 ** -16) * np.abs(want) + (2.0 ** -25 if dtype else 0)
+    off = np.abs(y.double().cpu().numpy() - want)
+    assert (off <= tol).all(), [(g, u) for g, u, bad in zip(gate, up, (off > tol).any(0)) if bad]
