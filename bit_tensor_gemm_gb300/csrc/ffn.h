@@ -65,10 +65,10 @@ struct MoeParams {
 };
 
 // How a call runs on this device, and the scratch that it needs.
-size_t w4_linear_scratch(W4LinearParams* p, int sm_count);
+size_t w4_linear_scratch(const W4LinearParams& p, int sm_count);
 cudaError_t launch_w4_linear(int dtype, const W4LinearParams& p, void* scratch, int sm_count,
                              int* launches, cudaStream_t s);
-size_t moe_w4_scratch(MoeParams* p, int sm_count);
+size_t moe_w4_scratch(const MoeParams& p, int sm_count);
 cudaError_t launch_moe_w4(int dtype, const MoeParams& p, void* scratch, int sm_count,
                           int* launches, cudaStream_t s);
 

@@ -192,7 +192,7 @@ lbgemm_status lbgemm_w4_linear(int dtype, int64_t M, int64_t N, int64_t K, int64
     p.y_stride = y_stride;
     p.status = dev.status;
     cudaStream_t s = as_stream(stream);
-    return with_scratch(dev, w4_linear_scratch(&p, dev.sm_count), s, "4-bit linear layer launch",
+    return with_scratch(dev, w4_linear_scratch(p, dev.sm_count), s, "4-bit linear layer launch",
                         [&](void* scratch, int* launches) {
                           return launch_w4_linear(dtype, p, scratch, dev.sm_count, launches, s);
                         });
@@ -293,7 +293,7 @@ lbgemm_status lbgemm_moe_w4(int dtype, int64_t tokens, int64_t hidden, int64_t i
     p.y_stride = y_stride;
     p.status = dev.status;
     cudaStream_t s = as_stream(stream);
-    return with_scratch(dev, moe_w4_scratch(&p, dev.sm_count), s, "experts launch",
+    return with_scratch(dev, moe_w4_scratch(p, dev.sm_count), s, "experts launch",
                         [&](void* scratch, int* launches) {
                           return launch_moe_w4(dtype, p, scratch, dev.sm_count, launches, s);
                         });

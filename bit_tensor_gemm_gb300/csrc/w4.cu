@@ -7,8 +7,8 @@
 
 namespace lbg {
 
-size_t w4_linear_scratch(W4LinearParams* p, int sm_count) {
-  return w4_rows_take_linear(*p, sm_count) ? 0 : w4_tiles_linear_scratch(*p, sm_count);
+size_t w4_linear_scratch(const W4LinearParams& p, int sm_count) {
+  return w4_rows_take_linear(p, sm_count) ? 0 : w4_tiles_linear_scratch(p, sm_count);
 }
 
 cudaError_t launch_w4_linear(int dtype, const W4LinearParams& p, void* scratch, int sm_count,
@@ -18,9 +18,9 @@ cudaError_t launch_w4_linear(int dtype, const W4LinearParams& p, void* scratch, 
              : launch_w4_tiles_linear(dtype, p, scratch, sm_count, launches, s);
 }
 
-size_t moe_w4_scratch(MoeParams* p, int sm_count) {
-  return w4_rows_take_moe(*p, sm_count) ? (size_t)p->tokens * p->top_k * p->inter * 2
-                                        : w4_tiles_moe_scratch(*p);
+size_t moe_w4_scratch(const MoeParams& p, int sm_count) {
+  return w4_rows_take_moe(p, sm_count) ? (size_t)p.tokens * p.top_k * p.inter * 2
+                                       : w4_tiles_moe_scratch(p);
 }
 
 cudaError_t launch_moe_w4(int dtype, const MoeParams& p, void* scratch, int sm_count,

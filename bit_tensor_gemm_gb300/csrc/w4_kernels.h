@@ -49,7 +49,7 @@ struct W4TilesParams {
   bool vector = false;  // (linear) Y's rows are 16-byte aligned
   int m = 0;  // tokens (linear) or picks
   int experts = 1;
-  const int *offsets = nullptr, *token_of = nullptr;  // [experts + 1]; [picks]
+  const int* offsets = nullptr;  // [experts + 1]
   // The cut: blocks of tokens (linear), tiles of rows, slices of k; tiles that are not cut
   // along k, parts of the others and a part's slices, and where their shares go.
   int blocks = 0, row_tiles = 0, slices = 0, whole = 0, parts = 1, part_slices = 0;

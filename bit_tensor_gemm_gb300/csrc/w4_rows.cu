@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
   constexpr int COLS = 8, SHARE = 16 * COLS;  // columns; numbers of a tile
   extern __shared__ __align__(128) uint8_t smem[];
   float* shares = reinterpret_cast<float*>(smem + p.at_shares);  // [batch + kWarps][SHARE]
-  // down: the picks' outputs [rows][picks]; linear: sums between pieces of k [rows][COLS]
+  // down: the picks' outputs [rows][picks]
   float* values = reinterpret_cast<float*>(smem + p.at_values);
   uint8_t* staged = smem + p.at_tokens;
   // (the linear layer's only segment is all rows and the tokens in their order)

@@ -948,7 +948,6 @@ cudaError_t launch_w4_tiles_moe(int dtype, const MoeParams& m, void* scratch, in
   W4TilesParams p;
   p.experts = m.experts;
   p.offsets = q.offsets;
-  p.token_of = q.token_of;
   p.group = m.group;
   p.m = (int)picks;
   p.status = m.status;
