@@ -669,14 +669,23 @@ cudaError_t launch_any(int dtype, const W4RowsParams& p, int warps, bool staged,
 
 }  // namespace
 
-// Up to 8 tokens, where they fit shared memory beside the ring, and rows of up to 8192
-// (a launch has some 4 us before and after its stream here, tiles 6; but tiles cut k for
-// themselves and stream as fast).  Measured, rows against tiles: 1, 4 and 8 tokens x 11008 x
-// 4096: 10.9, 11.2, 12.1 and 12.6 us; x 4096 x 11008: 13.3, 13.7, 15.0 and 11.9; 1 x 128000
-// x 4096: 66 and 94; 8 x 19456 x 8192 (k in parts): 28 and 24; 1 x 1024 x 1024: 4.5 and 6.3.
-// Two blocks of 8 columns a pass: 12 x 4096 x 11008 16.5 us, tiles 12.2.
+// Up to 8 tokens, where they fit shared memory beside the ring.  Rows of more than 8192 go to
+// tiles where those cut k for themselves (with row tiles for at most half of the SMs: up to
+// 9728 rows).  Measured, rows against tiles, in graphs over weights beyond L2:
+//   tokens x rows x k       rows   tiles, us
+//   1 x 4096 x 11008        13.8   13.1   (from L2 1, 4, 8 tokens: 13.3, 13.7, 15.0 and 11.9)
+//   1, 4 x 4096 x 14336     16.2, 15.9   14.6
+//   1 x 8192 x 28672        46.9   38.2
+//   1, 4 x 9728 x 12288     21.9, 22.0   20.6, 20.4
+//   1, 4 x 11008 x 12288    25.5, 25.0   30.2, 29.9
+//   1 x 16384 x 16384       42.7   59.2
+//   1 x 19456 x 28672       75.7   71.1
+//   1, 4 x 32768 x 8320     40.5, 40.3   51.1, 46.6
+// and from L2, shorter rows: 1, 4 and 8 x 11008 x 4096 10.9, 11.2, 12.1 and 12.6; 1 x 128000 x
+// 4096 66 and 94; 1 x 1024 x 1024 4.5 and 6.3.  Two blocks of 8 columns a pass: 12 x 4096 x
+// 11008 16.5 us, tiles 12.2.
 static bool linear_params(const W4LinearParams& l, int sm_count, W4RowsParams* p) {
-  if (l.m > 8 || l.k > 8192) return false;
+  if (l.m > 8 || (l.k > 8192 && 2 * ((l.n + 127) / 128) <= sm_count)) return false;
   p->n = l.n;
   p->k = (int)l.k;
   p->group = l.group;

@@ -6,6 +6,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import ffn_util as U  # noqa: E402
+import test_gpu_ffn_exact as X  # noqa: E402
 from bit_tensor_gemm_gb300 import build as bld  # noqa: E402
 from bit_tensor_gemm_gb300 import lbgemm as L  # noqa: E402
 
@@ -47,3 +48,17 @@ def test_moe_gates_of_every_size(dtype, tokens):
     tol = (U.ROUND[dtype] + 2.0 ** -16) * np.abs(want) + (2.0 ** -25 if dtype else 0)
     off = np.abs(y.double().cpu().numpy() - want)
     assert (off <= tol).all(), [(g, u) for g, u, bad in zip(gate, up, (off > tol).any(0)) if bad]
+
+
+# ---- few tokens on long rows ------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("case", [
+    # up to 9728 rows of more than 8192 elements go to tiles, more of them stream by rows while the
+    # tokens fit shared memory: both sides of each edge
+    (1, 9728, 8224, 32), (1, 9729, 8224, 32), (4, 9729, 8192, 64), (4, 9800, 12320, 32), (8, 9800, 8320, 128),
+    (1, 11008, 28672, 128), (1, 10001, 49152, 128), (1, 10001, 65536, 64), (2, 20011, 16384, 32),
+])
+def test_linear_long_rows(case, dtype):
+    X.test_linear(case, dtype)
