@@ -105,8 +105,8 @@ __host__ __device__ constexpr int hm_xstride(int K) { return (K + 127) / 128 * 1
 // Output element (x, w) goes to out[x * NW + w], or out[w * MX + x] when TRANS.
 template <int MT, bool TRANS, bool LINEAR>
 __global__ void __launch_bounds__(kHmWarps * 32)
-    hmma_skinny_kernel(const int8_t* __restrict__ X, const int8_t* __restrict__ W, int MX, int NW,
-                       int K, int32_t* __restrict__ C, const float* __restrict__ sx,
+    hmma_skinny_kernel(const int8_t* X, const int8_t* __restrict__ W, int MX, int NW,
+                       int K, int32_t* __restrict__ C, const float* sx,
                        const float* __restrict__ sw, __nv_bfloat16* __restrict__ Y,
                        int chunk_steps, int U, int KP) {
   constexpr int NACC = 4 / MT;  // independent accumulators per (m tile, n8 tile)

@@ -106,7 +106,7 @@ __global__ void cvt_s8_f16_kernel(CvtJob ja, CvtJob jb, int64_t K, int64_t Kp, Z
     const int8_t* src = static_cast<const int8_t*>(j.src) + r * K + c;
     __align__(16) __half h[8];
     if (j.fast && c + 8 <= K) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+      const uint2 w = *reinterpret_cast<const uint2*>(src);
       const uint32_t lo = w.x, hi = w.y;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -147,9 +147,9 @@ __device__ __forceinline__ uint4 s8x8_f16x8(int2 v) {
 }
 
 // units: 8-byte groups; na of operand a, then nb of operand b
-__global__ void cvt_s8_f16_flat_kernel(const int2* __restrict__ a, int64_t na, uint4* ea,
-                                       const int2* __restrict__ b, int64_t nb, uint4* eb,
-                                       ZeroRect z) {
+// (a or b may come from the grid before: neither is loaded as constant)
+__global__ void cvt_s8_f16_flat_kernel(const int2* a, int64_t na, uint4* ea, const int2* b,
+                                       int64_t nb, uint4* eb, ZeroRect z) {
   allow_dependent_launch();
   wait_prior_grid();
   zero_rect(z);
@@ -161,7 +161,7 @@ __global__ void cvt_s8_f16_flat_kernel(const int2* __restrict__ a, int64_t na, u
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int64_t u = i + q * nt;
-      v[q] = u < na ? __ldg(a + u) : __ldg(b + (u - na));
+      v[q] = u < na ? a[u] : b[u - na];
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -175,9 +175,9 @@ __global__ void cvt_s8_f16_flat_kernel(const int2* __restrict__ a, int64_t na, u
   }
   for (; i < total; i += nt) {
     if (i < na)
-      ea[i] = s8x8_f16x8(__ldg(a + i));
+      ea[i] = s8x8_f16x8(a[i]);
     else
-      eb[i - na] = s8x8_f16x8(__ldg(b + (i - na)));
+      eb[i - na] = s8x8_f16x8(b[i - na]);
   }
 }
 
@@ -352,8 +352,7 @@ __device__ __forceinline__ void skinny_load_step(int4 (&dst)[NR], const int8_t* 
 template <int MT, int NR, bool LINEAR>
 __device__ __forceinline__ void skinny_finish(int (&acc)[MT * NR], int lane, int M, int N, int n0,
                                               int32_t* __restrict__ C,
-                                              const float* __restrict__ sx,
-                                              const float* __restrict__ sw,
+                                              const float* sx, const float* __restrict__ sw,
                                               __nv_bfloat16* __restrict__ Y) {
   constexpr int NV = MT * NR;
   int n = NV;
@@ -398,13 +397,13 @@ __device__ __forceinline__ void skinny_finish(int (&acc)[MT * NR], int lane, int
 
 template <int MT, int NR, int PF, int MINB, bool LINEAR>
 __global__ void __launch_bounds__(kSkWarps * 32, MINB)
-    skinny_s8_kernel(const int8_t* __restrict__ A, const int8_t* __restrict__ B, int M, int N,
-                     int K, int32_t* __restrict__ C, const float* __restrict__ sx,
+    skinny_s8_kernel(const int8_t* A, const int8_t* __restrict__ B, int M, int N,
+                     int K, int32_t* __restrict__ C, const float* sx,
                      const float* __restrict__ sw, __nv_bfloat16* __restrict__ Y) {
   constexpr int NV = MT * NR;
   // launched as a programmatic dependent: A (and its scales) may come from
   // the grid before this one (the activation quantiser), which may still be
-  // running; wait for it before the first read
+  // running; wait for it before the first read (and load neither as constant)
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
   const int nwarps = gridDim.x * kSkWarps;
@@ -427,7 +426,7 @@ __global__ void __launch_bounds__(kSkWarps * 32, MINB)
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const int4 a = (m < M && k < K)
-                             ? __ldg(reinterpret_cast<const int4*>(A + (int64_t)m * K + k))
+                             ? *reinterpret_cast<const int4*>(A + (int64_t)m * K + k)
                              : make_int4(0, 0, 0, 0);
 #pragma unroll
           for (int r = 0; r < NR; ++r) {

@@ -119,8 +119,8 @@ __device__ __forceinline__ int4 lds16(uint32_t addr) {
 // first stages are requested before waiting on that grid.
 template <bool TRANS, bool LINEAR, bool EARLY_W>
 __global__ void __launch_bounds__(kStThreads, 1)
-    stream_mma_kernel(const int8_t* __restrict__ X, const int8_t* __restrict__ W, int MX, int NW,
-                      int K, int S, int32_t* __restrict__ C, const float* __restrict__ sx,
+    stream_mma_kernel(const int8_t* X, const int8_t* __restrict__ W, int MX, int NW,
+                      int K, int S, int32_t* __restrict__ C, const float* sx,
                       const float* __restrict__ sw, __nv_bfloat16* __restrict__ Y, int* status) {
   extern __shared__ __align__(128) uint8_t st_smem_buf[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
     __syncwarp();
   } else {
     // ---- consumers: warp `warp` owns K slice [warp KS, warp KS + KS) ---------------------
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // X may come from the grid before
+    // X may come from the grid before (so it is not loaded as constant, nor is sx)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int kb = warp * KS;
     const int blocks = KS / 64;  // 1..4
     uint32_t xa[4][2][8];        // [block j][row g / g + 8][fp16 pairs]
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
         const int x = g + 8 * r, k = kb + 64 * j + 16 * t;
         int4 v = make_int4(0, 0, 0, 0);
         if (j < blocks && x < MX && k < K)
-          v = __ldg(reinterpret_cast<const int4*>(X + (int64_t)x * K + k));
+          v = *reinterpret_cast<const int4*>(X + (int64_t)x * K + k);
         cvt16(v, xa[j][r]);
       }
     }

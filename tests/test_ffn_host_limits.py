@@ -59,3 +59,18 @@ def test_dependents_take_inputs_only_for_constant(name):
         for p in re.findall(r"__ldg\(\s*([\w.]+)", body):
             assert p.split(".")[-1] in INPUTS, f"{kernel}: {p}"
     assert waiting == {"w4_tiles.cu": 5, "w4_rows.cu": 1}[name]
+
+
+@pytest.mark.parametrize("name,kernel,written", [
+    ("simt.cu", "skinny_s8_kernel", {"A", "sx"}), ("stream_mma.cu", "stream_mma_kernel", {"X", "sx"}),
+    ("hmma_skinny.cu", "hmma_skinny_kernel", {"X", "sx"}),
+    ("simt.cu", "cvt_s8_f16_flat_kernel", {"a", "b"}), ("simt.cu", "cvt_s8_f16_kernel", {"src"})])
+def test_quantised_activations_are_not_constant(name, kernel, written):
+    """What the activations' quantiser may still be writing when the 8-bit kernel behind it
+    starts: neither __restrict__ nor loaded by __ldg there."""
+    found = [(p, body) for k, p, body in kernels(name) if k == kernel]
+    assert len(found) == 1
+    parameters, body = found[0]
+    assert not written & set(re.findall(r"__restrict__\s+(\w+)", parameters))
+    loads = re.findall(r"__ldg\((?:reinterpret_cast<[^>]*>\()?\s*(\w+)", body)
+    assert not written & set(loads)
