@@ -90,7 +90,7 @@ lbgemm_status check_norm(int dtype, int64_t tokens, int64_t width, const void* X
   if (!(eps >= 0.0f) || std::isinf(eps)) return bad(LBGEMM_ERR_INVALID_ARG, "eps must be >= 0");
   if (!std::isfinite(a) || !std::isfinite(b))
     return bad(LBGEMM_ERR_INVALID_ARG, "the residual's and the block's scale must be finite");
-  if (!Y && (w_post || gate))
+  if (!Y && (w_post || gate) && tokens > 0)  // (an empty tensor has no address)
     return bad(LBGEMM_ERR_INVALID_ARG, "a norm or gate of a block needs its output Y");
   if (!aligned(w_post, 16) || !aligned(w_next, 16))
     return bad(LBGEMM_ERR_ALIGNMENT, "norm weights must be 16-byte aligned");

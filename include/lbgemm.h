@@ -737,7 +737,8 @@ lbgemm_status lbgemm_moe_w4(int dtype, int64_t tokens, int64_t hidden, int64_t i
  * tokens (gate_stride 0), or a row for every token (gate_stride >= width).  Y
  * NULL: no block before (w_post and gate NULL); X_out may then be NULL too, for
  * the norm alone.  dtype: any; width: a multiple of 8 up to 16384 (8192 in fp32).
- * Each output may be one of the inputs, with the same stride. */
+ * With no tokens the pointers to rows may be NULL, whatever else is given.  Each
+ * output may be one of the inputs, with the same stride. */
 lbgemm_status lbgemm_residual_norm(int dtype, int64_t tokens, int64_t width, const void* X,
                                    int64_t x_stride, const void* Y, int64_t y_stride,
                                    const void* w_post, const void* gate, int64_t gate_stride,

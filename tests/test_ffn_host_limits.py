@@ -8,7 +8,7 @@ torch = pytest.importorskip("torch")
 
 from bit_tensor_gemm_gb300 import build as bld  # noqa: E402
 from bit_tensor_gemm_gb300 import lbgemm as L  # noqa: E402
-from test_ffn_host import BAD, _lib, moe, refused  # noqa: E402,F401
+from test_ffn_host import ALIGN, BAD, P, _lib, back, moe, norm, refused  # noqa: E402,F401
 
 
 @pytest.mark.parametrize("tokens,top", [
@@ -27,6 +27,28 @@ def test_moe_takes_the_most_picks():
         with pytest.raises(L.LbgemmError) as e:
             moe(tokens=tokens, top=top, experts=64)
         assert e.value.status != BAD
+
+
+# ---- no tokens ------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("gate", [P, None])
+@pytest.mark.parametrize("post", [P, None])
+def test_norm_of_no_tokens_takes_no_rows(post, gate):
+    """Tensors without elements have no address: weights may be given all the same."""
+    norm(tokens=0, X=None, Y=None, post=post, gate=gate, Xo=None, No=None)
+    rows = dict(dXo=None, dN=None, X=None, Y=None, dX=None, dY=None)
+    if post or gate or torch.cuda.is_available():
+        if torch.cuda.is_available():
+            pytest.skip("addresses that nothing may write")
+        with pytest.raises(L.LbgemmError) as e:  # (their gradients are zeros, which takes a device)
+            back(tokens=0, post=post, gate=gate, dpost=post, dgate=gate, **rows)
+        assert e.value.status not in (BAD, ALIGN)
+    else:
+        back(tokens=0, post=None, gate=None, nxt=None, dpost=None, dgate=None, dnext=None, **rows)
+    # a token needs its rows
+    refused(BAD, norm, Y=None, post=P, gate=None)
+    refused(BAD, back, Y=None, post=P, gate=None, dgate=None, dY=None)
 
 
 # ---- what a dependent launch may take for constant ---------------------------------------

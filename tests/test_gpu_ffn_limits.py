@@ -8,6 +8,7 @@ pytestmark = pytest.mark.gpu
 import ffn_util as U  # noqa: E402
 import test_gpu_ffn_exact as X  # noqa: E402
 from bit_tensor_gemm_gb300 import build as bld  # noqa: E402
+from bit_tensor_gemm_gb300 import decoder_block as blocks  # noqa: E402
 from bit_tensor_gemm_gb300 import lbgemm as L  # noqa: E402
 
 
@@ -62,3 +63,33 @@ def test_moe_gates_of_every_size(dtype, tokens):
 ])
 def test_linear_long_rows(case, dtype):
     X.test_linear(case, dtype)
+
+
+# ---- no tokens --------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+@pytest.mark.parametrize("gate", [None, "channel", "token"])
+def test_norm_of_no_tokens(dtype, gate):
+    """Tensors without elements, weights as ever: summed gradients are zeros."""
+    t = U.DTYPES[dtype]
+    none, w = torch.empty((0, 96), dtype=t, device="cuda"), torch.ones(96, dtype=t, device="cuda")
+    g, stride = {None: (None, 0), "channel": (w, 0), "token": (none, 96)}[gate]
+    args = (none, 96, none, 96, w, g, stride, 1.0, 0.5, w, 1e-6)
+    L.lbgemm_residual_norm(dtype, 0, 96, *args, none, 96, none, 96)
+    sums = [torch.full((96,), 7.0, device="cuda") for _ in range(3)]
+    dgate = {None: None, "channel": sums[2], "token": none}[gate]
+    L.lbgemm_residual_norm_backward(dtype, 0, 96, none, 96, none, 96, *args, none, 96, none, 96, dgate, stride,
+                                    sums[0], sums[1])
+    L.lbgemm_device_status()
+    assert (sums[0] == 0).all() and (sums[1] == 0).all()
+    assert (sums[2] == (0 if gate == "channel" else 7)).all()
+
+
+def test_block_of_no_tokens():
+    block = blocks.random_block(4, 2, 64, 256, 64, 8, 64, 2, 32)
+    cache = blocks.PagedCache(2, 64, 2, 64, 16)
+    x = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
+    assert block.step(x, cache, cache.extend([0, 0])).shape == (0, 256)
+    assert block.experts.step(x).shape == (0, 256)
+    L.lbgemm_device_status()
