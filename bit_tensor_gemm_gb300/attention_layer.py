@@ -79,6 +79,9 @@ class AttentionLayer:
 
     def __init__(self, heads_q, heads_kv, dim, qkv, qkv_scale, out, out_scale, q_norm, k_norm,
                  cosines, sines, eps=1e-6, interleaved=False, window=0):
+        if qkv.shape[0] != (heads_q + 2 * heads_kv) * dim or \
+                tuple(out.shape) != (qkv.shape[1], heads_q * dim):
+            raise ValueError("qkv and out are not those of this many heads")
         self.heads_q, self.heads_kv, self.dim = heads_q, heads_kv, dim
         self.qkv, self.qkv_scale, self.out, self.out_scale = qkv, qkv_scale, out, out_scale
         self.q_norm, self.k_norm, self.cosines, self.sines = q_norm, k_norm, cosines, sines
@@ -91,6 +94,12 @@ class AttentionLayer:
         belongs to that stream (torch hands memory out again in the order of the
         stream that it belongs to)."""
         import torch  # noqa: PLC0415
+        # (the library sees addresses only; the projections read rows without gaps)
+        if x.dim() != 2 or x.shape[1] != self.qkv.shape[1] or x.dtype != torch.bfloat16 or \
+                not x.is_contiguous() or x.device != self.qkv.device:
+            raise ValueError(f"x: contiguous bf16 rows of {self.qkv.shape[1]} are needed on "
+                             f"{self.qkv.device}, not {x.dtype} {tuple(x.shape)} with strides "
+                             f"{x.stride()} on {x.device}")
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), x.device)
