@@ -2119,7 +2119,7 @@ lbgemm_status lbgemm_device_status(void* stream) {
     cudaMemcpy(d->status, &zero, sizeof zero, cudaMemcpyHostToDevice);
     if (word == lbg::kStatusBadIndex)  // no time-out bit beside it
       return fail(LBGEMM_ERR_INVALID_ARG,
-                  "a kernel met a position, slot, page or length out of range");
+                  "a kernel met a position, slot, page, length or expert out of range");
     return fail(LBGEMM_ERR_TIMEOUT, "a device-side wait ran out of time (status %d)", word);
   }
   return LBGEMM_OK;

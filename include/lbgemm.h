@@ -683,10 +683,11 @@ lbgemm_status lbgemm_w4_quantize(int dtype, int64_t N, int64_t K, int64_t group,
 
 /* Y[m][n] = sum_k X[m][k] W[n][k], X [M, K], Y [M, N], W in 4 bits as above.
  * dtype: LBGEMM_BF16 or LBGEMM_F16.  M, N up to 2^30; Y's stride is any from N
- * on (rows need not be aligned).  Sums are fp32, and the row scale multiplies
- * them before the one rounding.  A token's result does not depend on the other
- * tokens of the call, but for the order of its sum, which goes by M.  Scratch for
- * partial sums is taken as in lbgemm_run. */
+ * on (rows need not be aligned).  Sums of X * code * scale are fp32 (and have to
+ * stay within its range), and the row scale multiplies them before the one
+ * rounding.  A token's result does not depend on the other tokens of the call, but
+ * for the order of its sum, which goes by M.  Scratch for partial sums is taken as
+ * in lbgemm_run. */
 lbgemm_status lbgemm_w4_linear(int dtype, int64_t M, int64_t N, int64_t K, int64_t group,
                                const void* X, int64_t x_stride, const void* codes,
                                const void* scales, const float* row_scales, void* Y,
@@ -715,10 +716,14 @@ lbgemm_status lbgemm_moe_route(int dtype, int64_t tokens, int64_t experts, int64
  *       expert is row i of its Gate, row 2i + 1 row i of its Up;
  *   down: [experts][hidden], K = inter.
  * hidden and inter: multiples of `group`.  dtype: LBGEMM_BF16 or LBGEMM_F16; the
- * inner vector silu(..) * (..) is rounded to dtype (in fp16 it must stay below
- * 65520), everything else is summed in fp32 and rounded once.  experts up to
- * 1024, top_k up to 32, tokens * top_k up to 2^24.  The sum over j runs in the
- * order of j.  Scratch for the inner vectors is taken as in lbgemm_run. */
+ * inner vector silu(..) * (..) is rounded to dtype, as the second product's operand
+ * (in fp16 it must stay below 65520), which makes the result's error some 1.4 times
+ * what its own rounding leaves.  Everything else is summed in fp32 and rounded once.  experts up to 1024, top_k up
+ * to 32, tokens * top_k up to 2^24.  The sum over j runs in the order of j.
+ * Scratch is taken as in lbgemm_run: 2 inter bytes a pick (token and choice), and
+ * with more than a few picks an expert 4 hidden + 8 beside them (32768 tokens of 8
+ * choices, hidden 7168, inter 2048: 8.6 GB).  A caller that has not got them gives
+ * the tokens in pieces. */
 lbgemm_status lbgemm_moe_w4(int dtype, int64_t tokens, int64_t hidden, int64_t inter,
                             int64_t experts, int64_t top_k, int64_t group, const void* X,
                             int64_t x_stride, const int32_t* ids, const float* weights,
@@ -732,13 +737,15 @@ lbgemm_status lbgemm_moe_w4(int dtype, int64_t tokens, int64_t hidden, int64_t i
  *   z  = Y * rstd(Y) * w_post       (z = Y where w_post is NULL)
  *   X_out = residual_scale * X + block_scale * gate * z
  *   N_out = x' * rstd(x') * w_next  with x' = X_out before its rounding
- * and rstd(v) = 1 / sqrt(mean(v^2) + eps).  w_post, w_next: [width] of dtype;
- * w_next and N_out may both be NULL.  gate: NULL (1), one row of dtype for all
- * tokens (gate_stride 0), or a row for every token (gate_stride >= width).  Y
- * NULL: no block before (w_post and gate NULL); X_out may then be NULL too, for
- * the norm alone.  dtype: any; width: a multiple of 8 up to 16384 (8192 in fp32).
- * With no tokens the pointers to rows may be NULL, whatever else is given.  Each
- * output may be one of the inputs, with the same stride. */
+ * and rstd(v) = 1 / sqrt(mean(v^2) + eps), squares being summed in fp32 (a row whose
+ * sum passes its range, with elements of some 2^64 / sqrt(width), has rstd 0).
+ * w_post, w_next: [width] of dtype; w_next and N_out may both be NULL.  gate: NULL
+ * (1), one row of dtype for all tokens (gate_stride 0), or a row for every token
+ * (gate_stride >= width).  Y NULL: no block before (w_post and gate NULL); X_out may
+ * then be NULL too, for the norm alone.  dtype: any; width: a multiple of 8 up to
+ * 16384 (8192 in fp32).  With no tokens the pointers to rows may be NULL, whatever
+ * else is given.  Each output may be one of the row-by-row inputs, with the same
+ * stride. */
 lbgemm_status lbgemm_residual_norm(int dtype, int64_t tokens, int64_t width, const void* X,
                                    int64_t x_stride, const void* Y, int64_t y_stride,
                                    const void* w_post, const void* gate, int64_t gate_stride,
