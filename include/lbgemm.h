@@ -718,8 +718,9 @@ lbgemm_status lbgemm_moe_route(int dtype, int64_t tokens, int64_t experts, int64
  * hidden and inter: multiples of `group`.  dtype: LBGEMM_BF16 or LBGEMM_F16; the
  * inner vector silu(..) * (..) is rounded to dtype, as the second product's operand
  * (in fp16 it must stay below 65520), which makes the result's error some 1.4 times
- * what its own rounding leaves.  Everything else is summed in fp32 and rounded once.  experts up to 1024, top_k up
- * to 32, tokens * top_k up to 2^24.  The sum over j runs in the order of j.
+ * what its own rounding leaves.  Everything else is summed in fp32 and rounded once.
+ * experts up to 1024, top_k up to 32, tokens * top_k up to 2^24.  The sum over j
+ * runs in the order of j.
  * Scratch is taken as in lbgemm_run: 2 inter bytes a pick (token and choice), and
  * with more than a few picks an expert 4 hidden + 8 beside them (32768 tokens of 8
  * choices, hidden 7168, inter 2048: 8.6 GB).  A caller that has not got them gives
