@@ -9,9 +9,9 @@
 // behind it by issue slots: a word of eight codes takes twelve operations to
 // become halves (w4_codes.cuh).  So the codes go to the MMA's 16-row side, which
 // has no row to spare, and the tokens to its 8-column side.  Measured: 1 token x 128000 x
-// 4096 in 63 us (4.2 TB/s), x 11008 x 4096 in 10.7 (4 of them launch, staging and the last
-// sums); 24 tokens, 6 of 64 experts of 2048 / 1024, in 68 us (2.8 TB/s; logic operations
-// half of the time).
+// 4096 in 64 us (4.2 TB/s), x 11008 x 4096 in 13.0 beyond L2 and 10.7 from it (4 of them
+// launch, staging and the last sums); 24 tokens, 6 of 64 experts of 2048 / 1024, in 68 us (2.8
+// TB/s; logic operations half of the time).
 //
 // A CTA an SM, 24 warps.  CTAs take equal runs of weight rows: of the rows of all
 // experts with a pick one after the other (linear, up), or, so that a token's
@@ -233,7 +233,7 @@ struct Run {
 
 // kWarps: 24, as many as registers allow.  A mixture of few picks takes 12 and half of the
 // shared memory, so that the CTAs of `down` stand beside those of `up`: they look up their
-// picks and copy their first codes while `up` runs (1 token, 6 experts: 17.4 -> 14.9 us).
+// picks and copy their first codes while `up` runs (1 token, 6 experts: 17.4 -> 14.9 us from L2).
 constexpr int kAllWarps = 24, kFewWarps = 12, kFewPicks = 16;
 // Tiles of 8 columns in a round (24 tokens to 64 experts, 49 and 58 tiles a CTA: 68.3 us,
 // 69.7 with room for 48; no gain from 80).

@@ -24,9 +24,9 @@
 // one's MMAs.  A reader has a row a lane and turns 32 tokens through shared memory
 // into vectors along the rows.  A linear layer with few tiles is cut along k and joined by join().
 //
-// Measured: 4096 tokens x 11008 x 4096 in 217 us (1.70 PFLOP/s, what a plain product of
-// 16-bit numbers reaches being 1.90), 64 x 19456 x 8192 in 25 us (3.4 TB/s of weights), 12 x
-// 4096 x 11008 in 12.5; 4096 tokens, 6 of 64 experts of 2048 / 1024, in 348 us (0.87
+// Measured beyond L2: 4096 tokens x 11008 x 4096 in 215 us (1.71 PFLOP/s, what a plain product
+// of 16-bit numbers reaches being 1.90), 64 x 19456 x 8192 in 25 us (3.4 TB/s of weights), 12 x
+// 4096 x 11008 in 13.4; 4096 tokens, 6 of 64 experts of 2048 / 1024, in 350 us (0.87
 // PFLOP/s: blocks of tokens three quarters full; 67 us of sorting, gathering and joining).
 //
 // In a pair the full barriers and the accumulators' empty ones are the even CTA's and

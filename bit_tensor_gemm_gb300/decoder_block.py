@@ -6,7 +6,8 @@ A step of new tokens goes through
     lbgemm_residual_norm    the norm before attention
     AttentionLayer.step     attention over the 4-bit cache
     lbgemm_residual_norm    the norm after it, the residual stream, the next norm
-    lbgemm_w4_linear        the router's logits
+    lbgemm_w4_linear        the router's logits (its weights too are in 4 bits here: the
+                            library has no product of two 16-bit operands)
     lbgemm_moe_route        the experts of every token
     lbgemm_moe_w4           their products
     lbgemm_residual_norm    the norm after them and the residual stream
