@@ -681,9 +681,9 @@ cudaError_t launch_any(int dtype, const W4RowsParams& p, int warps, bool staged,
 //   1 x 16384 x 16384       42.7   59.2
 //   1 x 19456 x 28672       75.7   71.1
 //   1, 4 x 32768 x 8320     40.5, 40.3   51.1, 46.6
-// and from L2, shorter rows: 1, 4 and 8 x 11008 x 4096 10.9, 11.2, 12.1 and 12.6; 1 x 128000 x
-// 4096 66 and 94; 1 x 1024 x 1024 4.5 and 6.3.  Two blocks of 8 columns a pass: 12 x 4096 x
-// 11008 16.5 us, tiles 12.2.
+//   1 x 128000 x 4096       66     94
+// and from L2 1, 4 and 8 x 11008 x 4096 10.9, 11.2, 12.1 and 12.6; 1 x 1024 x 1024 4.5 and 6.3.
+// Two blocks of 8 columns a pass: 12 x 4096 x 11008 16.5 us, tiles 12.2.
 static bool linear_params(const W4LinearParams& l, int sm_count, W4RowsParams* p) {
   if (l.m > 8 || (l.k > 8192 && 2 * ((l.n + 127) / 128) <= sm_count)) return false;
   p->n = l.n;
